@@ -253,6 +253,102 @@ msa_status msa_select_rows(const msa_shape *shape, const float *scores_hbt,
                            const int32_t *seq_lens, int32_t *selected, void *workspace,
                            size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- the whole cache: dense decode, accumulated weights, eviction --------
+ * The three calls below work on every cached position instead of selected
+ * blocks.  They share msa_shape, the layouts above, the conventions above and
+ * one workspace; msa_workspace_init and msa_check_device_status work on it as
+ * on the other.  Differences to the calls above:
+ *   - num_q_heads is any multiple G of num_kv_heads with 1 <= G <= 64: query
+ *     head h uses KV head h / G;
+ *   - seq_lens[r] may be 0: an idle slot of a padded batch.  Its out rows are
+ *     0, its lse -inf, its weights untouched, its new length 0; its block
+ *     table row is not read.  A negative length, or one the table cannot
+ *     hold, is reported through the error word;
+ *   - topk, init_blocks and local_blocks are not looked at (topk is, where a
+ *     `selected` table is given), nor the index fields where no index keys are
+ *     given; num_requests * max_blocks_per_seq * num_kv_heads * the query rows'
+ *     tiles stays below 2^31, num_pages * num_kv_heads * 288 too, else
+ *     MSA_ERR_UNSUPPORTED;
+ *   - decode_ctas > 0 sets the persistent CTAs of the dense decode and of the
+ *     accumulation (at most 8192); 0 takes one per SM;
+ *   - bytes of a page behind the last cached position may hold anything
+ *     (infinities and NaN among it);
+ *   - nothing is kept in the workspace between calls but the error word.  Calls
+ *     on two streams that may overlap, and CUDA graphs that may, need a
+ *     workspace each. */
+
+/* Bytes of device workspace for the three calls below (0 if the shape is
+ * invalid or unsupported).  Pure host function. */
+size_t msa_cache_workspace_bytes(const msa_shape *shape);
+
+/* Attention of each token over all positions it sees (0 .. seq_lens[r] + j - 1):
+ * the result of msa_sparse_decode with every block selected, without its limit
+ * of 256 blocks.  The pages of a request are read once for all its tokens, are
+ * split over persistent CTAs and joined in a fixed order (no atomics: the same
+ * inputs give the same bits).  out: bf16, lse: fp32. */
+msa_status msa_dense_decode(const msa_shape *shape, const void *q, const void *kv_pool,
+                            const int32_t *block_table, const int32_t *seq_lens, void *out,
+                            float *lse, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/* The attention weight of every cached position, accumulated over steps:
+ *   weights_out[r][g][p] = decay * weights_in[r][g][p]
+ *                          + sum over tokens j and heads h of KV head g that see p
+ *                            of exp(softmax_scale * q . k[p] - lse)
+ * for p < seq_lens[r] + q_per_req - 1 (other elements stay as they are), with
+ * the lse that msa_dense_decode (selected = NULL) or msa_sparse_decode
+ * (selected = its table: only positions in blocks a token selected count for
+ * it) returned for the same inputs.  A token with lse = -inf adds nothing.
+ *   selected     int32 [T][Hs][topk] or NULL
+ *   weights_in   fp32 [num_requests][Hkv][max_blocks_per_seq * 128], or NULL
+ *                for zeros; positions of this step's own tokens
+ *                (p >= seq_lens[r] - 1) count as 0 whatever it holds, so rows
+ *                need no clearing when a token is cached (or a rejected draft
+ *                token's row is written again)
+ *   weights_out  the same layout; may be weights_in
+ *   decay        finite; 1 keeps the plain sum, less fades older steps */
+msa_status msa_weight_accumulate(const msa_shape *shape, const void *q, const void *kv_pool,
+                                 const int32_t *block_table, const int32_t *seq_lens,
+                                 const int32_t *selected, const float *lse, float decay,
+                                 const float *weights_in, float *weights_out, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/* Eviction by accumulated weight: of the n = seq_lens[r] + q_per_req - 1 cached
+ * positions of request r, min(n, keep) stay -- the first `first`, the last
+ * `last`, and those with the largest weights (NaN above every number), ties
+ * to the lower position -- and their rows are copied, in ascending order of
+ * position, to positions 0, 1, ... of new pages.  One list a request when
+ * num_index_heads is 1, on the maximum over KV heads of their weights; one per
+ * KV head otherwise (Hs lists, as for block tables), index head i moving with
+ * KV head i / (Hi / Hkv).
+ *   weights      fp32 [num_requests][Hkv][max_blocks_per_seq * 128]
+ *   new_table    int32 [num_requests][ceil(keep / 128)]: pages of kv_pool (and
+ *                idxk_pool) that receive the rows.  Only entries below
+ *                ceil(min(n, keep) / 128) are read, only the rows copied are
+ *                written.  The new pages are pages that no block table row of
+ *                the call reads and no other new row names, else the copied
+ *                rows are unspecified; old pages are not written and may be
+ *                shared between requests
+ *   kv_pool, idxk_pool, idxk_scales  the pools of the layouts above;
+ *                idxk_pool may be NULL (no index keys), idxk_scales is used for
+ *                MSA_NVFP4 index keys.  Stored bytes are moved as they are
+ *   new_weights  fp32 [num_requests][Hkv][ceil(keep / 128) * 128] or NULL: the
+ *                weights of the kept positions (elements below min(n, keep))
+ *   kept         int32 [num_requests][Hs][keep], ascending, -1 padded
+ *   new_lens     int32 [num_requests]: min(n, keep) - q_per_req + 1, the
+ *                seq_lens of the shortened cache (0 for an idle slot)
+ * keep >= max(1, q_per_req), first >= 0, last >= q_per_req - 1 and
+ * first + last <= keep, else MSA_ERR_INVALID_ARGUMENT; so are
+ * new_table == block_table, new_weights == weights and new_lens == seq_lens.
+ * keep above 2097152 is MSA_ERR_UNSUPPORTED.  A page id outside the pool is
+ * reported through the error word and its rows are skipped. */
+msa_status msa_cache_evict(const msa_shape *shape, int32_t keep, int32_t first, int32_t last,
+                           const float *weights, const int32_t *block_table,
+                           const int32_t *seq_lens, const int32_t *new_table, void *kv_pool,
+                           void *idxk_pool, void *idxk_scales, float *new_weights, int32_t *kept,
+                           int32_t *new_lens, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
 /* Size of the fixed device scratch used by msa_sparse_decode_noalloc. */
 #define MSA_NOALLOC_SCRATCH_BYTES (8u << 20)
 

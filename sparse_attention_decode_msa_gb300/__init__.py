@@ -71,6 +71,12 @@ _SIGNATURES = {
                                      ctypes.c_size_t, _p]),
     "msa_select_rows": (ctypes.c_int, [ctypes.POINTER(MsaShape), _p, _p, _p, _p, ctypes.c_size_t,
                                        _p]),
+    "msa_cache_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MsaShape)]),
+    "msa_dense_decode": (ctypes.c_int, [ctypes.POINTER(MsaShape)] + [_p] * 7 + [ctypes.c_size_t, _p]),
+    "msa_weight_accumulate": (ctypes.c_int, [ctypes.POINTER(MsaShape)] + [_p] * 6 + [
+        ctypes.c_float, _p, _p, _p, ctypes.c_size_t, _p]),
+    "msa_cache_evict": (ctypes.c_int, [ctypes.POINTER(MsaShape)] + [ctypes.c_int32] * 3 + [_p] * 11 + [
+        ctypes.c_size_t, _p]),
     "msa_set_decode_wait_limit": (ctypes.c_int, [ctypes.c_int64]),
     "msa_check_device_status": (ctypes.c_int, [_p, _p]),
     "msa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -114,6 +120,19 @@ def _ptr(x):
         return None
     if isinstance(x, int):
         return x
+    return x.data_ptr()
+
+
+def _buf(x):
+    """Device pointer of a whole-cache operator's buffer: a tensor must be dense and on the
+    current device (the library sees only an address), an int is taken as it is."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("buffers must be contiguous CUDA tensors")
+    import torch
+    if x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"buffer on {x.device}, but the current device is {torch.cuda.current_device()}")
     return x.data_ptr()
 
 
@@ -203,6 +222,39 @@ def msa_select_rows(shape, scores_hbt, seq_lens, selected, workspace, workspace_
     _check(load().msa_select_rows(ctypes.byref(shape), _ptr(scores_hbt), _ptr(seq_lens),
                                   _ptr(selected), _ptr(workspace), int(workspace_bytes),
                                   _stream(stream)), "msa_select_rows")
+
+
+def msa_cache_workspace_bytes(shape: MsaShape) -> int:
+    """Workspace of the whole-cache operators below (0: shape not taken)."""
+    return int(load().msa_cache_workspace_bytes(ctypes.byref(shape)))
+
+
+def msa_dense_decode(shape, q, kv_pool, block_table, seq_lens, out, lse, workspace, workspace_bytes,
+                     stream=None):
+    """Attention over every cached position a token sees."""
+    _check(load().msa_dense_decode(ctypes.byref(shape), _buf(q), _buf(kv_pool), _buf(block_table),
+                                   _buf(seq_lens), _buf(out), _buf(lse), _buf(workspace),
+                                   int(workspace_bytes), _stream(stream)), "msa_dense_decode")
+
+
+def msa_weight_accumulate(shape, q, kv_pool, block_table, seq_lens, selected, lse, decay, weights_in,
+                          weights_out, workspace, workspace_bytes, stream=None):
+    """Add this step's attention weights to every cached position's sum (selected: None after a
+    dense step, the block tables after a sparse one)."""
+    _check(load().msa_weight_accumulate(ctypes.byref(shape), _buf(q), _buf(kv_pool), _buf(block_table),
+                                        _buf(seq_lens), _buf(selected), _buf(lse), float(decay),
+                                        _buf(weights_in), _buf(weights_out), _buf(workspace),
+                                        int(workspace_bytes), _stream(stream)), "msa_weight_accumulate")
+
+
+def msa_cache_evict(shape, keep, first, last, weights, block_table, seq_lens, new_table, kv_pool, idxk_pool,
+                    idxk_scales, new_weights, kept, new_lens, workspace, workspace_bytes, stream=None):
+    """Keep the heaviest positions of every request, copied in order to the pages of new_table."""
+    _check(load().msa_cache_evict(ctypes.byref(shape), int(keep), int(first), int(last), _buf(weights),
+                                  _buf(block_table), _buf(seq_lens), _buf(new_table), _buf(kv_pool),
+                                  _buf(idxk_pool), _buf(idxk_scales), _buf(new_weights), _buf(kept),
+                                  _buf(new_lens), _buf(workspace), int(workspace_bytes),
+                                  _stream(stream)), "msa_cache_evict")
 
 
 def msa_check_device_status(workspace, stream=None) -> int:

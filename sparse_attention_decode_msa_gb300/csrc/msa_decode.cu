@@ -1627,8 +1627,9 @@ cudaError_t launch_umma_t(const DecodeParams &p, const CUtensorMap &kv, const CU
 
 } // namespace
 
-bool encode_2d_sw128(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
-                     uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows)
+bool encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
+               uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
+               CUtensorMapSwizzle swizzle)
 {
     EncodeFn enc = get_encode();
     if (!enc)
@@ -1638,8 +1639,15 @@ bool encode_2d_sw128(CUtensorMap *map, CUtensorMapDataType dtype, const void *ba
     const cuuint32_t box[2] = {box_inner, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_2d_sw128(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
+                     uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows)
+{
+    return encode_2d(map, dtype, base, inner, rows, row_bytes, box_inner, box_rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 cudaError_t launch_sparse_decode(const DecodeParams &p, const void *kv_pool, int kv_dtype, int ctas,

@@ -144,8 +144,12 @@ __host__ __device__ constexpr size_t align_to(size_t v, size_t a)
 }
 
 // Tensor map of a row-major 2-D array [rows][inner] (row pitch `row_bytes`)
-// loaded in boxes of box_inner x box_rows with the 128-byte swizzle; false if
-// the driver's encoder is unavailable or rejects the map.
+// loaded in boxes of box_inner x box_rows with the given swizzle (the 128-byte
+// one in encode_2d_sw128); false if the driver's encoder is unavailable or
+// rejects the map.
+bool encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
+               uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
+               CUtensorMapSwizzle swizzle);
 bool encode_2d_sw128(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
                      uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows);
 

@@ -8,8 +8,9 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (make_shape, msa_decode_step, msa_index_score, msa_kv_update, msa_select_topk,
-               msa_sparse_decode, msa_workspace_bytes, msa_workspace_init)
+from . import (make_shape, msa_cache_evict, msa_cache_workspace_bytes, msa_decode_step, msa_dense_decode,
+               msa_index_score, msa_kv_update, msa_select_topk, msa_sparse_decode, msa_weight_accumulate,
+               msa_workspace_bytes, msa_workspace_init)
 
 
 def _dev(a, device):
@@ -70,6 +71,7 @@ class DeviceProblem:
         dp.shape = type(self.shape).from_buffer_copy(self.shape)
         dp.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         msa_workspace_init(dp.ws, dp.ws_bytes)
+        dp.cache_ws = None
         return dp
 
     def set_decode_ctas(self, n: int):
@@ -103,6 +105,43 @@ class DeviceProblem:
                         self.block_scores if keep_intermediates else None,
                         self.selected if keep_intermediates else None,
                         self.out, self.lse, self.ws, self.ws_bytes, stream)
+
+    # ---- the whole cache ----
+    def _cache_workspace(self):
+        import torch
+
+        need = msa_cache_workspace_bytes(self.shape)
+        if getattr(self, "cache_ws", None) is None or self.cache_ws.numel() < need:
+            self.cache_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            msa_workspace_init(self.cache_ws, need)
+        return self.cache_ws, self.cache_ws.numel()
+
+    def dense_decode(self, stream=None):
+        """Attention over every cached position, into out and lse."""
+        msa_dense_decode(self.shape, self.q, self.kv, self.block_table, self.seq_lens, self.out,
+                         self.lse, *self._cache_workspace(), stream)
+
+    def weight_accumulate(self, weights_in, weights_out, decay: float = 1.0, sparse: bool = False,
+                          stream=None):
+        """Add the weights of the step whose lse this problem holds (sparse: of its selection)."""
+        msa_weight_accumulate(self.shape, self.q, self.kv, self.block_table, self.seq_lens,
+                              self.selected if sparse else None, self.lse, decay, weights_in,
+                              weights_out, *self._cache_workspace(), stream)
+
+    def evict(self, weights, new_table, keep: int, first: int = 0, last: int = 0, stream=None) -> dict:
+        """Copy the kept positions to new_table's pages; the lists, lengths and weights of the
+        shortened cache (block_table and seq_lens stay as they are)."""
+        import torch
+
+        R, Hkv = self.shape.num_requests, self.shape.num_kv_heads
+        Hs = 1 if self.shape.num_index_heads == 1 else Hkv
+        kept = torch.empty((R, Hs, keep), dtype=torch.int32, device=self.device)
+        lens = torch.empty(R, dtype=torch.int32, device=self.device)
+        new_weights = torch.zeros((R, Hkv, -(-keep // 128) * 128), device=self.device)
+        msa_cache_evict(self.shape, keep, first, last, weights, self.block_table, self.seq_lens,
+                        new_table, self.kv, self.idxk, self.idxk_scales, new_weights, kept, lens,
+                        *self._cache_workspace(), stream)
+        return {"kept": kept, "seq_lens": lens, "weights": new_weights}
 
     def kv_update(self, update: dict, stream=None):
         """Write this step's new tokens (synth.make_update arrays) into the pools."""
