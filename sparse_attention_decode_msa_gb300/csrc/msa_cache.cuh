@@ -20,7 +20,7 @@
 namespace msa {
 
 constexpr int kMaxGroup = 64;      // query heads per KV head of the whole-cache operators
-constexpr int kCacheCtaBound = 256; // workspace bound on the default persistent CTAs
+constexpr int kCacheCtaBound = 160; // workspace bound on the default persistent CTAs
 
 // KV formats of the kernel instances
 constexpr int kFmtBf16 = 0, kFmtFp8 = 1, kFmtF4 = 2;
@@ -71,6 +71,8 @@ struct EvictParams {
 };
 
 cudaError_t launch_dense_decode(const DenseParams &p, int kv_dtype, int ctas, cudaStream_t stream);
+// Units of more than 16 query rows, on the tcgen05 tensor cores (the join is the caller's).
+cudaError_t launch_dense_umma(const DenseParams &p, const CUtensorMap &map, int kv_dtype, int ctas, cudaStream_t stream);
 cudaError_t launch_weight_accumulate(const WeightParams &p, int kv_dtype, int ctas,
                                      cudaStream_t stream);
 cudaError_t launch_cache_evict(const EvictParams &p, cudaStream_t stream);

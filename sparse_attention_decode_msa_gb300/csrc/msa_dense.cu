@@ -632,36 +632,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the partials of one row of one cut unit, in CTA order: blockIdx.x + 1
-// is the CTA at whose start the unit was first cut, blockIdx.y the row.  Four
-// warps take every fourth partial; lane l has dimensions 4 l .. 4 l + 3.
-__global__ void __launch_bounds__(128) dense_join_kernel(const DenseParams p, int tile_rows)
+// Joins the partials of the rows of one cut unit, in CTA order: blockIdx.x + 1
+// is the CTA at whose start the unit was first cut.  SPLIT warps share a row
+// (warp s takes every SPLIT-th partial, as many units are cut often only where
+// they have few rows); lane l has dimensions 4 l .. 4 l + 3.
+template <int SPLIT>
+__global__ void __launch_bounds__(256) dense_join_kernel(const DenseParams p, int tile_rows)
 {
-    __shared__ float sm_m[4], sm_l[4];
-    __shared__ float4 sm_o[4][32];
-    const int row = blockIdx.y, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    __shared__ float sm_m[8], sm_l[8];
+    __shared__ float4 sm_o[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % SPLIT;
     grid_dependency_wait();
     const int4 jn = p.joins[blockIdx.x + 1];
     if (jn.z < 0)
         return;
+    const int row = blockIdx.y * (8 / SPLIT) + warp / SPLIT;
     const int g = jn.y / p.tiles, i = (jn.y - g * p.tiles) * tile_rows + row;
-    if (i >= p.rows)
+    const bool real = row < tile_rows && i < p.rows;
+    if (SPLIT == 1 && !real)
         return;
     const float ninf = __uint_as_float(0xFF800000u);
     const size_t floats = (size_t)tile_rows * (kDim + 2);
     float M = ninf, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = jn.z + w; c <= jn.w; c += 16) {
+    for (int c = jn.z + w; c <= jn.w && real; c += 4 * SPLIT) {
         float m[4], l[4];
         float4 v[4];
-        const int k = min(4, (jn.w - c) / 4 + 1);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
+            const int cc = c + SPLIT * s;
             m[s] = ninf;
             l[s] = 0.f;
             v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (s < k) {
-                const int cc = c + 4 * s;
+            if (cc <= jn.w) {
                 const float *slot = p.partial + (size_t)(2 * cc + (cc < jn.w ? 1 : 0)) * floats;
                 m[s] = slot[(size_t)tile_rows * kDim + row];
                 l[s] = slot[(size_t)tile_rows * (kDim + 1) + row];
@@ -669,36 +672,41 @@ __global__ void __launch_bounds__(128) dense_join_kernel(const DenseParams p, in
             }
         }
         const float n = fmaxf(M, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-        if (n != ninf) {
-            const float f = M == ninf ? 0.f : ex2(M - n);
-            L *= f;
-            o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        const float ref = n == ninf ? 0.f : n;
+        const float f = ex2(M - ref);
+        L *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float e = m[s] == ninf ? 0.f : ex2(m[s] - n);
-                L += l[s] * e;
-                o.x += v[s].x * e, o.y += v[s].y * e, o.z += v[s].z * e, o.w += v[s].w * e;
-            }
-            M = n;
+        for (int s = 0; s < 4; ++s) {
+            const float e = ex2(m[s] - ref);
+            L += l[s] * e;
+            o.x += v[s].x * e, o.y += v[s].y * e, o.z += v[s].z * e, o.w += v[s].w * e;
         }
+        M = n;
     }
-    if (lane == 0) {
-        sm_m[w] = M;
-        sm_l[w] = L;
-    }
-    sm_o[w][lane] = o;
-    __syncthreads();
-    if (w != 0)
-        return;
-    M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    L = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (SPLIT > 1) {
+        if (lane == 0) {
+            sm_m[warp] = M;
+            sm_l[warp] = L;
+        }
+        sm_o[warp][lane] = o;
+        __syncthreads();
+        if (w != 0 || !real)
+            return;
+        M = ninf;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const float e = sm_m[s] == ninf ? 0.f : ex2(sm_m[s] - M);
-        const float4 v = sm_o[s][lane];
-        L += sm_l[s] * e;
-        o.x += v.x * e, o.y += v.y * e, o.z += v.z * e, o.w += v.w * e;
+        for (int s = 0; s < SPLIT; ++s)
+            M = fmaxf(M, sm_m[warp + s]);
+        const float ref = M == ninf ? 0.f : M;
+        L = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < SPLIT; ++s) {
+            const float e = ex2(sm_m[warp + s] - ref);
+            const float4 v = sm_o[warp + s][lane];
+            L += sm_l[warp + s] * e;
+            o.x += v.x * e, o.y += v.y * e, o.z += v.z * e, o.w += v.w * e;
+        }
     }
     const float f = L > 0.f || L != L ? p.v_scale / L : 0.f;
     const int j = i / p.G;
@@ -706,6 +714,14 @@ __global__ void __launch_bounds__(128) dense_join_kernel(const DenseParams p, in
     reinterpret_cast<uint2 *>(p.out + out * kDim)[lane] = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
     if (lane == 0)
         p.lse[out] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+cudaError_t launch_join(const DenseParams &p, int tile_rows, int ctas, cudaStream_t stream)
+{
+    const int rows = p.rows < tile_rows ? p.rows : tile_rows;
+    if (tile_rows == 16)
+        return launch_kernel(dense_join_kernel<4>, dim3(ctas - 1, (rows + 1) / 2), dim3(256), 0, stream, true, p, tile_rows);
+    return launch_kernel(dense_join_kernel<1>, dim3(ctas - 1, (rows + 7) / 8), dim3(256), 0, stream, true, p, tile_rows);
 }
 
 template <int FMT, int MT>
@@ -717,25 +733,21 @@ cudaError_t launch_t(const DenseParams &p, const CUtensorMap &map, int ctas, cud
         return e;
     e = launch_kernel(dense_stream_kernel<FMT, MT>, dim3(ctas), dim3(kThreads), smem, stream, false, map, p);
     if (e == cudaSuccess && ctas > 1)
-        e = launch_kernel(dense_join_kernel, dim3(ctas - 1, min(16 * MT, p.rows)), dim3(128), 0, stream, true, p, 16 * MT);
+        e = launch_join(p, 16 * MT, ctas, stream);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int FMT>
 cudaError_t launch_fmt(const DenseParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
 {
-    switch (dense_tile_rows(p.rows)) {
-    case 16: return launch_t<FMT, 1>(p, map, ctas, stream);
-    case 32: return launch_t<FMT, 2>(p, map, ctas, stream);
-    default: return launch_t<FMT, 4>(p, map, ctas, stream);
-    }
+    return launch_t<FMT, 1>(p, map, ctas, stream);
 }
 
 } // namespace
 
 int dense_tile_rows(int rows)
 {
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
 }
 
 cudaError_t launch_dense_decode(const DenseParams &p, int kv_dtype, int ctas, cudaStream_t stream)
@@ -743,6 +755,12 @@ cudaError_t launch_dense_decode(const DenseParams &p, int kv_dtype, int ctas, cu
     CUtensorMap map;
     if (!encode_pool_map(&map, p.kv, kv_dtype, p.num_pages, p.Hkv))
         return cudaErrorInvalidValue;
+    if (p.rows > 16) {
+        cudaError_t e = launch_dense_umma(p, map, kv_dtype, ctas, stream);
+        if (e == cudaSuccess && ctas > 1)
+            e = launch_join(p, dense_tile_rows(p.rows), ctas, stream);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
     if (kv_dtype == MSA_BF16)
         return launch_fmt<kFmtBf16>(p, map, ctas, stream);
     if (kv_dtype == MSA_FP8_E4M3)

@@ -1,0 +1,808 @@
+// msa_dense_umma.cu -- dense decode for many query rows (speculative tokens, a
+// prompt's last chunk): S = Q K^T and O += P V on the tcgen05 tensor cores.
+//
+// Mathematics as in msa_dense.cu: a running maximum m, l = sum 2^(s - m) and
+// O = sum 2^(s - m) V per query row, fp32, one pass over the pages.  Rows are
+// the M dimension, 128 of them per accumulator, one thread per row: the
+// softmax needs no exchange between threads.
+//
+// Two streams share a CTA's pages, so that the tensor cores work for one while
+// the other is in its softmax.  With more than 128 query rows a (request, KV
+// head), stream t has rows 128 t .. of a 256-row tile and both use every page;
+// with fewer, both have the same rows, stream t takes every second page, and
+// the two (m, l, O) are added at the end.
+//
+// Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA
+// lands them (K-major), P in tensor memory over the S it came from, V tiles as
+// landed (MN-major).  bf16 P is a pair hi + lo (16 significant bits; the
+// rounding of P to bf16 alone would weigh as much as the output's); E4M3 and
+// NVFP4 tiles are widened to f16 by converter warps and P is one f16 (11 bits).
+//
+// TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
+// Warps: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 V check of last pages
+// (bf16), 3 outputs of idle slots, 4-7 and 8-11 softmax of stream 0 and 1,
+// 12-19 converters (E4M3, NVFP4).
+//
+// What bounds it: the tensor cores (S and P V of 128 x 128 x 128 are 512 clocks
+// each, 1024 for P V with hi + lo) when rows are many, HBM when they are few.
+#include "msa_cache.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kTile16 = 32768;   // a 16-bit K, V or Q tile
+constexpr int kConvWarps = 8;
+constexpr int kStaged = 4;       // widened tiles in flight
+constexpr float kSlack = 8.f;    // how far (log2) a row's maximum may pass its reference before O is rescaled
+constexpr float kPUp16 = 7.f;    // f16 P: 2^7 2^(s - m), at most 2^15 with the slack
+
+__host__ __device__ constexpr int threads_of(int fmt)
+{
+    return fmt == kFmtBf16 ? 384 : 384 + 32 * kConvWarps;
+}
+
+// Tiles (K or V) in the ring.
+__host__ __device__ constexpr int ring_tiles(int fmt, bool two)
+{
+    return fmt == kFmtBf16 ? (two ? 5 : 6) : fmt == kFmtFp8 ? (two ? 2 : 4) : (two ? 3 : 7);
+}
+
+struct Smem {
+    int ring, staged, q, ml, bars, misc, total;
+};
+
+__host__ __device__ constexpr Smem smem_layout(int fmt, bool two)
+{
+    Smem s{};
+    s.ring = 0;
+    s.staged = ring_tiles(fmt, two) * tile_bytes(fmt);
+    s.q = s.staged + (fmt == kFmtBf16 ? 0 : kStaged * kTile16);
+    s.ml = s.q + (two ? 2 : 1) * kTile16; // m[128], l[128] of stream 1 (one row tile)
+    s.bars = s.ml + (two ? 0 : 2 * 128 * 4);
+    s.misc = s.bars + (2 * ring_tiles(fmt, two) + 2 * kStaged + 16) * 8;
+    s.total = s.misc + 64 + 1024;
+    return s;
+}
+static_assert(smem_layout(kFmtBf16, true).total <= 232448 && smem_layout(kFmtBf16, false).total <= 232448 &&
+                  smem_layout(kFmtFp8, true).total <= 232448 && smem_layout(kFmtFp8, false).total <= 232448 &&
+                  smem_layout(kFmtF4, true).total <= 232448 && smem_layout(kFmtF4, false).total <= 232448,
+              "shared memory");
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, issued by one thread.
+__device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// 32 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+
+__device__ __forceinline__ void tmem_wait_ld()
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+        : "memory");
+}
+
+// One stored K (0) or V (1) value in global memory, without its tensor scale.
+template <int FMT>
+__device__ __noinline__ float stored_value(const uint8_t *kv, long long tile, int row, int d)
+{
+    float a, b;
+    if (FMT == kFmtBf16)
+        return __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t *>(kv + (tile * kPage + row) * 256 + 2 * d) << 16);
+    if (FMT == kFmtFp8) {
+        f16x2_to_f32x2(e4m3x2_to_f16x2(kv[(tile * kPage + row) * 128 + d]), a, b);
+        return a;
+    }
+    const uint8_t *t = kv + tile * 9216;
+    const uint32_t byte = t[row * 64 + (d >> 1)];
+    f16x2_to_f32x2(e2m1x2_to_f16x2(d & 1 ? byte >> 4 : byte & 15u), a, b);
+    const float v = a;
+    f16x2_to_f32x2(e4m3x2_to_f16x2(t[8192 + row * 8 + (d >> 4)]), a, b);
+    return v * a;
+}
+
+__device__ __forceinline__ bool finite(float v)
+{
+    return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
+}
+
+// The share of a CTA, unit by unit.  Every role walks it alike.
+struct Walk {
+    int x, x1, r, u, b, nb, seq_len, seg;
+    __device__ __forceinline__ int pages() const { return min(nb - b, x1 - x); }
+    __device__ __forceinline__ void next(const DenseParams &p, int heads)
+    {
+        x += pages();
+        ++seg;
+        b = 0;
+        if (++u == heads) {
+            u = 0;
+            bool bad;
+            do {
+                if (++r >= p.R)
+                    break;
+                seq_len = p.seq_lens[r];
+                nb = cached_blocks(seq_len, p.nq, p.maxB, &bad);
+            } while (nb == 0);
+        }
+    }
+};
+
+// Place of a tile in the order in which the issuer uses the tiles of n pages.
+template <bool TWO>
+__device__ __forceinline__ int order_of_k(int page)
+{
+    return TWO ? 2 * page : page < 2 ? page : 2 * page - 1;
+}
+template <bool TWO>
+__device__ __forceinline__ int order_of_v(int page, int n)
+{
+    return TWO ? 2 * page + 1 : min(2 * page + 2, 2 * n - 1);
+}
+
+template <int FMT, bool TWO>
+__global__ void __launch_bounds__(threads_of(FMT), 1)
+    dense_umma_kernel(const __grid_constant__ CUtensorMap map, const DenseParams p)
+{
+    constexpr int TILES = ring_tiles(FMT, TWO), TB = tile_bytes(FMT), NT = threads_of(FMT);
+    constexpr bool CONV = FMT != kFmtBf16;
+    constexpr int ROWS = TWO ? 256 : 128;
+    constexpr Smem L = smem_layout(FMT, TWO);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int scan_tmp[NT / 32 + 1];
+    __shared__ int start_r, start_before;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int later_bad[8]; // unit counter + 1 where V rows of draft tokens are not finite
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *gsm = smem_raw + (smem - smem_u32(smem_raw));
+    const uint32_t full = smem + L.bars, empty = full + TILES * 8, sfull = empty + TILES * 8, sempty = sfull + kStaged * 8;
+    const uint32_t q_full = sempty + kStaged * 8, q_free = q_full + 16, s_full = q_free + 8, p_full = s_full + 16,
+                   o_done = p_full + 16, o_free = o_done + 16, v_fixed = o_free + 16, v_landed = v_fixed + 8,
+                   drain = v_landed + 8;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gsm + L.misc);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int heads = p.Hkv * p.tiles;
+    const long long wl = p.wait_limit;
+
+    launch_dependents();
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&map);
+        for (int i = 0; i < TILES; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, CONV ? kConvWarps : 1);
+        }
+        for (int i = 0; i < kStaged; ++i) {
+            mbar_init(sfull + 8 * i, kConvWarps);
+            mbar_init(sempty + 8 * i, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(q_full + 8 * t, 4);
+            mbar_init(s_full + 8 * t, 1);
+            mbar_init(p_full + 8 * t, 4);
+            mbar_init(o_done + 8 * t, 1);
+            mbar_init(o_free + 8 * t, 4);
+        }
+        mbar_init(q_free, 1);
+        mbar_init(v_fixed, 1);
+        mbar_init(v_landed, 1);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        *abort_flag = 0;
+    }
+    if (threadIdx.x < 8)
+        later_bad[threadIdx.x] = 0;
+    if (warp == 1)
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+
+    const int per = (p.R + NT - 1) / NT;
+    const int lo = min(p.R, (int)threadIdx.x * per), hi = min(p.R, lo + per);
+    int total;
+    const int before = scan_blocks(p, lo, hi, scan_tmp, &total);
+    const int W = total * heads;
+    Walk w{};
+    w.x = range_start(blockIdx.x, W, gridDim.x);
+    w.x1 = range_start(blockIdx.x + 1, W, gridDim.x);
+    w.nb = 1;
+    if (w.x < w.x1) {
+        int b = before;
+        for (int r = lo; r < hi; ++r) {
+            bool bad;
+            const int nb = cached_blocks(p.seq_lens[r], p.nq, p.maxB, &bad);
+            if (nb > 0 && b * heads <= w.x && w.x < (b + nb) * heads) {
+                start_r = r;
+                start_before = b;
+            }
+            b += nb;
+        }
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = tmem_slot;
+    if (w.x < w.x1) {
+        bool bad;
+        w.r = start_r;
+        w.seq_len = p.seq_lens[w.r];
+        w.nb = cached_blocks(w.seq_len, p.nq, p.maxB, &bad);
+        const int in = w.x - start_before * heads;
+        w.u = in / w.nb;
+        w.b = in - w.u * w.nb;
+    }
+    if (threadIdx.x == 0) {
+        int c0 = -1, c1 = -1;
+        if (w.x < w.x1 && w.b > 0) {
+            c0 = range_of(w.x - w.b, W, gridDim.x);
+            c1 = range_of(w.x - w.b + w.nb - 1, W, gridDim.x);
+            if (c0 != (int)blockIdx.x - 1)
+                c0 = c1 = -1;
+        }
+        p.joins[blockIdx.x] = make_int4(w.r, w.u, c0, c1);
+    }
+    // a wait that ran out: the CTA's roles run on without waiting, so that all
+    // reach the end; what they compute is unspecified
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!ring_wait(bar, parity, abort_flag, wl) && !*abort_flag) {
+            *abort_flag = 1;
+            set_error(p.err, kErrTimeout);
+        }
+    };
+
+    if (warp == 0) {
+        // ---- producer: K and V tiles in the order of their use ----
+        int z = 0, st = 0;
+        uint32_t ph = 0;
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages(), g = w.u / p.tiles;
+            const int32_t *row = p.block_table + (size_t)w.r * p.maxB + w.b;
+            // two windows of 32 table entries: K runs at most two pages ahead of V
+            int ent = 0, ent0 = -1, prev = 0;
+            int kp = 0, vp = 0;
+            for (int i = 0; i < 2 * n; ++i) {
+                const bool is_k = kp < n && order_of_k<TWO>(kp) == i;
+                const int pg = is_k ? kp++ : vp++;
+                const int win = pg >> 5;
+                if (win > ent0) {
+                    prev = ent;
+                    ent0 = win;
+                    ent = 32 * win + lane < n ? row[32 * win + lane] : 0;
+                }
+                long long page = __shfl_sync(0xffffffffu, win == ent0 ? ent : prev, pg & 31);
+                if (page < 0 || page >= p.num_pages) {
+                    if (lane == 0)
+                        set_error(p.err, kErrPage);
+                    page = 0; // in the pool: the outputs of the call are unspecified
+                }
+                if (z >= TILES)
+                    wait(empty + 8 * st, ph ^ 1u);
+                if (__any_sync(0xffffffffu, *abort_flag != 0))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full + 8 * st, TB);
+                    load_tile<FMT>(smem + st * TB, &map, p.kv, (page * 2 + (is_k ? 0 : 1)) * p.Hkv + g, full + 8 * st);
+                }
+                __syncwarp();
+                ++z;
+                if (++st == TILES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (__any_sync(0xffffffffu, *abort_flag != 0))
+                break;
+        }
+        if (lane == 0) // the CTA's memory must outlive the copies in flight
+            for (int i = max(0, z - TILES); i < z; ++i)
+                mbar_wait_bounded(full + 8 * (i % TILES), (uint32_t)(i / TILES) & 1u);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- MMA issuer ----
+        if (lane == 0) {
+            constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
+            constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, 0, 0) & kTypes;
+            constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
+            int z0 = 0, fixes = 0;
+            uint32_t steps[2] = {0u, 0u};
+            auto tile_wait = [&](int z) {
+                wait(CONV ? sfull + 8 * (z % kStaged) : full + 8 * (z % TILES), (uint32_t)(z / (CONV ? kStaged : TILES)) & 1u);
+            };
+            auto tile_at = [&](int z) { return CONV ? smem + L.staged + (z % kStaged) * kTile16 : smem + (z % TILES) * TB; };
+            auto tile_free = [&](int z) { umma_commit(CONV ? sempty + 8 * (z % kStaged) : empty + 8 * (z % TILES)); };
+            for (; w.x < w.x1; w.next(p, heads)) {
+                const int n = w.pages();
+                const int cnt[2] = {TWO ? n : (n + 1) / 2, TWO ? n : n / 2};
+                int scores_left = cnt[0] + cnt[1];
+                wait(q_full, w.seg & 1);
+                if (TWO)
+                    wait(q_full + 8, w.seg & 1);
+                tcgen05_after_sync();
+                auto scores = [&](int t, int i) {
+                    const int z = z0 + order_of_k<TWO>(TWO ? i : 2 * i + t);
+                    tile_wait(z);
+                    if (*abort_flag)
+                        return;
+                    tcgen05_after_sync();
+                    const uint32_t k = tile_at(z), q = smem + L.q + (TWO ? t * kTile16 : 0);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16(tmem + 128 * t, umma_desc_sw128(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                  umma_desc_sw128(k + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), idesc_s, ks > 0);
+                    umma_commit(s_full + 8 * t);
+                    if (!TWO || t == 1)
+                        tile_free(z);
+                    if (--scores_left == 0)
+                        umma_commit(q_free);
+                };
+                for (int t = 0; t < 2; ++t)
+                    if (cnt[t] > 0)
+                        scores(t, 0);
+                for (int i = 0; i < cnt[0]; ++i)
+                    for (int t = 0; t < 2; ++t) {
+                        if (i >= cnt[t])
+                            continue;
+                        const int page = TWO ? i : 2 * i + t, z = z0 + order_of_v<TWO>(page, n);
+                        wait(p_full + 8 * t, steps[t]++ & 1u);
+                        if (i == 0 && w.seg > 0)
+                            wait(o_free + 8 * t, (w.seg - 1) & 1);
+                        tile_wait(z);
+                        if (!CONV && (!TWO || t == 0) && (w.b + page + 1) * kPage > w.seq_len)
+                        {
+                            mbar_arrive(v_landed); // checked by warp 2, which waits for this and not
+                            wait(v_fixed, fixes++ & 1); // for the copy: phases it does not follow
+                        }
+                        if (*abort_flag)
+                            break;
+                        tcgen05_after_sync();
+                        const uint32_t v = tile_at(z), o = tmem + 256 + 128 * t;
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks) { // V, MN-major: 16 positions are 16 rows of 128 bytes
+                            const uint64_t bv = umma_desc_sw128(v + ks * 2048, 16384, 1024);
+                            const uint32_t a = tmem + 128 * t + 32 * (ks >> 1) + 8 * (ks & 1);
+                            umma_ta(o, a, bv, idesc_o, i > 0 || ks > 0);
+                            if (!CONV)
+                                umma_ta(o, a + 16, bv, idesc_o, 1);
+                        }
+                        if (!TWO || t == 1)
+                            tile_free(z);
+                        if (i == cnt[t] - 1)
+                            umma_commit(o_done + 8 * t);
+                        else
+                            scores(t, i + 1);
+                    }
+                z0 += 2 * n;
+                if (*abort_flag)
+                    break;
+            }
+            // nothing of this CTA's may be in flight when its tensor memory is freed
+            umma_commit(drain);
+            mbar_wait_bounded(drain, 0);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---- last pages, bf16: V rows that are not cached become zeros, and so do infinities
+        // and NaN of rows that only later tokens see (added at the end of the unit) ----
+        if (!CONV) {
+            int z0 = 0, fixes = 0;
+            for (; w.x < w.x1; w.next(p, heads)) {
+                const int n = w.pages(), cached = w.seq_len + p.nq - 1;
+                for (int i = max(0, w.seq_len / kPage - w.b); i < n; ++i) {
+                    const int page0 = (w.b + i) * kPage;
+                    const int z = z0 + order_of_v<TWO>(i, n);
+                    wait(v_landed, fixes++ & 1);
+                    uint8_t *v = gsm + (z % TILES) * TB;
+                    const int from = max(0, w.seq_len - page0), past = cached - page0;
+                    bool bad = false;
+                    for (int k = from * 16 + lane; k < kPage * 16; k += 32) { // 16-byte pieces
+                        const int row = k >> 4, piece = k & 15;
+                        uint4 *at = reinterpret_cast<uint4 *>(v + (piece >> 3) * 16384 + row * 128 + (piece & 7) * 16);
+                        if (row >= past) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint4 d = *at;
+                        uint32_t *e = &d.x;
+                        bool any = false;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if ((e[c] & 0x7F80u) == 0x7F80u)
+                                e[c] &= 0xFFFF0000u, any = true;
+                            if ((e[c] & 0x7F800000u) == 0x7F800000u)
+                                e[c] &= 0x0000FFFFu, any = true;
+                        }
+                        if (any)
+                            *at = d;
+                        bad |= any;
+                    }
+                    if (bad)
+                        later_bad[w.seg & 7] = w.seg + 1;
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(v_fixed);
+                }
+                z0 += 2 * n;
+            }
+        }
+    } else if (warp == 3) {
+        // ---- idle slots: outputs of requests without cached positions ----
+        for (int q = blockIdx.x; q < p.R; q += gridDim.x) {
+            bool bad;
+            if (cached_blocks(p.seq_lens[q], p.nq, p.maxB, &bad) > 0)
+                continue;
+            const size_t rows = (size_t)p.nq * p.Hkv * p.G;
+            uint4 *out = reinterpret_cast<uint4 *>(p.out + q * rows * kDim);
+            for (size_t i = lane; i < rows * (kDim / 8); i += 32)
+                out[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (size_t i = lane; i < rows; i += 32)
+                p.lse[q * rows + i] = __uint_as_float(0xFF800000u);
+        }
+    } else if (warp < 12) {
+        // ---- softmax: thread = query row ----
+        const int t = (warp - 4) >> 2, mine = threadIdx.x & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21); // this warp's lane quarter
+        const uint32_t s_at = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
+        const float ninf = __uint_as_float(0xFF800000u);
+        float *ml = reinterpret_cast<float *>(gsm + L.ml);
+        uint32_t steps = 0, done0 = 0, done1 = 0;
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages(), cnt = TWO ? n : (n + 1 - t) / 2;
+            const int g = w.u / p.tiles, base = (w.u - g * p.tiles) * ROWS + (TWO ? 128 * t : 0);
+            const int i_row = base + mine, i_read = min(i_row, p.rows - 1), j = i_read / p.G;
+            const size_t out_row = (size_t)w.r * p.nq * p.Hkv * p.G + (size_t)j * p.Hkv * p.G + (size_t)g * p.G + (i_read - j * p.G);
+            const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + out_row * kDim);
+            float inv = 1.f, up = 1.f;
+            if (CONV) { // scale the row into f16's range by a power of two (see load_queries)
+                float mx = 0.f;
+                for (int i = 0; i < 16; ++i) {
+                    const uint4 d = qrow[i];
+                    const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(e[c] << 16)), fabsf(__uint_as_float(e[c] & 0xFFFF0000u))));
+                }
+                int e = (int)(__float_as_uint(mx) >> 23) - 127;
+                e = e < -100 ? -100 : e > 127 ? 127 : e;
+                up = __uint_as_float((uint32_t)(8 - e + 127) << 23);
+                inv = __uint_as_float((uint32_t)(e - 8 + 127) << 23);
+            }
+            if (TWO || t == 0) {
+                if (w.seg > 0)
+                    wait(q_free, (w.seg - 1) & 1);
+                uint8_t *dst = gsm + L.q + (TWO ? t * kTile16 : 0) + mine * 128;
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    uint4 d = qrow[i];
+                    if (CONV) {
+                        uint32_t *e = &d.x;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            e[c] = pack_f16(__uint_as_float(e[c] << 16) * up, __uint_as_float(e[c] & 0xFFFF0000u) * up);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + (i >> 3) * 16384 + (((i & 7) ^ (mine & 7)) << 4)) = d;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full + 8 * t);
+            }
+            const float sc = p.scale_log2 * inv;
+            const int lim = w.seq_len + j;
+            float m = ninf, l = 0.f; // reference maximum and denominator
+            for (int i = 0; i < cnt; ++i) {
+                const int page0 = (w.b + (TWO ? i : 2 * i + t)) * kPage;
+                const bool tail = page0 + kPage > w.seq_len;
+                const int seen = tail ? lim - page0 : kPage; // columns this row sees
+                wait(s_full + 8 * t, steps++ & 1u);
+                tcgen05_after_sync();
+                float mx = ninf;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(s_at + 32 * c, v);
+                    tmem_wait_ld();
+                    if (!tail) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            mx = fmaxf(mx, __uint_as_float(v[k]) * sc);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k < seen)
+                                mx = fmaxf(mx, __uint_as_float(v[k]) * sc);
+                    }
+                }
+                if (CONV)
+                    mx -= kPUp16;
+                float f = 1.f;
+                if (mx > m + kSlack || (m == ninf && mx > ninf)) {
+                    f = ex2(m - mx);
+                    m = mx;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                    // the products of the steps before are complete: their MMAs went before S
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(o_at + 32 * c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                        tmem_st32(o_at + 32 * c, v);
+                    }
+                }
+                l *= f;
+                const float ref = m == ninf ? 0.f : m;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(s_at + 32 * c, v);
+                    tmem_wait_ld();
+                    float sum0 = 0.f, sum1 = 0.f;
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float e0 = ex2(fmaf(__uint_as_float(v[2 * k]), sc, -ref));
+                        float e1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), sc, -ref));
+                        if (tail) {
+                            e0 = 32 * c + 2 * k < seen ? e0 : 0.f;
+                            e1 = 32 * c + 2 * k + 1 < seen ? e1 : 0.f;
+                        }
+                        sum0 += e0;
+                        sum1 += e1;
+                        if (CONV) {
+                            hi[k] = pack_f16(e0, e1);
+                        } else {
+                            hi[k] = pack_bf16(e0, e1);
+                            lo[k] = pack_bf16(e0 - __uint_as_float(hi[k] << 16), e1 - __uint_as_float(hi[k] & 0xFFFF0000u));
+                        }
+                    }
+                    l += sum0 + sum1;
+                    tmem_st16(s_at + 32 * c, hi);
+                    if (!CONV)
+                        tmem_st16(s_at + 32 * c + 16, lo);
+                }
+                tmem_wait_st();
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_full + 8 * t);
+            }
+
+            // ---- end of the unit's share ----
+            float M = m, Lsum = l, fa = 1.f, fb = 0.f;
+            bool other = false;
+            if (!TWO) {
+                if (t == 1) {
+                    ml[mine] = m;
+                    ml[128 + mine] = l;
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                const float mb = ml[mine], lb = ml[128 + mine];
+                asm volatile("bar.sync 2, 256;" ::: "memory");
+                if (t == 1)
+                    continue; // stream 0 reads both accumulators
+                other = n > 1;
+                if (other) {
+                    M = fmaxf(m, mb);
+                    fa = m == ninf ? 0.f : ex2(m - M);
+                    fb = mb == ninf ? 0.f : ex2(mb - M);
+                    Lsum = l * fa + lb * fb;
+                }
+            }
+            wait(o_done + 8 * t, (TWO || t == 0 ? done0++ : done1++) & 1u);
+            if (other)
+                wait(o_done + 8, done1++ & 1u);
+            tcgen05_after_sync();
+            const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
+            float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * (ROWS * (kDim + 2));
+            const int slot_row = (TWO ? 128 * t : 0) + mine;
+            const float fin = Lsum > 0.f || Lsum != Lsum ? p.v_scale / Lsum : 0.f;
+            const bool bad = later_bad[w.seg & 7] == w.seg + 1;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                float a[16], b2[16];
+                __syncwarp();
+                tmem_ld16(o_at + 16 * c, a);
+                if (other)
+                    tmem_ld16(o_at + 128 + 16 * c, b2);
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    a[k] = other ? a[k] * fa + b2[k] * fb : a[k];
+                if (bad) { // infinities and NaN of draft tokens' V, for the rows that see them
+                    const float ref = M == ninf ? 0.f : M;
+                    for (int pos = max(w.seq_len, w.b * kPage); pos < min(lim, (w.b + n) * kPage); ++pos) {
+                        const long long page = p.block_table[(size_t)w.r * p.maxB + pos / kPage];
+                        if (page < 0 || page >= p.num_pages)
+                            continue;
+                        float pr = 0.f;
+                        bool have = false;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float v = stored_value<FMT>(p.kv, (page * 2 + 1) * p.Hkv + g, pos % kPage, 16 * c + k);
+                            if (finite(v))
+                                continue;
+                            if (!have) {
+                                const uint16_t *qv = p.q + out_row * kDim;
+                                for (int d = 0; d < kDim; ++d)
+                                    pr = fmaf(__uint_as_float((uint32_t)qv[d] << 16),
+                                              stored_value<FMT>(p.kv, page * 2 * p.Hkv + g, pos % kPage, d), pr);
+                                pr = ex2(fmaf(pr, p.scale_log2, -ref));
+                                have = true;
+                            }
+                            a[k] = fmaf(pr, v, a[k]);
+                        }
+                    }
+                }
+                if (i_row < p.rows) {
+                    if (whole) {
+                        uint4 d[2];
+                        uint32_t *e = &d[0].x;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            e[k] = pack_bf16(a[2 * k] * fin, a[2 * k + 1] * fin);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + out_row * kDim + 16 * c);
+                        dst[0] = d[0];
+                        dst[1] = d[1];
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(slot + (size_t)slot_row * kDim + 16 * c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            dst[k] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+                    }
+                }
+            }
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(o_free + 8 * t);
+                if (!TWO)
+                    mbar_arrive(o_free + 8);
+            }
+            if (i_row < p.rows) {
+                if (whole) {
+                    p.lse[out_row] = Lsum == 0.f ? ninf : (M + log2f(Lsum)) * 0.6931471805599453f;
+                } else {
+                    slot[(size_t)ROWS * kDim + slot_row] = M;
+                    slot[(size_t)ROWS * (kDim + 1) + slot_row] = Lsum;
+                }
+            }
+        }
+    } else if (CONV) {
+        // ---- converters: a ring tile to a 16-bit tile, in the order of use ----
+        const int cw = warp - 12, row = (cw & 3) * 32 + lane;
+        int z = 0;
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages(), cached = w.seq_len + p.nq - 1;
+            int kp = 0, vp = 0;
+            for (int i = 0; i < 2 * n; ++i, ++z) {
+                const bool is_k = kp < n && order_of_k<TWO>(kp) == i;
+                const int page0 = (w.b + (is_k ? kp++ : vp++)) * kPage;
+                const bool drop = !is_k && page0 + row >= cached;              // not cached
+                const bool check = !is_k && !drop && page0 + row >= w.seq_len; // seen by later tokens only
+                wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
+                if (z >= kStaged)
+                    wait(sempty + 8 * (z % kStaged), (uint32_t)(z / kStaged - 1) & 1u);
+                const uint8_t *src = gsm + (z % TILES) * TB;
+                uint8_t *dst = gsm + L.staged + (z % kStaged) * kTile16 + row * 128;
+                bool bad = false;
+                if (FMT == kFmtFp8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = (cw >> 2) * 4 + k; // 16 dimensions
+                        const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
+                        uint32_t e[4] = {d.x, d.y, d.z, d.w}, o[8];
+                        if (check)
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                if (((e[q >> 2] >> (8 * (q & 3))) & 0x7Fu) == 0x7Fu)
+                                    e[q >> 2] &= ~(0xFFu << (8 * (q & 3))), bad = true;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            e4m3x4_to_f16x2x2(drop ? 0u : e[q], o[2 * q], o[2 * q + 1]);
+                        uint8_t *at = dst + (c >> 2) * 16384;
+                        *reinterpret_cast<uint4 *>(at + (((2 * c) & 7) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(at + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                } else {
+                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(src + 8192 + row * 8 + (cw >> 2) * 4);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int c = (cw >> 2) * 2 + k; // 32 dimensions, two scales
+                        const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+                        const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+                        uint8_t *at = dst + (c >> 1) * 16384;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t code = (sc >> (8 * (2 * k + (q >> 1)))) & 0xFFu;
+                            bool zero = drop;
+                            if (check && (code & 0x7Fu) == 0x7Fu)
+                                zero = bad = true;
+                            uint32_t o[4];
+                            e2m1x8_scaled_f16x2(e[q], e4m3x2_to_f16x2(code | code << 8), o);
+                            *reinterpret_cast<uint4 *>(at + ((((c & 1) * 4 + q) ^ (row & 7)) << 4)) =
+                                zero ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+                if (bad)
+                    later_bad[w.seg & 7] = w.seg + 1;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(empty + 8 * (z % TILES));
+                    mbar_arrive(sfull + 8 * (z % kStaged));
+                }
+            }
+        }
+    }
+
+    tcgen05_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tcgen05_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int FMT, bool TWO>
+cudaError_t launch_t(const DenseParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
+{
+    constexpr int smem = smem_layout(FMT, TWO).total;
+    cudaError_t e = cudaFuncSetAttribute(dense_umma_kernel<FMT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    e = launch_kernel(dense_umma_kernel<FMT, TWO>, dim3(ctas), dim3(threads_of(FMT)), smem, stream, false, map, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_dense_umma(const DenseParams &p, const CUtensorMap &map, int kv_dtype, int ctas, cudaStream_t stream)
+{
+    const bool two = p.rows > 128;
+    if (kv_dtype == MSA_BF16)
+        return two ? launch_t<kFmtBf16, true>(p, map, ctas, stream) : launch_t<kFmtBf16, false>(p, map, ctas, stream);
+    if (kv_dtype == MSA_FP8_E4M3)
+        return two ? launch_t<kFmtFp8, true>(p, map, ctas, stream) : launch_t<kFmtFp8, false>(p, map, ctas, stream);
+    return two ? launch_t<kFmtF4, true>(p, map, ctas, stream) : launch_t<kFmtF4, false>(p, map, ctas, stream);
+}
+
+} // namespace msa

@@ -111,9 +111,10 @@ def test_dense_decode(torch_cuda, kv, contexts, nq, Hkv, G):
 
 
 @pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("nq", [1, 3, 20])  # 16, 48 and 320 query rows
 @pytest.mark.parametrize("ctas", [1, 2, 5, 37, 152, 400])
-def test_dense_decode_does_not_depend_on_the_split(torch_cuda, kv, ctas):
-    c = Cache([3000, 129, 1500, 1], 1, 2, 16, kv, seed=5, ctas=ctas)
+def test_dense_decode_does_not_depend_on_the_split(torch_cuda, kv, nq, ctas):
+    c = Cache([3000, 129, 1500, nq, 20], nq, 2, 16, kv, seed=5, ctas=ctas)
     c.decode()
     c.check_decode()
 
@@ -264,8 +265,10 @@ def test_bad_pages_and_lengths_are_reported(torch_cuda, kv):
     c.check_decode()
 
 
-def test_a_wait_that_runs_out_is_reported(torch_cuda):
-    c = Cache([20000, 3000], 1, 2, 16, seed=29)
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("nq", [1, 4, 24])
+def test_a_wait_that_runs_out_is_reported(torch_cuda, kv, nq):
+    c = Cache([20000, 3000], nq, 2, 16, kv, seed=29)
     w = c.torch.zeros((2, 2, c.pb.max_blocks * 128), device="cuda")
     c.decode()
     c.check_decode()
