@@ -21,7 +21,7 @@
 // TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
 // Warps: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 V check of last pages
 // (bf16), 3 outputs of idle slots, 4-7 and 8-11 softmax of stream 0 and 1,
-// 12-19 converters (E4M3, NVFP4).
+// 12-15 converters (E4M3, NVFP4).
 //
 // What bounds it: the tensor cores (S and P V of 128 x 128 x 128 are 512 clocks
 // each, 1024 for P V with hi + lo) when rows are many, HBM when they are few.
@@ -31,7 +31,7 @@ namespace msa {
 namespace {
 
 constexpr int kTile16 = 32768;   // a 16-bit K, V or Q tile
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 4;
 constexpr int kStaged = 4;       // widened tiles in flight
 constexpr float kSlack = 8.f;    // how far (log2) a row's maximum may pass its reference before O is rescaled
 constexpr float kPUp16 = 7.f;    // f16 P: 2^7 2^(s - m), at most 2^15 with the slack
@@ -78,7 +78,7 @@ __device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64
 }
 
 // 32 consecutive TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *r)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -90,25 +90,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32])
         : "r"(a));
 }
 
-__device__ __forceinline__ void tmem_wait_ld()
+// Wait for the loads issued so far; r (the registers of one of them) is read
+// and written here so that no use of its values can move before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *r)
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
-        : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r)
@@ -120,9 +117,36 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r)
         : "memory");
 }
 
+// Two fp32 at a time (the packed forms issue once for both).
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // One stored K (0) or V (1) value in global memory, without its tensor scale.
 template <int FMT>
-__device__ __noinline__ float stored_value(const uint8_t *kv, long long tile, int row, int d)
+__device__ __forceinline__ float stored_value(const uint8_t *kv, long long tile, int row, int d)
 {
     float a, b;
     if (FMT == kFmtBf16)
@@ -531,23 +555,31 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const int seen = tail ? lim - page0 : kPage; // columns this row sees
                 wait(s_full + 8 * t, steps++ & 1u);
                 tcgen05_after_sync();
-                float mx = ninf;
+                // the extreme logit of the row (the scale's sign says which end), 64 columns at a
+                // time; columns 64 .. 127 stay in v for the exponentials
+                uint32_t v[64];
+                const bool neg = sc < 0.f;
+                float mx = neg ? -ninf : ninf;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(s_at + 32 * c, v);
-                    tmem_wait_ld();
-                    if (!tail) {
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld32(s_at + 64 * h, v);
+                    tmem_ld32(s_at + 64 * h + 32, v + 32);
+                    tmem_wait_ld(v);
+                    tmem_wait_ld(v + 32);
+                    if (tail || neg) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            mx = fmaxf(mx, __uint_as_float(v[k]) * sc);
+                        for (int k = 0; k < 64; ++k)
+                            if (64 * h + k < seen)
+                                mx = neg ? fminf(mx, __uint_as_float(v[k])) : fmaxf(mx, __uint_as_float(v[k]));
                     } else {
+                        float m4[4] = {ninf, ninf, ninf, ninf};
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * c + k < seen)
-                                mx = fmaxf(mx, __uint_as_float(v[k]) * sc);
+                        for (int k = 0; k < 64; k += 2)
+                            m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                     }
                 }
+                mx *= sc;
                 if (CONV)
                     mx -= kPUp16;
                 float f = 1.f;
@@ -558,46 +590,60 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
                     // the products of the steps before are complete: their MMAs went before S
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(o_at + 32 * c, v);
-                        tmem_wait_ld();
+                    for (int c = 0; c < 8; ++c) {
+                        float o[16];
+                        tmem_ld16(o_at + 16 * c, o);
+                        uint32_t r[16];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                        tmem_st32(o_at + 32 * c, v);
+                        for (int k = 0; k < 16; ++k)
+                            r[k] = __float_as_uint(o[k] * f);
+                        tmem_st16(o_at + 16 * c, r);
                     }
                 }
                 l *= f;
                 const float ref = m == ninf ? 0.f : m;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(s_at + 32 * c, v);
-                    tmem_wait_ld();
-                    float sum0 = 0.f, sum1 = 0.f;
+                const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref), minus = pair(-1.f, -1.f);
+                uint64_t sum[2] = {0ull, 0ull};
+                auto exponentials = [&](int c, const uint32_t *x) { // 32 columns of S become P
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        float e0 = ex2(fmaf(__uint_as_float(v[2 * k]), sc, -ref));
-                        float e1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), sc, -ref));
+                        const int at = 32 * c + 2 * k;
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, ref2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
                         if (tail) {
-                            e0 = 32 * c + 2 * k < seen ? e0 : 0.f;
-                            e1 = 32 * c + 2 * k + 1 < seen ? e1 : 0.f;
+                            e0 = at < seen ? e0 : 0.f;
+                            e1 = at + 1 < seen ? e1 : 0.f;
                         }
-                        sum0 += e0;
-                        sum1 += e1;
+                        const uint64_t e = pair(e0, e1);
+                        sum[k & 1] = add2(sum[k & 1], e);
                         if (CONV) {
                             hi[k] = pack_f16(e0, e1);
                         } else {
                             hi[k] = pack_bf16(e0, e1);
-                            lo[k] = pack_bf16(e0 - __uint_as_float(hi[k] << 16), e1 - __uint_as_float(hi[k] & 0xFFFF0000u));
+                            float d0, d1;
+                            unpair(fma2(pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u)), minus, e), d0, d1);
+                            lo[k] = pack_bf16(d0, d1);
                         }
                     }
-                    l += sum0 + sum1;
                     tmem_st16(s_at + 32 * c, hi);
                     if (!CONV)
                         tmem_st16(s_at + 32 * c + 16, lo);
+                };
+                exponentials(2, v);
+                tmem_ld32(s_at, v);
+                exponentials(3, v + 32);
+                tmem_wait_ld(v);
+                tmem_ld32(s_at + 32, v + 32);
+                exponentials(0, v);
+                tmem_wait_ld(v + 32);
+                exponentials(1, v + 32);
+                {
+                    float a, b;
+                    unpair(add2(sum[0], sum[1]), a, b);
+                    l += a + b;
                 }
                 tmem_wait_st();
                 tcgen05_before_sync();
@@ -707,7 +753,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
     } else if (CONV) {
         // ---- converters: a ring tile to a 16-bit tile, in the order of use ----
-        const int cw = warp - 12, row = (cw & 3) * 32 + lane;
+        const int row = (warp - 12) * 32 + lane;
         int z = 0;
         for (; w.x < w.x1; w.next(p, heads)) {
             const int n = w.pages(), cached = w.seq_len + p.nq - 1;
@@ -715,8 +761,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (int i = 0; i < 2 * n; ++i, ++z) {
                 const bool is_k = kp < n && order_of_k<TWO>(kp) == i;
                 const int page0 = (w.b + (is_k ? kp++ : vp++)) * kPage;
-                const bool drop = !is_k && page0 + row >= cached;              // not cached
-                const bool check = !is_k && !drop && page0 + row >= w.seq_len; // seen by later tokens only
+                const bool tail = !is_k && page0 + kPage > w.seq_len;
+                const bool drop = tail && page0 + row >= cached;              // not cached
+                const bool check = tail && !drop && page0 + row >= w.seq_len; // seen by later tokens only
                 wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
                 if (z >= kStaged)
                     wait(sempty + 8 * (z % kStaged), (uint32_t)(z / kStaged - 1) & 1u);
@@ -725,40 +772,51 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 bool bad = false;
                 if (FMT == kFmtFp8) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = (cw >> 2) * 4 + k; // 16 dimensions
+                    for (int c = 0; c < 8; ++c) { // 16 dimensions
                         const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
                         uint32_t e[4] = {d.x, d.y, d.z, d.w}, o[8];
-                        if (check)
+                        if (tail) {
 #pragma unroll
                             for (int q = 0; q < 16; ++q)
-                                if (((e[q >> 2] >> (8 * (q & 3))) & 0x7Fu) == 0x7Fu)
+                                if (check && ((e[q >> 2] >> (8 * (q & 3))) & 0x7Fu) == 0x7Fu)
                                     e[q >> 2] &= ~(0xFFu << (8 * (q & 3))), bad = true;
 #pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                e[q] = drop ? 0u : e[q];
+                        }
+#pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            e4m3x4_to_f16x2x2(drop ? 0u : e[q], o[2 * q], o[2 * q + 1]);
+                            e4m3x4_to_f16x2x2(e[q], o[2 * q], o[2 * q + 1]);
                         uint8_t *at = dst + (c >> 2) * 16384;
                         *reinterpret_cast<uint4 *>(at + (((2 * c) & 7) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
                         *reinterpret_cast<uint4 *>(at + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                 } else {
-                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(src + 8192 + row * 8 + (cw >> 2) * 4);
+                    uint64_t sc = *reinterpret_cast<const uint64_t *>(src + 8192 + row * 8);
+                    uint32_t zero = 0u; // 16-dim groups that become zeros
+                    if (tail) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int c = (cw >> 2) * 2 + k; // 32 dimensions, two scales
+                        for (int q = 0; q < 8; ++q)
+                            if (check && ((sc >> (8 * q)) & 0x7Fu) == 0x7Fu)
+                                zero |= 1u << q, bad = true;
+                        zero = drop ? 0xFFu : zero;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if ((zero >> q) & 1u)
+                                sc &= ~(0xFFull << (8 * q)); // a scale of 0: products of 0
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) { // 32 dimensions, two scales
                         const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
                         const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+                        const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)(sc >> (16 * c)) & 0xFFFFu);
+                        const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
                         uint8_t *at = dst + (c >> 1) * 16384;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const uint32_t code = (sc >> (8 * (2 * k + (q >> 1)))) & 0xFFu;
-                            bool zero = drop;
-                            if (check && (code & 0x7Fu) == 0x7Fu)
-                                zero = bad = true;
                             uint32_t o[4];
-                            e2m1x8_scaled_f16x2(e[q], e4m3x2_to_f16x2(code | code << 8), o);
-                            *reinterpret_cast<uint4 *>(at + ((((c & 1) * 4 + q) ^ (row & 7)) << 4)) =
-                                zero ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[0], o[1], o[2], o[3]);
+                            e2m1x8_scaled_f16x2(e[q], q < 2 ? sa : sb, o);
+                            *reinterpret_cast<uint4 *>(at + ((((c & 1) * 4 + q) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                     }
                 }

@@ -268,7 +268,8 @@ def test_bad_pages_and_lengths_are_reported(torch_cuda, kv):
 @pytest.mark.parametrize("kv", KV)
 @pytest.mark.parametrize("nq", [1, 4, 24])
 def test_a_wait_that_runs_out_is_reported(torch_cuda, kv, nq):
-    c = Cache([20000, 3000], nq, 2, 16, kv, seed=29)
+    # four CTAs with far more pages than their rings hold: a producer or its consumers wait
+    c = Cache([20000, 3000], nq, 2, 16, kv, seed=29, ctas=4)
     w = c.torch.zeros((2, 2, c.pb.max_blocks * 128), device="cuda")
     c.decode()
     c.check_decode()
