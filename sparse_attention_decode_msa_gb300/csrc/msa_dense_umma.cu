@@ -68,12 +68,41 @@ static_assert(smem_layout(kFmtBf16, true).total <= 232448 && smem_layout(kFmtBf1
                   smem_layout(kFmtF4, true).total <= 232448 && smem_layout(kFmtF4, false).total <= 232448,
               "shared memory");
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, issued by one thread.
-__device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+// The MMAs below are executed by a whole warp and issued by the lane with `one`
+// set.  Their operands live in uniform registers: a value the compiler cannot
+// prove uniform costs moves before every MMA (about 100 clocks an MMA, where the
+// tensor cores need 64).  A reduction over the warp gives a value that it can.
+__device__ __forceinline__ uint32_t uniform(uint32_t v)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+    return __reduce_or_sync(0xffffffffu, v);
+}
+
+// Shared-memory operand descriptor (128-byte swizzle, version 1) from its low
+// word: address / 16 and the leading offset / 16 in bits 16 ..; stride 1024.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead)
+{
+    return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+                 "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(one), "r"(kDescHigh)
+                 : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " mov.b64 b, {%2, %6};\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(one), "r"(kDescHigh)
                  : "memory");
 }
 
@@ -357,84 +386,95 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 mbar_wait_bounded(full + 8 * (i % TILES), (uint32_t)(i / TILES) & 1u);
         __syncwarp();
     } else if (warp == 1) {
-        // ---- MMA issuer ----
-        if (lane == 0) {
-            constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
-            constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, 0, 0) & kTypes;
-            constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
-            int z0 = 0, fixes = 0;
-            uint32_t steps[2] = {0u, 0u};
-            auto tile_wait = [&](int z) {
-                wait(CONV ? sfull + 8 * (z % kStaged) : full + 8 * (z % TILES), (uint32_t)(z / (CONV ? kStaged : TILES)) & 1u);
-            };
-            auto tile_at = [&](int z) { return CONV ? smem + L.staged + (z % kStaged) * kTile16 : smem + (z % TILES) * TB; };
-            auto tile_free = [&](int z) { umma_commit(CONV ? sempty + 8 * (z % kStaged) : empty + 8 * (z % TILES)); };
-            for (; w.x < w.x1; w.next(p, heads)) {
-                const int n = w.pages();
-                const int cnt[2] = {TWO ? n : (n + 1) / 2, TWO ? n : n / 2};
-                int scores_left = cnt[0] + cnt[1];
-                wait(q_full, w.seg & 1);
-                if (TWO)
-                    wait(q_full + 8, w.seg & 1);
+        // ---- MMA issuer: the whole warp, lane 0 issuing ----
+        const uint32_t one = lane == 0, tm = uniform(tmem), base = uniform(smem);
+        constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
+        constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, 0, 0) & kTypes;
+        constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
+        constexpr int DEPTH = CONV ? kStaged : TILES;
+        constexpr uint32_t STEP = CONV ? kTile16 : TB, RING = CONV ? L.staged : 0;
+        int z0 = 0, fixes = 0;
+        auto aborted = [&] { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; }; // all lanes alike
+        uint32_t steps[2] = {0u, 0u};
+        auto tile_wait = [&](int z) { wait((CONV ? sfull : full) + 8 * (z % DEPTH), (uint32_t)(z / DEPTH) & 1u); };
+        auto tile_free = [&](int z) {
+            if (one)
+                umma_commit((CONV ? sempty : empty) + 8 * (z % DEPTH));
+        };
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages();
+            const int cnt[2] = {TWO ? n : (n + 1) / 2, TWO ? n : n / 2};
+            int scores_left = cnt[0] + cnt[1];
+            wait(q_full, w.seg & 1);
+            if (TWO)
+                wait(q_full + 8, w.seg & 1);
+            tcgen05_after_sync();
+            auto scores = [&](int t, int i) {
+                const int z = z0 + order_of_k<TWO>(TWO ? i : 2 * i + t);
+                tile_wait(z);
+                if (aborted())
+                    return;
                 tcgen05_after_sync();
-                auto scores = [&](int t, int i) {
-                    const int z = z0 + order_of_k<TWO>(TWO ? i : 2 * i + t);
-                    tile_wait(z);
-                    if (*abort_flag)
-                        return;
-                    tcgen05_after_sync();
-                    const uint32_t k = tile_at(z), q = smem + L.q + (TWO ? t * kTile16 : 0);
+                const uint32_t k = uniform(desc_low(base + RING + (z % DEPTH) * STEP, 16));
+                const uint32_t q = uniform(desc_low(base + L.q + (TWO ? t * kTile16 : 0), 16));
+                const uint32_t d = uniform(tm + 128 * t);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16(tmem + 128 * t, umma_desc_sw128(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                  umma_desc_sw128(k + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), idesc_s, ks > 0);
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t at = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                    umma_ss(one, d, q + at, k + at, idesc_s, ks > 0);
+                }
+                if (one)
                     umma_commit(s_full + 8 * t);
+                if (!TWO || t == 1)
+                    tile_free(z);
+                if (--scores_left == 0 && one)
+                    umma_commit(q_free);
+            };
+            for (int t = 0; t < 2; ++t)
+                if (cnt[t] > 0)
+                    scores(t, 0);
+            for (int i = 0; i < cnt[0]; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (i >= cnt[t])
+                        continue;
+                    const int page = TWO ? i : 2 * i + t, z = z0 + order_of_v<TWO>(page, n);
+                    wait(p_full + 8 * t, steps[t]++ & 1u);
+                    if (i == 0 && w.seg > 0)
+                        wait(o_free + 8 * t, (w.seg - 1) & 1);
+                    tile_wait(z);
+                    if (!CONV && (!TWO || t == 0) && (w.b + page + 1) * kPage > w.seq_len) {
+                        if (one)
+                            mbar_arrive(v_landed);    // checked by warp 2, which waits for this and not
+                        wait(v_fixed, fixes++ & 1); // for the copy: phases it does not follow
+                    }
+                    if (aborted())
+                        break;
+                    tcgen05_after_sync();
+                    const uint32_t v = uniform(desc_low(base + RING + (z % DEPTH) * STEP, 16384));
+                    const uint32_t d = uniform(tm + 256 + 128 * t), a = uniform(tm + 128 * t), more = uniform(i > 0);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) { // V, MN-major: 16 positions are 16 rows of 128 bytes
+                        const uint32_t pa = a + 32 * (ks >> 1) + 8 * (ks & 1), b = v + ks * (2048 >> 4);
+                        umma_ts(one, d, pa, b, idesc_o, ks > 0 ? 1u : more);
+                        if (!CONV)
+                            umma_ts(one, d, pa + 16, b, idesc_o, 1u);
+                    }
                     if (!TWO || t == 1)
                         tile_free(z);
-                    if (--scores_left == 0)
-                        umma_commit(q_free);
-                };
-                for (int t = 0; t < 2; ++t)
-                    if (cnt[t] > 0)
-                        scores(t, 0);
-                for (int i = 0; i < cnt[0]; ++i)
-                    for (int t = 0; t < 2; ++t) {
-                        if (i >= cnt[t])
-                            continue;
-                        const int page = TWO ? i : 2 * i + t, z = z0 + order_of_v<TWO>(page, n);
-                        wait(p_full + 8 * t, steps[t]++ & 1u);
-                        if (i == 0 && w.seg > 0)
-                            wait(o_free + 8 * t, (w.seg - 1) & 1);
-                        tile_wait(z);
-                        if (!CONV && (!TWO || t == 0) && (w.b + page + 1) * kPage > w.seq_len)
-                        {
-                            mbar_arrive(v_landed); // checked by warp 2, which waits for this and not
-                            wait(v_fixed, fixes++ & 1); // for the copy: phases it does not follow
-                        }
-                        if (*abort_flag)
-                            break;
-                        tcgen05_after_sync();
-                        const uint32_t v = tile_at(z), o = tmem + 256 + 128 * t;
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) { // V, MN-major: 16 positions are 16 rows of 128 bytes
-                            const uint64_t bv = umma_desc_sw128(v + ks * 2048, 16384, 1024);
-                            const uint32_t a = tmem + 128 * t + 32 * (ks >> 1) + 8 * (ks & 1);
-                            umma_ta(o, a, bv, idesc_o, i > 0 || ks > 0);
-                            if (!CONV)
-                                umma_ta(o, a + 16, bv, idesc_o, 1);
-                        }
-                        if (!TWO || t == 1)
-                            tile_free(z);
-                        if (i == cnt[t] - 1)
+                    if (i == cnt[t] - 1) {
+                        if (one)
                             umma_commit(o_done + 8 * t);
-                        else
-                            scores(t, i + 1);
+                    } else {
+                        scores(t, i + 1);
                     }
-                z0 += 2 * n;
-                if (*abort_flag)
-                    break;
-            }
-            // nothing of this CTA's may be in flight when its tensor memory is freed
+                }
+            z0 += 2 * n;
+            if (aborted())
+                break;
+        }
+        // nothing of this CTA's may be in flight when its tensor memory is freed
+        if (one) {
             umma_commit(drain);
             mbar_wait_bounded(drain, 0);
         }
