@@ -7,10 +7,12 @@
 // softmax needs no exchange between threads.
 //
 // Two streams share a CTA's pages, so that the tensor cores work for one while
-// the other is in its softmax.  With more than 128 query rows a (request, KV
-// head), stream t has rows 128 t .. of a 256-row tile and both use every page;
-// with fewer, both have the same rows, stream t takes every second page, and
-// the two (m, l, O) are added at the end.
+// the other is in its softmax, and each stream works in steps of 64 positions
+// with two S buffers, so that the S of its next step is ready when a softmax
+// ends.  With more than 128 query rows a (request, KV head), stream t has rows
+// 128 t .. of a 256-row tile and takes both halves of every page; with fewer,
+// both have the same rows, stream t takes half t of every page, and the two
+// (m, l, O) are added at the end.
 //
 // Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA
 // lands them (K-major), P in tensor memory over the S it came from, V tiles as
@@ -18,13 +20,15 @@
 // rounding of P to bf16 alone would weigh as much as the output's); E4M3 and
 // NVFP4 tiles are widened to f16 by converter warps and P is one f16 (11 bits).
 //
-// TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
-// Warps: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 V check of last pages
-// (bf16), 3 outputs of idle slots, 4-7 and 8-11 softmax of stream 0 and 1,
+// TMEM columns: S/P of step s of stream t at 128 t + 64 (s & 1), O of stream t at 256 + 128 t.
+// Warps: 0 TMA producer, 1 and 3 MMA issuers of stream 0 and 1 (1 owns the TMEM),
+// 2 V check of last pages (bf16) and outputs of idle slots, 4-7 and 8-11 softmax of stream 0 and 1,
 // 12-15 converters (E4M3, NVFP4).
 //
-// What bounds it: the tensor cores (S and P V of 128 x 128 x 128 are 512 clocks
-// each, 1024 for P V with hi + lo) when rows are many, HBM when they are few.
+// What bounds it: the tensor cores when rows are many (measured: an MMA of
+// 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50; a page of 128
+// rows is 16 of these for S and 8, or 16 with lo, of those for P V), HBM when
+// they are few.
 #include "msa_cache.cuh"
 
 namespace msa {
@@ -59,7 +63,7 @@ __host__ __device__ constexpr Smem smem_layout(int fmt, bool two)
     s.q = s.staged + (fmt == kFmtBf16 ? 0 : kStaged * kTile16);
     s.ml = s.q + (two ? 2 : 1) * kTile16; // m[128], l[128] of stream 1 (one row tile)
     s.bars = s.ml + (two ? 0 : 2 * 128 * 4);
-    s.misc = s.bars + (2 * ring_tiles(fmt, two) + 2 * kStaged + 16) * 8;
+    s.misc = s.bars + (2 * ring_tiles(fmt, two) + 2 * kStaged + 21) * 8;
     s.total = s.misc + 64 + 1024;
     return s;
 }
@@ -247,8 +251,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *gsm = smem_raw + (smem - smem_u32(smem_raw));
     const uint32_t full = smem + L.bars, empty = full + TILES * 8, sfull = empty + TILES * 8, sempty = sfull + kStaged * 8;
-    const uint32_t q_full = sempty + kStaged * 8, q_free = q_full + 16, s_full = q_free + 8, p_full = s_full + 16,
-                   o_done = p_full + 16, o_free = o_done + 16, v_fixed = o_free + 16, v_landed = v_fixed + 8,
+    const uint32_t q_full = sempty + kStaged * 8, q_free = q_full + 16, s_full = q_free + 8, p_full = s_full + 32,
+                   pv_done = p_full + 32, o_free = pv_done + 32, v_fixed = o_free + 16, v_landed = v_fixed + 8,
                    drain = v_landed + 8;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gsm + L.misc);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -260,23 +264,27 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         prefetch_tensormap(&map);
         for (int i = 0; i < TILES; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, CONV ? kConvWarps : 1);
+            mbar_init(empty + 8 * i, CONV ? kConvWarps : 2);
         }
         for (int i = 0; i < kStaged; ++i) {
             mbar_init(sfull + 8 * i, kConvWarps);
-            mbar_init(sempty + 8 * i, 1);
+            mbar_init(sempty + 8 * i, 2);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full + 8 * t, 4);
-            mbar_init(s_full + 8 * t, 1);
-            mbar_init(p_full + 8 * t, 4);
-            mbar_init(o_done + 8 * t, 1);
+            mbar_init(s_full + 16 * t, 1);
+            mbar_init(s_full + 16 * t + 8, 1);
+            mbar_init(p_full + 16 * t, 4);
+            mbar_init(p_full + 16 * t + 8, 4);
+            mbar_init(pv_done + 16 * t, 1);
+            mbar_init(pv_done + 16 * t + 8, 1);
             mbar_init(o_free + 8 * t, 4);
         }
-        mbar_init(q_free, 1);
+        mbar_init(q_free, 2);
         mbar_init(v_fixed, 1);
-        mbar_init(v_landed, 1);
+        mbar_init(v_landed, 2);
         mbar_init(drain, 1);
+        mbar_init(drain + 8, 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -385,98 +393,84 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (int i = max(0, z - TILES); i < z; ++i)
                 mbar_wait_bounded(full + 8 * (i % TILES), (uint32_t)(i / TILES) & 1u);
         __syncwarp();
-    } else if (warp == 1) {
-        // ---- MMA issuer: the whole warp, lane 0 issuing ----
-        const uint32_t one = lane == 0, tm = uniform(tmem), base = uniform(smem);
+    } else if (warp == 1 || warp == 3) {
+        // ---- MMA issuer of stream t: the whole warp, lane 0 issuing ----
+        const int t = warp >> 1;
+        const uint32_t one = lane == 0, tm = uniform(tmem + 128 * t), base = uniform(smem);
         constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
-        constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, 0, 0) & kTypes;
+        constexpr uint32_t idesc_s = umma_idesc_bf16(128, 64, 0, 0) & kTypes;
         constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
         constexpr int DEPTH = CONV ? kStaged : TILES;
         constexpr uint32_t STEP = CONV ? kTile16 : TB, RING = CONV ? L.staged : 0;
+        const uint32_t tile_full = CONV ? sfull : full, tile_free = CONV ? sempty : empty;
+        const uint32_t q = uniform(desc_low(base + L.q + (TWO ? t * kTile16 : 0), 16));
         int z0 = 0, fixes = 0;
-        auto aborted = [&] { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; }; // all lanes alike
-        uint32_t steps[2] = {0u, 0u};
-        auto tile_wait = [&](int z) { wait((CONV ? sfull : full) + 8 * (z % DEPTH), (uint32_t)(z / DEPTH) & 1u); };
-        auto tile_free = [&](int z) {
-            if (one)
-                umma_commit((CONV ? sempty : empty) + 8 * (z % DEPTH));
-        };
+        uint32_t taken0 = 0, taken1 = 0; // steps of either S buffer
         for (; w.x < w.x1; w.next(p, heads)) {
             const int n = w.pages();
-            const int cnt[2] = {TWO ? n : (n + 1) / 2, TWO ? n : n / 2};
-            int scores_left = cnt[0] + cnt[1];
-            wait(q_full, w.seg & 1);
-            if (TWO)
-                wait(q_full + 8, w.seg & 1);
-            tcgen05_after_sync();
-            auto scores = [&](int t, int i) {
-                const int z = z0 + order_of_k<TWO>(TWO ? i : 2 * i + t);
-                tile_wait(z);
-                if (aborted())
-                    return;
+            const int nsteps = TWO ? 2 * n : n;
+            wait(q_full + (TWO ? 8 * t : 0), w.seg & 1);
+            auto scores = [&](int i) { // S of step i: 64 positions, half of a K tile
+                const int z = z0 + order_of_k<TWO>(TWO ? i >> 1 : i), st = z % DEPTH;
+                const uint32_t k = uniform(desc_low(base + RING + st * STEP, 16) + (TWO ? i & 1 : t) * (64 * 128 >> 4));
+                const uint32_t d = uniform(tm + 64 * (i & 1));
+                wait(tile_full + 8 * st, (uint32_t)(z / DEPTH) & 1u);
                 tcgen05_after_sync();
-                const uint32_t k = uniform(desc_low(base + RING + (z % DEPTH) * STEP, 16));
-                const uint32_t q = uniform(desc_low(base + L.q + (TWO ? t * kTile16 : 0), 16));
-                const uint32_t d = uniform(tm + 128 * t);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
                     const uint32_t at = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
                     umma_ss(one, d, q + at, k + at, idesc_s, ks > 0);
                 }
-                if (one)
-                    umma_commit(s_full + 8 * t);
-                if (!TWO || t == 1)
-                    tile_free(z);
-                if (--scores_left == 0 && one)
-                    umma_commit(q_free);
-            };
-            for (int t = 0; t < 2; ++t)
-                if (cnt[t] > 0)
-                    scores(t, 0);
-            for (int i = 0; i < cnt[0]; ++i)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (i >= cnt[t])
-                        continue;
-                    const int page = TWO ? i : 2 * i + t, z = z0 + order_of_v<TWO>(page, n);
-                    wait(p_full + 8 * t, steps[t]++ & 1u);
-                    if (i == 0 && w.seg > 0)
-                        wait(o_free + 8 * t, (w.seg - 1) & 1);
-                    tile_wait(z);
-                    if (!CONV && (!TWO || t == 0) && (w.b + page + 1) * kPage > w.seq_len) {
-                        if (one)
-                            mbar_arrive(v_landed);    // checked by warp 2, which waits for this and not
-                        wait(v_fixed, fixes++ & 1); // for the copy: phases it does not follow
-                    }
-                    if (aborted())
-                        break;
-                    tcgen05_after_sync();
-                    const uint32_t v = uniform(desc_low(base + RING + (z % DEPTH) * STEP, 16384));
-                    const uint32_t d = uniform(tm + 256 + 128 * t), a = uniform(tm + 128 * t), more = uniform(i > 0);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) { // V, MN-major: 16 positions are 16 rows of 128 bytes
-                        const uint32_t pa = a + 32 * (ks >> 1) + 8 * (ks & 1), b = v + ks * (2048 >> 4);
-                        umma_ts(one, d, pa, b, idesc_o, ks > 0 ? 1u : more);
-                        if (!CONV)
-                            umma_ts(one, d, pa + 16, b, idesc_o, 1u);
-                    }
-                    if (!TWO || t == 1)
-                        tile_free(z);
-                    if (i == cnt[t] - 1) {
-                        if (one)
-                            umma_commit(o_done + 8 * t);
-                    } else {
-                        scores(t, i + 1);
-                    }
+                if (one) {
+                    umma_commit(s_full + 16 * t + 8 * (i & 1));
+                    if (!TWO || (i & 1))
+                        umma_commit(tile_free + 8 * st);
+                    if (i == nsteps - 1)
+                        umma_commit(q_free);
                 }
+            };
+            scores(0);
+            if (nsteps > 1)
+                scores(1);
+            for (int i = 0; i < nsteps; ++i) {
+                const int page = TWO ? i >> 1 : i, z = z0 + order_of_v<TWO>(page, n), st = z % DEPTH;
+                const uint32_t v = uniform(desc_low(base + RING + st * STEP, 16384) + (TWO ? i & 1 : t) * (64 * 128 >> 4));
+                const uint32_t a = uniform(tm + 64 * (i & 1)), more = uniform(i > 0);
+                const uint32_t d = uniform(tm + 256);
+                wait(tile_full + 8 * st, (uint32_t)(z / DEPTH) & 1u);
+                if (!CONV && (!TWO || !(i & 1)) && (w.b + page + 1) * kPage > w.seq_len) {
+                    // checked by warp 2, which waits for both issuers and not for the copy: a
+                    // barrier whose phases it does not follow
+                    if (one)
+                        mbar_arrive(v_landed);
+                    wait(v_fixed, fixes++ & 1);
+                }
+                if (i == 0 && w.seg > 0)
+                    wait(o_free + 8 * t, (w.seg - 1) & 1);
+                wait(p_full + 16 * t + 8 * (i & 1), (i & 1 ? taken1++ : taken0++) & 1u);
+                tcgen05_after_sync();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) { // V, MN-major: 16 positions are 16 rows of 128 bytes
+                    umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
+                    if (!CONV)
+                        umma_ts(one, d, a + 32 + 8 * ks, v + ks * (2048 >> 4), idesc_o, 1u);
+                }
+                if (one) {
+                    umma_commit(pv_done + 16 * t + 8 * (i & 1));
+                    if (!TWO || (i & 1))
+                        umma_commit(tile_free + 8 * st);
+                }
+                if (i + 2 < nsteps)
+                    scores(i + 2);
+            }
             z0 += 2 * n;
-            if (aborted())
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) // all lanes alike
                 break;
         }
         // nothing of this CTA's may be in flight when its tensor memory is freed
         if (one) {
-            umma_commit(drain);
-            mbar_wait_bounded(drain, 0);
+            umma_commit(drain + 8 * t);
+            mbar_wait_bounded(drain + 8 * t, 0);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -524,7 +518,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 z0 += 2 * n;
             }
         }
-    } else if (warp == 3) {
         // ---- idle slots: outputs of requests without cached positions ----
         for (int q = blockIdx.x; q < p.R; q += gridDim.x) {
             bool bad;
@@ -544,9 +537,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const uint32_t s_at = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
         const float ninf = __uint_as_float(0xFF800000u);
         float *ml = reinterpret_cast<float *>(gsm + L.ml);
-        uint32_t steps = 0, done0 = 0, done1 = 0;
+        // steps that took either S buffer so far, alike for both streams.  Every
+        // barrier of a step exists once per buffer: its next phase needs a step that
+        // this warp has not given yet, so a wait cannot fall two phases behind.
+        uint32_t fills0 = 0, fills1 = 0;
+        auto product_wait = [&](int k, int i) { // P V of step i (the last of its buffer) of stream k
+            wait(pv_done + 16 * k + 8 * (i & 1), ((i & 1 ? fills1 : fills0) - 1) & 1u);
+        };
         for (; w.x < w.x1; w.next(p, heads)) {
-            const int n = w.pages(), cnt = TWO ? n : (n + 1 - t) / 2;
+            const int n = w.pages(), nsteps = TWO ? 2 * n : n;
             const int g = w.u / p.tiles, base = (w.u - g * p.tiles) * ROWS + (TWO ? 128 * t : 0);
             const int i_row = base + mine, i_read = min(i_row, p.rows - 1), j = i_read / p.G;
             const size_t out_row = (size_t)w.r * p.nq * p.Hkv * p.G + (size_t)j * p.Hkv * p.G + (size_t)g * p.G + (i_read - j * p.G);
@@ -589,35 +588,32 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const float sc = p.scale_log2 * inv;
             const int lim = w.seq_len + j;
             float m = ninf, l = 0.f; // reference maximum and denominator
-            for (int i = 0; i < cnt; ++i) {
-                const int page0 = (w.b + (TWO ? i : 2 * i + t)) * kPage;
-                const bool tail = page0 + kPage > w.seq_len;
-                const int seen = tail ? lim - page0 : kPage; // columns this row sees
-                wait(s_full + 8 * t, steps++ & 1u);
+            for (int i = 0; i < nsteps; ++i) {
+                const int pos0 = (w.b + (TWO ? i >> 1 : i)) * kPage + 64 * (TWO ? i & 1 : t);
+                const bool tail = pos0 + 64 > w.seq_len;
+                const int seen = tail ? lim - pos0 : 64; // columns this row sees
+                const uint32_t at_s = s_at + 64 * (i & 1);
+                wait(s_full + 16 * t + 8 * (i & 1), (i & 1 ? fills1++ : fills0++) & 1u);
                 tcgen05_after_sync();
-                // the extreme logit of the row (the scale's sign says which end), 64 columns at a
-                // time; columns 64 .. 127 stay in v for the exponentials
                 uint32_t v[64];
+                tmem_ld32(at_s, v);
+                tmem_ld32(at_s + 32, v + 32);
+                tmem_wait_ld(v);
+                tmem_wait_ld(v + 32);
+                // the extreme logit of the row (the scale's sign says which end)
                 const bool neg = sc < 0.f;
                 float mx = neg ? -ninf : ninf;
+                if (tail || neg) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    tmem_ld32(s_at + 64 * h, v);
-                    tmem_ld32(s_at + 64 * h + 32, v + 32);
-                    tmem_wait_ld(v);
-                    tmem_wait_ld(v + 32);
-                    if (tail || neg) {
+                    for (int k = 0; k < 64; ++k)
+                        if (k < seen)
+                            mx = neg ? fminf(mx, __uint_as_float(v[k])) : fmaxf(mx, __uint_as_float(v[k]));
+                } else {
+                    float m4[4] = {ninf, ninf, ninf, ninf};
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (64 * h + k < seen)
-                                mx = neg ? fminf(mx, __uint_as_float(v[k])) : fmaxf(mx, __uint_as_float(v[k]));
-                    } else {
-                        float m4[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
-                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                    }
+                    for (int k = 0; k < 64; k += 2)
+                        m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
                 mx *= sc;
                 if (CONV)
@@ -628,7 +624,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     m = mx;
                 }
                 if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                    // the products of the steps before are complete: their MMAs went before S
+                    product_wait(t, i - 1); // O holds every step before this one
+                    tcgen05_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
                         float o[16];
@@ -644,13 +641,14 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const float ref = m == ninf ? 0.f : m;
                 const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref), minus = pair(-1.f, -1.f);
                 uint64_t sum[2] = {0ull, 0ull};
-                auto exponentials = [&](int c, const uint32_t *x) { // 32 columns of S become P
+#pragma unroll
+                for (int c = 0; c < 2; ++c) { // 32 columns of S become P
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const int at = 32 * c + 2 * k;
                         float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, ref2), e0, e1);
+                        unpair(fma2(pair(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), sc2, ref2), e0, e1);
                         e0 = ex2(e0);
                         e1 = ex2(e1);
                         if (tail) {
@@ -668,18 +666,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             lo[k] = pack_bf16(d0, d1);
                         }
                     }
-                    tmem_st16(s_at + 32 * c, hi);
+                    tmem_st16(at_s + 16 * c, hi);
                     if (!CONV)
-                        tmem_st16(s_at + 32 * c + 16, lo);
-                };
-                exponentials(2, v);
-                tmem_ld32(s_at, v);
-                exponentials(3, v + 32);
-                tmem_wait_ld(v);
-                tmem_ld32(s_at + 32, v + 32);
-                exponentials(0, v);
-                tmem_wait_ld(v + 32);
-                exponentials(1, v + 32);
+                        tmem_st16(at_s + 32 + 16 * c, lo);
+                }
                 {
                     float a, b;
                     unpair(add2(sum[0], sum[1]), a, b);
@@ -689,12 +679,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(p_full + 8 * t);
+                    mbar_arrive(p_full + 16 * t + 8 * (i & 1));
             }
 
             // ---- end of the unit's share ----
             float M = m, Lsum = l, fa = 1.f, fb = 0.f;
-            bool other = false;
             if (!TWO) {
                 if (t == 1) {
                     ml[mine] = m;
@@ -704,18 +693,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const float mb = ml[mine], lb = ml[128 + mine];
                 asm volatile("bar.sync 2, 256;" ::: "memory");
                 if (t == 1)
-                    continue; // stream 0 reads both accumulators
-                other = n > 1;
-                if (other) {
-                    M = fmaxf(m, mb);
-                    fa = m == ninf ? 0.f : ex2(m - M);
-                    fb = mb == ninf ? 0.f : ex2(mb - M);
-                    Lsum = l * fa + lb * fb;
-                }
+                    continue; // stream 0 reads both accumulators (of as many steps)
+                M = fmaxf(m, mb);
+                fa = m == ninf ? 0.f : ex2(m - M);
+                fb = mb == ninf ? 0.f : ex2(mb - M);
+                Lsum = l * fa + lb * fb;
             }
-            wait(o_done + 8 * t, (TWO || t == 0 ? done0++ : done1++) & 1u);
-            if (other)
-                wait(o_done + 8, done1++ & 1u);
+            product_wait(t, nsteps - 1);
+            if (!TWO)
+                product_wait(1, nsteps - 1);
             tcgen05_after_sync();
             const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
             float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * (ROWS * (kDim + 2));
@@ -727,11 +713,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 float a[16], b2[16];
                 __syncwarp();
                 tmem_ld16(o_at + 16 * c, a);
-                if (other)
+                if (!TWO) {
                     tmem_ld16(o_at + 128 + 16 * c, b2);
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    a[k] = other ? a[k] * fa + b2[k] * fb : a[k];
+                    for (int k = 0; k < 16; ++k)
+                        a[k] = a[k] * fa + b2[k] * fb;
+                }
                 if (bad) { // infinities and NaN of draft tokens' V, for the rows that see them
                     const float ref = M == ninf ? 0.f : M;
                     for (int pos = max(w.seq_len, w.b * kPage); pos < min(lim, (w.b + n) * kPage); ++pos) {
