@@ -123,25 +123,34 @@ __device__ __forceinline__ int cached_blocks(int seq_len, int nq, int maxB, bool
     return (int)nb;
 }
 
-// Wait for phase `parity` of a ring barrier; false after `limit` SM clocks or
-// once another thread of the CTA gave up.  A short limit (a test's) polls, as
-// the suspending form may sleep past it.
-__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag, long long limit)
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
 {
-    if (limit >= (1 << 16))
-        return mbar_wait_or_abort(bar, parity, abort_flag, limit);
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+static __device__ __noinline__ bool ring_wait_slow(uint32_t bar, uint32_t parity, const volatile int *abort_flag, long long limit)
+{
+    const bool poll = limit < (1 << 16); // a test's limit: the suspending form may sleep past it
     const long long start = clock64();
-    for (;;) {
-        uint32_t ok;
-        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                     : "=r"(ok)
-                     : "r"(bar), "r"(parity)
-                     : "memory");
-        if (ok)
-            return true;
+    while (!(poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
         if (*abort_flag || clock64() - start > limit)
             return false;
     }
+    return true;
+}
+
+// Wait for phase `parity` of a ring barrier; false after `limit` SM clocks or
+// once another thread of the CTA gave up.  The waiting itself is a call: the
+// roles of these kernels share the instruction caches, and a dozen inlined wait
+// loops push their inner loops out.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag, long long limit)
+{
+    return mbar_test_wait(bar, parity) || ring_wait_slow(bar, parity, abort_flag, limit);
 }
 
 // Copy tile (page, kv, g) into the ring (one thread; `bytes` already expected).

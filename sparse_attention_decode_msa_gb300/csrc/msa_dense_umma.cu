@@ -16,19 +16,22 @@
 //
 // Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA
 // lands them (K-major), P in tensor memory over the S it came from, V tiles as
-// landed (MN-major).  bf16 P is a pair hi + lo (16 significant bits; the
-// rounding of P to bf16 alone would weigh as much as the output's); E4M3 and
-// NVFP4 tiles are widened to f16 by converter warps and P is one f16 (11 bits).
+// landed (MN-major).  bf16 P is a pair hi + lo (16 significant bits)
+// in steps where some position weighs 1/64 or more of its row's denominator so
+// far; elsewhere hi alone, whose errors (2^-8 of each p at most, independent)
+// add up to some 2^-12 of the largest |v|.  E4M3 and NVFP4 tiles are widened to f16 by
+// converter warps and P is one f16 (11 bits).
 //
-// TMEM columns: S/P of step s of stream t at 128 t + 64 (s & 1), O of stream t at 256 + 128 t.
-// Warps: 0 TMA producer, 1 and 3 MMA issuers of stream 0 and 1 (1 owns the TMEM),
-// 2 V check of last pages (bf16) and outputs of idle slots, 4-7 and 8-11 softmax of stream 0 and 1,
+// TMEM columns: S/P of step s of stream t at 128 t + 64 (s & 1) (one row tile: at
+// 128 (s & 1) + 64 t), O of stream t at 256 + 128 t.
+// Warps: 0 TMA producer (and outputs of idle slots), 1 issues S (and owns the TMEM),
+// 2 and 3 issue P V of stream 0 and 1, 4-7 and 8-11 softmax of stream 0 and 1,
 // 12-15 converters (E4M3, NVFP4).
 //
 // What bounds it: the tensor cores when rows are many (measured: an MMA of
-// 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50; a page of 128
-// rows is 16 of these for S and 8, or 16 with lo, of those for P V), HBM when
-// they are few.
+// 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50 as both read 4 KiB
+// of Q from shared memory; a page of 128 rows is 16 of these for S, or 8 of those
+// with one row tile, and 8, or 16 with lo, of those for P V), HBM when they are few.
 #include "msa_cache.cuh"
 
 namespace msa {
@@ -201,6 +204,40 @@ __device__ __forceinline__ bool finite(float v)
     return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
 }
 
+// Rows of 64 positions (from row0) of a staged bf16 V tile on a last page: rows from `past` on are
+// not cached and become zeros, and so do infinities and NaN of rows from `seen` on, which only
+// later tokens see (a probability of 0 does not hide them; those tokens get them at the
+// end of the unit, told by *bad).  One warp; done twice it does no more.
+__device__ __noinline__ void clear_values(uint8_t *v, int row0, int seen, int past, volatile int *bad, int mark)
+{
+    const int from = max(row0, seen);
+    for (int k = from * 16 + (int)(threadIdx.x & 31); k < (row0 + 64) * 16; k += 32) { // 16-byte pieces
+        const int row = k >> 4, piece = k & 15;
+        uint4 *at = reinterpret_cast<uint4 *>(v + (piece >> 3) * 16384 + row * 128 + (piece & 7) * 16);
+        if (row >= past) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        uint4 d = *at;
+        uint32_t *e = &d.x;
+        bool any = false;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if ((e[c] & 0x7F80u) == 0x7F80u)
+                e[c] &= 0xFFFF0000u, any = true;
+            if ((e[c] & 0x7F800000u) == 0x7F800000u)
+                e[c] &= 0x0000FFFFu, any = true;
+        }
+        if (any) {
+            *bad = mark; // told before the value is gone
+            __threadfence_block();
+            *at = d;
+        }
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
 // The share of a CTA, unit by unit.  Every role walks it alike.
 struct Walk {
     int x, x1, r, u, b, nb, seq_len, seg;
@@ -247,13 +284,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     __shared__ int scan_tmp[NT / 32 + 1];
     __shared__ int start_r, start_before;
     __shared__ uint32_t tmem_slot;
+    __shared__ int with_lo[2][2]; // [stream][S buffer]: P of the step is a pair hi + lo
     __shared__ int later_bad[8]; // unit counter + 1 where V rows of draft tokens are not finite
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *gsm = smem_raw + (smem - smem_u32(smem_raw));
     const uint32_t full = smem + L.bars, empty = full + TILES * 8, sfull = empty + TILES * 8, sempty = sfull + kStaged * 8;
     const uint32_t q_full = sempty + kStaged * 8, q_free = q_full + 16, s_full = q_free + 8, p_full = s_full + 32,
-                   pv_done = p_full + 32, o_free = pv_done + 32, v_fixed = o_free + 16, v_landed = v_fixed + 8,
-                   drain = v_landed + 8;
+                   pv_done = p_full + 32, o_free = pv_done + 32, drain = o_free + 16;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gsm + L.misc);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int heads = p.Hkv * p.tiles;
@@ -280,11 +317,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             mbar_init(pv_done + 16 * t + 8, 1);
             mbar_init(o_free + 8 * t, 4);
         }
-        mbar_init(q_free, 2);
-        mbar_init(v_fixed, 1);
-        mbar_init(v_landed, 2);
-        mbar_init(drain, 1);
-        mbar_init(drain + 8, 1);
+        mbar_init(q_free, 1);
+        for (int i = 0; i < 3; ++i)
+            mbar_init(drain + 8 * i, 1);
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -393,131 +428,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (int i = max(0, z - TILES); i < z; ++i)
                 mbar_wait_bounded(full + 8 * (i % TILES), (uint32_t)(i / TILES) & 1u);
         __syncwarp();
-    } else if (warp == 1 || warp == 3) {
-        // ---- MMA issuer of stream t: the whole warp, lane 0 issuing ----
-        const int t = warp >> 1;
-        const uint32_t one = lane == 0, tm = uniform(tmem + 128 * t), base = uniform(smem);
-        constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
-        constexpr uint32_t idesc_s = umma_idesc_bf16(128, 64, 0, 0) & kTypes;
-        constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
-        constexpr int DEPTH = CONV ? kStaged : TILES;
-        constexpr uint32_t STEP = CONV ? kTile16 : TB, RING = CONV ? L.staged : 0;
-        const uint32_t tile_full = CONV ? sfull : full, tile_free = CONV ? sempty : empty;
-        const uint32_t q = uniform(desc_low(base + L.q + (TWO ? t * kTile16 : 0), 16));
-        int z0 = 0, fixes = 0;
-        uint32_t taken0 = 0, taken1 = 0; // steps of either S buffer
-        for (; w.x < w.x1; w.next(p, heads)) {
-            const int n = w.pages();
-            const int nsteps = TWO ? 2 * n : n;
-            wait(q_full + (TWO ? 8 * t : 0), w.seg & 1);
-            auto scores = [&](int i) { // S of step i: 64 positions, half of a K tile
-                const int z = z0 + order_of_k<TWO>(TWO ? i >> 1 : i), st = z % DEPTH;
-                const uint32_t k = uniform(desc_low(base + RING + st * STEP, 16) + (TWO ? i & 1 : t) * (64 * 128 >> 4));
-                const uint32_t d = uniform(tm + 64 * (i & 1));
-                wait(tile_full + 8 * st, (uint32_t)(z / DEPTH) & 1u);
-                tcgen05_after_sync();
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t at = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                    umma_ss(one, d, q + at, k + at, idesc_s, ks > 0);
-                }
-                if (one) {
-                    umma_commit(s_full + 16 * t + 8 * (i & 1));
-                    if (!TWO || (i & 1))
-                        umma_commit(tile_free + 8 * st);
-                    if (i == nsteps - 1)
-                        umma_commit(q_free);
-                }
-            };
-            scores(0);
-            if (nsteps > 1)
-                scores(1);
-            for (int i = 0; i < nsteps; ++i) {
-                const int page = TWO ? i >> 1 : i, z = z0 + order_of_v<TWO>(page, n), st = z % DEPTH;
-                const uint32_t v = uniform(desc_low(base + RING + st * STEP, 16384) + (TWO ? i & 1 : t) * (64 * 128 >> 4));
-                const uint32_t a = uniform(tm + 64 * (i & 1)), more = uniform(i > 0);
-                const uint32_t d = uniform(tm + 256);
-                wait(tile_full + 8 * st, (uint32_t)(z / DEPTH) & 1u);
-                if (!CONV && (!TWO || !(i & 1)) && (w.b + page + 1) * kPage > w.seq_len) {
-                    // checked by warp 2, which waits for both issuers and not for the copy: a
-                    // barrier whose phases it does not follow
-                    if (one)
-                        mbar_arrive(v_landed);
-                    wait(v_fixed, fixes++ & 1);
-                }
-                if (i == 0 && w.seg > 0)
-                    wait(o_free + 8 * t, (w.seg - 1) & 1);
-                wait(p_full + 16 * t + 8 * (i & 1), (i & 1 ? taken1++ : taken0++) & 1u);
-                tcgen05_after_sync();
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) { // V, MN-major: 16 positions are 16 rows of 128 bytes
-                    umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
-                    if (!CONV)
-                        umma_ts(one, d, a + 32 + 8 * ks, v + ks * (2048 >> 4), idesc_o, 1u);
-                }
-                if (one) {
-                    umma_commit(pv_done + 16 * t + 8 * (i & 1));
-                    if (!TWO || (i & 1))
-                        umma_commit(tile_free + 8 * st);
-                }
-                if (i + 2 < nsteps)
-                    scores(i + 2);
-            }
-            z0 += 2 * n;
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) // all lanes alike
-                break;
-        }
-        // nothing of this CTA's may be in flight when its tensor memory is freed
-        if (one) {
-            umma_commit(drain + 8 * t);
-            mbar_wait_bounded(drain + 8 * t, 0);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ---- last pages, bf16: V rows that are not cached become zeros, and so do infinities
-        // and NaN of rows that only later tokens see (added at the end of the unit) ----
-        if (!CONV) {
-            int z0 = 0, fixes = 0;
-            for (; w.x < w.x1; w.next(p, heads)) {
-                const int n = w.pages(), cached = w.seq_len + p.nq - 1;
-                for (int i = max(0, w.seq_len / kPage - w.b); i < n; ++i) {
-                    const int page0 = (w.b + i) * kPage;
-                    const int z = z0 + order_of_v<TWO>(i, n);
-                    wait(v_landed, fixes++ & 1);
-                    uint8_t *v = gsm + (z % TILES) * TB;
-                    const int from = max(0, w.seq_len - page0), past = cached - page0;
-                    bool bad = false;
-                    for (int k = from * 16 + lane; k < kPage * 16; k += 32) { // 16-byte pieces
-                        const int row = k >> 4, piece = k & 15;
-                        uint4 *at = reinterpret_cast<uint4 *>(v + (piece >> 3) * 16384 + row * 128 + (piece & 7) * 16);
-                        if (row >= past) {
-                            *at = make_uint4(0u, 0u, 0u, 0u);
-                            continue;
-                        }
-                        uint4 d = *at;
-                        uint32_t *e = &d.x;
-                        bool any = false;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if ((e[c] & 0x7F80u) == 0x7F80u)
-                                e[c] &= 0xFFFF0000u, any = true;
-                            if ((e[c] & 0x7F800000u) == 0x7F800000u)
-                                e[c] &= 0x0000FFFFu, any = true;
-                        }
-                        if (any)
-                            *at = d;
-                        bad |= any;
-                    }
-                    if (bad)
-                        later_bad[w.seg & 7] = w.seg + 1;
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(v_fixed);
-                }
-                z0 += 2 * n;
-            }
-        }
         // ---- idle slots: outputs of requests without cached positions ----
         for (int q = blockIdx.x; q < p.R; q += gridDim.x) {
             bool bad;
@@ -530,11 +440,107 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (size_t i = lane; i < rows; i += 32)
                 p.lse[q * rows + i] = __uint_as_float(0xFF800000u);
         }
-    } else if (warp < 12) {
+    } else if (warp < 4) {
+        // ---- MMA issuers: warp 1 issues S (one row tile: an S tile is a whole page, stream
+        // t takes columns 64 t ..), warps 2 and 3 P V of stream 0 and 1.  An issuer's own
+        // instructions between two MMAs take longer than an MMA, so that one issuer cannot
+        // keep the tensor cores busy ----
+        const uint32_t one = lane == 0, tm = uniform(tmem), base = uniform(smem);
+        constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
+        constexpr uint32_t idesc_s = umma_idesc_bf16(128, TWO ? 64 : 128, 0, 0) & kTypes;
+        constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
+        constexpr int DEPTH = CONV ? kStaged : TILES;
+        constexpr uint32_t STEP = CONV ? kTile16 : TB, RING = CONV ? L.staged : 0, HALF = 64 * 128 >> 4;
+        const uint32_t tile_full = CONV ? sfull : full, tile_free = CONV ? sempty : empty;
+        uint32_t fill0 = 0, fill1 = 0; // steps of either S buffer so far
+        int z0 = 0;
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages();
+            const int nsteps = TWO ? 2 * n : n;
+            if (warp == 1) {
+                wait(q_full, w.seg & 1);
+                if (TWO)
+                    wait(q_full + 8, w.seg & 1);
+                const uint32_t q = uniform(desc_low(base + L.q, 16));
+                for (int i = 0; i < nsteps; ++i) {
+                    const int z = z0 + order_of_k<TWO>(TWO ? i >> 1 : i), st = z % DEPTH;
+                    const uint32_t k = uniform(desc_low(base + RING + st * STEP, 16) + (TWO && (i & 1) ? HALF : 0u));
+                    const uint32_t fill = i & 1 ? fill1++ : fill0++;
+                    wait(tile_full + 8 * st, (uint32_t)(z / DEPTH) & 1u);
+#pragma unroll
+                    for (int t = 0; t < (TWO ? 2 : 1); ++t) {
+                        // the buffer's last P has been multiplied
+                        if (fill > 0) {
+                            wait(pv_done + 16 * t + 8 * (i & 1), (fill - 1) & 1u);
+                            if (!TWO)
+                                wait(pv_done + 16 + 8 * (i & 1), (fill - 1) & 1u);
+                        }
+                        tcgen05_after_sync();
+                        const uint32_t d = tm + uniform(TWO ? 128 * t + 64 * (i & 1) : 128 * (i & 1));
+                        const uint32_t qt = q + t * (kTile16 >> 4);
+#pragma unroll
+                        for (uint32_t ks = 0; ks < 8; ++ks)
+                            umma_ss(one, d, qt + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 1024 + (ks & 3) * 2, idesc_s, ks > 0);
+                        if (one)
+                            umma_commit(s_full + 16 * t + 8 * (i & 1));
+                    }
+                    if (one && (!TWO || (i & 1))) { // a tile is given back twice: V by either stream
+                        umma_commit(tile_free + 8 * st);
+                        umma_commit(tile_free + 8 * st);
+                    }
+                }
+                if (one)
+                    umma_commit(q_free);
+            } else {
+                const int t = warp - 2;
+                const uint32_t d = tm + uniform(256 + 128 * t);
+                for (int i = 0; i < nsteps; ++i) {
+                    const int page = TWO ? i >> 1 : i, z = z0 + order_of_v<TWO>(page, n), st = z % DEPTH;
+                    const uint32_t v = uniform(desc_low(base + RING + st * STEP, 16384) + ((TWO ? i & 1 : t) ? HALF : 0u));
+                    const uint32_t a = tm + uniform(TWO ? 128 * t + 64 * (i & 1) : 128 * (i & 1) + 64 * t);
+                    const uint32_t more = uniform(i > 0);
+                    wait(tile_full + 8 * st, (uint32_t)(z / DEPTH) & 1u);
+                    if (!CONV && (w.b + page + 1) * kPage > w.seq_len) // (converters do it for their tiles)
+                        clear_values(gsm + st * TB, (TWO ? i & 1 : t) * 64, w.seq_len - (w.b + page) * kPage,
+                                     w.seq_len + p.nq - 1 - (w.b + page) * kPage, &later_bad[w.seg & 7], w.seg + 1);
+                    if (i == 0 && w.seg > 0)
+                        wait(o_free + 8 * t, (w.seg - 1) & 1);
+                    wait(p_full + 16 * t + 8 * (i & 1), (i & 1 ? fill1++ : fill0++) & 1u);
+                    tcgen05_after_sync();
+                    // V, MN-major: 16 positions are 16 rows of 128 bytes
+                    if (!CONV && __any_sync(0xffffffffu, with_lo[t][i & 1])) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
+                            umma_ts(one, d, a + 32 + 8 * ks, v + ks * (2048 >> 4), idesc_o, 1u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
+                    }
+                    if (one) {
+                        umma_commit(pv_done + 16 * t + 8 * (i & 1));
+                        if (!TWO || (i & 1))
+                            umma_commit(tile_free + 8 * st);
+                    }
+                }
+            }
+            z0 += 2 * n;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) // all lanes alike
+                break;
+        }
+        // nothing of this CTA's may be in flight when its tensor memory is freed
+        if (one) {
+            umma_commit(drain + 8 * (warp - 1));
+            mbar_wait_bounded(drain + 8 * (warp - 1), 0);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
         // ---- softmax: thread = query row ----
         const int t = (warp - 4) >> 2, mine = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21); // this warp's lane quarter
-        const uint32_t s_at = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
+        const uint32_t o_at = lanes + 256 + 128 * t;
         const float ninf = __uint_as_float(0xFF800000u);
         float *ml = reinterpret_cast<float *>(gsm + L.ml);
         // steps that took either S buffer so far, alike for both streams.  Every
@@ -592,8 +598,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const int pos0 = (w.b + (TWO ? i >> 1 : i)) * kPage + 64 * (TWO ? i & 1 : t);
                 const bool tail = pos0 + 64 > w.seq_len;
                 const int seen = tail ? lim - pos0 : 64; // columns this row sees
-                const uint32_t at_s = s_at + 64 * (i & 1);
-                wait(s_full + 16 * t + 8 * (i & 1), (i & 1 ? fills1++ : fills0++) & 1u);
+                const uint32_t at_s = lanes + (TWO ? 128 * t + 64 * (i & 1) : 128 * (i & 1) + 64 * t);
+                wait(s_full + (TWO ? 16 * t : 0) + 8 * (i & 1), (i & 1 ? fills1++ : fills0++) & 1u);
                 tcgen05_after_sync();
                 uint32_t v[64];
                 tmem_ld32(at_s, v);
@@ -638,6 +644,21 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     }
                 }
                 l *= f;
+                // lo matters where a single position weighs much: the rounding of P to bf16
+                // (2^-8 of p) is left in only for steps in which every p is under 1/64 of its
+                // row's denominator so far (see the top)
+                bool lo_too = false;
+                if (!CONV) {
+                    uint32_t any = m != ninf && !(ex2(mx - m) * 64.f < l);
+                    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n"
+                                 " selp.u32 %0, 1, 0, q;\n}\n"
+                                 : "=r"(any)
+                                 : "r"(any), "r"(3 + t)
+                                 : "memory");
+                    lo_too = any != 0u;
+                    if (mine == 0)
+                        with_lo[t][i & 1] = lo_too;
+                }
                 const float ref = m == ninf ? 0.f : m;
                 const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref), minus = pair(-1.f, -1.f);
                 uint64_t sum[2] = {0ull, 0ull};
@@ -661,13 +682,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             hi[k] = pack_f16(e0, e1);
                         } else {
                             hi[k] = pack_bf16(e0, e1);
+                            if (!lo_too)
+                                continue;
                             float d0, d1;
                             unpair(fma2(pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u)), minus, e), d0, d1);
                             lo[k] = pack_bf16(d0, d1);
                         }
                     }
                     tmem_st16(at_s + 16 * c, hi);
-                    if (!CONV)
+                    if (!CONV && lo_too)
                         tmem_st16(at_s + 32 + 16 * c, lo);
                 }
                 {
@@ -778,7 +801,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 }
             }
         }
-    } else if (CONV) {
+    } else if (CONV && warp >= 12) {
         // ---- converters: a ring tile to a 16-bit tile, in the order of use ----
         const int row = (warp - 12) * 32 + lane;
         int z = 0;
