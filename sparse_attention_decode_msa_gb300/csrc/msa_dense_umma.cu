@@ -32,7 +32,7 @@
 // 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50 as both read 4 KiB
 // of Q from shared memory; a page of 128 rows is 16 of these for S, or 8 of those
 // with one row tile, and 8, or 16 with lo, of those for P V), HBM when they are few.
-#include "msa_cache.cuh"
+#include "msa_umma.cuh"
 
 namespace msa {
 namespace {
@@ -74,111 +74,6 @@ static_assert(smem_layout(kFmtBf16, true).total <= 232448 && smem_layout(kFmtBf1
                   smem_layout(kFmtFp8, true).total <= 232448 && smem_layout(kFmtFp8, false).total <= 232448 &&
                   smem_layout(kFmtF4, true).total <= 232448 && smem_layout(kFmtF4, false).total <= 232448,
               "shared memory");
-
-// The MMAs below are executed by a whole warp and issued by the lane with `one`
-// set.  Their operands live in uniform registers: a value the compiler cannot
-// prove uniform costs moves before every MMA (about 100 clocks an MMA, where the
-// tensor cores need 64).  A reduction over the warp gives a value that it can.
-__device__ __forceinline__ uint32_t uniform(uint32_t v)
-{
-    return __reduce_or_sync(0xffffffffu, v);
-}
-
-// Shared-memory operand descriptor (128-byte swizzle, version 1) from its low
-// word: address / 16 and the leading offset / 16 in bits 16 ..; stride 1024.
-constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
-
-__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead)
-{
-    return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16;
-}
-
-// D[tmem] (+)= A[smem] * B[smem]
-__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile("{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-                 " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
-                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
-                 "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(one), "r"(kDescHigh)
-                 : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile("{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-                 " mov.b64 b, {%2, %6};\n"
-                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(one), "r"(kDescHigh)
-                 : "memory");
-}
-
-// 32 consecutive TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-}
-
-// Wait for the loads issued so far; r (the registers of one of them) is read
-// and written here so that no use of its values can move before the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t *r)
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st()
-{
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
-        : "memory");
-}
-
-// Two fp32 at a time (the packed forms issue once for both).
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-
-__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 // One stored K (0) or V (1) value in global memory, without its tensor scale.
 template <int FMT>
@@ -237,28 +132,6 @@ __device__ __noinline__ void clear_values(uint8_t *v, int row0, int seen, int pa
     fence_async_smem();
     __syncwarp();
 }
-
-// The share of a CTA, unit by unit.  Every role walks it alike.
-struct Walk {
-    int x, x1, r, u, b, nb, seq_len, seg;
-    __device__ __forceinline__ int pages() const { return min(nb - b, x1 - x); }
-    __device__ __forceinline__ void next(const DenseParams &p, int heads)
-    {
-        x += pages();
-        ++seg;
-        b = 0;
-        if (++u == heads) {
-            u = 0;
-            bool bad;
-            do {
-                if (++r >= p.R)
-                    break;
-                seq_len = p.seq_lens[r];
-                nb = cached_blocks(seq_len, p.nq, p.maxB, &bad);
-            } while (nb == 0);
-        }
-    }
-};
 
 // Place of a tile in the order in which the issuer uses the tiles of n pages.
 template <bool TWO>

@@ -1,0 +1,178 @@
+// msa_umma.cuh -- tcgen05 issue helpers, tensor-memory loads and stores, packed
+// fp32 arithmetic and the per-CTA walk shared by the whole-cache kernels.
+#pragma once
+
+#include "msa_cache.cuh"
+
+#ifdef __CUDACC__
+
+namespace msa {
+
+// The MMAs below are executed by a whole warp and issued by the lane with `one`
+// set.  Their operands live in uniform registers: a value the compiler cannot
+// prove uniform costs moves before every MMA (about 100 clocks an MMA, where the
+// tensor cores need 64).  A reduction over the warp gives a value that it can.
+__device__ __forceinline__ uint32_t uniform(uint32_t v)
+{
+    return __reduce_or_sync(0xffffffffu, v);
+}
+
+// Shared-memory operand descriptor (128-byte swizzle, version 1) from its low
+// word: address / 16 and the leading offset / 16 in bits 16 ..; stride 1024.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead)
+{
+    return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+                 "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(one), "r"(kDescHigh)
+                 : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " mov.b64 b, {%2, %6};\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(one), "r"(kDescHigh)
+                 : "memory");
+}
+
+// 32 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+
+// Wait for the loads issued so far; r (the registers of one of them) is read
+// and written here so that no use of its values can move before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+        : "memory");
+}
+
+// Two fp32 at a time (the packed forms issue once for both).
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// One row of an E4M3 or NVFP4 tile as the TMA lands it, widened to f16 in the
+// layout of a 16-bit tile (two halves of 64 dimensions, 128-byte swizzle).
+template <int FMT>
+__device__ __forceinline__ void widen_row(const uint8_t *src, uint8_t *tile, int row)
+{
+    uint8_t *dst = tile + row * 128;
+    if (FMT == kFmtFp8) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) { // 16 dimensions
+            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
+            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                e4m3x4_to_f16x2x2(e[q], o[2 * q], o[2 * q + 1]);
+            uint8_t *at = dst + (c >> 2) * 16384;
+            *reinterpret_cast<uint4 *>(at + (((2 * c) & 7) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(at + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    } else {
+        const uint64_t sc = *reinterpret_cast<const uint64_t *>(src + 8192 + row * 8);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) { // 32 dimensions, two scales
+            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+            const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)(sc >> (16 * c)) & 0xFFFFu);
+            const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+            uint8_t *at = dst + (c >> 1) * 16384;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[4];
+                e2m1x8_scaled_f16x2(e[q], q < 2 ? sa : sb, o);
+                *reinterpret_cast<uint4 *>(at + ((((c & 1) * 4 + q) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+}
+
+// The share of a CTA, unit by unit.  Every role walks it alike.
+struct Walk {
+    int x, x1, r, u, b, nb, seq_len, seg;
+    __device__ __forceinline__ int pages() const { return min(nb - b, x1 - x); }
+    __device__ __forceinline__ void next(const CacheParams &p, int heads)
+    {
+        x += pages();
+        ++seg;
+        b = 0;
+        if (++u == heads) {
+            u = 0;
+            bool bad;
+            do {
+                if (++r >= p.R)
+                    break;
+                seq_len = p.seq_lens[r];
+                nb = cached_blocks(seq_len, p.nq, p.maxB, &bad);
+            } while (nb == 0);
+        }
+    }
+};
+
+} // namespace msa
+
+#endif // __CUDACC__

@@ -8,362 +8,489 @@
 // step's own tokens.  With the log-sum-exp of the step's attention the
 // probabilities need no second softmax: one read of K, no V.
 //
+// S^T = K Q^T on the tcgen05 tensor cores: positions are the 128 lanes of an
+// accumulator and query rows its columns, so the sum over rows is a sum over a
+// thread's own columns, and a warp reads and writes 32 consecutive weights.  No
+// exchange between threads, no atomics; rows are added in a fixed order.
+//
 // What bounds it: the bytes of K and of the weights with few rows, the
-// exponentials (16 a clock and SM) with many.  Layout: K tiles are B
-// fragments, 16 positions per warp, kept in registers while the query rows
-// pass by as A fragments staged once per (request, KV head) in shared memory;
-// the sum over rows is then a sum over a lane's own accumulators and one
-// reduction of 8 lanes per page.  Every element is written by one thread, in
-// row order: no atomics.
+// exponentials with many.  Two groups (an MMA issuer, four softmax warps and, for
+// E4M3 and NVFP4 keys that are widened to f16, four converter warps each) take
+// the pages in turn, so that one page's waits pass behind the other's work; the
+// query rows of a (request, KV head), up to 512 (bf16) or 256 at a time, stay in
+// shared memory.
 //
 // After a sparse step only pages that some token of the request selected are
 // read; a bitmap of 64 token bits per page, built in shared memory, says which
 // rows count.  The weights of the other pages are only faded.
-#include "msa_cache.cuh"
+//
+// Warps: 0 producer and bitmaps, 1 and 2 issuers, 4-7 and 8-11 softmax, 12-15
+// and 16-19 converters of group 0 and 1.
+#include "msa_umma.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kConsumers = 8;
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kQTiles = 16;     // 16-row query tiles staged at a time (256 rows, 64 KiB)
-constexpr int kPagesAtATime = 512; // pages whose token masks are held at a time
+constexpr int kPagesAtATime = 512; // pages whose bitmaps are held at a time
+constexpr int kTile16 = 32768;     // a 16-bit K tile
+constexpr int kMaxRing = 16;
 
-__host__ __device__ constexpr int ring_stages(int fmt)
+__host__ __device__ constexpr int threads_of(int fmt)
 {
-    return fmt == kFmtBf16 ? 4 : fmt == kFmtFp8 ? 8 : 14;
+    return fmt == kFmtBf16 ? 384 : 640;
 }
 
+// Query rows in shared memory at a time (E4M3 and NVFP4 keys need staged tiles besides).
+__host__ __device__ constexpr int query_rows(int fmt)
+{
+    return fmt == kFmtBf16 ? 512 : 256;
+}
+
+// Shared memory by the query rows held (a multiple of 32): the rest is the ring
+// of K tiles.  Ring and staged tiles are even in number: a slot belongs to one
+// group, which follows all of its barriers' phases.
 struct Smem {
-    int ring, q, rows, mask, bars, misc, total;
+    int ring, staged, q, cols, tok, mask, bars, misc, total;
+    int depth, nstaged;
 };
 
-__host__ __device__ constexpr Smem smem_layout(int fmt)
+__host__ __device__ inline Smem smem_layout(int fmt, int qpad, bool masks)
 {
     Smem s{};
-    s.ring = 0;
-    s.q = ring_stages(fmt) * tile_bytes(fmt);
-    s.rows = s.q + kQTiles * 4096;           // float4 per row: logit scale, lse, token
-    s.mask = s.rows + kQTiles * 16 * 16;     // uint64 per page
-    s.bars = s.mask + kPagesAtATime * 8;
-    s.misc = s.bars + 2 * ring_stages(fmt) * 8;
+    const int rest = qpad * (256 + 8 + 1) + (masks ? 2 * kPagesAtATime * 8 : 0) + (2 * kMaxRing + 32) * 8 + 64 + 1024 + 256;
+    int room = 232448 - rest;
+    s.nstaged = fmt == kFmtBf16 ? 0 : room >= 6 * kTile16 ? 4 : 2;
+    room -= s.nstaged * kTile16;
+    s.depth = room / tile_bytes(fmt) / 2 * 2;
+    s.depth = s.depth > kMaxRing ? kMaxRing : s.depth;
+    s.staged = 0;
+    s.q = s.nstaged * kTile16;
+    s.ring = s.q + qpad * 256;
+    s.cols = s.ring + s.depth * tile_bytes(fmt);
+    s.tok = s.cols + qpad * 8;
+    s.mask = (s.tok + qpad + 15) / 16 * 16;
+    s.bars = s.mask + (masks ? 2 * kPagesAtATime * 8 : 0);
+    s.misc = s.bars + (2 * kMaxRing + 32) * 8;
     s.total = s.misc + 64 + 1024;
     return s;
 }
 
-// K fragments of 16 positions, all 8 k-steps: {tile 0: b0, b1, tile 1: b0, b1}.
 template <int FMT>
-__device__ __forceinline__ void load_keys(uint32_t (&kb)[8][4], uint32_t tile, int pos0)
+__global__ void __launch_bounds__(threads_of(FMT), 1)
+    weight_kernel(const __grid_constant__ CUtensorMap map, const WeightParams p, const Smem L)
 {
-    const int lane = threadIdx.x & 31, mi = lane >> 3;
-    if (FMT == kFmtBf16) {
-        const int row = pos0 + (lane & 7) + (mi >> 1) * 8;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            const int chunk = 2 * (ks & 3) + (mi & 1);
-            ldsm_x4(kb[ks], tile + row * 128 + (ks >> 2) * 16384 + ((chunk ^ (row & 7)) << 4));
-        }
-    } else if (FMT == kFmtFp8) {
-        const int row = pos0 + (lane & 7) + (mi & 1) * 8;
-#pragma unroll
-        for (int k2 = 0; k2 < 4; ++k2) {
-            uint32_t b[4];
-            const int chunk = 2 * k2 + (mi >> 1);
-            ldsm_x4(b, tile + row * 128 + ((chunk ^ (row & 7)) << 4));
-            e4m3x4_to_f16x2x2(b[0], kb[2 * k2][0], kb[2 * k2][1]);
-            e4m3x4_to_f16x2x2(b[1], kb[2 * k2][2], kb[2 * k2][3]);
-            e4m3x4_to_f16x2x2(b[2], kb[2 * k2 + 1][0], kb[2 * k2 + 1][1]);
-            e4m3x4_to_f16x2x2(b[3], kb[2 * k2 + 1][2], kb[2 * k2 + 1][3]);
-        }
-    } else {
-        const int row = pos0 + (lane & 7) + (mi & 1) * 8;
-        uint32_t sc[2][4];
-        load_k_scales(tile, pos0, sc);
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-            uint32_t b[4];
-            const int chunk = 2 * k2 + (mi >> 1);
-            ldsm_x4(b, tile + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    uint32_t x[4];
-                    e2m1x8_scaled_f16x2(b[2 * h + t], sc[t][2 * k2 + h], x);
-                    kb[4 * k2 + 2 * h][2 * t] = x[0];
-                    kb[4 * k2 + 2 * h][2 * t + 1] = x[1];
-                    kb[4 * k2 + 2 * h + 1][2 * t] = x[2];
-                    kb[4 * k2 + 2 * h + 1][2 * t + 1] = x[3];
-                }
-        }
-    }
-}
-
-template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1)
-    weight_kernel(const __grid_constant__ CUtensorMap map, const WeightParams p)
-{
-    constexpr int STAGES = ring_stages(FMT), TB = tile_bytes(FMT);
+    constexpr int TB = tile_bytes(FMT), NT = threads_of(FMT);
+    constexpr bool CONV = FMT != kFmtBf16;
+    constexpr int kQRows = query_rows(FMT);
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int scan_tmp[kThreads / 32 + 1];
+    __shared__ int scan_tmp[NT / 32 + 1];
     __shared__ int start_r, start_before;
-    constexpr Smem L = smem_layout(FMT);
+    __shared__ uint32_t tmem_slot;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = smem + L.bars, empty = full + STAGES * 8;
     uint8_t *gsm = smem_raw + (smem - smem_u32(smem_raw));
-    uint4 *qf = reinterpret_cast<uint4 *>(gsm + L.q);         // [tile][k-step][lane]
-    float4 *rows4 = reinterpret_cast<float4 *>(gsm + L.rows); // [row]
-    unsigned long long *mask = reinterpret_cast<unsigned long long *>(gsm + L.mask);
+    const uint32_t full = smem + L.bars, empty = full + kMaxRing * 8, sfull = empty + kMaxRing * 8, sempty = sfull + 32,
+                   q_full = sempty + 32, q_free = q_full + 8, s_full = q_free + 8, s_free = s_full + 32, m_full = s_free + 32,
+                   m_free = m_full + 16, drain = m_free + 16;
+    float4 *cols = reinterpret_cast<float4 *>(gsm + L.cols); // per column pair: scales, -lse
+    uint8_t *tok = gsm + L.tok;                              // token of a column
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gsm + L.misc);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n8 = lane >> 2, c4 = lane & 3;
-    const int rows = p.nq * p.G;
+    const int rows = p.nq * p.G, heads = p.Hkv;
+    const bool sparse = p.selected != nullptr;
+    const long long wl = p.wait_limit;
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map);
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < L.depth; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, kConsumers);
+            mbar_init(empty + 8 * i, CONV ? 4 : 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(sfull + 8 * i, 4);
+            mbar_init(sempty + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(s_free + 8 * i, 4);
+        }
+        mbar_init(q_full, 8);
+        mbar_init(q_free, 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(m_full + 8 * i, 1);
+            mbar_init(m_free + 8 * i, CONV ? 18 : 10);
+            mbar_init(drain + 8 * i, 1);
         }
         fence_mbar_init();
         *abort_flag = 0;
     }
-    const int per = (p.R + kThreads - 1) / kThreads;
+    if (warp == 1)
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+    const int per = (p.R + NT - 1) / NT;
     const int lo = min(p.R, (int)threadIdx.x * per), hi = min(p.R, lo + per);
     int total;
     const int before = scan_blocks(p, lo, hi, scan_tmp, &total);
-    const int W = total * p.Hkv;
-    const int x0 = range_start(blockIdx.x, W, gridDim.x), x1 = range_start(blockIdx.x + 1, W, gridDim.x);
-    if (x0 == x1)
-        return;
-    for (int r = lo, b = before; r < hi; ++r) {
-        bool bad;
-        const int nb = cached_blocks(p.seq_lens[r], p.nq, p.maxB, &bad);
-        if (nb > 0 && b * p.Hkv <= x0 && x0 < (b + nb) * p.Hkv) {
-            start_r = r;
-            start_before = b;
+    const int W = total * heads;
+    Walk w{};
+    w.x = range_start(blockIdx.x, W, gridDim.x);
+    w.x1 = range_start(blockIdx.x + 1, W, gridDim.x);
+    w.nb = 1;
+    if (w.x < w.x1)
+        for (int r = lo, b = before; r < hi; ++r) {
+            bool bad;
+            const int nb = cached_blocks(p.seq_lens[r], p.nq, p.maxB, &bad);
+            if (nb > 0 && b * heads <= w.x && w.x < (b + nb) * heads) {
+                start_r = r;
+                start_before = b;
+            }
+            b += nb;
         }
-        b += nb;
-    }
+    tcgen05_before_sync();
     __syncthreads();
-    bool bad;
-    int r = start_r, seq_len = p.seq_lens[r];
-    int nb = cached_blocks(seq_len, p.nq, p.maxB, &bad);
-    const int in = x0 - start_before * p.Hkv;
-    int g = in / nb, b = in - g * nb;
-
-    int st = 0, issued = 0;
+    tcgen05_after_sync();
+    const uint32_t tmem = tmem_slot;
+    if (w.x < w.x1) {
+        bool bad;
+        w.r = start_r;
+        w.seq_len = p.seq_lens[w.r];
+        w.nb = cached_blocks(w.seq_len, p.nq, p.maxB, &bad);
+        const int in = w.x - start_before * heads;
+        w.u = in / w.nb;
+        w.b = in - w.u * w.nb;
+    }
+    // a wait that ran out: the CTA's roles run on without waiting, so that all reach the end
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!ring_wait(bar, parity, abort_flag, wl) && !*abort_flag) {
+            *abort_flag = 1;
+            set_error(p.err, kErrTimeout);
+        }
+    };
+    // Every role walks units, chunks of query rows and (after a sparse step) runs of
+    // pages alike: `round` counts the runs, z the pages that are read (group z & 1),
+    // st / ph the ring slot of page z.
+    int round = 0, z = 0, st = 0;
     uint32_t ph = 0;
-    bool stop = false;
-    for (int x = x0; x < x1;) {
-        const int n = min(nb - b, x1 - x); // pages b .. b + n - 1 of (r, g)
-        const size_t first_row = (size_t)r * p.nq * p.Hkv * p.G + (size_t)g * p.G;
-        const size_t pitch = (size_t)p.Hkv * p.G;
-        const size_t wrow = ((size_t)r * p.Hkv + g) * p.maxB * kPage;
-        for (int q0 = 0; q0 < rows; q0 += 16 * kQTiles) {
-            const int tiles = min(kQTiles, (rows - q0 + 15) / 16);
-            for (int s0 = 0; s0 < n; s0 += kPagesAtATime) {
-                const int sn = min(kPagesAtATime, n - s0), sb = b + s0;
-                __syncthreads(); // the last pages' queries and masks are done with
-                if (p.selected)
-                    for (int i = threadIdx.x; i < sn; i += kThreads)
-                        mask[i] = 0ull;
-                if (s0 == 0)
-                    for (int t = warp; t < tiles; t += kThreads / 32) {
-                        const int i0 = q0 + 16 * t + n8, i1 = i0 + 8;
-                        const int j0 = min(i0, rows - 1) / p.G, j1 = min(i1, rows - 1) / p.G;
-                        const size_t a0 = first_row + j0 * pitch + (min(i0, rows - 1) - j0 * p.G);
-                        const size_t a1 = first_row + j1 * pitch + (min(i1, rows - 1) - j1 * p.G);
-                        uint32_t q[8][4];
-                        float inv0, inv1;
-                        // padding rows repeat the last row: zeros would turn an infinite key into NaN
-                        load_queries<FMT>(q, p.q + a0 * kDim, p.q + a1 * kDim, inv0, inv1);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            qf[(t * 8 + ks) * 32 + lane] = make_uint4(q[ks][0], q[ks][1], q[ks][2], q[ks][3]);
-                        if (c4 == 0) {
-                            // rows that count nothing (padding, or a token that attended to nothing:
-                            // lse = -inf) get lse = +inf
-                            const float inf = __uint_as_float(0x7F800000u);
-                            float e0 = i0 < rows ? p.lse[a0] : inf, e1 = i1 < rows ? p.lse[a1] : inf;
-                            e0 = e0 == -inf ? inf : e0 * 1.4426950408889634f;
-                            e1 = e1 == -inf ? inf : e1 * 1.4426950408889634f;
-                            rows4[16 * t + n8] = make_float4(p.scale_log2 * inv0, e0, __int_as_float(j0), 0.f);
-                            rows4[16 * t + n8 + 8] = make_float4(p.scale_log2 * inv1, e1, __int_as_float(j1), 0.f);
-                        }
-                    }
-                if (p.selected) {
-                    __syncthreads();
-                    // one bit per token for every page of [sb, sb + sn) in its table
-                    for (int i = threadIdx.x; i < p.nq * p.k; i += kThreads) {
-                        const int j = i / p.k;
-                        const int blk = p.selected[(((size_t)r * p.nq + j) * p.Hs + (p.Hs > 1 ? g : 0)) * p.k + (i - j * p.k)];
-                        if (blk < -1 || (blk >= 0 && (long long)blk * kPage >= seq_len + j))
-                            set_error(p.err, kErrSelection);
-                        else if (blk >= sb && blk < sb + sn)
-                            atomicOr(&mask[blk - sb], 1ull << j);
-                    }
-                }
-                __syncthreads();
+    auto bits_of = [&](int i) { // token bits of page i of the run
+        return sparse ? reinterpret_cast<const volatile unsigned long long *>(gsm + L.mask)[(round & 1) * kPagesAtATime + i] : ~0ull;
+    };
+    auto next_tile = [&] {
+        ++z;
+        if (++st == L.depth) {
+            st = 0;
+            ph ^= 1u;
+        }
+    };
+    auto run_begins = [&] {
+        if (sparse)
+            wait(m_full + 8 * (round & 1), (uint32_t)(round >> 1) & 1u);
+    };
+    auto run_ends = [&] {
+        if (sparse) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(m_free + 8 * (round & 1));
+        }
+        ++round;
+    };
 
-                if (warp == kConsumers) {
-                    const int32_t *row = p.block_table + (size_t)r * p.maxB;
-                    for (int i = 0; i < sn && !stop; i += 32) {
-                        const bool want = i + lane < sn && (!p.selected || mask[i + lane] != 0ull);
+    if (warp == 0) {
+        // ---- producer ----
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages(), g = w.u;
+            const int32_t *row = p.block_table + (size_t)w.r * p.maxB;
+            for (int q0 = 0; q0 < rows; q0 += kQRows)
+                for (int s0 = 0; s0 < n; s0 += sparse ? kPagesAtATime : n, ++round) {
+                    const int sb = w.b + s0, sn = sparse ? min(kPagesAtATime, n - s0) : n;
+                    unsigned long long *mask = reinterpret_cast<unsigned long long *>(gsm + L.mask) + (round & 1) * kPagesAtATime;
+                    if (sparse) {
+                        if (round >= 2)
+                            wait(m_free + 8 * (round & 1), (uint32_t)((round >> 1) - 1) & 1u);
+                        for (int i = lane; i < sn; i += 32)
+                            mask[i] = 0ull;
+                        __syncwarp();
+                        // one bit per token for every page of [sb, sb + sn) in its table
+                        for (int i = lane; i < p.nq * p.k; i += 32) {
+                            const int j = i / p.k;
+                            const int blk = p.selected[(((size_t)w.r * p.nq + j) * p.Hs + (p.Hs > 1 ? g : 0)) * p.k + (i - j * p.k)];
+                            if (blk < -1 || (blk >= 0 && (long long)blk * kPage >= w.seq_len + j))
+                                set_error(p.err, kErrSelection);
+                            else if (blk >= sb && blk < sb + sn)
+                                atomicOr(&mask[blk - sb], 1ull << j);
+                        }
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(m_full + 8 * (round & 1));
+                    }
+                    for (int i = 0; i < sn; i += 32) {
+                        const bool want = i + lane < sn && (!sparse || bits_of(i + lane) != 0ull);
                         const int mine = want ? row[sb + i + lane] : 0;
-                        uint32_t todo = __ballot_sync(0xffffffffu, want);
-                        while (todo) {
-                            const int k = __ffs(todo) - 1;
-                            todo &= todo - 1;
-                            long long page = __shfl_sync(0xffffffffu, mine, k);
+                        for (uint32_t todo = __ballot_sync(0xffffffffu, want); todo; todo &= todo - 1) {
+                            long long page = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
                             if (page < 0 || page >= p.num_pages) {
                                 if (lane == 0)
                                     set_error(p.err, kErrPage);
                                 page = 0; // in the pool: the outputs of the call are unspecified
                             }
-                            const bool ok = issued < STAGES ||
-                                            ring_wait(empty + 8 * st, ph ^ 1u, abort_flag, p.wait_limit);
-                            if (__any_sync(0xffffffffu, !ok)) {
-                                *abort_flag = 1;
-                                stop = true;
-                                if (lane == 0)
-                                    set_error(p.err, kErrTimeout);
-                                break;
-                            }
+                            if (z >= L.depth)
+                                wait(empty + 8 * st, ph ^ 1u);
+                            if (__any_sync(0xffffffffu, *abort_flag != 0))
+                                continue;
                             if (lane == 0) {
-                                const uint32_t bar = full + 8 * st;
-                                mbar_arrive_expect_tx(bar, TB);
-                                load_tile<FMT>(smem + st * TB, &map, p.kv, (page * 2) * p.Hkv + g, bar);
+                                mbar_arrive_expect_tx(full + 8 * st, TB);
+                                load_tile<FMT>(smem + L.ring + st * TB, &map, p.kv, (page * 2) * p.Hkv + g, full + 8 * st);
                             }
                             __syncwarp();
-                            ++issued;
-                            if (++st == STAGES) {
-                                st = 0;
-                                ph ^= 1u;
-                            }
-                        }
-                    }
-                } else {
-                    for (int i = 0; i < sn; ++i) {
-                        const int page0 = (sb + i) * kPage;
-                        const unsigned long long m = p.selected ? mask[i] : ~0ull;
-                        if (m == 0ull) { // no row looks at this page: its weights fade
-                            if ((i & 7) == warp && q0 == 0) {
-                                const size_t at = wrow + page0 + 4 * lane;
-                                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (p.weights_in)
-                                    v = *reinterpret_cast<const float4 *>(p.weights_in + at);
-                                float e[4] = {v.x * p.decay, v.y * p.decay, v.z * p.decay, v.w * p.decay};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int pos = page0 + 4 * lane + k;
-                                    if (pos < seq_len + p.nq - 1)
-                                        p.weights_out[at + k] = pos < seq_len - 1 ? e[k] : 0.f;
-                                }
-                            }
-                            continue;
-                        }
-                        // this warp's 16 positions: lanes of the first row write two pairs
-                        const int pos = 16 * warp + 2 * c4;
-                        float old[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (n8 == 0) {
-                            const float *src = q0 > 0 ? p.weights_out : p.weights_in;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int at = page0 + pos + (k & 1) + 8 * (k >> 1);
-                                if (q0 > 0 ? at < seq_len + p.nq - 1 : src && at < seq_len - 1)
-                                    old[k] = src[wrow + at];
-                                if (q0 == 0)
-                                    old[k] *= p.decay;
-                            }
-                        }
-                        if (!ring_wait(full + 8 * st, ph, abort_flag, p.wait_limit) && !*abort_flag) {
-                            *abort_flag = 1;
-                            if (lane == 0)
-                                set_error(p.err, kErrTimeout);
-                        }
-                        uint32_t kb[8][4];
-                        load_keys<FMT>(kb, smem + st * TB, 16 * warp);
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(empty + 8 * st);
-                        if (++st == STAGES) {
-                            st = 0;
-                            ph ^= 1u;
-                        }
-                        const bool part = page0 + kPage > seq_len || p.selected;
-                        float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                        for (int t = 0; t < tiles; ++t) {
-                            float s[2][2][4];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                s[k >> 3][(k >> 2) & 1][k & 3] = 0.f;
-#pragma unroll
-                            for (int ks = 0; ks < 8; ++ks) {
-                                const uint4 v = qf[(t * 8 + ks) * 32 + lane];
-                                const uint32_t a[4] = {v.x, v.y, v.z, v.w};
-                                mma_fmt<FMT>(s[ks & 1][0], a, kb[ks][0], kb[ks][1]);
-                                mma_fmt<FMT>(s[ks & 1][1], a, kb[ks][2], kb[ks][3]);
-                            }
-                            const float4 ra = rows4[16 * t + n8], rb = rows4[16 * t + n8 + 8];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float4 &rr = e < 2 ? ra : rb;
-                                    float v = ex2(fmaf(s[0][k][e] + s[1][k][e], rr.x, -rr.y));
-                                    if (part) {
-                                        const int j = __float_as_int(rr.z), at = page0 + pos + 8 * k + (e & 1);
-                                        if (at >= seq_len + j || !((m >> j) & 1ull))
-                                            v = 0.f;
-                                    }
-                                    w[2 * k + (e & 1)] += v;
-                                }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            w[k] += __shfl_xor_sync(0xffffffffu, w[k], 4);
-                            w[k] += __shfl_xor_sync(0xffffffffu, w[k], 8);
-                            w[k] += __shfl_xor_sync(0xffffffffu, w[k], 16);
-                        }
-                        if (n8 == 0) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int at = page0 + pos + (k & 1) + 8 * (k >> 1);
-                                if (at < seq_len + p.nq - 1)
-                                    p.weights_out[wrow + at] = old[k] + w[k];
-                            }
+                            next_tile();
                         }
                     }
                 }
+        }
+        if (lane == 0) // the CTA's memory must outlive the copies in flight
+            for (int i = max(0, z - L.depth); i < z; ++i)
+                mbar_wait_bounded(full + 8 * (i % L.depth), (uint32_t)(i / L.depth) & 1u);
+        __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+        // ---- MMA issuers: the whole warp, lane 0 issuing ----
+        const int grp = warp - 1;
+        const uint32_t one = lane == 0, tm = uniform(tmem + 256 * grp), base = uniform(smem), q = uniform(desc_low(base + L.q, 16));
+        const uint32_t idesc = umma_idesc_bf16(128, 0, 0, 0) & (CONV ? ~((1u << 7) | (1u << 10)) : ~0u);
+        uint32_t item = 0, qround = 0;
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages();
+            for (int q0 = 0; q0 < rows; q0 += kQRows, ++qround) {
+                const int qpad = min(kQRows, (rows - q0 + 31) / 32 * 32);
+                const uint32_t half = uniform(qpad * 128 >> 4);
+                wait(q_full, qround & 1u);
+                for (int s0 = 0; s0 < n; s0 += sparse ? kPagesAtATime : n) {
+                    const int sn = sparse ? min(kPagesAtATime, n - s0) : n;
+                    run_begins();
+                    for (int i = 0; i < sn; ++i) {
+                        if (bits_of(i) == 0ull)
+                            continue;
+                        if ((z & 1) == grp) {
+                            const int slot = CONV ? z % L.nstaged : st;
+                            const uint32_t k = uniform(desc_low(base + (CONV ? L.staged + slot * kTile16 : L.ring + slot * TB), 16));
+                            wait(CONV ? sfull + 8 * slot : full + 8 * st, CONV ? (uint32_t)(z / L.nstaged) & 1u : ph);
+                            for (int c = 0; c < qpad; c += 128, ++item) {
+                                const uint32_t d = tm + uniform(128 * (item & 1u)), b = q + uniform(c * 128 >> 4);
+                                const uint32_t id = uniform(idesc | (uint32_t)(min(128, qpad - c) >> 3) << 17);
+                                if (item >= 2)
+                                    wait(s_free + 16 * grp + 8 * (item & 1u), ((item >> 1) - 1) & 1u);
+                                tcgen05_after_sync();
+#pragma unroll
+                                for (uint32_t ks = 0; ks < 4; ++ks)
+                                    umma_ss(one, d, k + ks * 2, b + ks * 2, id, ks > 0);
+#pragma unroll
+                                for (uint32_t ks = 0; ks < 4; ++ks)
+                                    umma_ss(one, d, k + 1024 + ks * 2, b + half + ks * 2, id, 1u);
+                                if (one)
+                                    umma_commit(s_full + 16 * grp + 8 * (item & 1u));
+                            }
+                            if (one)
+                                umma_commit(CONV ? sempty + 8 * slot : empty + 8 * st);
+                        }
+                        next_tile();
+                    }
+                    run_ends();
+                }
+                if (one)
+                    umma_commit(q_free);
             }
         }
-        x += n;
-        b = 0;
-        if (++g == p.Hkv) {
-            g = 0;
-            do {
-                if (++r >= p.R)
-                    break;
-                seq_len = p.seq_lens[r];
-                nb = cached_blocks(seq_len, p.nq, p.maxB, &bad);
-            } while (nb == 0);
+        if (one) { // nothing of this CTA's may be in flight when its tensor memory is freed
+            umma_commit(drain + 8 * grp);
+            mbar_wait_bounded(drain + 8 * grp, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        // ---- softmax: thread = position ----
+        const int grp = (warp - 4) >> 2, mine = (warp & 3) * 32 + lane, me = threadIdx.x - 128;
+        const uint32_t s_at = tmem + 256 * grp + ((uint32_t)(warp & 3) << 21);
+        const float inf = __uint_as_float(0x7F800000u);
+        uint32_t item = 0, qround = 0;
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages(), g = w.u, cached = w.seq_len + p.nq - 1;
+            const size_t first_row = (size_t)w.r * p.nq * p.Hkv * p.G + (size_t)g * p.G, pitch = (size_t)p.Hkv * p.G;
+            const size_t wrow = ((size_t)w.r * p.Hkv + g) * p.maxB * kPage;
+            for (int q0 = 0; q0 < rows; q0 += kQRows, ++qround) {
+                const int qpad = min(kQRows, (rows - q0 + 31) / 32 * 32);
+                asm volatile("bar.sync 1, 256;" ::: "memory"); // the last rows' columns are done with
+                if (qround > 0)
+                    wait(q_free, (qround - 1) & 1u);
+                for (int i = me; i < qpad; i += 256) {
+                    // padding columns repeat the last row (zeros would turn an infinite key into
+                    // NaN) and count nothing, as do tokens that attended to nothing (lse = -inf)
+                    const int at = min(q0 + i, rows - 1), j = at / p.G;
+                    const size_t src = first_row + j * pitch + (at - j * p.G);
+                    const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + src * kDim);
+                    float inv = 1.f, up = 1.f;
+                    if (CONV) { // into f16's range by a power of two (see load_queries)
+                        float mx = 0.f;
+                        for (int c = 0; c < 16; ++c) {
+                            const uint4 d = qrow[c];
+                            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+                        }
+                        int e = (int)(__float_as_uint(mx) >> 23) - 127;
+                        e = e < -100 ? -100 : e > 127 ? 127 : e;
+                        up = __uint_as_float((uint32_t)(8 - e + 127) << 23);
+                        inv = __uint_as_float((uint32_t)(e - 8 + 127) << 23);
+                    }
+                    uint8_t *dst = gsm + L.q + i * 128;
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        uint4 d = qrow[c];
+                        if (CONV) {
+                            uint32_t *e = &d.x;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                e[k] = pack_f16(__uint_as_float(e[k] << 16) * up, __uint_as_float(e[k] & 0xFFFF0000u) * up);
+                        }
+                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * qpad * 128 + (((c & 7) ^ (i & 7)) << 4)) = d;
+                    }
+                    const float e = q0 + i < rows ? p.lse[src] : inf;
+                    float *info = reinterpret_cast<float *>(cols + (i >> 1)) + (i & 1);
+                    info[0] = p.scale_log2 * inv;
+                    info[2] = e == -inf ? -inf : e * -1.4426950408889634f;
+                    tok[i] = (uint8_t)j;
+                }
+                fence_async_smem();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (lane == 0)
+                    mbar_arrive(q_full);
+                const float *src = q0 > 0 ? p.weights_out : p.weights_in;
+                for (int s0 = 0; s0 < n; s0 += sparse ? kPagesAtATime : n) {
+                    const int sn = sparse ? min(kPagesAtATime, n - s0) : n, sb = w.b + s0;
+                    run_begins();
+                    for (int i = 0; i < sn; ++i) {
+                        const unsigned long long bits = bits_of(i);
+                        if (bits == 0ull)
+                            continue;
+                        if ((z++ & 1) != grp)
+                            continue;
+                        const int at = (sb + i) * kPage + mine;
+                        float old = 0.f;
+                        if (q0 > 0 ? at < cached : src && at < w.seq_len - 1)
+                            old = src[wrow + at];
+                        const bool part = sparse || (sb + i + 1) * kPage > w.seq_len;
+                        uint64_t sum[2] = {0ull, 0ull};
+                        for (int c0 = 0; c0 < qpad; c0 += 128, ++item) {
+                            const int cn = min(128, qpad - c0);
+                            wait(s_full + 16 * grp + 8 * (item & 1u), (item >> 1) & 1u);
+                            tcgen05_after_sync();
+                            const uint32_t s_buf = s_at + 128 * (item & 1u);
+                            uint32_t v[32];
+#pragma unroll 1
+                            for (int c = 0; c < cn; c += 32) {
+                                tmem_ld32(s_buf + c, v);
+                                tmem_wait_ld(v);
+                                const float4 *info = cols + ((c0 + c) >> 1);
+                                if (!part) {
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        const float4 f = info[k];
+                                        float e0, e1;
+                                        unpair(fma2(pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), pair(f.x, f.y),
+                                                    pair(f.z, f.w)), e0, e1);
+                                        sum[k & 1] = add2(sum[k & 1], pair(ex2(e0), ex2(e1)));
+                                    }
+                                } else {
+                                    // a token counts where it looked at this block and sees the position
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        const float4 f = info[k];
+                                        const int j0 = tok[c0 + c + 2 * k], j1 = tok[c0 + c + 2 * k + 1];
+                                        const bool u0 = ((bits >> j0) & 1ull) && at < w.seq_len + j0;
+                                        const bool u1 = ((bits >> j1) & 1ull) && at < w.seq_len + j1;
+                                        const float e0 = ex2(fmaf(__uint_as_float(v[2 * k]), f.x, f.z));
+                                        const float e1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), f.y, f.w));
+                                        sum[k & 1] = add2(sum[k & 1], pair(u0 ? e0 : 0.f, u1 ? e1 : 0.f));
+                                    }
+                                    __syncwarp();
+                                }
+                            }
+                            tcgen05_before_sync();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(s_free + 16 * grp + 8 * (item & 1u));
+                        }
+                        float a, b;
+                        unpair(add2(sum[0], sum[1]), a, b);
+                        if (at < cached)
+                            p.weights_out[wrow + at] = (q0 > 0 ? old : old * p.decay) + (a + b);
+                    }
+                    if (sparse && q0 == 0) { // pages that no token looked at: their weights fade
+                        const int w8 = warp - 4;
+                        for (int i = w8; i < sn; i += 8) {
+                            if (bits_of(i) != 0ull)
+                                continue;
+                            const size_t o = wrow + (size_t)(sb + i) * kPage + 4 * lane;
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (src)
+                                v = *reinterpret_cast<const float4 *>(src + o);
+                            const int at = (sb + i) * kPage + 4 * lane;
+                            v.x *= p.decay, v.y *= p.decay, v.z *= p.decay, v.w *= p.decay;
+                            if (at + 4 <= w.seq_len - 1) {
+                                *reinterpret_cast<float4 *>(p.weights_out + o) = v;
+                            } else {
+                                const float e[4] = {v.x, v.y, v.z, v.w};
+                                for (int k = 0; k < 4; ++k)
+                                    if (at + k < cached)
+                                        p.weights_out[o + k] = at + k < w.seq_len - 1 ? e[k] : 0.f;
+                            }
+                        }
+                    }
+                    run_ends();
+                }
+            }
+        }
+    } else if (CONV && warp >= 12) {
+        // ---- converters: a ring tile to a 16-bit tile ----
+        const int grp = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
+        for (; w.x < w.x1; w.next(p, heads)) {
+            const int n = w.pages();
+            for (int q0 = 0; q0 < rows; q0 += kQRows)
+                for (int s0 = 0; s0 < n; s0 += sparse ? kPagesAtATime : n) {
+                    const int sn = sparse ? min(kPagesAtATime, n - s0) : n;
+                    run_begins();
+                    for (int i = 0; i < sn; ++i) {
+                        if (bits_of(i) == 0ull)
+                            continue;
+                        if ((z & 1) == grp) {
+                            const int slot = z % L.nstaged;
+                            wait(full + 8 * st, ph);
+                            if (z >= L.nstaged)
+                                wait(sempty + 8 * slot, (uint32_t)(z / L.nstaged - 1) & 1u);
+                            widen_row<FMT>(gsm + L.ring + st * TB, gsm + L.staged + slot * kTile16, row);
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(empty + 8 * st);
+                                mbar_arrive(sfull + 8 * slot);
+                            }
+                        }
+                        next_tile();
+                    }
+                    run_ends();
+                }
         }
     }
-    // the CTA's memory must outlive the copies in flight, also after a wait ran out
-    if (warp == kConsumers && lane == 0)
-        for (int i = max(0, issued - STAGES); i < issued; ++i)
-            mbar_wait_bounded(full + 8 * (i % STAGES), (uint32_t)(i / STAGES) & 1u);
+
+    tcgen05_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tcgen05_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
 template <int FMT>
 cudaError_t launch_t(const WeightParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
 {
-    constexpr int smem = smem_layout(FMT).total;
-    cudaError_t e = cudaFuncSetAttribute(weight_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int rows = p.nq * p.G, qpad = rows >= query_rows(FMT) ? query_rows(FMT) : (rows + 31) / 32 * 32;
+    const Smem L = smem_layout(FMT, qpad, p.selected != nullptr);
+    cudaError_t e = cudaFuncSetAttribute(weight_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
     if (e == cudaSuccess)
-        e = launch_kernel(weight_kernel<FMT>, dim3(ctas), dim3(kThreads), smem, stream, false, map, p);
+        e = launch_kernel(weight_kernel<FMT>, dim3(ctas), dim3(threads_of(FMT)), (size_t)L.total, stream, false, map, p, L);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
