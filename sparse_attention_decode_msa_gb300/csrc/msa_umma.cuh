@@ -36,6 +36,16 @@ __device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d, uint32_t a_low
                  : "memory");
 }
 
+// The same with 8-bit operands.
+__device__ __forceinline__ void umma_ss8(uint32_t one, uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+                 "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(one), "r"(kDescHigh)
+                 : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, uint32_t accumulate)
 {
@@ -111,6 +121,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+
+// Two floats to E4M3 (round to nearest, saturating): a -> low byte, b -> high byte.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b)
+{
+    uint32_t out;
+    asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n cvt.u32.u16 %0, t;\n}\n"
+        : "=r"(out)
+        : "f"(a), "f"(b));
+    return out;
 }
 
 // One row of an E4M3 or NVFP4 tile as the TMA lands it, widened to f16 in the

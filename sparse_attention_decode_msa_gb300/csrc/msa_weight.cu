@@ -13,9 +13,15 @@
 // thread's own columns, and a warp reads and writes 32 consecutive weights.  No
 // exchange between threads, no atomics; rows are added in a fixed order.
 //
+// bf16 keys are operands as they land.  So are E4M3 keys with up to 64 query rows:
+// each bf16 query row then is two columns, an E4M3 pair hi + lo after a power of
+// two that brings its largest element near 448.  The pair carries bf16's 8 bits for
+// elements down to 2^-14 of the row's largest and is at most 2^-19 of that off below.
+// With more rows, and for NVFP4 keys, converter warps widen K to f16.
+//
 // What bounds it: the bytes of K and of the weights with few rows, the
-// exponentials with many.  Two groups (an MMA issuer, four softmax warps and, for
-// E4M3 and NVFP4 keys that are widened to f16, four converter warps each) take
+// exponentials with many.  Two groups (an MMA issuer, four softmax warps and,
+// where keys are widened, four converter warps each) take
 // the pages in turn, so that one page's waits pass behind the other's work; the
 // query rows of a (request, KV head), up to 512 (bf16) or 256 at a time, stay in
 // shared memory.
@@ -26,6 +32,8 @@
 //
 // Warps: 0 producer and bitmaps, 1 and 2 issuers, 4-7 and 8-11 softmax, 12-15
 // and 16-19 converters of group 0 and 1.
+#include <type_traits>
+
 #include "msa_umma.cuh"
 
 namespace msa {
@@ -35,18 +43,37 @@ constexpr int kPagesAtATime = 512; // pages whose bitmaps are held at a time
 constexpr int kTile16 = 32768;     // a 16-bit K tile
 constexpr int kMaxRing = 16;
 
+// Key formats of the kernel instances: as stored, or (kFmtPair) E4M3 keys as operands.
+constexpr int kFmtPair = 3;
+
+__host__ __device__ constexpr int stored_fmt(int fmt)
+{
+    return fmt == kFmtPair ? kFmtFp8 : fmt;
+}
+
+__host__ __device__ constexpr bool widened(int fmt)
+{
+    return fmt == kFmtFp8 || fmt == kFmtF4;
+}
+
 __host__ __device__ constexpr int threads_of(int fmt)
 {
-    return fmt == kFmtBf16 ? 384 : 640;
+    return widened(fmt) ? 640 : 384;
 }
 
 // Query rows in shared memory at a time (E4M3 and NVFP4 keys need staged tiles besides).
 __host__ __device__ constexpr int query_rows(int fmt)
 {
-    return fmt == kFmtBf16 ? 512 : 256;
+    return fmt == kFmtBf16 ? 512 : fmt == kFmtPair ? 64 : 256;
 }
 
-// Shared memory by the query rows held (a multiple of 32): the rest is the ring
+// Rows held are padded to whole loads of 32 accumulator columns.
+__host__ __device__ constexpr int padded(int fmt, int rows)
+{
+    return fmt == kFmtPair ? (rows + 15) / 16 * 16 : (rows + 31) / 32 * 32;
+}
+
+// Shared memory by the query rows held: the rest is the ring
 // of K tiles.  Ring and staged tiles are even in number: a slot belongs to one
 // group, which follows all of its barriers' phases.
 struct Smem {
@@ -59,14 +86,14 @@ __host__ __device__ inline Smem smem_layout(int fmt, int qpad, bool masks)
     Smem s{};
     const int rest = qpad * (256 + 8 + 1) + (masks ? 2 * kPagesAtATime * 8 : 0) + (2 * kMaxRing + 32) * 8 + 64 + 1024 + 256;
     int room = 232448 - rest;
-    s.nstaged = fmt == kFmtBf16 ? 0 : room >= 6 * kTile16 ? 4 : 2;
+    s.nstaged = !widened(fmt) ? 0 : room >= 6 * kTile16 ? 4 : 2;
     room -= s.nstaged * kTile16;
-    s.depth = room / tile_bytes(fmt) / 2 * 2;
+    s.depth = room / tile_bytes(stored_fmt(fmt)) / 2 * 2;
     s.depth = s.depth > kMaxRing ? kMaxRing : s.depth;
     s.staged = 0;
     s.q = s.nstaged * kTile16;
     s.ring = s.q + qpad * 256;
-    s.cols = s.ring + s.depth * tile_bytes(fmt);
+    s.cols = s.ring + s.depth * tile_bytes(stored_fmt(fmt));
     s.tok = s.cols + qpad * 8;
     s.mask = (s.tok + qpad + 15) / 16 * 16;
     s.bars = s.mask + (masks ? 2 * kPagesAtATime * 8 : 0);
@@ -79,8 +106,8 @@ template <int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
     weight_kernel(const __grid_constant__ CUtensorMap map, const WeightParams p, const Smem L)
 {
-    constexpr int TB = tile_bytes(FMT), NT = threads_of(FMT);
-    constexpr bool CONV = FMT != kFmtBf16;
+    constexpr int TB = tile_bytes(stored_fmt(FMT)), NT = threads_of(FMT);
+    constexpr bool CONV = widened(FMT), PAIR = FMT == kFmtPair;
     constexpr int kQRows = query_rows(FMT);
     extern __shared__ uint8_t smem_raw[];
     __shared__ int scan_tmp[NT / 32 + 1];
@@ -234,7 +261,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                                 continue;
                             if (lane == 0) {
                                 mbar_arrive_expect_tx(full + 8 * st, TB);
-                                load_tile<FMT>(smem + L.ring + st * TB, &map, p.kv, (page * 2) * p.Hkv + g, full + 8 * st);
+                                load_tile<stored_fmt(FMT)>(smem + L.ring + st * TB, &map, p.kv, (page * 2) * p.Hkv + g, full + 8 * st);
                             }
                             __syncwarp();
                             next_tile();
@@ -250,12 +277,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         // ---- MMA issuers: the whole warp, lane 0 issuing ----
         const int grp = warp - 1;
         const uint32_t one = lane == 0, tm = uniform(tmem + 256 * grp), base = uniform(smem), q = uniform(desc_low(base + L.q, 16));
-        const uint32_t idesc = umma_idesc_bf16(128, 0, 0, 0) & (CONV ? ~((1u << 7) | (1u << 10)) : ~0u);
+        const uint32_t idesc = umma_idesc_bf16(128, 0, 0, 0) & (FMT != kFmtBf16 ? ~((1u << 7) | (1u << 10)) : ~0u); // f16 or E4M3, or bf16
         uint32_t item = 0, qround = 0;
         for (; w.x < w.x1; w.next(p, heads)) {
             const int n = w.pages();
             for (int q0 = 0; q0 < rows; q0 += kQRows, ++qround) {
-                const int qpad = min(kQRows, (rows - q0 + 31) / 32 * 32);
+                const int qpad = padded(FMT, min(kQRows, rows - q0));
+                const int ncols = PAIR ? 2 * qpad : qpad;
                 const uint32_t half = uniform(qpad * 128 >> 4);
                 wait(q_full, qround & 1u);
                 for (int s0 = 0; s0 < n; s0 += sparse ? kPagesAtATime : n) {
@@ -268,18 +296,24 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             const int slot = CONV ? z % L.nstaged : st;
                             const uint32_t k = uniform(desc_low(base + (CONV ? L.staged + slot * kTile16 : L.ring + slot * TB), 16));
                             wait(CONV ? sfull + 8 * slot : full + 8 * st, CONV ? (uint32_t)(z / L.nstaged) & 1u : ph);
-                            for (int c = 0; c < qpad; c += 128, ++item) {
+                            for (int c = 0; c < ncols; c += 128, ++item) {
                                 const uint32_t d = tm + uniform(128 * (item & 1u)), b = q + uniform(c * 128 >> 4);
-                                const uint32_t id = uniform(idesc | (uint32_t)(min(128, qpad - c) >> 3) << 17);
+                                const uint32_t id = uniform(idesc | (uint32_t)(min(128, ncols - c) >> 3) << 17);
                                 if (item >= 2)
                                     wait(s_free + 16 * grp + 8 * (item & 1u), ((item >> 1) - 1) & 1u);
                                 tcgen05_after_sync();
+                                if (PAIR) { // 32 dimensions an MMA
 #pragma unroll
-                                for (uint32_t ks = 0; ks < 4; ++ks)
-                                    umma_ss(one, d, k + ks * 2, b + ks * 2, id, ks > 0);
+                                    for (uint32_t ks = 0; ks < 4; ++ks)
+                                        umma_ss8(one, d, k + ks * 2, b + ks * 2, id, ks > 0);
+                                } else {
 #pragma unroll
-                                for (uint32_t ks = 0; ks < 4; ++ks)
-                                    umma_ss(one, d, k + 1024 + ks * 2, b + half + ks * 2, id, 1u);
+                                    for (uint32_t ks = 0; ks < 4; ++ks)
+                                        umma_ss(one, d, k + ks * 2, b + ks * 2, id, ks > 0);
+#pragma unroll
+                                    for (uint32_t ks = 0; ks < 4; ++ks)
+                                        umma_ss(one, d, k + 1024 + ks * 2, b + half + ks * 2, id, 1u);
+                                }
                                 if (one)
                                     umma_commit(s_full + 16 * grp + 8 * (item & 1u));
                             }
@@ -310,7 +344,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const size_t first_row = (size_t)w.r * p.nq * p.Hkv * p.G + (size_t)g * p.G, pitch = (size_t)p.Hkv * p.G;
             const size_t wrow = ((size_t)w.r * p.Hkv + g) * p.maxB * kPage;
             for (int q0 = 0; q0 < rows; q0 += kQRows, ++qround) {
-                const int qpad = min(kQRows, (rows - q0 + 31) / 32 * 32);
+                const int qpad = padded(FMT, min(kQRows, rows - q0));
                 asm volatile("bar.sync 1, 256;" ::: "memory"); // the last rows' columns are done with
                 if (qround > 0)
                     wait(q_free, (qround - 1) & 1u);
@@ -321,7 +355,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     const size_t src = first_row + j * pitch + (at - j * p.G);
                     const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + src * kDim);
                     float inv = 1.f, up = 1.f;
-                    if (CONV) { // into f16's range by a power of two (see load_queries)
+                    if (FMT != kFmtBf16) { // into the operand's range by a power of two (see load_queries)
                         float mx = 0.f;
                         for (int c = 0; c < 16; ++c) {
                             const uint4 d = qrow[c];
@@ -334,11 +368,30 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                         e = e < -100 ? -100 : e > 127 ? 127 : e;
                         up = __uint_as_float((uint32_t)(8 - e + 127) << 23);
                         inv = __uint_as_float((uint32_t)(e - 8 + 127) << 23);
+                        if (PAIR && mx * up > 448.f) // E4M3's largest
+                            up *= 0.5f, inv *= 2.f;
                     }
-                    uint8_t *dst = gsm + L.q + i * 128;
+                    uint8_t *dst = gsm + L.q + i * (PAIR ? 256 : 128);
 #pragma unroll 4
                     for (int c = 0; c < 16; ++c) {
                         uint4 d = qrow[c];
+                        if (PAIR) { // columns 2 i (hi) and 2 i + 1 (lo), 8 bytes each
+                            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+                            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float x = __uint_as_float(e[k] << 16) * up, y = __uint_as_float(e[k] & 0xFFFF0000u) * up;
+                                const uint32_t h = to_e4m3x2(x, y);
+                                float hx, hy;
+                                f16x2_to_f32x2(e4m3x2_to_f16x2(h), hx, hy);
+                                hi[k >> 1] |= h << (16 * (k & 1));
+                                lo[k >> 1] |= to_e4m3x2(x - hx, y - hy) << (16 * (k & 1));
+                            }
+                            const int sw = (((c >> 1) ^ ((2 * i) & 7)) << 4) + (c & 1) * 8, sl = (((c >> 1) ^ ((2 * i + 1) & 7)) << 4) + (c & 1) * 8;
+                            *reinterpret_cast<uint2 *>(dst + sw) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2 *>(dst + 128 + sl) = make_uint2(lo[0], lo[1]);
+                            continue;
+                        }
                         if (CONV) {
                             uint32_t *e = &d.x;
 #pragma unroll
@@ -373,46 +426,57 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             old = src[wrow + at];
                         const bool part = sparse || (sb + i + 1) * kPage > w.seq_len;
                         uint64_t sum[2] = {0ull, 0ull};
-                        for (int c0 = 0; c0 < qpad; c0 += 128, ++item) {
-                            const int cn = min(128, qpad - c0);
-                            wait(s_full + 16 * grp + 8 * (item & 1u), (item >> 1) & 1u);
-                            tcgen05_after_sync();
-                            const uint32_t s_buf = s_at + 128 * (item & 1u);
-                            uint32_t v[32];
+                        const int ncols = PAIR ? 2 * qpad : qpad;
+                        // 32 accumulator columns: 32 query rows, or 16 as hi + lo
+                        auto add_rows = [&](auto partly, int col, const uint32_t *v) {
+                            constexpr int ROWS = PAIR ? 16 : 32;
+                            const int row0 = PAIR ? col >> 1 : col;
+                            const float4 *info = cols + (row0 >> 1);
+#pragma unroll
+                            for (int k = 0; k < ROWS / 2; ++k) {
+                                const float4 f = info[k];
+                                uint64_t x;
+                                if (PAIR)
+                                    x = add2(pair(__uint_as_float(v[(4 * k) & 31]), __uint_as_float(v[(4 * k + 2) & 31])),
+                                             pair(__uint_as_float(v[(4 * k + 1) & 31]), __uint_as_float(v[(4 * k + 3) & 31])));
+                                else
+                                    x = pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+                                float e0, e1;
+                                unpair(fma2(x, pair(f.x, f.y), pair(f.z, f.w)), e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                if (partly.value) { // a token counts where it looked at this block and sees the position
+                                    const int j0 = tok[row0 + 2 * k], j1 = tok[row0 + 2 * k + 1];
+                                    e0 = ((bits >> j0) & 1ull) && at < w.seq_len + j0 ? e0 : 0.f;
+                                    e1 = ((bits >> j1) & 1ull) && at < w.seq_len + j1 ? e1 : 0.f;
+                                }
+                                sum[k & 1] = add2(sum[k & 1], pair(e0, e1));
+                            }
+                        };
+                        auto add_page = [&](auto partly) {
+                            for (int c0 = 0; c0 < ncols; c0 += 128, ++item) {
+                                const int cn = min(128, ncols - c0);
+                                wait(s_full + 16 * grp + 8 * (item & 1u), (item >> 1) & 1u);
+                                tcgen05_after_sync();
+                                const uint32_t s_buf = s_at + 128 * (item & 1u);
+                                uint32_t v[32]; // (a second one, loaded meanwhile, measured no faster)
 #pragma unroll 1
-                            for (int c = 0; c < cn; c += 32) {
-                                tmem_ld32(s_buf + c, v);
-                                tmem_wait_ld(v);
-                                const float4 *info = cols + ((c0 + c) >> 1);
-                                if (!part) {
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        const float4 f = info[k];
-                                        float e0, e1;
-                                        unpair(fma2(pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), pair(f.x, f.y),
-                                                    pair(f.z, f.w)), e0, e1);
-                                        sum[k & 1] = add2(sum[k & 1], pair(ex2(e0), ex2(e1)));
-                                    }
-                                } else {
-                                    // a token counts where it looked at this block and sees the position
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        const float4 f = info[k];
-                                        const int j0 = tok[c0 + c + 2 * k], j1 = tok[c0 + c + 2 * k + 1];
-                                        const bool u0 = ((bits >> j0) & 1ull) && at < w.seq_len + j0;
-                                        const bool u1 = ((bits >> j1) & 1ull) && at < w.seq_len + j1;
-                                        const float e0 = ex2(fmaf(__uint_as_float(v[2 * k]), f.x, f.z));
-                                        const float e1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), f.y, f.w));
-                                        sum[k & 1] = add2(sum[k & 1], pair(u0 ? e0 : 0.f, u1 ? e1 : 0.f));
-                                    }
+                                for (int c = 0; c < cn; c += 32) {
+                                    tmem_ld32(s_buf + c, v);
+                                    tmem_wait_ld(v);
+                                    add_rows(partly, c0 + c, v);
                                     __syncwarp();
                                 }
+                                tcgen05_before_sync();
+                                __syncwarp();
+                                if (lane == 0)
+                                    mbar_arrive(s_free + 16 * grp + 8 * (item & 1u));
                             }
-                            tcgen05_before_sync();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(s_free + 16 * grp + 8 * (item & 1u));
-                        }
+                        };
+                        if (part)
+                            add_page(std::true_type{});
+                        else
+                            add_page(std::false_type{});
                         float a, b;
                         unpair(add2(sum[0], sum[1]), a, b);
                         if (at < cached)
@@ -486,7 +550,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 template <int FMT>
 cudaError_t launch_t(const WeightParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
 {
-    const int rows = p.nq * p.G, qpad = rows >= query_rows(FMT) ? query_rows(FMT) : (rows + 31) / 32 * 32;
+    const int rows = p.nq * p.G, qpad = padded(FMT, rows < query_rows(FMT) ? rows : query_rows(FMT));
     const Smem L = smem_layout(FMT, qpad, p.selected != nullptr);
     cudaError_t e = cudaFuncSetAttribute(weight_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
     if (e == cudaSuccess)
@@ -503,8 +567,8 @@ cudaError_t launch_weight_accumulate(const WeightParams &p, int kv_dtype, int ct
         return cudaErrorInvalidValue;
     if (kv_dtype == MSA_BF16)
         return launch_t<kFmtBf16>(p, map, ctas, stream);
-    if (kv_dtype == MSA_FP8_E4M3)
-        return launch_t<kFmtFp8>(p, map, ctas, stream);
+    if (kv_dtype == MSA_FP8_E4M3) // measured on 16 rows: 150 us with widened keys
+        return p.nq * p.G <= query_rows(kFmtPair) ? launch_t<kFmtPair>(p, map, ctas, stream) : launch_t<kFmtFp8>(p, map, ctas, stream);
     return launch_t<kFmtF4>(p, map, ctas, stream);
 }
 
