@@ -123,17 +123,23 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _buf(x):
-    """Device pointer of a whole-cache operator's buffer: a tensor must be dense and on the
-    current device (the library sees only an address), an int is taken as it is."""
-    if x is None or isinstance(x, int):
-        return x
-    if not x.is_cuda or not x.is_contiguous():
-        raise ValueError("buffers must be contiguous CUDA tensors")
-    import torch
-    if x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"buffer on {x.device}, but the current device is {torch.cuda.current_device()}")
-    return x.data_ptr()
+def _bufs(*xs):
+    """Device pointers of a whole-cache operator's buffers: tensors must be dense and on the
+    current device (the library sees only addresses), ints and None are taken as they are."""
+    device, out = None, []
+    for x in xs:
+        if x is None or isinstance(x, int):
+            out.append(x)
+            continue
+        if not x.is_cuda or not x.is_contiguous():
+            raise ValueError("buffers must be contiguous CUDA tensors")
+        if device is None:
+            import torch
+            device = torch.cuda.current_device()
+        if x.get_device() != device:
+            raise ValueError(f"buffer on {x.device}, but the current device is {device}")
+        out.append(x.data_ptr())
+    return out
 
 
 def _stream(stream):
@@ -232,29 +238,28 @@ def msa_cache_workspace_bytes(shape: MsaShape) -> int:
 def msa_dense_decode(shape, q, kv_pool, block_table, seq_lens, out, lse, workspace, workspace_bytes,
                      stream=None):
     """Attention over every cached position a token sees."""
-    _check(load().msa_dense_decode(ctypes.byref(shape), _buf(q), _buf(kv_pool), _buf(block_table),
-                                   _buf(seq_lens), _buf(out), _buf(lse), _buf(workspace),
-                                   int(workspace_bytes), _stream(stream)), "msa_dense_decode")
+    *bufs, ws = _bufs(q, kv_pool, block_table, seq_lens, out, lse, workspace)
+    _check(load().msa_dense_decode(ctypes.byref(shape), *bufs, ws, int(workspace_bytes),
+                                   _stream(stream)), "msa_dense_decode")
 
 
 def msa_weight_accumulate(shape, q, kv_pool, block_table, seq_lens, selected, lse, decay, weights_in,
                           weights_out, workspace, workspace_bytes, stream=None):
     """Add this step's attention weights to every cached position's sum (selected: None after a
     dense step, the block tables after a sparse one)."""
-    _check(load().msa_weight_accumulate(ctypes.byref(shape), _buf(q), _buf(kv_pool), _buf(block_table),
-                                        _buf(seq_lens), _buf(selected), _buf(lse), float(decay),
-                                        _buf(weights_in), _buf(weights_out), _buf(workspace),
+    *bufs, w_in, w_out, ws = _bufs(q, kv_pool, block_table, seq_lens, selected, lse, weights_in, weights_out,
+                                   workspace)
+    _check(load().msa_weight_accumulate(ctypes.byref(shape), *bufs, float(decay), w_in, w_out, ws,
                                         int(workspace_bytes), _stream(stream)), "msa_weight_accumulate")
 
 
 def msa_cache_evict(shape, keep, first, last, weights, block_table, seq_lens, new_table, kv_pool, idxk_pool,
                     idxk_scales, new_weights, kept, new_lens, workspace, workspace_bytes, stream=None):
     """Keep the heaviest positions of every request, copied in order to the pages of new_table."""
-    _check(load().msa_cache_evict(ctypes.byref(shape), int(keep), int(first), int(last), _buf(weights),
-                                  _buf(block_table), _buf(seq_lens), _buf(new_table), _buf(kv_pool),
-                                  _buf(idxk_pool), _buf(idxk_scales), _buf(new_weights), _buf(kept),
-                                  _buf(new_lens), _buf(workspace), int(workspace_bytes),
-                                  _stream(stream)), "msa_cache_evict")
+    bufs = _bufs(weights, block_table, seq_lens, new_table, kv_pool, idxk_pool, idxk_scales, new_weights,
+                 kept, new_lens, workspace)
+    _check(load().msa_cache_evict(ctypes.byref(shape), int(keep), int(first), int(last), *bufs,
+                                  int(workspace_bytes), _stream(stream)), "msa_cache_evict")
 
 
 def msa_check_device_status(workspace, stream=None) -> int:

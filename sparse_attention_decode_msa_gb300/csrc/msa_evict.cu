@@ -8,15 +8,17 @@
 // their weights (a maximum, not a sum: exact whatever the order of the heads,
 // as the block select's reduction is); with more, one list per KV head.
 //
-// Select: comparisons only, so bit-exact.  A cluster of 8 CTAs per list, each
-// with an eighth of the positions, whose order-preserving 32-bit keys stay in
-// shared memory (up to 40960 a CTA; longer slices read the weights again).
-// Three digits (11, 11, 10 bits) from the top give the keep-th largest key:
-// histograms are summed over the cluster through distributed shared memory.
-// Prefix counts in position order then give each kept position its place.
+// Select: comparisons only, so bit-exact.  One CTA per list where the table
+// holds at most 8192 positions, else a cluster of 8, each CTA with an eighth of the
+// positions, whose order-preserving 32-bit keys stay in shared memory (up to
+// 40960 a CTA; longer slices read the weights again).  Three digits (11, 11, 10
+// bits) from the top give the keep-th largest key: the CTAs read one another's
+// histograms through distributed shared memory, one cluster barrier a digit, and
+// from the same words how many kept positions the CTAs before them have.  Prefix
+// counts in position order then give each kept position its place.
 //
-// Copy: 64 kept positions per CTA; every row is 16-byte pieces, several loads
-// in flight per thread.  Rows go to pages of their own (new_table), so pages
+// Copy: 128 (short lists: 32) kept positions per CTA; every row is 16-byte pieces,
+// eight loads in flight per thread over K, V and index-key rows alike.  Rows go to pages of their own (new_table), so pages
 // that other requests share stay as they are and no copy waits for another.
 #include "msa_cache.cuh"
 
@@ -41,13 +43,13 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A 32-bit word of another CTA's shared memory.
-__device__ __forceinline__ int ld_peer(const void *p, int rank)
+// Four 32-bit words of another CTA's shared memory.
+__device__ __forceinline__ int4 ld_peer4(const void *p, int rank)
 {
     uint32_t a;
-    int v;
+    int4 v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
 
@@ -103,15 +105,16 @@ __device__ __forceinline__ uint32_t position_key(const EvictParams &p, const flo
     return k;
 }
 
+template <int CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, int held)
 {
-    extern __shared__ uint32_t keys[]; // [held]
-    __shared__ int hist[2][kBins];
+    extern __shared__ __align__(16) uint32_t keys[]; // [held]
+    __shared__ __align__(16) int hist[3][kBins];
     __shared__ uint32_t scan_tmp[kSelWarps + 1];
-    __shared__ int s_digit, s_need, s_counts[2];
+    __shared__ int s_digit, s_need, s_before, s_equal;
 
     launch_dependents();
-    const int list = blockIdx.x / kCluster, rank = (int)cluster_rank();
+    const int list = blockIdx.x / CLUSTER, rank = CLUSTER > 1 ? (int)cluster_rank() : 0;
     const int r = list / p.Hs, hs = list - r * p.Hs;
     const int heads = p.Hkv / p.Hs;
     int32_t *out = p.kept + (size_t)list * p.keep;
@@ -124,20 +127,67 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     if (hs == 0 && rank == 0 && threadIdx.x == 0)
         p.new_lens[r] = n == 0 ? 0 : min(n, p.keep) - p.nq + 1;
     if (n <= p.keep) { // everything stays (the whole cluster takes this branch)
-        for (int i = rank * kSelThreads + threadIdx.x; i < p.keep; i += kCluster * kSelThreads)
+        for (int i = rank * kSelThreads + threadIdx.x; i < p.keep; i += CLUSTER * kSelThreads)
             out[i] = i < n ? i : -1;
         return;
     }
 
-    const int slice = ((n + kCluster - 1) / kCluster + 3) & ~3;
+    const int slice = ((n + CLUSTER - 1) / CLUSTER + 3) & ~3;
     const int lo = min(n, rank * slice), hi = min(n, lo + slice), count = hi - lo;
     const size_t pitch = (size_t)p.maxB * kPage;
     const float *w = p.weights + ((size_t)r * p.Hkv + (size_t)hs * heads) * pitch;
     const bool cached = count <= held;
-    if (cached)
-        for (int i = threadIdx.x; i < count; i += kSelThreads)
-            keys[i] = position_key(p, w, heads, pitch, lo + i, n);
+    for (int i = threadIdx.x; i < 3 * kBins; i += kSelThreads)
+        (&hist[0][0])[i] = 0;
+    if (threadIdx.x == 0)
+        s_before = 0;
+    __syncthreads();
     auto key = [&](int i) { return cached ? keys[i] : position_key(p, w, heads, pitch, lo + i, n); };
+    // keys four at a time (rows are multiples of 128 long), the first digit counted as they come
+    auto four_keys = [&](int i, uint32_t (&k)[4]) {
+        k[0] = k[1] = k[2] = k[3] = 0u;
+        for (int h = 0; h < heads; ++h) {
+            const float4 v = *reinterpret_cast<const float4 *>(w + h * pitch + lo + i);
+            k[0] = max(k[0], weight_key(v.x));
+            k[1] = max(k[1], weight_key(v.y));
+            k[2] = max(k[2], weight_key(v.z));
+            k[3] = max(k[3], weight_key(v.w));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (lo + i + e < p.first || lo + i + e >= n - p.last)
+                k[e] = 0xFFFFFFFFu;
+    };
+    constexpr int U = 4; // loads in flight a thread
+    // equal leading digits are common (weights of one magnitude, zeros): three copies of
+    // the first histogram, by lane, keep a warp's increments from queueing on one word
+    int *first_hist = hist[(threadIdx.x & 31) % 3];
+    for (int i0 = 4 * (int)threadIdx.x; i0 < count; i0 += 4 * U * kSelThreads) {
+        uint32_t k[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + 4 * u * kSelThreads < count)
+                four_keys(i0 + 4 * u * kSelThreads, k[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + 4 * u * kSelThreads;
+            if (i >= count)
+                break;
+            if (cached)
+                *reinterpret_cast<uint4 *>(keys + i) = make_uint4(k[u][0], k[u][1], k[u][2], k[u][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < count)
+                    atomicAdd(&first_hist[k[u][e] >> 21], 1);
+        }
+    }
+    __syncthreads();
+    for (int i = 4 * (int)threadIdx.x; i < kBins; i += 4 * kSelThreads) {
+        const int4 a = *reinterpret_cast<int4 *>(&hist[0][i]), b = *reinterpret_cast<int4 *>(&hist[1][i]), c = *reinterpret_cast<int4 *>(&hist[2][i]);
+        *reinterpret_cast<int4 *>(&hist[0][i]) = make_int4(a.x + b.x + c.x, a.y + b.y + c.y, a.z + b.z + c.z, a.w + b.w + c.w);
+        *reinterpret_cast<int4 *>(&hist[1][i]) = *reinterpret_cast<int4 *>(&hist[2][i]) = make_int4(0, 0, 0, 0);
+    }
+    __syncthreads();
 
     // the keep-th largest key, digit by digit
     uint32_t prefix = 0u;
@@ -145,128 +195,114 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        int *h = hist[pass & 1];
-        for (int i = threadIdx.x; i < kBins; i += kSelThreads)
-            h[i] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < count; i += kSelThreads) {
-            const uint32_t k = key(i);
-            if (pass == 0 || (k >> (shift + bits)) == prefix)
-                atomicAdd(&h[(k >> shift) & ((1u << bits) - 1u)], 1);
+        int *h = hist[pass];
+        if (pass > 0) {
+            auto add = [&](uint32_t k) {
+                if ((k >> (shift + bits)) == prefix)
+                    atomicAdd(&h[(k >> shift) & ((1u << bits) - 1u)], 1);
+            };
+            const int whole = cached ? count & ~3 : 0;
+            for (int i = 4 * (int)threadIdx.x; i < whole; i += 4 * kSelThreads) {
+                const uint4 k = *reinterpret_cast<const uint4 *>(keys + i);
+                add(k.x);
+                add(k.y);
+                add(k.z);
+                add(k.w);
+            }
+            for (int i = whole + threadIdx.x; i < count; i += kSelThreads)
+                add(key(i));
         }
-        cluster_sync();
-        // bins from the top: thread t has the 4 bins kBins - 1 - 4 t and below
-        int c[4];
-        uint32_t sum = 0u;
+        if (CLUSTER > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        // bins from the top: thread t has the 4 bins ending at kBins - 1 - 4 t; of all CTAs
+        // and of those before this one
+        const int bin0 = kBins - 4 - 4 * (int)threadIdx.x;
+        int c[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            c[k] = 0;
-            for (int q = 0; q < kCluster; ++q)
-                c[k] += ld_peer(&h[kBins - 1 - 4 * (int)threadIdx.x - k], q);
-            sum += (uint32_t)c[k];
+        for (int q = 0; q < CLUSTER; ++q) {
+            const int4 v = CLUSTER > 1 ? ld_peer4(&h[bin0], q) : *reinterpret_cast<const int4 *>(&h[bin0]);
+            c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
+            if (q < rank)
+                before[0] += v.w, before[1] += v.z, before[2] += v.y, before[3] += v.x;
         }
         uint32_t total;
-        int above = (int)cta_scan(sum, scan_tmp, &total);
+        int above = (int)cta_scan((uint32_t)(c[0] + c[1] + c[2] + c[3]), scan_tmp, &total);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (above < need && need <= above + c[k]) { // one bin of one thread
-                s_digit = kBins - 1 - 4 * (int)threadIdx.x - k;
+                s_digit = bin0 + 3 - k;
                 s_need = need - above;
+                s_equal = before[k];
             }
             above += c[k];
         }
         __syncthreads();
+        // positions of the CTAs before this one that are kept by this digit
+        int kept = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            kept += bin0 + 3 - k > s_digit ? before[k] : 0;
+        kept = __reduce_add_sync(0xffffffffu, kept);
+        if ((threadIdx.x & 31) == 0 && kept)
+            atomicAdd(&s_before, kept);
         prefix = (prefix << bits) | (uint32_t)s_digit;
         need = s_need;
         __syncthreads();
     }
     const uint32_t theta = prefix; // kept: keys above theta, and the first `need` equal to it
+    const int gt_before = s_before, eq_before = s_equal;
+    if (CLUSTER > 1) // no CTA leaves while another reads its histograms
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
+    // every thread has a run of consecutive positions, an odd number of 16-byte words of
+    // keys (no bank conflicts): one scan over the CTA places all of them
+    const int run = ((((count + kSelThreads - 1) / kSelThreads + 3) >> 2) | 1) << 2;
+    const int begin = min(count, run * (int)threadIdx.x), end = min(count, begin + run);
     int gt = 0, eq = 0;
-    for (int i = threadIdx.x; i < count; i += kSelThreads) {
-        const uint32_t k = key(i);
-        gt += k > theta;
-        eq += k == theta;
-    }
-    uint32_t total_gt, total_eq;
-    cta_scan((uint32_t)gt, scan_tmp, &total_gt);
-    cta_scan((uint32_t)eq, scan_tmp, &total_eq);
-    if (threadIdx.x == 0) {
-        s_counts[0] = (int)total_gt;
-        s_counts[1] = (int)total_eq;
-    }
-    cluster_sync();
-    int gt_before = 0, eq_before = 0;
-    for (int q = 0; q < rank; ++q) {
-        gt_before += ld_peer(&s_counts[0], q);
-        eq_before += ld_peer(&s_counts[1], q);
-    }
-    cluster_sync(); // no CTA leaves while another reads its counts
-
-    for (int i0 = 0; i0 < count; i0 += kSelThreads * 4) {
-        const int i = i0 + 4 * (int)threadIdx.x;
-        uint32_t k[4];
-        uint32_t mine = 0u; // at most 2048 of each kind: two 16-bit counts
+    for (int i = begin; i < end; i += 4) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            k[e] = i + e < count ? key(i + e) : 0u;
-            const bool in = i + e < count;
-            mine += (in && k[e] > theta ? 1u : 0u) + (in && k[e] == theta ? 0x10000u : 0u);
+            const bool in = i + e < end;
+            const uint32_t k = in ? key(i + e) : 0u;
+            gt += in && k > theta;
+            eq += in && k == theta;
         }
-        uint32_t total;
-        const uint32_t before = cta_scan(mine, scan_tmp, &total);
-        int g = gt_before + (int)(before & 0xFFFFu), q = eq_before + (int)(before >> 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (i + e >= count)
-                break;
-            const bool is_gt = k[e] > theta, is_eq = k[e] == theta;
-            if (is_gt || (is_eq && q < need))
-                out[g + min(q, need)] = lo + i + e;
-            g += is_gt;
-            q += is_eq;
-        }
-        gt_before += (int)(total & 0xFFFFu);
-        eq_before += (int)(total >> 16);
     }
+    uint32_t total;
+    int g = gt_before + (int)cta_scan((uint32_t)gt, scan_tmp, &total);
+    int q = eq_before + (int)cta_scan((uint32_t)eq, scan_tmp, &total);
+    if (gt || (eq && q < need))
+        for (int i = begin; i < end; ++i) {
+            const uint32_t k = key(i);
+            if (k > theta || (k == theta && q < need))
+                out[g + min(q, need)] = lo + i;
+            g += k > theta;
+            q += k == theta;
+        }
+    if (CLUSTER > 1)
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyRows = 64; // kept positions of a CTA
 
-// Copies `kinds` rows of PIECES pieces of type T for each of the CTA's `count`
-// positions: piece i of kind k from src row to dst row, at `base(k, page) + row * pitch`.
-template <typename T, typename F>
-__device__ __forceinline__ void copy_rows(int kinds, int pieces, int count, const int2 *from, const int2 *to, F &&at)
+__device__ __forceinline__ int log2_of(int v) // of a power of two
 {
-    const int total = kinds * kCopyRows * pieces;
-    constexpr int U = 8; // loads in flight
-    for (int i0 = threadIdx.x; i0 < total; i0 += U * kCopyThreads) {
-        T v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kCopyThreads, e = (i / pieces) % kCopyRows;
-            if (i < total && e < count && from[e].x >= 0 && to[e].x >= 0)
-                v[u] = *reinterpret_cast<const T *>(at(i / (pieces * kCopyRows), from[e], i % pieces));
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kCopyThreads, e = (i / pieces) % kCopyRows;
-            if (i < total && e < count && from[e].x >= 0 && to[e].x >= 0)
-                *reinterpret_cast<T *>(at(i / (pieces * kCopyRows), to[e], i % pieces)) = v[u];
-        }
-    }
+    return 31 - __clz(v);
 }
 
+// ROWS kept positions of one list.
+template <int ROWS>
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictParams p)
 {
-    __shared__ int2 from[kCopyRows], to[kCopyRows]; // page, row of the page; page -1: not copied
-    __shared__ int pos[kCopyRows];
+    __shared__ int2 from[ROWS], to[ROWS]; // page, row of the page; page -1: not copied
+    __shared__ int pos[ROWS];
     const int list = blockIdx.x, r = list / p.Hs, hs = list - r * p.Hs;
-    const int heads = p.Hkv / p.Hs, index_heads = p.Hi / p.Hs;
-    const int i0 = blockIdx.y * kCopyRows;
+    const int heads = p.Hkv / p.Hs, index_heads = p.idxk ? p.Hi / p.Hs : 0;
+    const int i0 = blockIdx.y * ROWS;
     grid_dependency_wait();
-    if (threadIdx.x < kCopyRows) {
+    if (threadIdx.x < ROWS) {
         const int i = i0 + threadIdx.x;
         int2 f = make_int2(-1, 0), t = make_int2(-1, 0);
         int at = -1;
@@ -285,73 +321,105 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
         pos[threadIdx.x] = at;
     }
     __syncthreads();
-    const int count = min(kCopyRows, p.keep - i0);
     if (pos[0] < 0)
         return; // the lists are filled from the front
 
-    // K rows of the list's KV heads, then V rows
-    const int fmt = p.kv_fmt;
+    // rows in 16-byte pieces: K of the list's KV heads, V of them, then their index keys.
+    // NVFP4 rows are 64 bytes of codes here and 8 of scales below.
+    const bool f4 = p.kv_fmt == kFmtF4;
+    const int kv_row = f4 ? 64 : p.kv_fmt == kFmtFp8 ? 128 : 256, idx_row = p.idx_f4 ? 64 : 256;
+    const int kv_shift = log2_of(kv_row >> 4), idx_shift = log2_of(idx_row >> 4), kv_page = f4 ? 9216 : kPage * kv_row;
     auto tile = [&](int k, int page) { // kind k: K of head k, then V
         const int v = k >= heads, g = hs * heads + (v ? k - heads : k);
         return ((size_t)page * 2 + v) * p.Hkv + g;
     };
-    if (fmt == kFmtF4) {
-        copy_rows<uint4>(2 * heads, 4, count, from, to, [&](int k, int2 a, int i) {
-            return p.kv + tile(k, a.x) * 9216 + a.y * 64 + i * 16;
-        });
-        copy_rows<uint2>(2 * heads, 1, count, from, to, [&](int k, int2 a, int) {
-            return p.kv + tile(k, a.x) * 9216 + 8192 + a.y * 8;
-        });
-    } else {
-        const int row_bytes = fmt == kFmtBf16 ? 256 : 128;
-        copy_rows<uint4>(2 * heads, row_bytes / 16, count, from, to, [&](int k, int2 a, int i) {
-            return p.kv + (tile(k, a.x) * kPage + a.y) * row_bytes + i * 16;
-        });
+    const int kv_pieces = 2 * heads * ROWS << kv_shift, pieces = kv_pieces + (index_heads * ROWS << idx_shift);
+    auto row_of = [&](int i) { return (i < kv_pieces ? i >> kv_shift : (i - kv_pieces) >> idx_shift) & (ROWS - 1); };
+    auto piece_at = [&](int i, int2 a) -> uint4 * {
+        if (i < kv_pieces)
+            return reinterpret_cast<uint4 *>(p.kv + tile(i >> kv_shift >> log2_of(ROWS), a.x) * kv_page + a.y * kv_row) + (i & ((1 << kv_shift) - 1));
+        i -= kv_pieces;
+        const size_t h = (size_t)a.x * p.Hi + hs * index_heads + (i >> idx_shift >> log2_of(ROWS));
+        return reinterpret_cast<uint4 *>(p.idxk + (h * kPage + a.y) * idx_row) + (i & ((1 << idx_shift) - 1));
+    };
+    constexpr int U = 8; // loads in flight
+    for (int j0 = threadIdx.x; j0 < pieces; j0 += U * kCopyThreads) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = j0 + u * kCopyThreads;
+            if (i < pieces && from[row_of(i)].x >= 0)
+                v[u] = *piece_at(i, from[row_of(i)]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = j0 + u * kCopyThreads;
+            if (i < pieces && from[row_of(i)].x >= 0)
+                *piece_at(i, to[row_of(i)]) = v[u];
+        }
     }
-    if (p.idxk) {
-        auto row = [&](int k, int2 a) { return ((size_t)a.x * p.Hi + hs * index_heads + k) * kPage + a.y; };
-        const int row_bytes = p.idx_f4 ? 64 : 256;
-        copy_rows<uint4>(index_heads, row_bytes / 16, count, from, to, [&](int k, int2 a, int i) {
-            return p.idxk + row(k, a) * row_bytes + i * 16;
-        });
-        if (p.idx_f4)
-            copy_rows<uint2>(index_heads, 1, count, from, to, [&](int k, int2 a, int) { return p.idxk_scales + row(k, a) * 8; });
-    }
+    if (f4) // 8 scales a row
+        for (int i = threadIdx.x; i < 2 * heads * ROWS; i += kCopyThreads) {
+            const int2 a = from[i % ROWS], b = to[i % ROWS];
+            if (a.x >= 0)
+                *reinterpret_cast<uint2 *>(p.kv + tile(i / ROWS, b.x) * 9216 + 8192 + b.y * 8) =
+                    *reinterpret_cast<const uint2 *>(p.kv + tile(i / ROWS, a.x) * 9216 + 8192 + a.y * 8);
+        }
+    if (p.idx_f4)
+        for (int i = threadIdx.x; i < index_heads * ROWS; i += kCopyThreads) {
+            const int2 a = from[i % ROWS], b = to[i % ROWS];
+            const int h = hs * index_heads + i / ROWS;
+            if (a.x >= 0)
+                *reinterpret_cast<uint2 *>(p.idxk_scales + (((size_t)b.x * p.Hi + h) * kPage + b.y) * 8) =
+                    *reinterpret_cast<const uint2 *>(p.idxk_scales + (((size_t)a.x * p.Hi + h) * kPage + a.y) * 8);
+        }
     if (p.new_weights)
-        for (int i = threadIdx.x; i < heads * kCopyRows; i += kCopyThreads) {
-            const int e = i % kCopyRows, g = hs * heads + i / kCopyRows;
-            if (e < count && pos[e] >= 0)
+        for (int i = threadIdx.x; i < heads * ROWS; i += kCopyThreads) {
+            const int e = i % ROWS, g = hs * heads + i / ROWS;
+            if (pos[e] >= 0)
                 p.new_weights[((size_t)r * p.Hkv + g) * p.newB * kPage + i0 + e] =
                     p.weights[((size_t)r * p.Hkv + g) * p.maxB * kPage + pos[e]];
         }
+}
+
+template <int CLUSTER>
+cudaError_t launch_select_t(const EvictParams &p, cudaStream_t stream)
+{
+    const int lists = p.R * p.Hs;
+    // keys of a slice of the longest row the table can hold, as far as they are held
+    const long long slice = ((long long)p.maxB * kPage + CLUSTER - 1) / CLUSTER + 4;
+    const int held = slice < kKeysHeld ? (int)slice : kKeysHeld;
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CLUSTER;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(lists * CLUSTER);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (size_t)held * 4;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<CLUSTER>, p, held);
 }
 
 } // namespace
 
 cudaError_t launch_cache_evict(const EvictParams &p, cudaStream_t stream)
 {
-    const int lists = p.R * p.Hs;
-    // keys of a slice of the longest row the table can hold, as far as they are held
-    const long long slice = ((long long)p.maxB * kPage + kCluster - 1) / kCluster + 3;
-    const int held = slice < kKeysHeld ? (int)slice : kKeysHeld;
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
+    cudaError_t e = p.maxB * kPage <= 8192 ? launch_select_t<1>(p, stream) : launch_select_t<kCluster>(p, stream);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(lists * kCluster);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)held * 4;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, held);
-    if (e == cudaSuccess)
-        e = launch_kernel(evict_copy_kernel, dim3(lists, (p.keep + kCopyRows - 1) / kCopyRows), dim3(kCopyThreads), 0, stream, true, p);
+    // short lists in more, smaller CTAs
+    const int lists = p.R * p.Hs;
+    if ((long long)lists * ((p.keep + 127) / 128) >= 304)
+        e = launch_kernel(evict_copy_kernel<128>, dim3(lists, (p.keep + 127) / 128), dim3(kCopyThreads), 0, stream, true, p);
+    else
+        e = launch_kernel(evict_copy_kernel<32>, dim3(lists, (p.keep + 31) / 32), dim3(kCopyThreads), 0, stream, true, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
