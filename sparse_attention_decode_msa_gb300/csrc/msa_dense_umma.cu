@@ -26,7 +26,7 @@
 // 128 (s & 1) + 64 t), O of stream t at 256 + 128 t.
 // Warps: 0 TMA producer (and outputs of idle slots), 1 issues S (and owns the TMEM),
 // 2 and 3 issue P V of stream 0 and 1, 4-7 and 8-11 softmax of stream 0 and 1,
-// 12-15 converters (E4M3, NVFP4).
+// 12-15 and 16-19 converters (E4M3, NVFP4).
 //
 // What bounds it: the tensor cores when rows are many (measured: an MMA of
 // 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50 as both read 4 KiB
@@ -38,7 +38,7 @@ namespace msa {
 namespace {
 
 constexpr int kTile16 = 32768;   // a 16-bit K, V or Q tile
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 8;     // two groups of four, taking the tiles in turn
 constexpr int kStaged = 4;       // widened tiles in flight
 constexpr float kSlack = 8.f;    // how far (log2) a row's maximum may pass its reference before O is rescaled
 constexpr float kPUp16 = 7.f;    // f16 P: 2^7 2^(s - m), at most 2^15 with the slack
@@ -48,10 +48,11 @@ __host__ __device__ constexpr int threads_of(int fmt)
     return fmt == kFmtBf16 ? 384 : 384 + 32 * kConvWarps;
 }
 
-// Tiles (K or V) in the ring.
+// Tiles (K or V) in the ring: an even number where converters widen them (a slot
+// belongs to one converter group, which follows all of its barriers' phases).
 __host__ __device__ constexpr int ring_tiles(int fmt, bool two)
 {
-    return fmt == kFmtBf16 ? (two ? 5 : 6) : fmt == kFmtFp8 ? (two ? 2 : 4) : (two ? 3 : 7);
+    return fmt == kFmtBf16 ? (two ? 5 : 6) : fmt == kFmtFp8 ? (two ? 2 : 4) : (two ? 2 : 6);
 }
 
 struct Smem {
@@ -174,10 +175,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         prefetch_tensormap(&map);
         for (int i = 0; i < TILES; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, CONV ? kConvWarps : 2);
+            mbar_init(empty + 8 * i, CONV ? 4 : 2);
         }
         for (int i = 0; i < kStaged; ++i) {
-            mbar_init(sfull + 8 * i, kConvWarps);
+            mbar_init(sfull + 8 * i, 4);
             mbar_init(sempty + 8 * i, 2);
         }
         for (int t = 0; t < 2; ++t) {
@@ -474,25 +475,33 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const uint32_t at_s = lanes + (TWO ? 128 * t + 64 * (i & 1) : 128 * (i & 1) + 64 * t);
                 wait(s_full + (TWO ? 16 * t : 0) + 8 * (i & 1), (i & 1 ? fills1++ : fills0++) & 1u);
                 tcgen05_after_sync();
-                uint32_t v[64];
-                tmem_ld32(at_s, v);
-                tmem_ld32(at_s + 32, v + 32);
-                tmem_wait_ld(v);
-                tmem_wait_ld(v + 32);
-                // the extreme logit of the row (the scale's sign says which end)
+                // the extreme logit of the row (the scale's sign says which end).  bf16: the
+                // 64 columns stay in registers; the widening instances have fewer registers
+                // a thread and keep columns 0 .. 31, the others are read again
+                constexpr int HELD = CONV ? 32 : 64;
+                uint32_t v[HELD];
                 const bool neg = sc < 0.f;
                 float mx = neg ? -ninf : ninf;
-                if (tail || neg) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (k < seen)
-                            mx = neg ? fminf(mx, __uint_as_float(v[k])) : fmaxf(mx, __uint_as_float(v[k]));
-                } else {
-                    float m4[4] = {ninf, ninf, ninf, ninf};
+                for (int c = 64 - HELD; c >= 0; c -= HELD) {
 #pragma unroll
-                    for (int k = 0; k < 64; k += 2)
-                        m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    for (int h = 0; h < HELD; h += 32)
+                        tmem_ld32(at_s + c + h, v + h);
+#pragma unroll
+                    for (int h = 0; h < HELD; h += 32)
+                        tmem_wait_ld(v + h);
+                    if (tail || neg) {
+#pragma unroll
+                        for (int k = 0; k < HELD; ++k)
+                            if (c + k < seen)
+                                mx = neg ? fminf(mx, __uint_as_float(v[k])) : fmaxf(mx, __uint_as_float(v[k]));
+                    } else {
+                        float m4[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+                        for (int k = 0; k < HELD; k += 2)
+                            m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                    }
                 }
                 mx *= sc;
                 if (CONV)
@@ -537,12 +546,17 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) { // 32 columns of S become P
+                    if (CONV && c == 1) {
+                        tmem_ld32(at_s + 32, v);
+                        tmem_wait_ld(v);
+                    }
+                    const uint32_t *x = v + (CONV ? 0 : 32 * c);
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const int at = 32 * c + 2 * k;
                         float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), sc2, ref2), e0, e1);
+                        unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, ref2), e0, e1);
                         e0 = ex2(e0);
                         e1 = ex2(e1);
                         if (tail) {
@@ -676,7 +690,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
     } else if (CONV && warp >= 12) {
         // ---- converters: a ring tile to a 16-bit tile, in the order of use ----
-        const int row = (warp - 12) * 32 + lane;
+        const int grp = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
         int z = 0;
         for (; w.x < w.x1; w.next(p, heads)) {
             const int n = w.pages(), cached = w.seq_len + p.nq - 1;
@@ -684,6 +698,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (int i = 0; i < 2 * n; ++i, ++z) {
                 const bool is_k = kp < n && order_of_k<TWO>(kp) == i;
                 const int page0 = (w.b + (is_k ? kp++ : vp++)) * kPage;
+                if ((z & 1) != grp)
+                    continue;
                 const bool tail = !is_k && page0 + kPage > w.seq_len;
                 const bool drop = tail && page0 + row >= cached;              // not cached
                 const bool check = tail && !drop && page0 + row >= w.seq_len; // seen by later tokens only
