@@ -21,10 +21,12 @@
 //
 // What bounds it: the bytes of K and of the weights with few rows, the
 // exponentials with many.  Two groups (an MMA issuer, four softmax warps and,
-// where keys are widened, four converter warps each) take
-// the pages in turn, so that one page's waits pass behind the other's work; the
-// query rows of a (request, KV head), up to 512 (bf16) or 256 at a time, stay in
-// shared memory.
+// where keys are widened, four converter warps each) share the work, so that one's
+// waits pass behind the other's work: up to 128 accumulator columns, each takes every
+// second page; with more, both work on every page (few K tiles fit beside that many
+// query rows), group g on columns 128 g .. of every 256, and group 1 hands its sums
+// to group 0.  The query rows of a (request, KV head), up to 512 (bf16) or 256 at a
+// time, stay in shared memory.
 //
 // After a sparse step only pages that some token of the request selected are
 // read; a bitmap of 64 token bits per page, built in shared memory, says which
@@ -77,14 +79,14 @@ __host__ __device__ constexpr int padded(int fmt, int rows)
 // of K tiles.  Ring and staged tiles are even in number: a slot belongs to one
 // group, which follows all of its barriers' phases.
 struct Smem {
-    int ring, staged, q, cols, tok, mask, bars, misc, total;
+    int ring, staged, q, cols, tok, mask, sums, bars, misc, total;
     int depth, nstaged;
 };
 
 __host__ __device__ inline Smem smem_layout(int fmt, int qpad, bool masks)
 {
     Smem s{};
-    const int rest = qpad * (256 + 8 + 1) + (masks ? 2 * kPagesAtATime * 8 : 0) + (2 * kMaxRing + 32) * 8 + 64 + 1024 + 256;
+    const int rest = qpad * (256 + 8 + 1) + (masks ? 2 * kPagesAtATime * 8 : 0) + 1024 + (2 * kMaxRing + 32) * 8 + 64 + 1024 + 256;
     int room = 232448 - rest;
     s.nstaged = !widened(fmt) ? 0 : room >= 6 * kTile16 ? 4 : 2;
     room -= s.nstaged * kTile16;
@@ -96,7 +98,8 @@ __host__ __device__ inline Smem smem_layout(int fmt, int qpad, bool masks)
     s.cols = s.ring + s.depth * tile_bytes(stored_fmt(fmt));
     s.tok = s.cols + qpad * 8;
     s.mask = (s.tok + qpad + 15) / 16 * 16;
-    s.bars = s.mask + (masks ? 2 * kPagesAtATime * 8 : 0);
+    s.sums = s.mask + (masks ? 2 * kPagesAtATime * 8 : 0);
+    s.bars = s.sums + 2 * 128 * 4; // group 1's sums of a page, twice
     s.misc = s.bars + (2 * kMaxRing + 32) * 8;
     s.total = s.misc + 64 + 1024;
     return s;
@@ -124,17 +127,18 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = p.nq * p.G, heads = p.Hkv;
     const bool sparse = p.selected != nullptr;
+    const bool share = (PAIR ? 2 : 1) * padded(FMT, min(kQRows, rows)) > 128; // both groups on every page
     const long long wl = p.wait_limit;
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map);
         for (int i = 0; i < L.depth; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, CONV ? 4 : 1);
+            mbar_init(empty + 8 * i, CONV ? 4 : share ? 2 : 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + 8 * i, 4);
-            mbar_init(sempty + 8 * i, 1);
+            mbar_init(sempty + 8 * i, share ? 2 : 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(s_free + 8 * i, 4);
         }
@@ -292,11 +296,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     for (int i = 0; i < sn; ++i) {
                         if (bits_of(i) == 0ull)
                             continue;
-                        if ((z & 1) == grp) {
+                        if (share || (z & 1) == grp) {
                             const int slot = CONV ? z % L.nstaged : st;
                             const uint32_t k = uniform(desc_low(base + (CONV ? L.staged + slot * kTile16 : L.ring + slot * TB), 16));
                             wait(CONV ? sfull + 8 * slot : full + 8 * st, CONV ? (uint32_t)(z / L.nstaged) & 1u : ph);
-                            for (int c = 0; c < ncols; c += 128, ++item) {
+                            for (int c = share ? 128 * grp : 0; c < ncols; c += share ? 256 : 128, ++item) {
                                 const uint32_t d = tm + uniform(128 * (item & 1u)), b = q + uniform(c * 128 >> 4);
                                 const uint32_t id = uniform(idesc | (uint32_t)(min(128, ncols - c) >> 3) << 17);
                                 if (item >= 2)
@@ -414,17 +418,42 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 for (int s0 = 0; s0 < n; s0 += sparse ? kPagesAtATime : n) {
                     const int sn = sparse ? min(kPagesAtATime, n - s0) : n, sb = w.b + s0;
                     run_begins();
+                    // pages that no token looked at: their weights fade (four loads in flight)
+                    for (int i0 = warp - 4; sparse && q0 == 0 && i0 < sn; i0 += 32) {
+                        float4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = i0 + 8 * k;
+                            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (src && i < sn && bits_of(i) == 0ull)
+                                v[k] = *reinterpret_cast<const float4 *>(src + wrow + (size_t)(sb + i) * kPage + 4 * lane);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = i0 + 8 * k, at = (sb + i) * kPage + 4 * lane;
+                            if (i >= sn || bits_of(i) != 0ull)
+                                continue;
+                            const float e[4] = {v[k].x * p.decay, v[k].y * p.decay, v[k].z * p.decay, v[k].w * p.decay};
+                            if (at + 4 <= w.seq_len - 1) {
+                                *reinterpret_cast<float4 *>(p.weights_out + wrow + at) = make_float4(e[0], e[1], e[2], e[3]);
+                            } else {
+                                for (int c = 0; c < 4; ++c)
+                                    if (at + c < cached)
+                                        p.weights_out[wrow + at + c] = at + c < w.seq_len - 1 ? e[c] : 0.f;
+                            }
+                        }
+                    }
                     for (int i = 0; i < sn; ++i) {
                         const unsigned long long bits = bits_of(i);
                         if (bits == 0ull)
                             continue;
-                        if ((z++ & 1) != grp)
+                        if (z++, !share && ((z - 1) & 1) != grp)
                             continue;
                         const int at = (sb + i) * kPage + mine;
                         float old = 0.f;
-                        if (q0 > 0 ? at < cached : src && at < w.seq_len - 1)
+                        if ((!share || grp == 0) && (q0 > 0 ? at < cached : src && at < w.seq_len - 1))
                             old = src[wrow + at];
-                        const bool part = sparse || (sb + i + 1) * kPage > w.seq_len;
+                        const bool whole_page = (sb + i + 1) * kPage <= w.seq_len, part = sparse || !whole_page;
                         uint64_t sum[2] = {0ull, 0ull};
                         const int ncols = PAIR ? 2 * qpad : qpad;
                         // 32 accumulator columns: 32 query rows, or 16 as hi + lo
@@ -454,7 +483,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             }
                         };
                         auto add_page = [&](auto partly) {
-                            for (int c0 = 0; c0 < ncols; c0 += 128, ++item) {
+                            for (int c0 = share ? 128 * grp : 0; c0 < ncols; c0 += share ? 256 : 128, ++item) {
                                 const int cn = min(128, ncols - c0);
                                 wait(s_full + 16 * grp + 8 * (item & 1u), (item >> 1) & 1u);
                                 tcgen05_after_sync();
@@ -462,9 +491,21 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                                 uint32_t v[32]; // (a second one, loaded meanwhile, measured no faster)
 #pragma unroll 1
                                 for (int c = 0; c < cn; c += 32) {
+                                    bool all = false;
+                                    if (partly.value) { // the tokens of these columns: none or all of them?
+                                        const int r0 = PAIR ? (c0 + c) >> 1 : c0 + c, r1 = r0 + (PAIR ? 15 : 31);
+                                        const int j0 = tok[r0], j1 = tok[r1];
+                                        const unsigned long long those = (~0ull >> (63 - (j1 - j0))) << j0;
+                                        if ((bits & those) == 0ull)
+                                            continue;
+                                        all = (bits & those) == those && whole_page;
+                                    }
                                     tmem_ld32(s_buf + c, v);
                                     tmem_wait_ld(v);
-                                    add_rows(partly, c0 + c, v);
+                                    if (partly.value && !all)
+                                        add_rows(std::true_type{}, c0 + c, v);
+                                    else
+                                        add_rows(std::false_type{}, c0 + c, v);
                                     __syncwarp();
                                 }
                                 tcgen05_before_sync();
@@ -479,29 +520,18 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             add_page(std::false_type{});
                         float a, b;
                         unpair(add2(sum[0], sum[1]), a, b);
+                        if (share) { // (the next barrier comes before this buffer is written again)
+                            float *sums = reinterpret_cast<float *>(gsm + L.sums) + (z & 1) * 128 + mine;
+                            if (grp == 1)
+                                *sums = a + b;
+                            asm volatile("bar.sync 2, 256;" ::: "memory");
+                            if (grp == 1)
+                                continue;
+                            a += b;
+                            b = *sums;
+                        }
                         if (at < cached)
                             p.weights_out[wrow + at] = (q0 > 0 ? old : old * p.decay) + (a + b);
-                    }
-                    if (sparse && q0 == 0) { // pages that no token looked at: their weights fade
-                        const int w8 = warp - 4;
-                        for (int i = w8; i < sn; i += 8) {
-                            if (bits_of(i) != 0ull)
-                                continue;
-                            const size_t o = wrow + (size_t)(sb + i) * kPage + 4 * lane;
-                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (src)
-                                v = *reinterpret_cast<const float4 *>(src + o);
-                            const int at = (sb + i) * kPage + 4 * lane;
-                            v.x *= p.decay, v.y *= p.decay, v.z *= p.decay, v.w *= p.decay;
-                            if (at + 4 <= w.seq_len - 1) {
-                                *reinterpret_cast<float4 *>(p.weights_out + o) = v;
-                            } else {
-                                const float e[4] = {v.x, v.y, v.z, v.w};
-                                for (int k = 0; k < 4; ++k)
-                                    if (at + k < cached)
-                                        p.weights_out[o + k] = at + k < w.seq_len - 1 ? e[k] : 0.f;
-                            }
-                        }
                     }
                     run_ends();
                 }
