@@ -56,7 +56,7 @@ __host__ __device__ constexpr int ring_tiles(int fmt, bool two)
 }
 
 struct Smem {
-    int ring, staged, q, ml, bars, misc, total;
+    int ring, staged, q, ml, inv, bars, misc, total;
 };
 
 __host__ __device__ constexpr Smem smem_layout(int fmt, bool two)
@@ -66,7 +66,8 @@ __host__ __device__ constexpr Smem smem_layout(int fmt, bool two)
     s.staged = ring_tiles(fmt, two) * tile_bytes(fmt);
     s.q = s.staged + (fmt == kFmtBf16 ? 0 : kStaged * kTile16);
     s.ml = s.q + (two ? 2 : 1) * kTile16; // m[128], l[128] of stream 1 (one row tile)
-    s.bars = s.ml + (two ? 0 : 2 * 128 * 4);
+    s.inv = s.ml + (two ? 0 : 2 * 128 * 4); // factors that undo the scaling of query rows
+    s.bars = s.inv + (fmt == kFmtBf16 ? 0 : (two ? 2 : 1) * 128 * 4);
     s.misc = s.bars + (2 * ring_tiles(fmt, two) + 2 * kStaged + 21) * 8;
     s.total = s.misc + 64 + 1024;
     return s;
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             mbar_init(sempty + 8 * i, 2);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(q_full + 8 * t, 4);
+            mbar_init(q_full + 8 * t, TWO ? 4 : 8);
             mbar_init(s_full + 16 * t, 1);
             mbar_init(s_full + 16 * t + 8, 1);
             mbar_init(p_full + 16 * t, 4);
@@ -424,48 +425,53 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         auto product_wait = [&](int k, int i) { // P V of step i (the last of its buffer) of stream k
             wait(pv_done + 16 * k + 8 * (i & 1), ((i & 1 ? fills1 : fills0) - 1) & 1u);
         };
-        for (; w.x < w.x1; w.next(p, heads)) {
+        auto or_of_stream = [&](uint32_t &any) { // over the stream's 128 threads
+            asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n"
+                         " selp.u32 %0, 1, 0, q;\n}\n"
+                         : "+r"(any)
+                         : "r"(3 + t)
+                         : "memory");
+        };
+        float *qinv = reinterpret_cast<float *>(gsm + L.inv) + (TWO ? 128 * t : 0);
+        auto sync_stream = [&] { // the warps that share a query tile
+            if (TWO)
+                asm volatile("bar.sync %0, 128;" ::"r"(3 + t) : "memory");
+            else
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+        };
+        // Query rows of unit u into the operand tile, once the last S of the unit before is
+        // done: before that unit's outputs are written, so that S goes on meanwhile.  Rows
+        // beyond the unit's are left as they are: nothing is read from what they give.
+        auto stage_queries = [&](const Walk &u) {
+            const int g = u.u / p.tiles, base = (u.u - g * p.tiles) * ROWS + (TWO ? 128 * t : 0);
+            const size_t first = (size_t)u.r * p.nq * p.Hkv * p.G + (size_t)g * p.G, pitch = (size_t)p.Hkv * p.G;
+            sync_stream();
+            if (u.seg > 0)
+                wait(q_free, (u.seg - 1) & 1);
+            stage_rows<CONV ? kRowsF16 : kRows16>(
+                gsm + L.q + (TWO ? t * kTile16 : 0), 16384, min(128, p.rows - base), TWO ? warp & 3 : warp - 4, TWO ? 4 : 8,
+                [&](int i) {
+                    const int j = (base + i) / p.G;
+                    return p.q + (first + j * pitch + (base + i - j * p.G)) * kDim;
+                },
+                [&](int i, float x) { qinv[i] = x; });
+            fence_async_smem();
+            if (CONV)
+                sync_stream();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_full + (TWO ? 8 * t : 0));
+        };
+        if (w.x < w.x1)
+            stage_queries(w);
+        Walk nx = w;
+        for (; w.x < w.x1; w = nx) {
             const int n = w.pages(), nsteps = TWO ? 2 * n : n;
             const int g = w.u / p.tiles, base = (w.u - g * p.tiles) * ROWS + (TWO ? 128 * t : 0);
             const int i_row = base + mine, i_read = min(i_row, p.rows - 1), j = i_read / p.G;
+            const bool idle = base + (warp & 3) * 32 >= p.rows; // no row of this warp's is the unit's
             const size_t out_row = (size_t)w.r * p.nq * p.Hkv * p.G + (size_t)j * p.Hkv * p.G + (size_t)g * p.G + (i_read - j * p.G);
-            const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + out_row * kDim);
-            float inv = 1.f, up = 1.f;
-            if (CONV) { // scale the row into f16's range by a power of two (see load_queries)
-                float mx = 0.f;
-                for (int i = 0; i < 16; ++i) {
-                    const uint4 d = qrow[i];
-                    const uint32_t e[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(e[c] << 16)), fabsf(__uint_as_float(e[c] & 0xFFFF0000u))));
-                }
-                int e = (int)(__float_as_uint(mx) >> 23) - 127;
-                e = e < -100 ? -100 : e > 127 ? 127 : e;
-                up = __uint_as_float((uint32_t)(8 - e + 127) << 23);
-                inv = __uint_as_float((uint32_t)(e - 8 + 127) << 23);
-            }
-            if (TWO || t == 0) {
-                if (w.seg > 0)
-                    wait(q_free, (w.seg - 1) & 1);
-                uint8_t *dst = gsm + L.q + (TWO ? t * kTile16 : 0) + mine * 128;
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    uint4 d = qrow[i];
-                    if (CONV) {
-                        uint32_t *e = &d.x;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            e[c] = pack_f16(__uint_as_float(e[c] << 16) * up, __uint_as_float(e[c] & 0xFFFF0000u) * up);
-                    }
-                    *reinterpret_cast<uint4 *>(dst + (i >> 3) * 16384 + (((i & 7) ^ (mine & 7)) << 4)) = d;
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(q_full + 8 * t);
-            }
-            const float sc = p.scale_log2 * inv;
+            const float sc = p.scale_log2 * (CONV && i_row < p.rows ? qinv[mine] : 1.f);
             const int lim = w.seq_len + j;
             float m = ninf, l = 0.f; // reference maximum and denominator
             for (int i = 0; i < nsteps; ++i) {
@@ -474,6 +480,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const int seen = tail ? lim - pos0 : 64; // columns this row sees
                 const uint32_t at_s = lanes + (TWO ? 128 * t + 64 * (i & 1) : 128 * (i & 1) + 64 * t);
                 wait(s_full + (TWO ? 16 * t : 0) + 8 * (i & 1), (i & 1 ? fills1++ : fills0++) & 1u);
+                if (idle) {
+                    if (lane == 0)
+                        mbar_arrive(p_full + 16 * t + 8 * (i & 1));
+                    if (!CONV) {
+                        uint32_t none = 0u;
+                        or_of_stream(none);
+                    }
+                    continue;
+                }
                 tcgen05_after_sync();
                 // the extreme logit of the row (the scale's sign says which end).  bf16: the
                 // 64 columns stay in registers; the widening instances have fewer registers
@@ -531,12 +546,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 // row's denominator so far (see the top)
                 bool lo_too = false;
                 if (!CONV) {
-                    uint32_t any = m != ninf && !(ex2(mx - m) * 64.f < l);
-                    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n"
-                                 " selp.u32 %0, 1, 0, q;\n}\n"
-                                 : "=r"(any)
-                                 : "r"(any), "r"(3 + t)
-                                 : "memory");
+                    uint32_t any = i_row < p.rows && m != ninf && !(ex2(mx - m) * 64.f < l);
+                    or_of_stream(any);
                     lo_too = any != 0u;
                     if (mine == 0)
                         with_lo[t][i & 1] = lo_too;
@@ -593,6 +604,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
 
             // ---- end of the unit's share ----
+            nx.next(p, heads);
+            if (nx.x < nx.x1)
+                stage_queries(nx);
             float M = m, Lsum = l, fa = 1.f, fb = 0.f;
             if (!TWO) {
                 if (t == 1) {

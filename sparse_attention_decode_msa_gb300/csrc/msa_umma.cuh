@@ -133,6 +133,80 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b)
     return out;
 }
 
+// Query rows 0 .. n - 1 (bf16, `row(i)` in global memory) into an operand tile in
+// shared memory, K-major with the 128-byte swizzle, by warp `wi` of `nw`: half a
+// warp takes a row, 16 bytes a lane, so that loads are whole lines and several rows
+// are in flight.
+//   kRows16   bf16 as they are (half of the dimensions `half` bytes after the other)
+//   kRowsF16  f16: each row scaled by a power of two that brings its largest element to
+//             [2^8, 2^9) (exact; elements 2^-23 below it lose bits)
+//   kRowsPair E4M3 pairs hi, lo in rows 2 i, 2 i + 1, after a power of two that brings the
+//             row's largest element near 448
+// inverse(i, x) is told the factor that undoes the scaling (one lane of the row).
+constexpr int kRows16 = 0, kRowsF16 = 1, kRowsPair = 2;
+
+template <int MODE, typename Row, typename Inverse>
+__device__ __forceinline__ void stage_rows(uint8_t *dst, int half, int n, int wi, int nw, Row &&row, Inverse &&inverse)
+{
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 31, c = lane & 15;
+    for (int i0 = 2 * wi; i0 < n; i0 += 2 * U * nw) {
+        uint4 d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + 2 * u * nw + (lane >> 4);
+            d[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < n)
+                d[u] = reinterpret_cast<const uint4 *>(row(i))[c];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + 2 * u * nw + (lane >> 4);
+            uint32_t *e = &d[u].x;
+            if (MODE != kRows16) {
+                float mx = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                // the exponent clamped so that neither factor overflows
+                int x = (int)(__float_as_uint(mx) >> 23) - 127;
+                x = x < -100 ? -100 : x > 127 ? 127 : x;
+                float up = __uint_as_float((uint32_t)(8 - x + 127) << 23), inv = __uint_as_float((uint32_t)(x - 8 + 127) << 23);
+                if (MODE == kRowsPair && mx * up > 448.f) // E4M3's largest
+                    up *= 0.5f, inv *= 2.f;
+                if (c == 0 && i < n)
+                    inverse(i, inv);
+                if (MODE == kRowsPair) {
+                    uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float a = __uint_as_float(e[k] << 16) * up, b = __uint_as_float(e[k] & 0xFFFF0000u) * up;
+                        const uint32_t h = to_e4m3x2(a, b);
+                        float ha, hb;
+                        f16x2_to_f32x2(e4m3x2_to_f16x2(h), ha, hb);
+                        hi[k >> 1] |= h << (16 * (k & 1));
+                        lo[k >> 1] |= to_e4m3x2(a - ha, b - hb) << (16 * (k & 1));
+                    }
+                    if (i < n) {
+                        uint8_t *at = dst + 256 * i + (c & 1) * 8;
+                        *reinterpret_cast<uint2 *>(at + (((c >> 1) ^ ((2 * i) & 7)) << 4)) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2 *>(at + 128 + (((c >> 1) ^ ((2 * i + 1) & 7)) << 4)) = make_uint2(lo[0], lo[1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        e[k] = pack_f16(__uint_as_float(e[k] << 16) * up, __uint_as_float(e[k] & 0xFFFF0000u) * up);
+                }
+            }
+            if (MODE != kRowsPair && i < n)
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * half + 128 * i + (((c & 7) ^ (i & 7)) << 4)) = d[u];
+        }
+    }
+}
+
 // One row of an E4M3 or NVFP4 tile as the TMA lands it, widened to f16 in the
 // layout of a 16-bit tile (two halves of 64 dimensions, 128-byte swizzle).
 template <int FMT>

@@ -352,64 +352,23 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 asm volatile("bar.sync 1, 256;" ::: "memory"); // the last rows' columns are done with
                 if (qround > 0)
                     wait(q_free, (qround - 1) & 1u);
-                for (int i = me; i < qpad; i += 256) {
-                    // padding columns repeat the last row (zeros would turn an infinite key into
-                    // NaN) and count nothing, as do tokens that attended to nothing (lse = -inf)
+                // padding columns repeat the last row (zeros would turn an infinite key into NaN)
+                // and count nothing, as do tokens that attended to nothing (lse = -inf)
+                auto source = [&](int i) {
                     const int at = min(q0 + i, rows - 1), j = at / p.G;
-                    const size_t src = first_row + j * pitch + (at - j * p.G);
-                    const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + src * kDim);
-                    float inv = 1.f, up = 1.f;
-                    if (FMT != kFmtBf16) { // into the operand's range by a power of two (see load_queries)
-                        float mx = 0.f;
-                        for (int c = 0; c < 16; ++c) {
-                            const uint4 d = qrow[c];
-                            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
-                        }
-                        int e = (int)(__float_as_uint(mx) >> 23) - 127;
-                        e = e < -100 ? -100 : e > 127 ? 127 : e;
-                        up = __uint_as_float((uint32_t)(8 - e + 127) << 23);
-                        inv = __uint_as_float((uint32_t)(e - 8 + 127) << 23);
-                        if (PAIR && mx * up > 448.f) // E4M3's largest
-                            up *= 0.5f, inv *= 2.f;
-                    }
-                    uint8_t *dst = gsm + L.q + i * (PAIR ? 256 : 128);
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        uint4 d = qrow[c];
-                        if (PAIR) { // columns 2 i (hi) and 2 i + 1 (lo), 8 bytes each
-                            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
-                            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float x = __uint_as_float(e[k] << 16) * up, y = __uint_as_float(e[k] & 0xFFFF0000u) * up;
-                                const uint32_t h = to_e4m3x2(x, y);
-                                float hx, hy;
-                                f16x2_to_f32x2(e4m3x2_to_f16x2(h), hx, hy);
-                                hi[k >> 1] |= h << (16 * (k & 1));
-                                lo[k >> 1] |= to_e4m3x2(x - hx, y - hy) << (16 * (k & 1));
-                            }
-                            const int sw = (((c >> 1) ^ ((2 * i) & 7)) << 4) + (c & 1) * 8, sl = (((c >> 1) ^ ((2 * i + 1) & 7)) << 4) + (c & 1) * 8;
-                            *reinterpret_cast<uint2 *>(dst + sw) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2 *>(dst + 128 + sl) = make_uint2(lo[0], lo[1]);
-                            continue;
-                        }
-                        if (CONV) {
-                            uint32_t *e = &d.x;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e[k] = pack_f16(__uint_as_float(e[k] << 16) * up, __uint_as_float(e[k] & 0xFFFF0000u) * up);
-                        }
-                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * qpad * 128 + (((c & 7) ^ (i & 7)) << 4)) = d;
-                    }
-                    const float e = q0 + i < rows ? p.lse[src] : inf;
+                    return first_row + j * pitch + (at - j * p.G);
+                };
+                for (int i = me; i < qpad; i += 256) {
+                    const float e = q0 + i < rows ? p.lse[source(i)] : inf;
                     float *info = reinterpret_cast<float *>(cols + (i >> 1)) + (i & 1);
-                    info[0] = p.scale_log2 * inv;
+                    if (FMT == kFmtBf16)
+                        info[0] = p.scale_log2;
                     info[2] = e == -inf ? -inf : e * -1.4426950408889634f;
-                    tok[i] = (uint8_t)j;
+                    tok[i] = (uint8_t)(min(q0 + i, rows - 1) / p.G);
                 }
+                stage_rows<FMT == kFmtBf16 ? kRows16 : PAIR ? kRowsPair : kRowsF16>(
+                    gsm + L.q, qpad * 128, qpad, warp - 4, 8, [&](int i) { return p.q + source(i) * kDim; },
+                    [&](int i, float inv) { reinterpret_cast<float *>(cols + (i >> 1))[i & 1] = p.scale_log2 * inv; });
                 fence_async_smem();
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (lane == 0)
