@@ -123,23 +123,31 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _bufs(*xs):
-    """Device pointers of a whole-cache operator's buffers: tensors must be dense and on the
-    current device (the library sees only addresses), ints and None are taken as they are."""
+def _bufs(stream, *xs):
+    """The stream handle and the device pointers of a whole-cache operator's buffers: tensors must
+    be dense and on the current device (the library sees only addresses), ints and None are taken
+    as they are.  A step of a small cache takes about 10 us on the GPU, so this path counts: the
+    current stream is read without building a Stream object (3 us)."""
+    import torch
+
     device, out = None, []
     for x in xs:
         if x is None or isinstance(x, int):
             out.append(x)
             continue
-        if not x.is_cuda or not x.is_contiguous():
-            raise ValueError("buffers must be contiguous CUDA tensors")
-        if device is None:
-            import torch
-            device = torch.cuda.current_device()
-        if x.get_device() != device:
-            raise ValueError(f"buffer on {x.device}, but the current device is {device}")
+        d = x.get_device()
+        if d != device:
+            if device is None and d >= 0:
+                device = torch.cuda.current_device()
+            if d != device:
+                raise ValueError(f"buffer on {x.device}: not on the current CUDA device")
+        if not x.is_contiguous():
+            raise ValueError("buffers must be contiguous")
         out.append(x.data_ptr())
-    return out
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and device is not None and raw is not None:
+        return raw(device), out
+    return _stream(stream), out
 
 
 def _stream(stream):
@@ -238,28 +246,28 @@ def msa_cache_workspace_bytes(shape: MsaShape) -> int:
 def msa_dense_decode(shape, q, kv_pool, block_table, seq_lens, out, lse, workspace, workspace_bytes,
                      stream=None):
     """Attention over every cached position a token sees."""
-    *bufs, ws = _bufs(q, kv_pool, block_table, seq_lens, out, lse, workspace)
-    _check(load().msa_dense_decode(ctypes.byref(shape), *bufs, ws, int(workspace_bytes),
-                                   _stream(stream)), "msa_dense_decode")
+    st, bufs = _bufs(stream, q, kv_pool, block_table, seq_lens, out, lse, workspace)
+    _check(load().msa_dense_decode(ctypes.byref(shape), *bufs, int(workspace_bytes), st),
+           "msa_dense_decode")
 
 
 def msa_weight_accumulate(shape, q, kv_pool, block_table, seq_lens, selected, lse, decay, weights_in,
                           weights_out, workspace, workspace_bytes, stream=None):
     """Add this step's attention weights to every cached position's sum (selected: None after a
     dense step, the block tables after a sparse one)."""
-    *bufs, w_in, w_out, ws = _bufs(q, kv_pool, block_table, seq_lens, selected, lse, weights_in, weights_out,
-                                   workspace)
+    st, (*bufs, w_in, w_out, ws) = _bufs(stream, q, kv_pool, block_table, seq_lens, selected, lse,
+                                         weights_in, weights_out, workspace)
     _check(load().msa_weight_accumulate(ctypes.byref(shape), *bufs, float(decay), w_in, w_out, ws,
-                                        int(workspace_bytes), _stream(stream)), "msa_weight_accumulate")
+                                        int(workspace_bytes), st), "msa_weight_accumulate")
 
 
 def msa_cache_evict(shape, keep, first, last, weights, block_table, seq_lens, new_table, kv_pool, idxk_pool,
                     idxk_scales, new_weights, kept, new_lens, workspace, workspace_bytes, stream=None):
     """Keep the heaviest positions of every request, copied in order to the pages of new_table."""
-    bufs = _bufs(weights, block_table, seq_lens, new_table, kv_pool, idxk_pool, idxk_scales, new_weights,
-                 kept, new_lens, workspace)
+    st, bufs = _bufs(stream, weights, block_table, seq_lens, new_table, kv_pool, idxk_pool, idxk_scales,
+                     new_weights, kept, new_lens, workspace)
     _check(load().msa_cache_evict(ctypes.byref(shape), int(keep), int(first), int(last), *bufs,
-                                  int(workspace_bytes), _stream(stream)), "msa_cache_evict")
+                                  int(workspace_bytes), st), "msa_cache_evict")
 
 
 def msa_check_device_status(workspace, stream=None) -> int:

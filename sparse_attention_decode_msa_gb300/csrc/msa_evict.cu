@@ -403,7 +403,7 @@ cudaError_t launch_select_t(const EvictParams &p, cudaStream_t stream)
     cfg.dynamicSmemBytes = (size_t)held * 4;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CLUSTER > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<CLUSTER>, p, held);
 }
 
