@@ -12,7 +12,13 @@
 // ends.  With more than 128 query rows a (request, KV head), stream t has rows
 // 128 t .. of a 256-row tile and takes both halves of every page; with fewer,
 // both have the same rows, stream t takes half t of every page, and the two
-// (m, l, O) are added at the end.
+// (m, l, O) are added at the end.  With E4M3 and NVFP4
+// tiles up to 64 rows are in the operand tile twice, rows 0 .. for stream 0 and 64 ..
+// for stream 1: a softmax warp can read one quarter of the accumulator lanes only,
+// and so the streams' warps with rows in them sit on different schedulers (32
+// requests of 2 tokens over 65536 NVFP4 positions: 487 us, 559 without; bf16, whose
+// schedulers have no converters beside them, lost to the longer end of a unit:
+// 79 us for 70 on 8 requests of 4 tokens).
 //
 // Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA
 // lands them (K-major), P in tensor memory over the S it came from, V tiles as
@@ -432,12 +438,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                          : "r"(3 + t)
                          : "memory");
         };
+        const bool twice = CONV && !TWO && p.rows <= 64;
+        const int lane0 = twice ? 64 * t : 0; // the stream's first accumulator lane
         float *qinv = reinterpret_cast<float *>(gsm + L.inv) + (TWO ? 128 * t : 0);
+        auto sync_all = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         auto sync_stream = [&] { // the warps that share a query tile
             if (TWO)
                 asm volatile("bar.sync %0, 128;" ::"r"(3 + t) : "memory");
             else
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                sync_all();
         };
         // Query rows of unit u into the operand tile, once the last S of the unit before is
         // done: before that unit's outputs are written, so that S goes on meanwhile.  Rows
@@ -445,12 +454,14 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         auto stage_queries = [&](const Walk &u) {
             const int g = u.u / p.tiles, base = (u.u - g * p.tiles) * ROWS + (TWO ? 128 * t : 0);
             const size_t first = (size_t)u.r * p.nq * p.Hkv * p.G + (size_t)g * p.G, pitch = (size_t)p.Hkv * p.G;
+            const int rows = min(128, p.rows - base);
             sync_stream();
             if (u.seg > 0)
                 wait(q_free, (u.seg - 1) & 1);
             stage_rows<CONV ? kRowsF16 : kRows16>(
-                gsm + L.q + (TWO ? t * kTile16 : 0), 16384, min(128, p.rows - base), TWO ? warp & 3 : warp - 4, TWO ? 4 : 8,
+                gsm + L.q + (TWO ? t * kTile16 : 0), 16384, twice ? 64 + rows : rows, TWO ? warp & 3 : warp - 4, TWO ? 4 : 8,
                 [&](int i) {
+                    i = twice ? min(i & 63, rows - 1) : i;
                     const int j = (base + i) / p.G;
                     return p.q + (first + j * pitch + (base + i - j * p.G)) * kDim;
                 },
@@ -468,10 +479,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         for (; w.x < w.x1; w = nx) {
             const int n = w.pages(), nsteps = TWO ? 2 * n : n;
             const int g = w.u / p.tiles, base = (w.u - g * p.tiles) * ROWS + (TWO ? 128 * t : 0);
-            const int i_row = base + mine, i_read = min(i_row, p.rows - 1), j = i_read / p.G;
-            const bool idle = base + (warp & 3) * 32 >= p.rows; // no row of this warp's is the unit's
+            const int i_row = base + mine - lane0, i_read = min(max(i_row, 0), p.rows - 1), j = i_read / p.G;
+            const bool real = i_row == i_read;
+            const int first = (warp & 3) * 32 - lane0;
+            const bool idle = first < 0 || base + first >= p.rows; // no row of this warp's is the unit's
             const size_t out_row = (size_t)w.r * p.nq * p.Hkv * p.G + (size_t)j * p.Hkv * p.G + (size_t)g * p.G + (i_read - j * p.G);
-            const float sc = p.scale_log2 * (CONV && i_row < p.rows ? qinv[mine] : 1.f);
+            const float sc = p.scale_log2 * (CONV && real ? qinv[mine] : 1.f);
             const int lim = w.seq_len + j;
             float m = ninf, l = 0.f; // reference maximum and denominator
             for (int i = 0; i < nsteps; ++i) {
@@ -546,10 +559,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 // row's denominator so far (see the top)
                 bool lo_too = false;
                 if (!CONV) {
-                    uint32_t any = i_row < p.rows && m != ninf && !(ex2(mx - m) * 64.f < l);
+                    uint32_t any = real && m != ninf && !(ex2(mx - m) * 64.f < l);
                     or_of_stream(any);
                     lo_too = any != 0u;
-                    if (mine == 0)
+                    if (mine == lane0)
                         with_lo[t][i & 1] = lo_too;
                 }
                 const float ref = m == ninf ? 0.f : m;
@@ -607,15 +620,52 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             nx.next(p, heads);
             if (nx.x < nx.x1)
                 stage_queries(nx);
+            const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
+            float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * (ROWS * (kDim + 2));
             float M = m, Lsum = l, fa = 1.f, fb = 0.f;
-            if (!TWO) {
+            // stream 1's O where rows are there twice: 16-byte piece k of row i at 64 k + i, in the place
+            // of rows 64 .. of the partial slot, which no output uses
+            float4 *other = reinterpret_cast<float4 *>(slot + (size_t)64 * kDim) + (mine & 63);
+            if (twice) {
+                if (t == 1) {
+                    if (w.seg > 0) // stream 0 has read the last unit's
+                        asm volatile("bar.sync 2, 256;" ::: "memory");
+                    product_wait(1, nsteps - 1);
+                    tcgen05_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < 8 && !idle; ++c) {
+                        float a[16];
+                        tmem_ld16(o_at + 16 * c, a);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            other[64 * (4 * c + k)] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+                    }
+                    if (real) {
+                        slot[(size_t)ROWS * kDim + mine] = m;
+                        slot[(size_t)ROWS * (kDim + 1) + mine] = l;
+                    }
+                    tcgen05_before_sync();
+                    sync_all();
+                    if (lane == 0)
+                        mbar_arrive(o_free + 8);
+                    continue;
+                }
+                sync_all();
+                if (real) {
+                    const float mb = __ldcg(slot + (size_t)ROWS * kDim + 64 + mine), lb = __ldcg(slot + (size_t)ROWS * (kDim + 1) + 64 + mine);
+                    M = fmaxf(m, mb);
+                    fa = m == ninf ? 0.f : ex2(m - M);
+                    fb = mb == ninf ? 0.f : ex2(mb - M);
+                    Lsum = l * fa + lb * fb;
+                }
+            } else if (!TWO) {
                 if (t == 1) {
                     ml[mine] = m;
                     ml[128 + mine] = l;
                 }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                sync_all();
                 const float mb = ml[mine], lb = ml[128 + mine];
-                asm volatile("bar.sync 2, 256;" ::: "memory");
+                sync_all();
                 if (t == 1)
                     continue; // stream 0 reads both accumulators (of as many steps)
                 M = fmaxf(m, mb);
@@ -624,21 +674,34 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 Lsum = l * fa + lb * fb;
             }
             product_wait(t, nsteps - 1);
-            if (!TWO)
+            if (!TWO && !twice)
                 product_wait(1, nsteps - 1);
             tcgen05_after_sync();
-            const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
-            float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * (ROWS * (kDim + 2));
             const int slot_row = (TWO ? 128 * t : 0) + mine;
             const float fin = Lsum > 0.f || Lsum != Lsum ? p.v_scale / Lsum : 0.f;
             const bool bad = later_bad[w.seg & 7] == w.seg + 1;
+            float4 ahead[4]; // stream 1's next 16 columns
+            if (twice)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    ahead[k] = __ldcg(other + 64 * k);
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
                 float a[16], b2[16];
                 __syncwarp();
                 tmem_ld16(o_at + 16 * c, a);
                 if (!TWO) {
-                    tmem_ld16(o_at + 128 + 16 * c, b2);
+                    if (twice) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 x = ahead[k];
+                            b2[4 * k] = x.x, b2[4 * k + 1] = x.y, b2[4 * k + 2] = x.z, b2[4 * k + 3] = x.w;
+                            if (c < 7)
+                                ahead[k] = __ldcg(other + 64 * (4 * (c + 1) + k));
+                        }
+                    } else {
+                        tmem_ld16(o_at + 128 + 16 * c, b2);
+                    }
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                         a[k] = a[k] * fa + b2[k] * fb;
@@ -668,7 +731,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                         }
                     }
                 }
-                if (i_row < p.rows) {
+                if (real) {
                     if (whole) {
                         uint4 d[2];
                         uint32_t *e = &d[0].x;
@@ -690,10 +753,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(o_free + 8 * t);
-                if (!TWO)
+                if (!TWO && !twice)
                     mbar_arrive(o_free + 8);
             }
-            if (i_row < p.rows) {
+            if (twice && nx.x < nx.x1)
+                asm volatile("bar.arrive 2, 256;" ::: "memory");
+            if (real) {
                 if (whole) {
                     p.lse[out_row] = Lsum == 0.f ? ninf : (M + log2f(Lsum)) * 0.6931471805599453f;
                 } else {
