@@ -169,15 +169,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
     }
 }
 
-template <int FMT>
-__device__ __forceinline__ void mma_fmt(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    if (FMT == kFmtBf16)
-        mma_bf16(d, a, b0, b1);
-    else
-        mma_f16(d, a, b0, b1);
-}
-
 __device__ __forceinline__ uint64_t lds64(uint32_t a)
 {
     uint64_t v;

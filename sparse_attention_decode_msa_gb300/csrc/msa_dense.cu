@@ -7,12 +7,16 @@
 // in one pass over the pages: a running maximum m (log2 units), the
 // denominator l = sum 2^(s - m) and O = sum 2^(s - m) V, all fp32, rescaled
 // when m rises.  The nq * G query rows of a (request, KV head) share every
-// page that is read.
+// page that is read.  This file has the kernel for up to 16 rows (one token of 16
+// heads, two of 8, ...), the join of cut units and the launch; more rows go to
+// the tcgen05 kernel of msa_dense_umma.cu.
 //
-// What bounds it: with few rows the bytes of the pages (16 heads: 16 flop a
-// byte of bf16 K/V), so the kernel is a ring of whole pages fed by TMA, with
-// as much in flight as shared memory holds (192 KiB an SM), and the tensor
-// work hides behind the copies.
+// What bounds it: the bytes of the pages (16 heads: 16 flop a byte of bf16 K/V),
+// so the kernel is a ring of whole pages fed by TMA, with as much in flight as
+// shared memory holds (192 KiB an SM), and mma.sync (m16n8k16: 16 rows are one
+// tile, no accumulator leaves the registers), whose work hides behind the copies:
+// 5.65 TB/s over 1.1 GB of E4M3 pages (48 requests, 196 us), 4.9 TB/s over 165 MB of
+// bf16 pages (8 heads, 34 us with the join).
 //
 // Work split: the pages of all (request, KV head, row tile) units in one line,
 // cut into equal ranges, one per persistent CTA.  A unit inside one range is
@@ -21,10 +25,9 @@
 // kernel launched as a programmatic dependent.  No atomics, nothing kept
 // between calls.
 //
-// Inside a CTA: one producer warp and eight consumer warps, MT groups of 16
-// query rows x 8 / MT groups of positions.  Each consumer warp keeps m, l and
-// O of its rows over its own share of every page, so warps meet only at the
-// end of a unit.
+// Inside a CTA: one producer warp and eight consumer warps with 16 positions of every
+// page each.  A consumer warp keeps m, l and O of the 16 rows over its own share of
+// the pages, so warps meet only at the end of a unit.
 #include "msa_cache.cuh"
 
 namespace msa {
@@ -210,14 +213,12 @@ __device__ __forceinline__ void store_bf16x2(uint16_t *row, int d, float a, floa
     *reinterpret_cast<uint32_t *>(row + d) = pack_bf16(a, b);
 }
 
-template <int FMT, int MT>
+template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_stream_kernel(const __grid_constant__ CUtensorMap map, const DenseParams p)
 {
     constexpr int STAGES = ring_stages(FMT), TB = tile_bytes(FMT);
-    constexpr int PG = kConsumers / MT;          // position groups
-    constexpr int CH = MT == 1 ? 1 : 2;          // 16-position chunks per softmax step
-    constexpr int ROWS = 16 * MT;
+    constexpr int ROWS = 16;
     constexpr int TG = FMT == kFmtBf16 ? 1 : FMT == kFmtFp8 ? 2 : 4; // n-tiles that interleave their dimensions
     extern __shared__ uint8_t smem_raw[];
     __shared__ int scan_tmp[kThreads / 32 + 1];
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *gsm = smem_raw + (smem - smem_u32(smem_raw));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gsm + L.misc);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int heads = p.Hkv * p.tiles; // units of a request
+    const int heads = p.Hkv; // units of a request
 
     launch_dependents();
     if (threadIdx.x == 0) {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = x0; x < x1 && !stop;) {
             const int n = min(nb - b, x1 - x);
             const int32_t *row = p.block_table + (size_t)r * p.maxB;
-            const int g = u / p.tiles;
+            const int g = u;
             for (int i = 0; i < n && !stop; i += 32) { // 32 table entries at a time, one per lane
                 const int mine = i + lane < n ? row[b + i + lane] : 0;
                 for (int k = 0; k < min(32, n - i); ++k) {
@@ -364,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ---- consumers ----
-    const int mt = warp % MT, pg = warp / MT;
     const int n8 = lane >> 2, c4 = lane & 3;
     float *sm_m = reinterpret_cast<float *>(gsm + L.ml), *sm_l = sm_m + 128;
     float *join = reinterpret_cast<float *>(gsm + L.join);
@@ -372,10 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 0;
     for (int x = x0; x < x1;) {
         const int n = min(nb - b, x1 - x);
-        const int g = u / p.tiles, row_base = (u - g * p.tiles) * ROWS;
+        const int g = u;
         const size_t first_row = (size_t)r * p.nq * p.Hkv * p.G + (size_t)g * p.G; // of token 0
         // query row i of the unit: token i / G, head i % G
-        const int i0 = row_base + mt * 16 + n8, i1 = i0 + 8;
+        const int i0 = n8, i1 = i0 + 8;
         const int j0 = min(i0, p.rows - 1) / p.G, j1 = min(i1, p.rows - 1) / p.G;
         const size_t pitch = (size_t)p.Hkv * p.G;
         uint32_t q[8][4];
@@ -402,113 +402,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t kt = smem + st * 2 * TB, vt = kt + TB;
             const int page0 = (b + i) * kPage;
             const bool tail = page0 + kPage > seq_len; // some row does not see all of the page
-#pragma unroll 1
-            for (int step = 0; step < MT / CH; ++step) {
-                const int pos = pg * (16 * MT) + step * (16 * CH);
-                float s[CH][2][4];
+            const int at = 16 * warp; // this warp's positions of the page
+            float s[2][4];
+            score16<FMT>(s, q, kt, at);
+            float a0 = ninf, a1 = ninf;
 #pragma unroll
-                for (int k = 0; k < CH; ++k)
-                    score16<FMT>(s[k], q, kt, pos + 16 * k);
-                float a0 = ninf, a1 = ninf;
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int k = 0; k < CH; ++k)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v = s[k][t][e] * (e < 2 ? sc0 : sc1);
-                            if (tail && page0 + pos + 16 * k + 8 * t + 2 * c4 + (e & 1) >= (e < 2 ? lim0 : lim1))
-                                v = ninf;
-                            s[k][t][e] = v;
-                            if (e < 2)
-                                a0 = fmaxf(a0, v);
-                            else
-                                a1 = fmaxf(a1, v);
-                        }
-                a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
-                a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-                a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
-                a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-                if (FMT != kFmtBf16) {
-                    a0 -= kPUp;
-                    a1 -= kPUp;
+                for (int e = 0; e < 4; ++e) {
+                    float v = s[t][e] * (e < 2 ? sc0 : sc1);
+                    if (tail && page0 + at + 8 * t + 2 * c4 + (e & 1) >= (e < 2 ? lim0 : lim1))
+                        v = ninf;
+                    s[t][e] = v;
+                    if (e < 2)
+                        a0 = fmaxf(a0, v);
+                    else
+                        a1 = fmaxf(a1, v);
                 }
-                if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
-                    const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
-                    const float f0 = n0 == ninf ? 1.f : ex2(m0 - n0), f1 = n1 == ninf ? 1.f : ex2(m1 - n1);
-                    m0 = n0;
-                    m1 = n1;
-                    l0 *= f0;
-                    l1 *= f1;
+            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
+            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
+            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+            if (FMT != kFmtBf16) {
+                a0 -= kPUp;
+                a1 -= kPUp;
+            }
+            if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
+                const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+                const float f0 = n0 == ninf ? 1.f : ex2(m0 - n0), f1 = n1 == ninf ? 1.f : ex2(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= f0;
+                l1 *= f1;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        o[k][0] *= f0;
-                        o[k][1] *= f0;
-                        o[k][2] *= f1;
-                        o[k][3] *= f1;
-                    }
+                for (int k = 0; k < 16; ++k) {
+                    o[k][0] *= f0;
+                    o[k][1] *= f0;
+                    o[k][2] *= f1;
+                    o[k][3] *= f1;
                 }
-                const float r0 = m0 == ninf ? 0.f : m0, r1 = m1 == ninf ? 0.f : m1;
+            }
+            const float r0 = m0 == ninf ? 0.f : m0, r1 = m1 == ninf ? 0.f : m1;
+            uint32_t hi4[4], lo4[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    uint32_t hi4[4], lo4[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const float e0 = ex2(s[k][t][0] - r0), e1 = ex2(s[k][t][1] - r0);
-                        const float e2 = ex2(s[k][t][2] - r1), e3 = ex2(s[k][t][3] - r1);
-                        l0 += e0 + e1;
-                        l1 += e2 + e3;
-                        s[k][t][0] = e0;
-                        s[k][t][1] = e1;
-                        s[k][t][2] = e2;
-                        s[k][t][3] = e3;
-                        if (FMT == kFmtBf16) {
-                            // P = hi + lo, 16 significant bits: the rounding of P to bf16 alone
-                            // (2^-9 relative) would weigh as much as the rounding of the output
-                            const uint32_t h0 = pack_bf16(e0, e1), h1 = pack_bf16(e2, e3);
-                            hi4[2 * t] = h0;
-                            hi4[2 * t + 1] = h1;
-                            lo4[2 * t] = pack_bf16(e0 - __uint_as_float(h0 << 16), e1 - __uint_as_float(h0 & 0xFFFF0000u));
-                            lo4[2 * t + 1] = pack_bf16(e2 - __uint_as_float(h1 << 16), e3 - __uint_as_float(h1 & 0xFFFF0000u));
-                        } else { // f16 of 2^15 P: 11 significant bits down to P = 2^-29
-                            hi4[2 * t] = pack_f16(e0, e1);
-                            hi4[2 * t + 1] = pack_f16(e2, e3);
-                        }
-                    }
-                    const int at = pos + 16 * k, past = cached - page0 - at; // rows from `past` on are not cached
-                    if (tail && page0 + at + 16 > seq_len && (past < 16 || p.nq > 1)) {
-                        uint32_t drop = past < 16 ? 0xFFFFu << max(past, 0) & 0xFFFFu : 0u;
-                        // positions that only later tokens see: their infinities and NaN are added
-                        // to the rows that see them, one position at a time, past the MMA
-                        uint32_t later = 0xFFFFu << max(seq_len - page0 - at, 0) & 0xFFFFu & ~drop;
-                        if (later)
-                            later &= nonfinite_rows<FMT>(vt, at);
-                        drop |= later;
-                        for (; later; later &= later - 1) {
-                            const int pp = __ffs(later) - 1, src = (lane & ~3) | ((pp & 7) >> 1);
-                            const float c0 = pp & 8 ? (pp & 1 ? s[k][1][1] : s[k][1][0]) : (pp & 1 ? s[k][0][1] : s[k][0][0]);
-                            const float c1 = pp & 8 ? (pp & 1 ? s[k][1][3] : s[k][1][2]) : (pp & 1 ? s[k][0][3] : s[k][0][2]);
-                            const float p0 = __shfl_sync(0xffffffffu, c0, src), p1 = __shfl_sync(0xffffffffu, c1, src);
-                            const bool see0 = page0 + at + pp < lim0, see1 = page0 + at + pp < lim1;
-#pragma unroll
-                            for (int t = 0; t < 16; ++t)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float v = value_at<FMT>(gsm + st * 2 * TB + TB, at + pp,
-                                                                  8 * TG * (t / TG) + TG * (2 * c4 + e) + t % TG);
-                                    if (see0)
-                                        o[t][e] = fmaf(p0, v, o[t][e]);
-                                    if (see1)
-                                        o[t][2 + e] = fmaf(p1, v, o[t][2 + e]);
-                                }
-                        }
-                        const uint32_t d0 = drop >> (2 * c4), d1 = d0 >> 8;
-                        accumulate16<FMT, true>(o, hi4, lo4, vt, at, (d0 & 1 ? 0u : 0xFFFFu) | (d0 & 2 ? 0u : 0xFFFF0000u),
-                                                (d1 & 1 ? 0u : 0xFFFFu) | (d1 & 2 ? 0u : 0xFFFF0000u));
-                    } else {
-                        accumulate16<FMT, false>(o, hi4, lo4, vt, at);
-                    }
+            for (int t = 0; t < 2; ++t) {
+                const float e0 = ex2(s[t][0] - r0), e1 = ex2(s[t][1] - r0);
+                const float e2 = ex2(s[t][2] - r1), e3 = ex2(s[t][3] - r1);
+                l0 += e0 + e1;
+                l1 += e2 + e3;
+                s[t][0] = e0;
+                s[t][1] = e1;
+                s[t][2] = e2;
+                s[t][3] = e3;
+                if (FMT == kFmtBf16) {
+                    // P = hi + lo, 16 significant bits: the rounding of P to bf16 alone
+                    // (up to 2^-8 relative) would weigh as much as the rounding of the output
+                    const uint32_t h0 = pack_bf16(e0, e1), h1 = pack_bf16(e2, e3);
+                    hi4[2 * t] = h0;
+                    hi4[2 * t + 1] = h1;
+                    lo4[2 * t] = pack_bf16(e0 - __uint_as_float(h0 << 16), e1 - __uint_as_float(h0 & 0xFFFF0000u));
+                    lo4[2 * t + 1] = pack_bf16(e2 - __uint_as_float(h1 << 16), e3 - __uint_as_float(h1 & 0xFFFF0000u));
+                } else { // f16 of 2^15 P: 11 significant bits down to P = 2^-29
+                    hi4[2 * t] = pack_f16(e0, e1);
+                    hi4[2 * t + 1] = pack_f16(e2, e3);
                 }
+            }
+            const int past = cached - page0 - at; // rows from `past` on are not cached
+            if (tail && page0 + at + 16 > seq_len && (past < 16 || p.nq > 1)) {
+                uint32_t drop = past < 16 ? 0xFFFFu << max(past, 0) & 0xFFFFu : 0u;
+                // positions that only later tokens see: their infinities and NaN are added
+                // to the rows that see them, one position at a time, past the MMA
+                uint32_t later = 0xFFFFu << max(seq_len - page0 - at, 0) & 0xFFFFu & ~drop;
+                if (later)
+                    later &= nonfinite_rows<FMT>(vt, at);
+                drop |= later;
+                for (; later; later &= later - 1) {
+                    const int pp = __ffs(later) - 1, src = (lane & ~3) | ((pp & 7) >> 1);
+                    const float c0 = pp & 8 ? (pp & 1 ? s[1][1] : s[1][0]) : (pp & 1 ? s[0][1] : s[0][0]);
+                    const float c1 = pp & 8 ? (pp & 1 ? s[1][3] : s[1][2]) : (pp & 1 ? s[0][3] : s[0][2]);
+                    const float p0 = __shfl_sync(0xffffffffu, c0, src), p1 = __shfl_sync(0xffffffffu, c1, src);
+                    const bool see0 = page0 + at + pp < lim0, see1 = page0 + at + pp < lim1;
+#pragma unroll
+                    for (int t = 0; t < 16; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float v = value_at<FMT>(gsm + st * 2 * TB + TB, at + pp,
+                                                          8 * TG * (t / TG) + TG * (2 * c4 + e) + t % TG);
+                            if (see0)
+                                o[t][e] = fmaf(p0, v, o[t][e]);
+                            if (see1)
+                                o[t][2 + e] = fmaf(p1, v, o[t][2 + e]);
+                        }
+                }
+                const uint32_t d0 = drop >> (2 * c4), d1 = d0 >> 8;
+                accumulate16<FMT, true>(o, hi4, lo4, vt, at, (d0 & 1 ? 0u : 0xFFFFu) | (d0 & 2 ? 0u : 0xFFFF0000u),
+                                        (d1 & 1 ? 0u : 0xFFFFu) | (d1 & 2 ? 0u : 0xFFFF0000u));
+            } else {
+                accumulate16<FMT, false>(o, hi4, lo4, vt, at);
             }
             __syncwarp();
             if (lane == 0)
@@ -525,23 +515,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
         if (c4 == 0) {
-            sm_m[pg * ROWS + mt * 16 + n8] = m0;
-            sm_m[pg * ROWS + mt * 16 + n8 + 8] = m1;
-            sm_l[pg * ROWS + mt * 16 + n8] = l0;
-            sm_l[pg * ROWS + mt * 16 + n8 + 8] = l1;
+            sm_m[ROWS * warp + n8] = m0;
+            sm_m[ROWS * warp + n8 + 8] = m1;
+            sm_l[ROWS * warp + n8] = l0;
+            sm_l[ROWS * warp + n8 + 8] = l1;
         }
         consumers_sync();
         float M0 = ninf, M1 = ninf, L0 = 0.f, L1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < PG; ++k) {
-            M0 = fmaxf(M0, sm_m[k * ROWS + mt * 16 + n8]);
-            M1 = fmaxf(M1, sm_m[k * ROWS + mt * 16 + n8 + 8]);
+        for (int k = 0; k < kConsumers; ++k) {
+            M0 = fmaxf(M0, sm_m[ROWS * k + n8]);
+            M1 = fmaxf(M1, sm_m[ROWS * k + n8 + 8]);
         }
 #pragma unroll
-        for (int k = 0; k < PG; ++k) {
-            const float a = sm_m[k * ROWS + mt * 16 + n8], c = sm_m[k * ROWS + mt * 16 + n8 + 8];
-            L0 += a == ninf ? 0.f : sm_l[k * ROWS + mt * 16 + n8] * ex2(a - M0);
-            L1 += c == ninf ? 0.f : sm_l[k * ROWS + mt * 16 + n8 + 8] * ex2(c - M1);
+        for (int k = 0; k < kConsumers; ++k) {
+            const float a = sm_m[ROWS * k + n8], c = sm_m[ROWS * k + n8 + 8];
+            L0 += a == ninf ? 0.f : sm_l[ROWS * k + n8] * ex2(a - M0);
+            L1 += c == ninf ? 0.f : sm_l[ROWS * k + n8 + 8] * ex2(c - M1);
         }
         const float f0 = m0 == ninf ? 0.f : ex2(m0 - M0), f1 = m1 == ninf ? 0.f : ex2(m1 - M1);
 #pragma unroll
@@ -551,27 +541,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[k][2] *= f1;
             o[k][3] *= f1;
         }
-        float *mine = join + ((pg % (PG / 2)) * MT + mt) * 2048 + lane;
-        if (pg >= PG / 2) {
+        float *mine = join + (warp % (kConsumers / 2)) * 2048 + lane;
+        if (warp >= kConsumers / 2) {
 #pragma unroll
             for (int k = 0; k < 64; ++k)
                 mine[k * 32] = o[k >> 2][k & 3];
         }
         consumers_sync();
-        if (pg < PG / 2) {
+        if (warp < kConsumers / 2) {
 #pragma unroll
             for (int k = 0; k < 64; ++k)
                 mine[k * 32] += o[k >> 2][k & 3];
         }
         consumers_sync();
 
-        // this warp finishes 16 / PG n-tiles of its row group, in groups of TG: 2 TG consecutive dimensions a lane
+        // this warp finishes two n-tiles, in groups of TG: 2 TG consecutive dimensions a lane
         const bool whole = b == 0 && n == nb; // no other CTA has a part of this unit
         const bool ends = b + n == nb;
         float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * (ROWS * (kDim + 2));
         const float g0 = L0 > 0.f || L0 != L0 ? p.v_scale / L0 : 0.f, g1 = L1 > 0.f || L1 != L1 ? p.v_scale / L1 : 0.f;
         const size_t out0 = first_row + j0 * pitch + (i0 - j0 * p.G), out1 = first_row + j1 * pitch + (i1 - j1 * p.G);
-        for (int grp = pg; grp < 16 / TG; grp += PG) {
+        for (int grp = warp; grp < 16 / TG; grp += kConsumers) {
             float v[2][2 * TG];
 #pragma unroll
             for (int t = 0; t < TG; ++t)
@@ -579,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     float a = 0.f;
 #pragma unroll
-                    for (int k = 0; k < PG / 2; ++k)
-                        a += join[(k * MT + mt) * 2048 + ((grp * TG + t) * 4 + e) * 32 + lane];
+                    for (int k = 0; k < kConsumers / 2; ++k)
+                        a += join[k * 2048 + ((grp * TG + t) * 4 + e) * 32 + lane];
                     v[e >> 1][(e & 1) * TG + t] = a;
                 }
             const int d = 8 * TG * grp + 2 * TG * c4;
@@ -593,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         store_bf16x2(p.out + out1 * kDim, d + k, v[1][k] * g1, v[1][k + 1] * g1);
                 }
             } else {
-                float *a = slot + (size_t)(mt * 16 + n8) * kDim + d;
+                float *a = slot + (size_t)n8 * kDim + d;
 #pragma unroll
                 for (int k = 0; k < 2 * TG; k += 2) {
                     *reinterpret_cast<float2 *>(a + k) = make_float2(v[0][k], v[0][k + 1]);
@@ -601,14 +591,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (pg == 0 && c4 == 0) {
+        if (warp == 0 && c4 == 0) {
             if (whole) {
                 if (i0 < p.rows)
                     p.lse[out0] = L0 == 0.f ? ninf : (M0 + log2f(L0)) * 0.6931471805599453f;
                 if (i1 < p.rows)
                     p.lse[out1] = L1 == 0.f ? ninf : (M1 + log2f(L1)) * 0.6931471805599453f;
             } else {
-                float *ml = slot + (size_t)ROWS * kDim + mt * 16 + n8;
+                float *ml = slot + (size_t)ROWS * kDim + n8;
                 ml[0] = M0;
                 ml[8] = M1;
                 ml[ROWS] = L0;
@@ -724,23 +714,14 @@ cudaError_t launch_join(const DenseParams &p, int tile_rows, int ctas, cudaStrea
     return launch_kernel(dense_join_kernel<1>, dim3(ctas - 1, (rows + 7) / 8), dim3(256), 0, stream, true, p, tile_rows);
 }
 
-template <int FMT, int MT>
+template <int FMT>
 cudaError_t launch_t(const DenseParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
 {
     constexpr int smem = smem_layout(FMT).total;
-    cudaError_t e = cudaFuncSetAttribute(dense_stream_kernel<FMT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
-        return e;
-    e = launch_kernel(dense_stream_kernel<FMT, MT>, dim3(ctas), dim3(kThreads), smem, stream, false, map, p);
-    if (e == cudaSuccess && ctas > 1)
-        e = launch_join(p, 16 * MT, ctas, stream);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <int FMT>
-cudaError_t launch_fmt(const DenseParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
-{
-    return launch_t<FMT, 1>(p, map, ctas, stream);
+    cudaError_t e = cudaFuncSetAttribute(dense_stream_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = launch_kernel(dense_stream_kernel<FMT>, dim3(ctas), dim3(kThreads), smem, stream, false, map, p);
+    return e;
 }
 
 } // namespace
@@ -755,17 +736,18 @@ cudaError_t launch_dense_decode(const DenseParams &p, int kv_dtype, int ctas, cu
     CUtensorMap map;
     if (!encode_pool_map(&map, p.kv, kv_dtype, p.num_pages, p.Hkv))
         return cudaErrorInvalidValue;
-    if (p.rows > 16) {
-        cudaError_t e = launch_dense_umma(p, map, kv_dtype, ctas, stream);
-        if (e == cudaSuccess && ctas > 1)
-            e = launch_join(p, dense_tile_rows(p.rows), ctas, stream);
-        return e != cudaSuccess ? e : cudaGetLastError();
-    }
-    if (kv_dtype == MSA_BF16)
-        return launch_fmt<kFmtBf16>(p, map, ctas, stream);
-    if (kv_dtype == MSA_FP8_E4M3)
-        return launch_fmt<kFmtFp8>(p, map, ctas, stream);
-    return launch_fmt<kFmtF4>(p, map, ctas, stream);
+    cudaError_t e;
+    if (p.rows > 16)
+        e = launch_dense_umma(p, map, kv_dtype, ctas, stream);
+    else if (kv_dtype == MSA_BF16)
+        e = launch_t<kFmtBf16>(p, map, ctas, stream);
+    else if (kv_dtype == MSA_FP8_E4M3)
+        e = launch_t<kFmtFp8>(p, map, ctas, stream);
+    else
+        e = launch_t<kFmtF4>(p, map, ctas, stream);
+    if (e == cudaSuccess && ctas > 1)
+        e = launch_join(p, dense_tile_rows(p.rows), ctas, stream);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 } // namespace msa
