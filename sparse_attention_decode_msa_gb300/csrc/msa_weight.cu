@@ -237,13 +237,21 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             mask[i] = 0ull;
                         __syncwarp();
                         // one bit per token for every page of [sb, sb + sn) in its table
-                        for (int i = lane; i < p.nq * p.k; i += 32) {
-                            const int j = i / p.k;
-                            const int blk = p.selected[(((size_t)w.r * p.nq + j) * p.Hs + (p.Hs > 1 ? g : 0)) * p.k + (i - j * p.k)];
-                            if (blk < -1 || (blk >= 0 && (long long)blk * kPage >= w.seq_len + j))
-                                set_error(p.err, kErrSelection);
-                            else if (blk >= sb && blk < sb + sn)
-                                atomicOr(&mask[blk - sb], 1ull << j);
+                        for (int i0 = lane; i0 < p.nq * p.k; i0 += 256) { // eight entries a lane in flight
+                            int blk[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const int i = i0 + 32 * c, j = i / p.k;
+                                blk[c] = i < p.nq * p.k ? p.selected[(((size_t)w.r * p.nq + j) * p.Hs + (p.Hs > 1 ? g : 0)) * p.k + (i - j * p.k)] : -1;
+                            }
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const int j = (i0 + 32 * c) / p.k;
+                                if (blk[c] < -1 || (blk[c] >= 0 && (long long)blk[c] * kPage >= w.seq_len + j))
+                                    set_error(p.err, kErrSelection);
+                                else if (blk[c] >= sb && blk[c] < sb + sn)
+                                    atomicOr(&mask[blk[c] - sb], 1ull << j);
+                            }
                         }
                         __syncwarp();
                         if (lane == 0)

@@ -7,8 +7,11 @@ at most d = 32 * 2^-23 * S + 4 * 2^-24 * |x| (an fp32 sum of 128 exact
 products, in at most 32 roundings or cuts of one step; the scale, the subtraction), and
 exp2's hardware form by 2^-22 relative.
   lse      d + 2^-22 + n 2^-24 (sum of n terms) + 2^-22 (1 + |lse|) (log2, the two products)
-  out      2^-8 |o| for its storage, and max |v| times: 2^-11 for P (its fp16
-           form, the larger of the two), 2 (d + 2^-22), n 2^-23 for the sums
+  out      2^-8 |o| for its storage, and max |v| times: 2^-11 for P, 2 (d + 2^-22), n 2^-23 for the
+           sums.  P is fp16 (2^-11 of each p) or a bf16 pair (2^-16), or bf16 alone where each p is at
+           most l / 64: then its errors, independent and 2^-8 / sqrt(3) p (rms) at most, add up to
+           2^-8 / sqrt(3) sqrt(sum p^2) / l <= 2^-8 / sqrt(3) / 8 = 2^-11.8 (rms) of max |v|, and of the
+           rms of v, a quarter of its maximum here, 5 sigma are 2^-11.5
   weights  relative d + 2^-22 + 2^-23 |lse| a term, rows 2^-24 for the sum, 2^-23 for decay
 """
 
@@ -198,6 +201,62 @@ def test_dense_decode_equals_the_sparse_decode_of_all_blocks(torch_cuda):
     # two results, each within the bound of the definition; the sparse decode's own is 4e-3, 1e-4
     assert np.abs(dense["out"] - sparse["out"]).max() <= 4e-3 + (2.0 ** -8 + 2.0 ** -11 + 2 * logit_error(S, S) + 2.0 ** -12) * V
     assert np.abs(dense["lse"] - sparse["lse"]).max() <= 1e-4 * np.abs(sparse["lse"]).max() + logit_error(S, S) + 2.0 ** -13
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("nq", [1, 3, 20])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
+def test_any_softmax_scale(torch_cuda, kv, nq, scale):
+    c = Cache([700, 200], nq, 1, 16, kv, seed=33)
+    c.pb.softmax_scale = scale
+    c.upload()
+    c.decode()
+    c.check_decode()
+    w = c.torch.zeros((2, 1, c.pb.max_blocks * 128), device="cuda")
+    c.accumulate(c.lse, None, w)
+    check_weights(c, w, c.lse, None, 1.0, None, after=w)
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("nq", [1, 3, 20])
+@pytest.mark.parametrize("e", [-100, -60, 60, 100])
+def test_queries_far_outside_f16(torch_cuda, kv, nq, e):
+    c = Cache([700, 200], nq, 1, 16, kv, seed=35)
+    c.q = synth.f32_to_bf16_bits(np.ldexp(synth.bf16_bits_to_f32(c.q), e).astype(np.float32))
+    c.pb.softmax_scale = float(np.ldexp(np.float32(0.0625), -e))
+    c.upload()
+    c.decode()
+    c.check_decode()
+    w = c.torch.zeros((2, 1, c.pb.max_blocks * 128), device="cuda")
+    c.accumulate(c.lse, None, w)
+    check_weights(c, w, c.lse, None, 1.0, None, after=w)
+
+
+def test_many_requests_most_of_them_idle(torch_cuda):
+    rng = np.random.default_rng(3)
+    contexts = [int(x) for x in rng.integers(1, 300, 3000)]
+    idle = tuple(int(x) for x in np.flatnonzero(rng.random(3000) < 0.9))
+    c = Cache(contexts, 1, 1, 4, "fp8", seed=37, idle=idle)
+    c.decode()
+    c.check_decode()
+
+
+def test_two_streams_at_once(torch_cuda):
+    torch = torch_cuda
+    a, b = Cache([9000, 3000], 4, 2, 16, seed=38), Cache([20000, 150], 1, 2, 16, "fp8", seed=39)
+    for c in (a, b):
+        c.w = torch.zeros((2, 2, c.pb.max_blocks * 128), device="cuda")
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        for c, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                c.decode()
+                c.accumulate(c.lse, None, c.w)
+    torch.cuda.synchronize()
+    for c in (a, b):
+        c.check_decode()
+        check_weights(c, c.w, c.lse, None, 1.0, None, after=c.w)
 
 
 def test_same_bits_each_time_and_on_another_stream(torch_cuda):
