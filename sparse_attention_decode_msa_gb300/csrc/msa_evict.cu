@@ -11,11 +11,13 @@
 // Select: comparisons only, so bit-exact.  One CTA per list where the table
 // holds at most 8192 positions, else a cluster of 8, each CTA with an eighth of the
 // positions, whose order-preserving 32-bit keys stay in shared memory (up to
-// 40960 a CTA; longer slices read the weights again).  Three digits (11, 11, 10
-// bits) from the top give the keep-th largest key: the CTAs read one another's
-// histograms through distributed shared memory, one cluster barrier a digit, and
-// from the same words how many kept positions the CTAs before them have.  Prefix
-// counts in position order then give each kept position its place.
+// 40960 a CTA; longer slices read the weights again).  Four 8-bit digits from the
+// top give the keep-th largest key: the CTAs read one another's histograms (256
+// words; with 11-bit digits their reading took as long as all the rest of a digit)
+// through distributed shared memory, one cluster barrier a digit, and from the same
+// words how many kept positions the CTAs before them have.  Eight copies of the
+// histogram, by lane, keep a warp's increments of one word apart.  Prefix counts in
+// position order then give each kept position its place.
 //
 // Copy: 128 (short lists: 32) kept positions per CTA; every row is 16-byte pieces,
 // eight loads in flight per thread over K, V and index-key rows alike.  Rows go to pages of their own (new_table), so pages
@@ -29,7 +31,8 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kKeysHeld = 40960;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
+constexpr int kCopies = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -43,13 +46,13 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Four 32-bit words of another CTA's shared memory.
-__device__ __forceinline__ int4 ld_peer4(const void *p, int rank)
+// A 32-bit word of another CTA's shared memory.
+__device__ __forceinline__ int ld_peer(const void *p, int rank)
 {
     uint32_t a;
-    int4 v;
+    int v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
 
@@ -109,7 +112,7 @@ template <int CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, int held)
 {
     extern __shared__ __align__(16) uint32_t keys[]; // [held]
-    __shared__ __align__(16) int hist[3][kBins];
+    __shared__ int copies[kCopies][kBins], hist[4][kBins];
     __shared__ uint32_t scan_tmp[kSelWarps + 1];
     __shared__ int s_digit, s_need, s_before, s_equal;
 
@@ -137,8 +140,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     const size_t pitch = (size_t)p.maxB * kPage;
     const float *w = p.weights + ((size_t)r * p.Hkv + (size_t)hs * heads) * pitch;
     const bool cached = count <= held;
-    for (int i = threadIdx.x; i < 3 * kBins; i += kSelThreads)
-        (&hist[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < kCopies * kBins; i += kSelThreads)
+        (&copies[0][0])[i] = 0;
     if (threadIdx.x == 0)
         s_before = 0;
     __syncthreads();
@@ -159,9 +162,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
                 k[e] = 0xFFFFFFFFu;
     };
     constexpr int U = 4; // loads in flight a thread
-    // equal leading digits are common (weights of one magnitude, zeros): three copies of
-    // the first histogram, by lane, keep a warp's increments from queueing on one word
-    int *first_hist = hist[(threadIdx.x & 31) % 3];
+    int *mine = copies[threadIdx.x & (kCopies - 1)];
     for (int i0 = 4 * (int)threadIdx.x; i0 < count; i0 += 4 * U * kSelThreads) {
         uint32_t k[U][4];
 #pragma unroll
@@ -178,28 +179,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (i + e < count)
-                    atomicAdd(&first_hist[k[u][e] >> 21], 1);
+                    atomicAdd(&mine[k[u][e] >> 24], 1);
         }
     }
-    __syncthreads();
-    for (int i = 4 * (int)threadIdx.x; i < kBins; i += 4 * kSelThreads) {
-        const int4 a = *reinterpret_cast<int4 *>(&hist[0][i]), b = *reinterpret_cast<int4 *>(&hist[1][i]), c = *reinterpret_cast<int4 *>(&hist[2][i]);
-        *reinterpret_cast<int4 *>(&hist[0][i]) = make_int4(a.x + b.x + c.x, a.y + b.y + c.y, a.z + b.z + c.z, a.w + b.w + c.w);
-        *reinterpret_cast<int4 *>(&hist[1][i]) = *reinterpret_cast<int4 *>(&hist[2][i]) = make_int4(0, 0, 0, 0);
-    }
-    __syncthreads();
-
     // the keep-th largest key, digit by digit
     uint32_t prefix = 0u;
     int need = p.keep;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        int *h = hist[pass];
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
         if (pass > 0) {
             auto add = [&](uint32_t k) {
-                if ((k >> (shift + bits)) == prefix)
-                    atomicAdd(&h[(k >> shift) & ((1u << bits) - 1u)], 1);
+                if ((k >> (shift + 8)) == prefix)
+                    atomicAdd(&mine[(k >> shift) & 255u], 1);
             };
             const int whole = cached ? count & ~3 : 0;
             for (int i = 4 * (int)threadIdx.x; i < whole; i += 4 * kSelThreads) {
@@ -212,42 +204,47 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             for (int i = whole + threadIdx.x; i < count; i += kSelThreads)
                 add(key(i));
         }
+        __syncthreads();
+        if (threadIdx.x < kBins) {
+            int sum = 0;
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) {
+                sum += copies[c][threadIdx.x];
+                copies[c][threadIdx.x] = 0;
+            }
+            hist[pass][threadIdx.x] = sum;
+        }
         if (CLUSTER > 1)
             cluster_sync();
         else
             __syncthreads();
-        // bins from the top: thread t has the 4 bins ending at kBins - 1 - 4 t; of all CTAs
-        // and of those before this one
-        const int bin0 = kBins - 4 - 4 * (int)threadIdx.x;
-        int c[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
+        // thread t has bin kBins - 1 - t: of all CTAs, and of those before this one
+        const int bin = kBins - 1 - (int)threadIdx.x;
+        int c = 0, before = 0;
+        if (bin >= 0) {
+            int v[CLUSTER];
 #pragma unroll
-        for (int q = 0; q < CLUSTER; ++q) {
-            const int4 v = CLUSTER > 1 ? ld_peer4(&h[bin0], q) : *reinterpret_cast<const int4 *>(&h[bin0]);
-            c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
-            if (q < rank)
-                before[0] += v.w, before[1] += v.z, before[2] += v.y, before[3] += v.x;
+            for (int q = 0; q < CLUSTER; ++q)
+                v[q] = CLUSTER > 1 ? ld_peer(&hist[pass][bin], q) : hist[pass][bin];
+#pragma unroll
+            for (int q = 0; q < CLUSTER; ++q) {
+                c += v[q];
+                before += q < rank ? v[q] : 0;
+            }
         }
         uint32_t total;
-        int above = (int)cta_scan((uint32_t)(c[0] + c[1] + c[2] + c[3]), scan_tmp, &total);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (above < need && need <= above + c[k]) { // one bin of one thread
-                s_digit = bin0 + 3 - k;
-                s_need = need - above;
-                s_equal = before[k];
-            }
-            above += c[k];
+        const int above = (int)cta_scan((uint32_t)c, scan_tmp, &total);
+        if (above < need && need <= above + c) { // one bin
+            s_digit = bin;
+            s_need = need - above;
+            s_equal = before;
         }
         __syncthreads();
         // positions of the CTAs before this one that are kept by this digit
-        int kept = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            kept += bin0 + 3 - k > s_digit ? before[k] : 0;
-        kept = __reduce_add_sync(0xffffffffu, kept);
+        const int kept = (int)__reduce_add_sync(0xffffffffu, bin > s_digit ? (uint32_t)before : 0u);
         if ((threadIdx.x & 31) == 0 && kept)
             atomicAdd(&s_before, kept);
-        prefix = (prefix << bits) | (uint32_t)s_digit;
+        prefix = (prefix << 8) | (uint32_t)s_digit;
         need = s_need;
         __syncthreads();
     }
@@ -260,26 +257,41 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     // keys (no bank conflicts): one scan over the CTA places all of them
     const int run = ((((count + kSelThreads - 1) / kSelThreads + 3) >> 2) | 1) << 2;
     const int begin = min(count, run * (int)threadIdx.x), end = min(count, begin + run);
+    auto four = [&](int i, uint32_t (&k)[4]) { // of this thread's run
+        if (cached) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(keys + i);
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                k[e] = i + e < end ? key(i + e) : 0u;
+        }
+    };
     int gt = 0, eq = 0;
     for (int i = begin; i < end; i += 4) {
+        uint32_t k[4];
+        four(i, k);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const bool in = i + e < end;
-            const uint32_t k = in ? key(i + e) : 0u;
-            gt += in && k > theta;
-            eq += in && k == theta;
+            gt += i + e < end && k[e] > theta;
+            eq += i + e < end && k[e] == theta;
         }
     }
     uint32_t total;
     int g = gt_before + (int)cta_scan((uint32_t)gt, scan_tmp, &total);
     int q = eq_before + (int)cta_scan((uint32_t)eq, scan_tmp, &total);
     if (gt || (eq && q < need))
-        for (int i = begin; i < end; ++i) {
-            const uint32_t k = key(i);
-            if (k > theta || (k == theta && q < need))
-                out[g + min(q, need)] = lo + i;
-            g += k > theta;
-            q += k == theta;
+        for (int i = begin; i < end; i += 4) {
+            uint32_t k[4];
+            four(i, k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool is_gt = i + e < end && k[e] > theta, is_eq = i + e < end && k[e] == theta;
+                if (is_gt || (is_eq && q < need))
+                    out[g + min(q, need)] = lo + i + e;
+                g += is_gt;
+                q += is_eq;
+            }
         }
     if (CLUSTER > 1)
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
