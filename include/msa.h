@@ -259,7 +259,7 @@ msa_status msa_select_rows(const msa_shape *shape, const float *scores_hbt,
  * one workspace; msa_workspace_init and msa_check_device_status work on it as
  * on the other.  Differences to the calls above:
  *   - num_q_heads is any multiple G of num_kv_heads with 1 <= G <= 64: query
- *     head h uses KV head h / G;
+ *     head h uses KV head h / G; num_kv_heads is at most 8192;
  *   - seq_lens[r] may be 0: an idle slot of a padded batch.  Its out rows are
  *     0, its lse -inf, its weights untouched, its new length 0; its block
  *     table row is not read.  A negative length, or one the table cannot
@@ -273,6 +273,8 @@ msa_status msa_select_rows(const msa_shape *shape, const float *scores_hbt,
  *     accumulation (at most 8192); 0 takes one per SM;
  *   - bytes of a page behind the last cached position may hold anything
  *     (infinities and NaN among it);
+ *   - outputs overlap neither inputs nor one another, but for weights_out,
+ *     which may be weights_in;
  *   - nothing is kept in the workspace between calls but the error word.  Calls
  *     on two streams that may overlap, and CUDA graphs that may, need a
  *     workspace each. */

@@ -20,6 +20,7 @@
 namespace msa {
 
 constexpr int kMaxGroup = 64;      // query heads per KV head of the whole-cache operators
+constexpr int kMaxKvHeads = 8192;  // list counts and a page's 16-byte pieces stay in int32
 constexpr int kCacheCtaBound = 160; // workspace bound on the default persistent CTAs
 
 // KV formats of the kernel instances

@@ -27,7 +27,7 @@ msa_status check_cache_shape(const msa_shape *s)
     if (!std::isfinite(s->softmax_scale) || !std::isfinite(s->k_scale) || !std::isfinite(s->v_scale))
         return MSA_ERR_INVALID_ARGUMENT;
     if (s->head_dim != kDim || s->page_size != kPage || s->num_q_heads % s->num_kv_heads != 0 ||
-        s->num_q_heads / s->num_kv_heads > kMaxGroup)
+        s->num_q_heads / s->num_kv_heads > kMaxGroup || s->num_kv_heads > kMaxKvHeads)
         return MSA_ERR_UNSUPPORTED;
     if (s->num_index_heads > kMaxIndexHeads ||
         (s->num_index_heads > 1 && s->num_index_heads % s->num_kv_heads != 0))

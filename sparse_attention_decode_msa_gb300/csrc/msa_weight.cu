@@ -44,6 +44,7 @@ namespace {
 constexpr int kPagesAtATime = 512; // pages whose bitmaps are held at a time
 constexpr int kTile16 = 32768;     // a 16-bit K tile
 constexpr int kMaxRing = 16;
+constexpr int kSmemMax = 231424;   // what the layouts below stay under (232448 with the static part)
 
 // Key formats of the kernel instances: as stored, or (kFmtPair) E4M3 keys as operands.
 constexpr int kFmtPair = 3;
@@ -549,7 +550,10 @@ cudaError_t launch_t(const WeightParams &p, const CUtensorMap &map, int ctas, cu
 {
     const int rows = p.nq * p.G, qpad = padded(FMT, rows < query_rows(FMT) ? rows : query_rows(FMT));
     const Smem L = smem_layout(FMT, qpad, p.selected != nullptr);
-    cudaError_t e = cudaFuncSetAttribute(weight_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+    // the same limit for every shape: another host thread may launch another shape meanwhile
+    if (L.total > kSmemMax)
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(weight_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e == cudaSuccess)
         e = launch_kernel(weight_kernel<FMT>, dim3(ctas), dim3(threads_of(FMT)), (size_t)L.total, stream, false, map, p, L);
     return e != cudaSuccess ? e : cudaGetLastError();

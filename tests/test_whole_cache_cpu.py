@@ -24,7 +24,8 @@ def shape(**kw):
 
 @pytest.mark.parametrize("kw", [dict(num_q_heads=4), dict(num_q_heads=20), dict(num_q_heads=256), dict(topk=0), dict(topk=5000),
                                 dict(init_blocks=50), dict(index_dim=64), dict(index_dtype=7), dict(kv_dtype="nvfp4"),
-                                dict(q_per_req=64, num_requests=128), dict(num_requests=0)])
+                                dict(q_per_req=64, num_requests=128), dict(num_requests=0),
+                                dict(num_kv_heads=8192, num_pages=1, num_requests=1, max_blocks_per_seq=1)])
 def test_shapes_that_are_taken(lib, kw):
     assert msa.msa_cache_workspace_bytes(shape(**kw)) > 256
 
@@ -35,6 +36,7 @@ def test_shapes_that_are_taken(lib, kw):
                                 dict(num_pages=0), dict(kv_dtype=3), dict(softmax_scale=float("inf")), dict(decode_ctas=-1),
                                 dict(decode_ctas=8193), dict(num_index_heads=0), dict(num_index_heads=6), dict(num_index_heads=68),
                                 dict(num_pages=2 ** 31 // (2 * 4 * 144) + 1),
+                                dict(num_kv_heads=8193, num_pages=1, num_requests=1, max_blocks_per_seq=1),
                                 dict(num_requests=8192, q_per_req=1, max_blocks_per_seq=16384, num_kv_heads=64)])
 def test_shapes_that_are_refused(lib, kw):
     s = shape(**kw)

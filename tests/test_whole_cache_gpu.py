@@ -259,6 +259,41 @@ def test_two_streams_at_once(torch_cuda):
         check_weights(c, c.w, c.lse, None, 1.0, None, after=c.w)
 
 
+def test_two_host_threads_at_once(torch_cuda):
+    # shapes with different shared-memory needs of one kernel instance
+    import threading
+
+    torch = torch_cuda
+    a, b = Cache([3000, 500], 1, 1, 16, seed=44), Cache([3000, 500], 20, 1, 16, seed=45)
+    want, failed = [], []
+    for c in (a, b):
+        c.decode()
+        c.w = torch.zeros((2, 1, c.pb.max_blocks * 128), device="cuda")
+        c.accumulate(c.lse, None, c.w)
+        want.append(c.w.clone())
+    torch.cuda.synchronize()
+
+    def work(c, w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(300):
+                    c.accumulate(c.lse, None, c.w)
+                    c.decode()
+            torch.cuda.synchronize()
+            assert torch.equal(c.w, w)
+        except BaseException as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip((a, b), want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for c in (a, b):
+        c.check_decode()
+
+
 def test_same_bits_each_time_and_on_another_stream(torch_cuda):
     c = Cache([5000, 70, 2222], 4, 2, 16, "fp8", seed=23)
     c.decode()
