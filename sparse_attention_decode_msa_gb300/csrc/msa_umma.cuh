@@ -150,20 +150,26 @@ __device__ __forceinline__ void stage_rows(uint8_t *dst, int half, int n, int wi
 {
     constexpr int U = 4;
     const int lane = threadIdx.x & 31, c = lane & 15;
-    for (int i0 = 2 * wi; i0 < n; i0 += 2 * U * nw) {
-        uint4 d[U];
+    if constexpr (MODE == kRows16) { // nothing passes through registers: all rows in flight at once
+        for (int i = 2 * wi + (lane >> 4); i < n; i += 2 * nw)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + (c >> 3) * half + 128 * i + (((c & 7) ^ (i & 7)) << 4))),
+                         "l"(reinterpret_cast<const uint4 *>(row(i)) + c)
+                         : "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        for (int i0 = 2 * wi; i0 < n; i0 += 2 * U * nw) {
+            uint4 d[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + 2 * u * nw + (lane >> 4);
-            d[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < n)
-                d[u] = reinterpret_cast<const uint4 *>(row(i))[c];
-        }
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + 2 * u * nw + (lane >> 4);
+                d[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (i < n)
+                    d[u] = reinterpret_cast<const uint4 *>(row(i))[c];
+            }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + 2 * u * nw + (lane >> 4);
-            uint32_t *e = &d[u].x;
-            if (MODE != kRows16) {
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + 2 * u * nw + (lane >> 4);
+                uint32_t *e = &d[u].x;
                 float mx = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -200,9 +206,9 @@ __device__ __forceinline__ void stage_rows(uint8_t *dst, int half, int n, int wi
                     for (int k = 0; k < 4; ++k)
                         e[k] = pack_f16(__uint_as_float(e[k] << 16) * up, __uint_as_float(e[k] & 0xFFFF0000u) * up);
                 }
+                if (MODE != kRowsPair && i < n)
+                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * half + 128 * i + (((c & 7) ^ (i & 7)) << 4)) = d[u];
             }
-            if (MODE != kRowsPair && i < n)
-                *reinterpret_cast<uint4 *>(dst + (c >> 3) * half + 128 * i + (((c & 7) ^ (i & 7)) << 4)) = d[u];
         }
     }
 }

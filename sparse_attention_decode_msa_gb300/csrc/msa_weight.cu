@@ -22,10 +22,9 @@
 // What bounds it: the bytes of K and of the weights with few rows, the
 // exponentials with many.  Two groups (an MMA issuer, four softmax warps and,
 // where keys are widened, four converter warps each) share the work, so that one's
-// waits pass behind the other's work: up to 128 accumulator columns, each takes every
-// second page; with more, both work on every page (few K tiles fit beside that many
-// query rows), group g on columns 128 g .. of every 256, and group 1 hands its sums
-// to group 0.  The query rows of a (request, KV head), up to 512 (bf16) or 256 at a
+// waits pass behind the other's work: each takes every second page, 128 accumulator
+// columns at a time in two buffers (both groups on every page, with half of the columns
+// each, was 5 .. 25% slower).  The query rows of a (request, KV head), up to 512 (bf16) or 256 at a
 // time, stay in shared memory.
 //
 // After a sparse step only pages that some token of the request selected are
@@ -44,7 +43,7 @@ namespace {
 constexpr int kPagesAtATime = 512; // pages whose bitmaps are held at a time
 constexpr int kTile16 = 32768;     // a 16-bit K tile
 constexpr int kMaxRing = 16;
-constexpr int kSmemMax = 231424;   // what the layouts below stay under (232448 with the static part)
+constexpr int kSmemMax = 232192;   // what the layouts below stay under (232448 with the static part)
 
 // Key formats of the kernel instances: as stored, or (kFmtPair) E4M3 keys as operands.
 constexpr int kFmtPair = 3;
@@ -80,14 +79,14 @@ __host__ __device__ constexpr int padded(int fmt, int rows)
 // of K tiles.  Ring and staged tiles are even in number: a slot belongs to one
 // group, which follows all of its barriers' phases.
 struct Smem {
-    int ring, staged, q, cols, tok, mask, sums, bars, misc, total;
+    int ring, staged, q, cols, tok, mask, bars, misc, total;
     int depth, nstaged;
 };
 
 __host__ __device__ inline Smem smem_layout(int fmt, int qpad, bool masks)
 {
     Smem s{};
-    const int rest = qpad * (256 + 8 + 1) + (masks ? 2 * kPagesAtATime * 8 : 0) + 1024 + (2 * kMaxRing + 32) * 8 + 64 + 1024 + 256;
+    const int rest = qpad * (256 + 8 + 1) + (masks ? 2 * kPagesAtATime * 8 : 0) + (2 * kMaxRing + 32) * 8 + 64 + 1024 + 256;
     int room = 232448 - rest;
     s.nstaged = !widened(fmt) ? 0 : room >= 6 * kTile16 ? 4 : 2;
     room -= s.nstaged * kTile16;
@@ -99,8 +98,7 @@ __host__ __device__ inline Smem smem_layout(int fmt, int qpad, bool masks)
     s.cols = s.ring + s.depth * tile_bytes(stored_fmt(fmt));
     s.tok = s.cols + qpad * 8;
     s.mask = (s.tok + qpad + 15) / 16 * 16;
-    s.sums = s.mask + (masks ? 2 * kPagesAtATime * 8 : 0);
-    s.bars = s.sums + 2 * 128 * 4; // group 1's sums of a page, twice
+    s.bars = s.mask + (masks ? 2 * kPagesAtATime * 8 : 0);
     s.misc = s.bars + (2 * kMaxRing + 32) * 8;
     s.total = s.misc + 64 + 1024;
     return s;
@@ -122,24 +120,25 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const uint32_t full = smem + L.bars, empty = full + kMaxRing * 8, sfull = empty + kMaxRing * 8, sempty = sfull + 32,
                    q_full = sempty + 32, q_free = q_full + 8, s_full = q_free + 8, s_free = s_full + 32, m_full = s_free + 32,
                    m_free = m_full + 16, drain = m_free + 16;
-    float4 *cols = reinterpret_cast<float4 *>(gsm + L.cols); // per column pair: scales, -lse
+    // bf16 keys: -lse of four query rows a word (one load for four: 137 -> 129 us at 256 rows);
+    // else the scales of two rows, then their -lse
+    float4 *cols = reinterpret_cast<float4 *>(gsm + L.cols);
     uint8_t *tok = gsm + L.tok;                              // token of a column
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gsm + L.misc);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = p.nq * p.G, heads = p.Hkv;
     const bool sparse = p.selected != nullptr;
-    const bool share = (PAIR ? 2 : 1) * padded(FMT, min(kQRows, rows)) > 128; // both groups on every page
     const long long wl = p.wait_limit;
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map);
         for (int i = 0; i < L.depth; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, CONV ? 4 : share ? 2 : 1);
+            mbar_init(empty + 8 * i, CONV ? 4 : 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + 8 * i, 4);
-            mbar_init(sempty + 8 * i, share ? 2 : 1);
+            mbar_init(sempty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(s_free + 8 * i, 4);
         }
@@ -305,11 +304,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     for (int i = 0; i < sn; ++i) {
                         if (bits_of(i) == 0ull)
                             continue;
-                        if (share || (z & 1) == grp) {
+                        if ((z & 1) == grp) {
                             const int slot = CONV ? z % L.nstaged : st;
                             const uint32_t k = uniform(desc_low(base + (CONV ? L.staged + slot * kTile16 : L.ring + slot * TB), 16));
                             wait(CONV ? sfull + 8 * slot : full + 8 * st, CONV ? (uint32_t)(z / L.nstaged) & 1u : ph);
-                            for (int c = share ? 128 * grp : 0; c < ncols; c += share ? 256 : 128, ++item) {
+                            for (int c = 0; c < ncols; c += 128, ++item) {
                                 const uint32_t d = tm + uniform(128 * (item & 1u)), b = q + uniform(c * 128 >> 4);
                                 const uint32_t id = uniform(idesc | (uint32_t)(min(128, ncols - c) >> 3) << 17);
                                 if (item >= 2)
@@ -369,10 +368,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 };
                 for (int i = me; i < qpad; i += 256) {
                     const float e = q0 + i < rows ? p.lse[source(i)] : inf;
-                    float *info = reinterpret_cast<float *>(cols + (i >> 1)) + (i & 1);
-                    if (FMT == kFmtBf16)
-                        info[0] = p.scale_log2;
-                    info[2] = e == -inf ? -inf : e * -1.4426950408889634f;
+                    reinterpret_cast<float *>(cols)[FMT == kFmtBf16 ? i : (i >> 1) * 4 + 2 + (i & 1)] = e == -inf ? -inf : e * -1.4426950408889634f;
                     tok[i] = (uint8_t)(min(q0 + i, rows - 1) / p.G);
                 }
                 stage_rows<FMT == kFmtBf16 ? kRows16 : PAIR ? kRowsPair : kRowsF16>(
@@ -415,11 +411,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                         const unsigned long long bits = bits_of(i);
                         if (bits == 0ull)
                             continue;
-                        if (z++, !share && ((z - 1) & 1) != grp)
+                        if ((z++ & 1) != grp)
                             continue;
                         const int at = (sb + i) * kPage + mine;
                         float old = 0.f;
-                        if ((!share || grp == 0) && (q0 > 0 ? at < cached : src && at < w.seq_len - 1))
+                        if (q0 > 0 ? at < cached : src && at < w.seq_len - 1)
                             old = src[wrow + at];
                         const bool whole_page = (sb + i + 1) * kPage <= w.seq_len, part = sparse || !whole_page;
                         uint64_t sum[2] = {0ull, 0ull};
@@ -428,10 +424,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                         auto add_rows = [&](auto partly, int col, const uint32_t *v) {
                             constexpr int ROWS = PAIR ? 16 : 32;
                             const int row0 = PAIR ? col >> 1 : col;
-                            const float4 *info = cols + (row0 >> 1);
+                            const float4 *info = cols + (row0 >> (FMT == kFmtBf16 ? 2 : 1));
+                            const uint64_t same = pair(p.scale_log2, p.scale_log2);
 #pragma unroll
                             for (int k = 0; k < ROWS / 2; ++k) {
-                                const float4 f = info[k];
+                                const float4 f = info[FMT == kFmtBf16 ? k >> 1 : k];
+                                const uint64_t scales = FMT == kFmtBf16 ? same : pair(f.x, f.y);
+                                const uint64_t minus = FMT == kFmtBf16 && k % 2 == 0 ? pair(f.x, f.y) : pair(f.z, f.w);
                                 uint64_t x;
                                 if (PAIR)
                                     x = add2(pair(__uint_as_float(v[(4 * k) & 31]), __uint_as_float(v[(4 * k + 2) & 31])),
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                                 else
                                     x = pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
                                 float e0, e1;
-                                unpair(fma2(x, pair(f.x, f.y), pair(f.z, f.w)), e0, e1);
+                                unpair(fma2(x, scales, minus), e0, e1);
                                 e0 = ex2(e0);
                                 e1 = ex2(e1);
                                 if (partly.value) { // a token counts where it looked at this block and sees the position
@@ -451,12 +450,34 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             }
                         };
                         auto add_page = [&](auto partly) {
-                            for (int c0 = share ? 128 * grp : 0; c0 < ncols; c0 += share ? 256 : 128, ++item) {
+                            for (int c0 = 0; c0 < ncols; c0 += 128, ++item) {
                                 const int cn = min(128, ncols - c0);
                                 wait(s_full + 16 * grp + 8 * (item & 1u), (item >> 1) & 1u);
                                 tcgen05_after_sync();
                                 const uint32_t s_buf = s_at + 128 * (item & 1u);
-                                uint32_t v[32]; // (a second one, loaded meanwhile, measured no faster)
+                                // whole buffers: the next 32 columns are loaded meanwhile (243 -> 228 us at
+                                // 512 rows; the instances with converters have no registers for it)
+                                if (!CONV && !partly.value && cn == 128) {
+                                    uint32_t v2[2][32];
+                                    tmem_ld32(s_buf, v2[0]);
+                                    tmem_wait_ld(v2[0]);
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) {
+                                        if (c < 3) {
+                                            tmem_ld32(s_buf + 32 * (c + 1), v2[(c + 1) & 1]);
+                                        } else {
+                                            tcgen05_before_sync();
+                                            __syncwarp();
+                                            if (lane == 0)
+                                                mbar_arrive(s_free + 16 * grp + 8 * (item & 1u));
+                                        }
+                                        add_rows(std::false_type{}, c0 + 32 * c, v2[c & 1]);
+                                        if (c < 3)
+                                            tmem_wait_ld(v2[(c + 1) & 1]);
+                                    }
+                                    continue;
+                                }
+                                uint32_t v[32];
 #pragma unroll 1
                                 for (int c = 0; c < cn; c += 32) {
                                     bool all = false;
@@ -488,16 +509,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             add_page(std::false_type{});
                         float a, b;
                         unpair(add2(sum[0], sum[1]), a, b);
-                        if (share) { // (the next barrier comes before this buffer is written again)
-                            float *sums = reinterpret_cast<float *>(gsm + L.sums) + (z & 1) * 128 + mine;
-                            if (grp == 1)
-                                *sums = a + b;
-                            asm volatile("bar.sync 2, 256;" ::: "memory");
-                            if (grp == 1)
-                                continue;
-                            a += b;
-                            b = *sums;
-                        }
                         if (at < cached)
                             p.weights_out[wrow + at] = (q0 > 0 ? old : old * p.decay) + (a + b);
                     }
