@@ -9,14 +9,19 @@
 // when m rises.  The nq * G query rows of a (request, KV head) share every
 // page that is read.  This file has the kernel for up to 16 rows (one token of 16
 // heads, two of 8, ...), the join of cut units and the launch; more rows go to
-// the tcgen05 kernel of msa_dense_umma.cu.
+// the tcgen05 kernel of msa_dense_umma.cu.  With 16 rows that kernel multiplies eight
+// times as many and widens every E4M3 tile: 352 us for 198 here (48 E4M3 contexts,
+// 1.1 GB), 41.9 for 37.5 (8 heads, 165 MB of bf16), 16.4 for 11.7 (one context of 4096
+// positions); with two row tiles here, 32 rows took 121 us for 70 there (349 MB).
 //
 // What bounds it: the bytes of the pages (16 heads: 16 flop a byte of bf16 K/V),
 // so the kernel is a ring of whole pages fed by TMA, with as much in flight as
 // shared memory holds (192 KiB an SM), and mma.sync (m16n8k16: 16 rows are one
 // tile, no accumulator leaves the registers), whose work hides behind the copies:
-// 5.65 TB/s over 1.1 GB of E4M3 pages (48 requests, 196 us), 4.9 TB/s over 165 MB of
-// bf16 pages (8 heads, 34 us with the join).
+// 5.6 TB/s over 1.1 GB of E4M3 pages (48 requests, 198 us), 4.4 TB/s over 165 MB of
+// bf16 pages (8 heads, 37 us with the join), 7.1 TB/s over 5.1 GB in units of 1024
+// pages.  A unit costs some 4 us of each CTA besides its pages (query rows, the sum over
+// warps, outputs): 6.6 TB/s with units of 128 pages.
 //
 // Work split: the pages of all (request, KV head, row tile) units in one line,
 // cut into equal ranges, one per persistent CTA.  A unit inside one range is

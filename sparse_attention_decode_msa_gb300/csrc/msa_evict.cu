@@ -9,8 +9,9 @@
 // as the block select's reduction is); with more, one list per KV head.
 //
 // Select: comparisons only, so bit-exact.  One CTA per list where the table
-// holds at most 8192 positions, else a cluster of 8, each CTA with an eighth of the
-// positions, whose order-preserving 32-bit keys stay in shared memory (up to
+// holds at most 8192 positions, else a cluster of 8 (a whole eviction of 8 x 2048
+// positions 13.9 us, 17.5 with clusters; of 2 x 4096 14.7 and 14.5; of 8 x 32768
+// 74 us with one CTA a list, 47 with clusters), each CTA with an eighth of the positions, whose order-preserving 32-bit keys stay in shared memory (up to
 // 40960 a CTA; longer slices read the weights again).  Four 8-bit digits from the
 // top give the keep-th largest key: the CTAs read one another's histograms (256
 // words; with 11-bit digits their reading took as long as all the rest of a digit)
@@ -19,9 +20,14 @@
 // histogram, by lane, keep a warp's increments of one word apart.  Prefix counts in
 // position order then give each kept position its place.
 //
-// Copy: 128 (short lists: 32) kept positions per CTA; every row is 16-byte pieces,
-// eight loads in flight per thread over K, V and index-key rows alike.  Rows go to pages of their own (new_table), so pages
+// Copy: 128 kept positions per CTA, or 32 where that leaves fewer CTAs than two per SM
+// (1024 positions cut to 512: 10.2 us for 15.6; 32 lists of 65536 positions: 168 us with
+// 32, 123 with 128); every row is 16-byte pieces, eight loads in flight per thread over
+// K, V and index-key rows alike.  Rows go to pages of their own (new_table), so pages
 // that other requests share stay as they are and no copy waits for another.
+//
+// What bounds it: HBM for long lists (507 MB copied in 94 us, 5.4 TB/s), the chain of
+// four digits before the copy (29 of 123 us), launch latency for short ones.
 #include "msa_cache.cuh"
 
 namespace msa {
@@ -426,7 +432,7 @@ cudaError_t launch_cache_evict(const EvictParams &p, cudaStream_t stream)
     cudaError_t e = p.maxB * kPage <= 8192 ? launch_select_t<1>(p, stream) : launch_select_t<kCluster>(p, stream);
     if (e != cudaSuccess)
         return e;
-    // short lists in more, smaller CTAs
+    // short lists in more, smaller CTAs (both measured: see the top)
     const int lists = p.R * p.Hs;
     if ((long long)lists * ((p.keep + 127) / 128) >= 304)
         e = launch_kernel(evict_copy_kernel<128>, dim3(lists, (p.keep + 127) / 128), dim3(kCopyThreads), 0, stream, true, p);
