@@ -213,40 +213,24 @@ __device__ __forceinline__ void stage_rows(uint8_t *dst, int half, int n, int wi
     }
 }
 
-// One row of an E4M3 or NVFP4 tile as the TMA lands it, widened to f16 in the
-// layout of a 16-bit tile (two halves of 64 dimensions, 128-byte swizzle).
-template <int FMT>
+// One row of an NVFP4 tile as the TMA lands it, widened to f16 in the layout of a
+// 16-bit tile (two halves of 64 dimensions, 128-byte swizzle).
 __device__ __forceinline__ void widen_row(const uint8_t *src, uint8_t *tile, int row)
 {
     uint8_t *dst = tile + row * 128;
-    if (FMT == kFmtFp8) {
+    const uint64_t sc = *reinterpret_cast<const uint64_t *>(src + 8192 + row * 8);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) { // 16 dimensions
-            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
-            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
-            uint32_t o[8];
+    for (int c = 0; c < 4; ++c) { // 32 dimensions, two scales
+        const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+        const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+        const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)(sc >> (16 * c)) & 0xFFFFu);
+        const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+        uint8_t *at = dst + (c >> 1) * 16384;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                e4m3x4_to_f16x2x2(e[q], o[2 * q], o[2 * q + 1]);
-            uint8_t *at = dst + (c >> 2) * 16384;
-            *reinterpret_cast<uint4 *>(at + (((2 * c) & 7) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(at + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-    } else {
-        const uint64_t sc = *reinterpret_cast<const uint64_t *>(src + 8192 + row * 8);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) { // 32 dimensions, two scales
-            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
-            const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)(sc >> (16 * c)) & 0xFFFFu);
-            const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
-            uint8_t *at = dst + (c >> 1) * 16384;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t o[4];
-                e2m1x8_scaled_f16x2(e[q], q < 2 ? sa : sb, o);
-                *reinterpret_cast<uint4 *>(at + ((((c & 1) * 4 + q) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+        for (int q = 0; q < 4; ++q) {
+            uint32_t o[4];
+            e2m1x8_scaled_f16x2(e[q], q < 2 ? sa : sb, o);
+            *reinterpret_cast<uint4 *>(at + ((((c & 1) * 4 + q) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }

@@ -13,13 +13,12 @@
 // thread's own columns, and a warp reads and writes 32 consecutive weights.  No
 // exchange between threads, no atomics; rows are added in a fixed order.
 //
-// bf16 keys are operands as they land.  So are E4M3 keys with up to 64 query rows:
-// each bf16 query row then is two columns, an E4M3 pair hi + lo after a power of
-// two that brings its largest element near 448.  The pair carries bf16's 8 bits for
-// elements down to 2^-14 of the row's largest and is at most 2^-19 of that off below.
-// With more rows, and for NVFP4 keys, converter warps widen K to f16.  (One token over
-// 0.59 GB of E4M3 keys: 116 us, 5.1 TB/s; 153 us widened.  More than 64 rows as pairs would
-// be more than the 128 columns of a buffer, and twice the work of the tensor cores.)
+// bf16 keys are operands as they land, and so are E4M3 keys: each bf16 query row then is
+// two columns, an E4M3 pair hi + lo after a power of two that brings its largest element
+// near 448.  The pair carries bf16's 8 bits for elements down to 2^-14 of the row's largest
+// and is at most 2^-19 of that off below.  (One token over 0.59 GB of E4M3 keys: 116 us,
+// 5.1 TB/s; 153 us with keys widened to f16.  8 tokens over 64 x 32768 positions: 109 us
+// for 133, 16 tokens 189 for 209.)  NVFP4 keys are widened to f16 by converter warps.
 //
 // What bounds it: the bytes of K and of the weights with few rows; with many the chain
 // of MMA, load from tensor memory and exponentials of a buffer, and that few K tiles fit
@@ -28,8 +27,8 @@
 // where keys are widened, four converter warps each) share the work, so that one's
 // waits pass behind the other's work: each takes every second page, 128 accumulator
 // columns at a time in two buffers (both groups on every page, with half of the columns
-// each, was 5 .. 25% slower).  The query rows of a (request, KV head), up to 512 (bf16) or 256 at a
-// time, stay in shared memory.
+// each, was 5 .. 25% slower).  The query rows of a (request, KV head), up to 512 (NVFP4:
+// 256) at a time, stay in shared memory.
 //
 // After a sparse step only pages that some token of the request selected are
 // read; a bitmap of 64 token bits per page, built in shared memory, says which
@@ -49,34 +48,21 @@ constexpr int kTile16 = 32768;     // a 16-bit K tile
 constexpr int kMaxRing = 16;
 constexpr int kSmemMax = 232192;   // what the layouts below stay under (232448 with the static part)
 
-// Key formats of the kernel instances: as stored, or (kFmtPair) E4M3 keys as operands.
-constexpr int kFmtPair = 3;
-
-__host__ __device__ constexpr int stored_fmt(int fmt)
-{
-    return fmt == kFmtPair ? kFmtFp8 : fmt;
-}
-
-__host__ __device__ constexpr bool widened(int fmt)
-{
-    return fmt == kFmtFp8 || fmt == kFmtF4;
-}
-
 __host__ __device__ constexpr int threads_of(int fmt)
 {
-    return widened(fmt) ? 640 : 384;
+    return fmt == kFmtF4 ? 640 : 384;
 }
 
-// Query rows in shared memory at a time (E4M3 and NVFP4 keys need staged tiles besides).
+// Query rows in shared memory at a time (NVFP4 keys need staged tiles besides).
 __host__ __device__ constexpr int query_rows(int fmt)
 {
-    return fmt == kFmtBf16 ? 512 : fmt == kFmtPair ? 64 : 256;
+    return fmt == kFmtF4 ? 256 : 512;
 }
 
 // Rows held are padded to whole loads of 32 accumulator columns.
 __host__ __device__ constexpr int padded(int fmt, int rows)
 {
-    return fmt == kFmtPair ? (rows + 15) / 16 * 16 : (rows + 31) / 32 * 32;
+    return fmt == kFmtFp8 ? (rows + 15) / 16 * 16 : (rows + 31) / 32 * 32;
 }
 
 // Shared memory by the query rows held: the rest is the ring
@@ -92,14 +78,14 @@ __host__ __device__ inline Smem smem_layout(int fmt, int qpad, bool masks)
     Smem s{};
     const int rest = qpad * (256 + 8 + 1) + (masks ? 2 * kPagesAtATime * 8 : 0) + (2 * kMaxRing + 32) * 8 + 64 + 1024 + 256;
     int room = 232448 - rest;
-    s.nstaged = !widened(fmt) ? 0 : room >= 6 * kTile16 ? 4 : 2;
+    s.nstaged = fmt != kFmtF4 ? 0 : room >= 6 * kTile16 ? 4 : 2;
     room -= s.nstaged * kTile16;
-    s.depth = room / tile_bytes(stored_fmt(fmt)) / 2 * 2;
+    s.depth = room / tile_bytes(fmt) / 2 * 2;
     s.depth = s.depth > kMaxRing ? kMaxRing : s.depth;
     s.staged = 0;
     s.q = s.nstaged * kTile16;
     s.ring = s.q + qpad * 256;
-    s.cols = s.ring + s.depth * tile_bytes(stored_fmt(fmt));
+    s.cols = s.ring + s.depth * tile_bytes(fmt);
     s.tok = s.cols + qpad * 8;
     s.mask = (s.tok + qpad + 15) / 16 * 16;
     s.bars = s.mask + (masks ? 2 * kPagesAtATime * 8 : 0);
@@ -112,8 +98,8 @@ template <int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
     weight_kernel(const __grid_constant__ CUtensorMap map, const WeightParams p, const Smem L)
 {
-    constexpr int TB = tile_bytes(stored_fmt(FMT)), NT = threads_of(FMT);
-    constexpr bool CONV = widened(FMT), PAIR = FMT == kFmtPair;
+    constexpr int TB = tile_bytes(FMT), NT = threads_of(FMT);
+    constexpr bool CONV = FMT == kFmtF4, PAIR = FMT == kFmtFp8;
     constexpr int kQRows = query_rows(FMT);
     extern __shared__ uint8_t smem_raw[];
     __shared__ int scan_tmp[NT / 32 + 1];
@@ -277,7 +263,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                                 continue;
                             if (lane == 0) {
                                 mbar_arrive_expect_tx(full + 8 * st, TB);
-                                load_tile<stored_fmt(FMT)>(smem + L.ring + st * TB, &map, p.kv, (page * 2) * p.Hkv + g, full + 8 * st);
+                                load_tile<FMT>(smem + L.ring + st * TB, &map, p.kv, (page * 2) * p.Hkv + g, full + 8 * st);
                             }
                             __syncwarp();
                             next_tile();
@@ -537,7 +523,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                             wait(full + 8 * st, ph);
                             if (z >= L.nstaged)
                                 wait(sempty + 8 * slot, (uint32_t)(z / L.nstaged - 1) & 1u);
-                            widen_row<FMT>(gsm + L.ring + st * TB, gsm + L.staged + slot * kTile16, row);
+                            widen_row(gsm + L.ring + st * TB, gsm + L.staged + slot * kTile16, row);
                             fence_async_smem();
                             __syncwarp();
                             if (lane == 0) {
@@ -583,8 +569,8 @@ cudaError_t launch_weight_accumulate(const WeightParams &p, int kv_dtype, int ct
         return cudaErrorInvalidValue;
     if (kv_dtype == MSA_BF16)
         return launch_t<kFmtBf16>(p, map, ctas, stream);
-    if (kv_dtype == MSA_FP8_E4M3) // (both measured: see the top)
-        return p.nq * p.G <= query_rows(kFmtPair) ? launch_t<kFmtPair>(p, map, ctas, stream) : launch_t<kFmtFp8>(p, map, ctas, stream);
+    if (kv_dtype == MSA_FP8_E4M3)
+        return launch_t<kFmtFp8>(p, map, ctas, stream);
     return launch_t<kFmtF4>(p, map, ctas, stream);
 }
 
