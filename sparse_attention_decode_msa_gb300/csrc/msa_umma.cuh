@@ -140,8 +140,9 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b)
 //   kRows16   bf16 as they are (half of the dimensions `half` bytes after the other)
 //   kRowsF16  f16: each row scaled by a power of two that brings its largest element to
 //             [2^8, 2^9) (exact; elements 2^-23 below it lose bits)
-//   kRowsPair E4M3 pairs hi, lo in rows 2 i, 2 i + 1, after a power of two that brings the
-//             row's largest element near 448
+//   kRowsPair E4M3 pairs hi, 16 lo in rows 2 i, 2 i + 1 (lo = what rounding to hi left, at
+//             most 16 itself), after a power of two that brings the row's largest element
+//             to (224, 448]
 // inverse(i, x) is told the factor that undoes the scaling (one lane of the row).
 constexpr int kRows16 = 0, kRowsF16 = 1, kRowsPair = 2;
 
@@ -194,7 +195,7 @@ __device__ __forceinline__ void stage_rows(uint8_t *dst, int half, int n, int wi
                         float ha, hb;
                         f16x2_to_f32x2(e4m3x2_to_f16x2(h), ha, hb);
                         hi[k >> 1] |= h << (16 * (k & 1));
-                        lo[k >> 1] |= to_e4m3x2(a - ha, b - hb) << (16 * (k & 1));
+                        lo[k >> 1] |= to_e4m3x2(16.f * (a - ha), 16.f * (b - hb)) << (16 * (k & 1));
                     }
                     if (i < n) {
                         uint8_t *at = dst + 256 * i + (c & 1) * 8;

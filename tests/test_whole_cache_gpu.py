@@ -400,14 +400,14 @@ def test_page_offsets_beyond_32_bits(torch_cuda):
 # ---------------------------------------------------------------------------
 # accumulated weights
 
-def check_weights(c, got, lse, before, decay, selected, after=None):
+def check_weights(c, got, lse, before, decay, selected, after=None, extra=0.0):
     lse = lse.double().cpu().numpy()
     got = got.double().cpu().numpy()
     host = lambda x: None if x is None else x.cpu().numpy()  # noqa: E731
     want = ref.weights(c.pb, c.q, lse, host(before), decay, host(selected), after=got)
     _, _, S, _ = ref.dense_decode(c.pb, c.q)
     top = np.abs(lse[np.isfinite(lse)]).max(initial=0)
-    rel = logit_error(S, S) + 2.0 ** -22 + 2.0 ** -22 * (1 + top) + c.nq * c.G * 2.0 ** -24 + 2.0 ** -23
+    rel = logit_error(S, S) + extra + 2.0 ** -22 + 2.0 ** -22 * (1 + top) + c.nq * c.G * 2.0 ** -24 + 2.0 ** -23
     # below 2^-126 the hardware exponential gives 0
     assert np.all(np.abs(got - want) <= rel * np.abs(want) + c.nq * c.G * 2.0 ** -126), np.abs(got - want).max()
     assert c.status() == msa.MSA_OK
@@ -438,6 +438,21 @@ def test_weights_after_a_dense_step(torch_cuda, kv, contexts, nq, Hkv, G, decay)
         c.accumulate(c.lse, None, got)
         total = sum(float(got[r, :, :n].double().sum()) for r, n in enumerate(contexts))
         assert abs(total / (len(contexts) * nq * G * Hkv) - 1) < 1e-4
+
+
+@pytest.mark.parametrize("nq", [1, 9])
+def test_weights_of_queries_with_a_large_element_that_meets_zeros(torch_cuda, nq):
+    # E4M3 keys take each query as an E4M3 pair, off by at most 2^-21.8 of the row's largest
+    # element: as much as Sum |k| of that more in a logit (the others' elements are 2^-12 of it)
+    c = Cache([700, 129 + nq], nq, 2, 16, "fp8", seed=47)
+    c.pb.kv_pool[:, 0, :, :, 5] = 0
+    c.q[..., 5] = synth.f32_to_bf16_bits(np.full(c.q.shape[:2], 4096.0, np.float32))
+    c.upload()
+    c.decode()
+    got = c.torch.full((2, 2, c.pb.max_blocks * 128), -3.0, device="cuda")
+    c.accumulate(c.lse, None, got)
+    _, _, S, _ = ref.dense_decode(c.pb, synth.f32_to_bf16_bits(np.full(c.q.shape, 4096.0, np.float32)))
+    check_weights(c, got, c.lse, None, 1.0, None, extra=2.0 ** -21.8 * np.max(S))
 
 
 @pytest.mark.parametrize("kv", KV)
