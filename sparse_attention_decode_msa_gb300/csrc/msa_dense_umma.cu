@@ -32,7 +32,7 @@
 // 128 (s & 1) + 64 t), O of stream t at 256 + 128 t.
 // Warps: 0 TMA producer (and outputs of idle slots), 1 issues S (and owns the TMEM),
 // 2 and 3 issue P V of stream 0 and 1, 4-7 and 8-11 softmax of stream 0 and 1,
-// 12-15 and 16-19 converters (E4M3, NVFP4).
+// 12-15 (and 16-19) converters (E4M3, NVFP4).
 //
 // What bounds it: the tensor cores when rows are many (measured: an MMA of
 // 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50 as both read 4 KiB
@@ -48,18 +48,26 @@ namespace msa {
 namespace {
 
 constexpr int kTile16 = 32768;   // a 16-bit K, V or Q tile
-constexpr int kConvWarps = 8;     // two groups of four, taking the tiles in turn
 constexpr int kStaged = 4;       // widened tiles in flight
 constexpr float kSlack = 8.f;    // how far (log2) a row's maximum may pass its reference before O is rescaled
 constexpr float kPUp16 = 7.f;    // f16 P: 2^7 2^(s - m), at most 2^15 with the slack
 
-__host__ __device__ constexpr int threads_of(int fmt)
+// Groups of four converter warps, which take the tiles in turn.  With one row tile two of
+// them (488 us for 545 on 32 requests of 2 tokens over 65536 NVFP4 positions); with two,
+// whose tiles have more to multiply, the second would only take registers from the softmax
+// (48 tokens over 2 x 131072: 424 us for 438, E4M3, and 412 for 433, NVFP4).
+__host__ __device__ constexpr int conv_groups(int fmt, bool two)
 {
-    return fmt == kFmtBf16 ? 384 : 384 + 32 * kConvWarps;
+    return fmt == kFmtBf16 ? 0 : two ? 1 : 2;
 }
 
-// Tiles (K or V) in the ring: an even number where converters widen them (a slot
-// belongs to one converter group, which follows all of its barriers' phases).
+__host__ __device__ constexpr int threads_of(int fmt, bool two)
+{
+    return 384 + 128 * conv_groups(fmt, two);
+}
+
+// Tiles (K or V) in the ring: an even number where two converter groups widen them (a slot
+// belongs to one group, which follows all of its barriers' phases).
 __host__ __device__ constexpr int ring_tiles(int fmt, bool two)
 {
     return fmt == kFmtBf16 ? (two ? 5 : 6) : fmt == kFmtFp8 ? (two ? 2 : 4) : (two ? 2 : 6);
@@ -158,10 +166,10 @@ __device__ __forceinline__ int order_of_v(int page, int n)
 }
 
 template <int FMT, bool TWO>
-__global__ void __launch_bounds__(threads_of(FMT), 1)
+__global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
     dense_umma_kernel(const __grid_constant__ CUtensorMap map, const DenseParams p)
 {
-    constexpr int TILES = ring_tiles(FMT, TWO), TB = tile_bytes(FMT), NT = threads_of(FMT);
+    constexpr int TILES = ring_tiles(FMT, TWO), TB = tile_bytes(FMT), NT = threads_of(FMT, TWO);
     constexpr bool CONV = FMT != kFmtBf16;
     constexpr int ROWS = TWO ? 256 : 128;
     constexpr Smem L = smem_layout(FMT, TWO);
@@ -507,10 +515,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     continue;
                 }
                 tcgen05_after_sync();
-                // the extreme logit of the row (the scale's sign says which end).  bf16: the
-                // 64 columns stay in registers; the widening instances have fewer registers
-                // a thread and keep columns 0 .. 31, the others are read again
-                constexpr int HELD = CONV ? 32 : 64;
+                // the extreme logit of the row (the scale's sign says which end).  The 64
+                // columns stay in registers; with two converter groups a thread has fewer of
+                // those, keeps columns 0 .. 31 and reads the others again
+                constexpr int HELD = conv_groups(FMT, TWO) == 2 ? 32 : 64;
                 uint32_t v[HELD];
                 const bool neg = sc < 0.f;
                 float mx = neg ? -ninf : ninf;
@@ -574,11 +582,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) { // 32 columns of S become P
-                    if (CONV && c == 1) {
+                    if (HELD == 32 && c == 1) {
                         tmem_ld32(at_s + 32, v);
                         tmem_wait_ld(v);
                     }
-                    const uint32_t *x = v + (CONV ? 0 : 32 * c);
+                    const uint32_t *x = v + (HELD == 32 ? 0 : 32 * c);
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -781,7 +789,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (int i = 0; i < 2 * n; ++i, ++z) {
                 const bool is_k = kp < n && order_of_k<TWO>(kp) == i;
                 const int page0 = (w.b + (is_k ? kp++ : vp++)) * kPage;
-                if ((z & 1) != grp)
+                if (conv_groups(FMT, TWO) == 2 && (z & 1) != grp)
                     continue;
                 const bool tail = !is_k && page0 + kPage > w.seq_len;
                 const bool drop = tail && page0 + row >= cached;              // not cached
@@ -869,7 +877,7 @@ cudaError_t launch_t(const DenseParams &p, const CUtensorMap &map, int ctas, cud
     cudaError_t e = cudaFuncSetAttribute(dense_umma_kernel<FMT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
-    e = launch_kernel(dense_umma_kernel<FMT, TWO>, dim3(ctas), dim3(threads_of(FMT)), smem, stream, false, map, p);
+    e = launch_kernel(dense_umma_kernel<FMT, TWO>, dim3(ctas), dim3(threads_of(FMT, TWO)), smem, stream, false, map, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
