@@ -16,19 +16,19 @@
 // bf16 keys are operands as they land, and so are E4M3 keys: each bf16 query row then is
 // two columns, an E4M3 pair hi + lo / 16 after a power of two that brings its largest
 // element to (224, 448].  The pair is exact for elements of 2^-6 or more, 2^-13.8 of the
-// row's largest, and off by at most 2^-14, 2^-21.8 of the largest, below.  (One token over 0.59 GB of E4M3 keys: 116 us,
-// 5.1 TB/s; 153 us with keys widened to f16.  8 tokens over 64 x 32768 positions: 109 us
-// for 133, 16 tokens 189 for 209.)  NVFP4 keys are widened to f16 by converter warps.
+// row's largest, and off by at most 2^-14, 2^-21.8 of the largest, below.  (One token over
+// 0.59 GB of E4M3 keys: 116 us, 5.1 TB/s; 153 us with keys widened to f16.  8 tokens over
+// 64 x 32768 positions: 109 us for 133, 16 tokens 189 for 209.)  NVFP4 keys are widened to
+// f16 by converter warps.
 //
 // What bounds it: the bytes of K and of the weights with few rows; with many the chain
 // of MMA, load from tensor memory and exponentials of a buffer, and that few K tiles fit
 // beside the query rows (32 tokens over 2 x 32768 bf16 positions: 46 us, 0.74 PFLOP/s).
-// Two groups (an MMA issuer, four softmax warps and,
-// where keys are widened, four converter warps each) share the work, so that one's
-// waits pass behind the other's work: each takes every second page, 128 accumulator
-// columns at a time in two buffers (both groups on every page, with half of the columns
-// each, was 5 .. 25% slower).  The query rows of a (request, KV head), up to 512 (NVFP4:
-// 256) at a time, stay in shared memory.
+// Two groups (an MMA issuer, four softmax warps and, where keys are widened, four
+// converter warps each) share the work, so that one's waits pass behind the other's work:
+// each takes every second page, 128 accumulator columns at a time in two buffers (both
+// groups on every page, with half of the columns each, was 5 .. 25% slower).  The query
+// rows of a (request, KV head), up to 512 (NVFP4: 256) at a time, stay in shared memory.
 //
 // After a sparse step only pages that some token of the request selected are
 // read; a bitmap of 64 token bits per page, built in shared memory, says which

@@ -107,6 +107,19 @@ class DeviceProblem:
                         self.out, self.lse, self.ws, self.ws_bytes, stream)
 
     # ---- the whole cache ----
+    @staticmethod
+    def _on(stream):
+        """The stream as the current one: what a call allocates and fills is ordered with its kernels."""
+        import contextlib
+
+        import torch
+
+        if stream is None:
+            return contextlib.nullcontext()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        return torch.cuda.stream(stream)
+
     def _cache_workspace(self):
         import torch
 
@@ -118,15 +131,17 @@ class DeviceProblem:
 
     def dense_decode(self, stream=None):
         """Attention over every cached position, into out and lse."""
-        msa_dense_decode(self.shape, self.q, self.kv, self.block_table, self.seq_lens, self.out,
-                         self.lse, *self._cache_workspace(), stream)
+        with self._on(stream):
+            msa_dense_decode(self.shape, self.q, self.kv, self.block_table, self.seq_lens, self.out,
+                             self.lse, *self._cache_workspace())
 
     def weight_accumulate(self, weights_in, weights_out, decay: float = 1.0, sparse: bool = False,
                           stream=None):
         """Add the weights of the step whose lse this problem holds (sparse: of its selection)."""
-        msa_weight_accumulate(self.shape, self.q, self.kv, self.block_table, self.seq_lens,
-                              self.selected if sparse else None, self.lse, decay, weights_in,
-                              weights_out, *self._cache_workspace(), stream)
+        with self._on(stream):
+            msa_weight_accumulate(self.shape, self.q, self.kv, self.block_table, self.seq_lens,
+                                  self.selected if sparse else None, self.lse, decay, weights_in,
+                                  weights_out, *self._cache_workspace())
 
     def evict(self, weights, new_table, keep: int, first: int = 0, last: int = 0, stream=None) -> dict:
         """Copy the kept positions to new_table's pages; the lists, lengths and weights of the
@@ -135,12 +150,13 @@ class DeviceProblem:
 
         R, Hkv = self.shape.num_requests, self.shape.num_kv_heads
         Hs = 1 if self.shape.num_index_heads == 1 else Hkv
-        kept = torch.empty((R, Hs, keep), dtype=torch.int32, device=self.device)
-        lens = torch.empty(R, dtype=torch.int32, device=self.device)
-        new_weights = torch.zeros((R, Hkv, -(-keep // 128) * 128), device=self.device)
-        msa_cache_evict(self.shape, keep, first, last, weights, self.block_table, self.seq_lens,
-                        new_table, self.kv, self.idxk, self.idxk_scales, new_weights, kept, lens,
-                        *self._cache_workspace(), stream)
+        with self._on(stream):
+            kept = torch.empty((R, Hs, keep), dtype=torch.int32, device=self.device)
+            lens = torch.empty(R, dtype=torch.int32, device=self.device)
+            new_weights = torch.zeros((R, Hkv, -(-keep // 128) * 128), device=self.device)
+            msa_cache_evict(self.shape, keep, first, last, weights, self.block_table, self.seq_lens,
+                            new_table, self.kv, self.idxk, self.idxk_scales, new_weights, kept, lens,
+                            *self._cache_workspace())
         return {"kept": kept, "seq_lens": lens, "weights": new_weights}
 
     def kv_update(self, update: dict, stream=None):

@@ -588,6 +588,35 @@ def test_evict_reports_bad_pages_and_writes_no_others(torch_cuda):
     assert torch.equal(before, c.kv)
 
 
+@pytest.mark.parametrize("as_int", [False, True])
+def test_problem_methods_on_a_stream_beside_a_busy_one(torch_cuda, as_int):
+    # what the methods allocate and fill belongs to the stream that is asked for
+    from sparse_attention_decode_msa_gb300.runner import DeviceProblem
+
+    torch = torch_cuda
+    pb = synth.make_problem(name="side", contexts=[600, 301], q_per_req=1, num_kv_heads=2, topk=4, seed=62, num_pages=16)
+    dp = DeviceProblem(pb)
+    free = [p for p in range(pb.num_pages) if p not in set(pb.block_table[pb.block_table >= 0].tolist())]
+    table = torch.tensor(free[:4], dtype=torch.int32, device="cuda").reshape(2, 2)
+    w = torch.rand((2, 2, pb.max_blocks * 128), device="cuda")
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_int else side
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # about 50 ms on the current stream
+    dp.dense_decode(stream)
+    dp.weight_accumulate(w, w, stream=stream)
+    new = dp.evict(w, table, keep=200, last=1, stream=stream)
+    torch.cuda.synchronize()
+    out, lse, S, V = ref.dense_decode(pb, pb.q)
+    res = dp.results()
+    check_attention(res["out"], res["lse"], out, lse, S, V, 700)
+    kept = new["kept"].cpu().numpy()
+    assert np.array_equal(kept, ref.evict_lists(pb.seq_lens, 1, w.cpu().numpy(), 1, 200, 0, 1)[0])
+    got = np.take_along_axis(w.cpu().numpy(), np.broadcast_to(kept, (2, 2, 200)).astype(np.int64), 2)
+    assert np.array_equal(new["weights"].cpu().numpy()[:, :, :200], got)
+    assert msa.msa_check_device_status(dp.cache_ws) == msa.MSA_OK
+
+
 @pytest.mark.parametrize("kv", KV)
 def test_a_run_of_steps_with_eviction(torch_cuda, kv):
     """A cache is weighed by a prompt's last tokens, cut, and decoded on: update, attention, weights, each step."""
