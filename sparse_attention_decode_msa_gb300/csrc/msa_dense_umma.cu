@@ -42,6 +42,8 @@
 // S, maximum, exponentials, P V of a step is longer than its MMAs: tensor pipe 46%);
 // 4 tokens, 349 MB of bf16 pages 70 us, 5.0 TB/s; 2 tokens, 1.2 GB of NVFP4 pages 487 us,
 // 2.5 TB/s (the schedulers, which widen every tile and have the softmax as well).
+#include <type_traits>
+
 #include "msa_umma.cuh"
 
 namespace msa {
@@ -546,26 +548,26 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                 mx *= sc;
                 if (CONV)
                     mx -= kPUp16;
-                float f = 1.f;
-                if (mx > m + kSlack || (m == ninf && mx > ninf)) {
-                    f = ex2(m - mx);
-                    m = mx;
-                }
-                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                    product_wait(t, i - 1); // O holds every step before this one
-                    tcgen05_after_sync();
+                const bool rise = mx > m + kSlack || (m == ninf && mx > ninf);
+                if (__any_sync(0xffffffffu, rise)) { // rare, and so everything that it needs is in here
+                    const float f = rise ? ex2(m - mx) : 1.f;
+                    m = rise ? mx : m;
+                    l *= f;
+                    if (i > 0) {
+                        product_wait(t, i - 1); // O holds every step before this one
+                        tcgen05_after_sync();
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        float o[16];
-                        tmem_ld16(o_at + 16 * c, o);
-                        uint32_t r[16];
+                        for (int c = 0; c < 8; ++c) {
+                            float o[16];
+                            tmem_ld16(o_at + 16 * c, o);
+                            uint32_t r[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            r[k] = __float_as_uint(o[k] * f);
-                        tmem_st16(o_at + 16 * c, r);
+                            for (int k = 0; k < 16; ++k)
+                                r[k] = __float_as_uint(o[k] * f);
+                            tmem_st16(o_at + 16 * c, r);
+                        }
                     }
                 }
-                l *= f;
                 // lo matters where a single position weighs much: the rounding of P to bf16
                 // (2^-8 of p) is left in only for steps in which every p is under 1/64 of its
                 // row's denominator so far (see the top)
@@ -580,42 +582,50 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                 const float ref = m == ninf ? 0.f : m;
                 const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref), minus = pair(-1.f, -1.f);
                 uint64_t sum[2] = {0ull, 0ull};
+                // the common step by itself: with the tests for the others in its unrolled
+                // loop 48 tokens over 2 x 131072 positions took 414 us, without 387
+                auto to_p = [&](auto plain) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) { // 32 columns of S become P
-                    if (HELD == 32 && c == 1) {
-                        tmem_ld32(at_s + 32, v);
-                        tmem_wait_ld(v);
-                    }
-                    const uint32_t *x = v + (HELD == 32 ? 0 : 32 * c);
-                    uint32_t hi[16], lo[16];
+                    for (int c = 0; c < 2; ++c) { // 32 columns of S become P
+                        if (HELD == 32 && c == 1) {
+                            tmem_ld32(at_s + 32, v);
+                            tmem_wait_ld(v);
+                        }
+                        const uint32_t *x = v + (HELD == 32 ? 0 : 32 * c);
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int at = 32 * c + 2 * k;
-                        float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, ref2), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        if (tail) {
-                            e0 = at < seen ? e0 : 0.f;
-                            e1 = at + 1 < seen ? e1 : 0.f;
+                        for (int k = 0; k < 16; ++k) {
+                            const int at = 32 * c + 2 * k;
+                            float e0, e1;
+                            unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, ref2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            if (!plain.value && tail) {
+                                e0 = at < seen ? e0 : 0.f;
+                                e1 = at + 1 < seen ? e1 : 0.f;
+                            }
+                            const uint64_t e = pair(e0, e1);
+                            sum[k & 1] = add2(sum[k & 1], e);
+                            if (CONV) {
+                                hi[k] = pack_f16(e0, e1);
+                            } else {
+                                hi[k] = pack_bf16(e0, e1);
+                                if (plain.value || !lo_too)
+                                    continue;
+                                float d0, d1;
+                                unpair(fma2(pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u)), minus, e), d0, d1);
+                                lo[k] = pack_bf16(d0, d1);
+                            }
                         }
-                        const uint64_t e = pair(e0, e1);
-                        sum[k & 1] = add2(sum[k & 1], e);
-                        if (CONV) {
-                            hi[k] = pack_f16(e0, e1);
-                        } else {
-                            hi[k] = pack_bf16(e0, e1);
-                            if (!lo_too)
-                                continue;
-                            float d0, d1;
-                            unpair(fma2(pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u)), minus, e), d0, d1);
-                            lo[k] = pack_bf16(d0, d1);
-                        }
+                        tmem_st16(at_s + 16 * c, hi);
+                        if (!CONV && !plain.value && lo_too)
+                            tmem_st16(at_s + 32 + 16 * c, lo);
                     }
-                    tmem_st16(at_s + 16 * c, hi);
-                    if (!CONV && lo_too)
-                        tmem_st16(at_s + 32 + 16 * c, lo);
-                }
+                };
+                if (tail || lo_too)
+                    to_p(std::false_type{});
+                else
+                    to_p(std::true_type{});
                 {
                     float a, b;
                     unpair(add2(sum[0], sum[1]), a, b);
@@ -801,7 +811,7 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                 uint8_t *dst = gsm + L.staged + (z % kStaged) * kTile16 + row * 128;
                 bool bad = false;
                 if (FMT == kFmtFp8) {
-#pragma unroll
+#pragma unroll 2 // (all: 426 us for 413, 48 tokens over 2 x 131072; NVFP4 loses with less, 507 for 488)
                     for (int c = 0; c < 8; ++c) { // 16 dimensions
                         const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
                         uint32_t e[4] = {d.x, d.y, d.z, d.w}, o[8];
