@@ -12,13 +12,13 @@
 // ends.  With more than 128 query rows a (request, KV head), stream t has rows
 // 128 t .. of a 256-row tile and takes both halves of every page; with fewer,
 // both have the same rows, stream t takes half t of every page, and the two
-// (m, l, O) are added at the end.  With E4M3 and NVFP4
-// tiles up to 64 rows are in the operand tile twice, rows 0 .. for stream 0 and 64 ..
-// for stream 1: a softmax warp can read one quarter of the accumulator lanes only,
-// and so the streams' warps with rows in them sit on different schedulers (32
-// requests of 2 tokens over 65536 NVFP4 positions: 487 us, 559 without; bf16, whose
-// schedulers have no converters beside them, lost to the longer end of a unit:
-// 79 us for 70 on 8 requests of 4 tokens).
+// (m, l, O) are added at the end.  With NVFP4 tiles up to 64 rows are in the operand
+// tile twice (TWICE), rows 0 .. for stream 0 and 64 .. for stream 1: a softmax warp can
+// read one quarter of the accumulator lanes only, and so the streams' warps with rows in
+// them sit on different schedulers (32 requests of 2 tokens over 65536 positions: 456 us,
+// 495 without).  E4M3 and bf16 lose more to the longer end of a unit
+// than they gain: 143 us for 137, 2 tokens over 64 x 32768 E4M3 positions, 79 for 70 on 8
+// requests of 4 bf16 tokens.
 //
 // Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA
 // lands them (K-major), P in tensor memory over the S it came from, V tiles as
@@ -38,10 +38,10 @@
 // 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50 as both read 4 KiB
 // of Q from shared memory; a page of 128 rows is 16 of these for S, or 8 of those
 // with one row tile, and 8, or 16 with lo, of those for P V), HBM when they are few.
-// Measured: 48 tokens over 2 x 131072 bf16 positions 420 us, 0.98 PFLOP/s (the chain
-// S, maximum, exponentials, P V of a step is longer than its MMAs: tensor pipe 46%);
-// 4 tokens, 349 MB of bf16 pages 70 us, 5.0 TB/s; 2 tokens, 1.2 GB of NVFP4 pages 487 us,
-// 2.5 TB/s (the schedulers, which widen every tile and have the softmax as well).
+// Measured: 48 tokens over 2 x 131072 bf16 positions 393 us, 1.05 PFLOP/s (the chain
+// S, maximum, exponentials, P V of a step is longer than its MMAs: tensor pipe half busy);
+// 4 tokens, 349 MB of bf16 pages 70 us, 5.0 TB/s; 2 tokens, 1.2 GB of NVFP4 pages 456 us,
+// 2.65 TB/s (the schedulers, which widen every tile and have the softmax as well).
 #include <type_traits>
 
 #include "msa_umma.cuh"
@@ -55,7 +55,7 @@ constexpr float kSlack = 8.f;    // how far (log2) a row's maximum may pass its 
 constexpr float kPUp16 = 7.f;    // f16 P: 2^7 2^(s - m), at most 2^15 with the slack
 
 // Groups of four converter warps, which take the tiles in turn.  With one row tile two of
-// them (488 us for 545 on 32 requests of 2 tokens over 65536 NVFP4 positions); with two,
+// them (456 us for 572 on 32 requests of 2 tokens over 65536 NVFP4 positions); with two,
 // whose tiles have more to multiply, the second would only take registers from the softmax
 // (48 tokens over 2 x 131072: 424 us for 438, E4M3, and 412 for 433, NVFP4).
 __host__ __device__ constexpr int conv_groups(int fmt, bool two)
@@ -167,7 +167,7 @@ __device__ __forceinline__ int order_of_v(int page, int n)
     return TWO ? 2 * page + 1 : min(2 * page + 2, 2 * n - 1);
 }
 
-template <int FMT, bool TWO>
+template <int FMT, bool TWO, bool TWICE>
 __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
     dense_umma_kernel(const __grid_constant__ CUtensorMap map, const DenseParams p)
 {
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                          : "r"(3 + t)
                          : "memory");
         };
-        const bool twice = CONV && !TWO && p.rows <= 64;
+        constexpr bool twice = TWICE;
         const int lane0 = twice ? 64 * t : 0; // the stream's first accumulator lane
         float *qinv = reinterpret_cast<float *>(gsm + L.inv) + (TWO ? 128 * t : 0);
         auto sync_all = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
@@ -880,14 +880,14 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
     }
 }
 
-template <int FMT, bool TWO>
+template <int FMT, bool TWO, bool TWICE = false>
 cudaError_t launch_t(const DenseParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
 {
     constexpr int smem = smem_layout(FMT, TWO).total;
-    cudaError_t e = cudaFuncSetAttribute(dense_umma_kernel<FMT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(dense_umma_kernel<FMT, TWO, TWICE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
-    e = launch_kernel(dense_umma_kernel<FMT, TWO>, dim3(ctas), dim3(threads_of(FMT, TWO)), smem, stream, false, map, p);
+    e = launch_kernel(dense_umma_kernel<FMT, TWO, TWICE>, dim3(ctas), dim3(threads_of(FMT, TWO)), smem, stream, false, map, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -900,7 +900,9 @@ cudaError_t launch_dense_umma(const DenseParams &p, const CUtensorMap &map, int 
         return two ? launch_t<kFmtBf16, true>(p, map, ctas, stream) : launch_t<kFmtBf16, false>(p, map, ctas, stream);
     if (kv_dtype == MSA_FP8_E4M3)
         return two ? launch_t<kFmtFp8, true>(p, map, ctas, stream) : launch_t<kFmtFp8, false>(p, map, ctas, stream);
-    return two ? launch_t<kFmtF4, true>(p, map, ctas, stream) : launch_t<kFmtF4, false>(p, map, ctas, stream);
+    return two ? launch_t<kFmtF4, true>(p, map, ctas, stream)
+           : p.rows <= 64 ? launch_t<kFmtF4, false, true>(p, map, ctas, stream)
+                          : launch_t<kFmtF4, false>(p, map, ctas, stream);
 }
 
 } // namespace msa
