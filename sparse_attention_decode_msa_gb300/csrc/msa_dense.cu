@@ -18,7 +18,7 @@
 // so the kernel is a ring of whole pages fed by TMA, with as much in flight as
 // shared memory holds (192 KiB an SM), and mma.sync (m16n8k16: 16 rows are one
 // tile, no accumulator leaves the registers), whose work hides behind the copies:
-// 5.6 TB/s over 1.1 GB of E4M3 pages (48 requests, 198 us), 4.4 TB/s over 165 MB of
+// 5.6 TB/s over 1.1 GB of E4M3 pages (48 requests, 197 us), 4.4 TB/s over 165 MB of
 // bf16 pages (8 heads, 37 us with the join), 7.1 TB/s over 5.1 GB in units of 1024
 // pages.  A unit costs some 4 us of each CTA besides its pages (query rows, the sum over
 // warps, outputs): 6.6 TB/s with units of 128 pages.
@@ -33,6 +33,8 @@
 // Inside a CTA: one producer warp and eight consumer warps with 16 positions of every
 // page each.  A consumer warp keeps m, l and O of the 16 rows over its own share of
 // the pages, so warps meet only at the end of a unit.
+#include <type_traits>
+
 #include "msa_cache.cuh"
 
 namespace msa {
@@ -211,6 +213,10 @@ __device__ __forceinline__ float value_at(const uint8_t *tile, int row, int d)
     f16x2_to_f32x2(e4m3x2_to_f16x2(tile[8192 + row * 8 + (d >> 4)]), a, b);
     return v * a;
 }
+
+struct Flag {
+    bool value;
+};
 
 // A 16-bit output pair at dimension d of one row.
 __device__ __forceinline__ void store_bf16x2(uint16_t *row, int d, float a, float b)
@@ -406,105 +412,115 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t kt = smem + st * 2 * TB, vt = kt + TB;
             const int page0 = (b + i) * kPage;
-            const bool tail = page0 + kPage > seq_len; // some row does not see all of the page
+            const bool tail = page0 + kPage > seq_len;
             const int at = 16 * warp; // this warp's positions of the page
-            float s[2][4];
-            score16<FMT>(s, q, kt, at);
-            float a0 = ninf, a1 = ninf;
+            auto use_page = [&](auto ends) { // ends: some row does not see all of the page
+                float s[2][4];
+                score16<FMT>(s, q, kt, at);
+                float a0 = ninf, a1 = ninf;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = s[t][e] * (e < 2 ? sc0 : sc1);
-                    if (tail && page0 + at + 8 * t + 2 * c4 + (e & 1) >= (e < 2 ? lim0 : lim1))
-                        v = ninf;
-                    s[t][e] = v;
-                    if (e < 2)
-                        a0 = fmaxf(a0, v);
-                    else
-                        a1 = fmaxf(a1, v);
+                    for (int e = 0; e < 4; ++e) {
+                        float v = s[t][e] * (e < 2 ? sc0 : sc1);
+                        if (ends.value && page0 + at + 8 * t + 2 * c4 + (e & 1) >= (e < 2 ? lim0 : lim1))
+                            v = ninf;
+                        s[t][e] = v;
+                        if (e < 2)
+                            a0 = fmaxf(a0, v);
+                        else
+                            a1 = fmaxf(a1, v);
+                    }
+                a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
+                a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
+                a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+                a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+                if (FMT != kFmtBf16) {
+                    a0 -= kPUp;
+                    a1 -= kPUp;
                 }
-            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
-            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
-            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-            if (FMT != kFmtBf16) {
-                a0 -= kPUp;
-                a1 -= kPUp;
-            }
-            if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
-                const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
-                const float f0 = n0 == ninf ? 1.f : ex2(m0 - n0), f1 = n1 == ninf ? 1.f : ex2(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= f0;
-                l1 *= f1;
+                if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
+                    const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+                    const float f0 = n0 == ninf ? 1.f : ex2(m0 - n0), f1 = n1 == ninf ? 1.f : ex2(m1 - n1);
+                    m0 = n0;
+                    m1 = n1;
+                    l0 *= f0;
+                    l1 *= f1;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    o[k][0] *= f0;
-                    o[k][1] *= f0;
-                    o[k][2] *= f1;
-                    o[k][3] *= f1;
+                    for (int k = 0; k < 16; ++k) {
+                        o[k][0] *= f0;
+                        o[k][1] *= f0;
+                        o[k][2] *= f1;
+                        o[k][3] *= f1;
+                    }
                 }
-            }
-            const float r0 = m0 == ninf ? 0.f : m0, r1 = m1 == ninf ? 0.f : m1;
-            uint32_t hi4[4], lo4[4] = {0u, 0u, 0u, 0u};
+                const float r0 = m0 == ninf ? 0.f : m0, r1 = m1 == ninf ? 0.f : m1;
+                uint32_t hi4[4], lo4[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const float e0 = ex2(s[t][0] - r0), e1 = ex2(s[t][1] - r0);
-                const float e2 = ex2(s[t][2] - r1), e3 = ex2(s[t][3] - r1);
-                l0 += e0 + e1;
-                l1 += e2 + e3;
-                s[t][0] = e0;
-                s[t][1] = e1;
-                s[t][2] = e2;
-                s[t][3] = e3;
-                if (FMT == kFmtBf16) {
-                    // P = hi + lo, 16 significant bits: the rounding of P to bf16 alone
-                    // (up to 2^-8 relative) would weigh as much as the rounding of the output
-                    const uint32_t h0 = pack_bf16(e0, e1), h1 = pack_bf16(e2, e3);
-                    hi4[2 * t] = h0;
-                    hi4[2 * t + 1] = h1;
-                    lo4[2 * t] = pack_bf16(e0 - __uint_as_float(h0 << 16), e1 - __uint_as_float(h0 & 0xFFFF0000u));
-                    lo4[2 * t + 1] = pack_bf16(e2 - __uint_as_float(h1 << 16), e3 - __uint_as_float(h1 & 0xFFFF0000u));
-                } else { // f16 of 2^15 P: 11 significant bits down to P = 2^-29
-                    hi4[2 * t] = pack_f16(e0, e1);
-                    hi4[2 * t + 1] = pack_f16(e2, e3);
+                for (int t = 0; t < 2; ++t) {
+                    const float e0 = ex2(s[t][0] - r0), e1 = ex2(s[t][1] - r0);
+                    const float e2 = ex2(s[t][2] - r1), e3 = ex2(s[t][3] - r1);
+                    l0 += e0 + e1;
+                    l1 += e2 + e3;
+                    s[t][0] = e0;
+                    s[t][1] = e1;
+                    s[t][2] = e2;
+                    s[t][3] = e3;
+                    if (FMT == kFmtBf16) {
+                        // P = hi + lo, 16 significant bits: the rounding of P to bf16 alone
+                        // (up to 2^-8 relative) would weigh as much as the rounding of the output
+                        const uint32_t h0 = pack_bf16(e0, e1), h1 = pack_bf16(e2, e3);
+                        hi4[2 * t] = h0;
+                        hi4[2 * t + 1] = h1;
+                        lo4[2 * t] = pack_bf16(e0 - __uint_as_float(h0 << 16), e1 - __uint_as_float(h0 & 0xFFFF0000u));
+                        lo4[2 * t + 1] = pack_bf16(e2 - __uint_as_float(h1 << 16), e3 - __uint_as_float(h1 & 0xFFFF0000u));
+                    } else { // f16 of 2^15 P: 11 significant bits down to P = 2^-29
+                        hi4[2 * t] = pack_f16(e0, e1);
+                        hi4[2 * t + 1] = pack_f16(e2, e3);
+                    }
                 }
-            }
-            const int past = cached - page0 - at; // rows from `past` on are not cached
-            if (tail && page0 + at + 16 > seq_len && (past < 16 || p.nq > 1)) {
-                uint32_t drop = past < 16 ? 0xFFFFu << max(past, 0) & 0xFFFFu : 0u;
-                // positions that only later tokens see: their infinities and NaN are added
-                // to the rows that see them, one position at a time, past the MMA
-                uint32_t later = 0xFFFFu << max(seq_len - page0 - at, 0) & 0xFFFFu & ~drop;
-                if (later)
-                    later &= nonfinite_rows<FMT>(vt, at);
-                drop |= later;
-                for (; later; later &= later - 1) {
-                    const int pp = __ffs(later) - 1, src = (lane & ~3) | ((pp & 7) >> 1);
-                    const float c0 = pp & 8 ? (pp & 1 ? s[1][1] : s[1][0]) : (pp & 1 ? s[0][1] : s[0][0]);
-                    const float c1 = pp & 8 ? (pp & 1 ? s[1][3] : s[1][2]) : (pp & 1 ? s[0][3] : s[0][2]);
-                    const float p0 = __shfl_sync(0xffffffffu, c0, src), p1 = __shfl_sync(0xffffffffu, c1, src);
-                    const bool see0 = page0 + at + pp < lim0, see1 = page0 + at + pp < lim1;
+                const int past = cached - page0 - at; // rows from `past` on are not cached
+                if (ends.value && page0 + at + 16 > seq_len && (past < 16 || p.nq > 1)) {
+                    uint32_t drop = past < 16 ? 0xFFFFu << max(past, 0) & 0xFFFFu : 0u;
+                    // positions that only later tokens see: their infinities and NaN are added
+                    // to the rows that see them, one position at a time, past the MMA
+                    uint32_t later = 0xFFFFu << max(seq_len - page0 - at, 0) & 0xFFFFu & ~drop;
+                    if (later)
+                        later &= nonfinite_rows<FMT>(vt, at);
+                    drop |= later;
+                    for (; later; later &= later - 1) {
+                        const int pp = __ffs(later) - 1, src = (lane & ~3) | ((pp & 7) >> 1);
+                        const float c0 = pp & 8 ? (pp & 1 ? s[1][1] : s[1][0]) : (pp & 1 ? s[0][1] : s[0][0]);
+                        const float c1 = pp & 8 ? (pp & 1 ? s[1][3] : s[1][2]) : (pp & 1 ? s[0][3] : s[0][2]);
+                        const float p0 = __shfl_sync(0xffffffffu, c0, src), p1 = __shfl_sync(0xffffffffu, c1, src);
+                        const bool see0 = page0 + at + pp < lim0, see1 = page0 + at + pp < lim1;
 #pragma unroll
-                    for (int t = 0; t < 16; ++t)
+                        for (int t = 0; t < 16; ++t)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float v = value_at<FMT>(gsm + st * 2 * TB + TB, at + pp,
-                                                          8 * TG * (t / TG) + TG * (2 * c4 + e) + t % TG);
-                            if (see0)
-                                o[t][e] = fmaf(p0, v, o[t][e]);
-                            if (see1)
-                                o[t][2 + e] = fmaf(p1, v, o[t][2 + e]);
-                        }
+                            for (int e = 0; e < 2; ++e) {
+                                const float v = value_at<FMT>(gsm + st * 2 * TB + TB, at + pp,
+                                                              8 * TG * (t / TG) + TG * (2 * c4 + e) + t % TG);
+                                if (see0)
+                                    o[t][e] = fmaf(p0, v, o[t][e]);
+                                if (see1)
+                                    o[t][2 + e] = fmaf(p1, v, o[t][2 + e]);
+                            }
+                    }
+                    const uint32_t d0 = drop >> (2 * c4), d1 = d0 >> 8;
+                    accumulate16<FMT, true>(o, hi4, lo4, vt, at, (d0 & 1 ? 0u : 0xFFFFu) | (d0 & 2 ? 0u : 0xFFFF0000u),
+                                            (d1 & 1 ? 0u : 0xFFFFu) | (d1 & 2 ? 0u : 0xFFFF0000u));
+                } else {
+                    accumulate16<FMT, false>(o, hi4, lo4, vt, at);
                 }
-                const uint32_t d0 = drop >> (2 * c4), d1 = d0 >> 8;
-                accumulate16<FMT, true>(o, hi4, lo4, vt, at, (d0 & 1 ? 0u : 0xFFFFu) | (d0 & 2 ? 0u : 0xFFFF0000u),
-                                        (d1 & 1 ? 0u : 0xFFFFu) | (d1 & 2 ? 0u : 0xFFFF0000u));
-            } else {
-                accumulate16<FMT, false>(o, hi4, lo4, vt, at);
-            }
+            };
+            // whole pages by themselves where V is widened: NVFP4 1040 -> 993 us, E4M3 714 -> 708 us
+            // over 19 x 131072 positions of 8 KV heads; bf16 8 heads lost, 37.5 -> 38.8 us
+            if constexpr (FMT == kFmtBf16)
+                use_page(Flag{tail});
+            else if (tail)
+                use_page(std::true_type{});
+            else
+                use_page(std::false_type{});
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(empty + 8 * st);
