@@ -17,16 +17,18 @@
 // read one quarter of the accumulator lanes only, and so the streams' warps with rows in
 // them sit on different schedulers (32 requests of 2 tokens over 65536 positions: 456 us,
 // 495 without).  E4M3 and bf16 lose more to the longer end of a unit
-// than they gain: 143 us for 137, 2 tokens over 64 x 32768 E4M3 positions, 79 for 70 on 8
+// than they gain: 143 us for 137, 2 tokens over 64 x 32768 E4M3 positions, 78 for 70 on 8
 // requests of 4 bf16 tokens.
 //
 // Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA
 // lands them (K-major), P in tensor memory over the S it came from, V tiles as
-// landed (MN-major).  bf16 P is a pair hi + lo (16 significant bits)
-// in steps where some position weighs 1/64 or more of its row's denominator so
-// far; elsewhere hi alone, whose errors (2^-8 of each p at most, independent)
-// add up to some 2^-12 of the largest |v|.  E4M3 and NVFP4 tiles are widened to f16 by
-// converter warps and P is one f16 (11 bits).
+// landed (MN-major).  bf16 P is a pair hi + lo (16 significant bits): the rounding to
+// bf16 alone is up to 2^-8 of each p, and where many positions have the same logit
+// (repeated keys, a scale near 0) all of them round the same way, so that an output would be
+// off by 2^-8 of the largest |v| however small the single p are (48 tokens over 2 x 131072
+// positions take 457 us with the pair, 394 with hi alone).  E4M3 and NVFP4 tiles are
+// widened to f16 by converter warps and P is one f16: off by 2^-11 of p at most, by as much of the
+// largest |v| at worst, an eighth of what the storage of the output takes.
 //
 // TMEM columns: S/P of step s of stream t at 128 t + 64 (s & 1) (one row tile: at
 // 128 (s & 1) + 64 t), O of stream t at 256 + 128 t.
@@ -37,8 +39,8 @@
 // What bounds it: the tensor cores when rows are many (measured: an MMA of
 // 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50 as both read 4 KiB
 // of Q from shared memory; a page of 128 rows is 16 of these for S, or 8 of those
-// with one row tile, and 8, or 16 with lo, of those for P V), HBM when they are few.
-// Measured: 48 tokens over 2 x 131072 bf16 positions 393 us, 1.05 PFLOP/s (the chain
+// with one row tile, and 8, or 16 as pairs, of those for P V), HBM when they are few.
+// Measured: 48 tokens over 2 x 131072 bf16 positions 457 us, 0.90 PFLOP/s (the chain
 // S, maximum, exponentials, P V of a step is longer than its MMAs: tensor pipe half busy);
 // 4 tokens, 349 MB of bf16 pages 70 us, 5.0 TB/s; 2 tokens, 1.2 GB of NVFP4 pages 456 us,
 // 2.65 TB/s (the schedulers, which widen every tile and have the softmax as well).
@@ -179,7 +181,6 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
     __shared__ int scan_tmp[NT / 32 + 1];
     __shared__ int start_r, start_before;
     __shared__ uint32_t tmem_slot;
-    __shared__ int with_lo[2][2]; // [stream][S buffer]: P of the step is a pair hi + lo
     __shared__ int later_bad[8]; // unit counter + 1 where V rows of draft tokens are not finite
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *gsm = smem_raw + (smem - smem_u32(smem_raw));
@@ -403,16 +404,11 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                     wait(p_full + 16 * t + 8 * (i & 1), (i & 1 ? fill1++ : fill0++) & 1u);
                     tcgen05_after_sync();
                     // V, MN-major: 16 positions are 16 rows of 128 bytes
-                    if (!CONV && __any_sync(0xffffffffu, with_lo[t][i & 1])) {
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
+                    for (int ks = 0; ks < 4; ++ks) {
+                        umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
+                        if (!CONV)
                             umma_ts(one, d, a + 32 + 8 * ks, v + ks * (2048 >> 4), idesc_o, 1u);
-                        }
-                    } else {
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
                     }
                     if (one) {
                         umma_commit(pv_done + 16 * t + 8 * (i & 1));
@@ -444,13 +440,6 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
         uint32_t fills0 = 0, fills1 = 0;
         auto product_wait = [&](int k, int i) { // P V of step i (the last of its buffer) of stream k
             wait(pv_done + 16 * k + 8 * (i & 1), ((i & 1 ? fills1 : fills0) - 1) & 1u);
-        };
-        auto or_of_stream = [&](uint32_t &any) { // over the stream's 128 threads
-            asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n"
-                         " selp.u32 %0, 1, 0, q;\n}\n"
-                         : "+r"(any)
-                         : "r"(3 + t)
-                         : "memory");
         };
         constexpr bool twice = TWICE;
         const int lane0 = twice ? 64 * t : 0; // the stream's first accumulator lane
@@ -510,10 +499,6 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                 if (idle) {
                     if (lane == 0)
                         mbar_arrive(p_full + 16 * t + 8 * (i & 1));
-                    if (!CONV) {
-                        uint32_t none = 0u;
-                        or_of_stream(none);
-                    }
                     continue;
                 }
                 tcgen05_after_sync();
@@ -568,22 +553,11 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                         }
                     }
                 }
-                // lo matters where a single position weighs much: the rounding of P to bf16
-                // (2^-8 of p) is left in only for steps in which every p is under 1/64 of its
-                // row's denominator so far (see the top)
-                bool lo_too = false;
-                if (!CONV) {
-                    uint32_t any = real && m != ninf && !(ex2(mx - m) * 64.f < l);
-                    or_of_stream(any);
-                    lo_too = any != 0u;
-                    if (mine == lane0)
-                        with_lo[t][i & 1] = lo_too;
-                }
                 const float ref = m == ninf ? 0.f : m;
                 const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref), minus = pair(-1.f, -1.f);
                 uint64_t sum[2] = {0ull, 0ull};
-                // the common step by itself: with the tests for the others in its unrolled
-                // loop 48 tokens over 2 x 131072 positions took 414 us, without 387
+                // the common step by itself: with the tests for a last page in its unrolled
+                // loop 48 tokens over 2 x 131072 positions took 473 us, without 468
                 auto to_p = [&](auto plain) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) { // 32 columns of S become P
@@ -610,19 +584,17 @@ __global__ void __launch_bounds__(threads_of(FMT, TWO), 1)
                                 hi[k] = pack_f16(e0, e1);
                             } else {
                                 hi[k] = pack_bf16(e0, e1);
-                                if (plain.value || !lo_too)
-                                    continue;
                                 float d0, d1;
                                 unpair(fma2(pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u)), minus, e), d0, d1);
                                 lo[k] = pack_bf16(d0, d1);
                             }
                         }
                         tmem_st16(at_s + 16 * c, hi);
-                        if (!CONV && !plain.value && lo_too)
+                        if (!CONV)
                             tmem_st16(at_s + 32 + 16 * c, lo);
                     }
                 };
-                if (tail || lo_too)
+                if (tail)
                     to_p(std::false_type{});
                 else
                     to_p(std::true_type{});

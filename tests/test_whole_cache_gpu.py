@@ -12,6 +12,7 @@ exp2's hardware form by 2^-22 relative.
            most l / 64: then its errors, independent and 2^-8 / sqrt(3) p (rms) at most, add up to
            2^-8 / sqrt(3) sqrt(sum p^2) / l <= 2^-8 / sqrt(3) / 8 = 2^-11.8 (rms) of max |v|, and of the
            rms of v, a quarter of its maximum here, 5 sigma are 2^-11.5
+           (that last case no longer occurs: equal logits round alike, so bf16 P is the pair in every step)
   weights  relative d + 2^-22 + 2^-23 |lse| a term, rows 2^-24 for the sum, 2^-23 for decay
 """
 
