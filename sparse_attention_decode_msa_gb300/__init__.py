@@ -126,8 +126,7 @@ def _ptr(x):
 def _bufs(stream, *xs):
     """The stream handle and the device pointers of a whole-cache operator's buffers: tensors must
     be dense and on the current device (the library sees only addresses), ints and None are taken
-    as they are.  A step of a small cache takes about 10 us on the GPU, so this path counts: the
-    current stream is read without building a Stream object (3 us)."""
+    as they are.  A step of a small cache takes about 10 us on the GPU, so this path counts."""
     import torch
 
     device, out = None, []
@@ -144,10 +143,19 @@ def _bufs(stream, *xs):
         if not x.is_contiguous():
             raise ValueError("buffers must be contiguous")
         out.append(x.data_ptr())
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if stream is None and device is not None and raw is not None:
-        return raw(device), out
+    if stream is None and device is not None:
+        return _current_stream(device), out
     return _stream(stream), out
+
+
+def _current_stream(device=None):
+    """The current stream's handle, without building a Stream object (3 us) where torch has a way."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return raw(torch.cuda.current_device() if device is None else device)
 
 
 def _stream(stream):

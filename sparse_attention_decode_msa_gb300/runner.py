@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (make_shape, msa_cache_evict, msa_cache_workspace_bytes, msa_decode_step, msa_dense_decode,
+from . import (_current_stream, make_shape, msa_cache_evict, msa_cache_workspace_bytes, msa_decode_step, msa_dense_decode,
                msa_index_score, msa_kv_update, msa_select_topk, msa_sparse_decode, msa_weight_accumulate,
                msa_workspace_bytes, msa_workspace_init)
 
@@ -56,6 +56,7 @@ class DeviceProblem:
             raise ValueError("shape rejected by msa_workspace_bytes")
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         msa_workspace_init(self.ws, self.ws_bytes)
+        self._new_cache_workspaces()
 
     def replicate(self) -> "DeviceProblem":
         """A copy of every buffer at new device addresses (same bytes)."""
@@ -71,7 +72,7 @@ class DeviceProblem:
         dp.shape = type(self.shape).from_buffer_copy(self.shape)
         dp.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         msa_workspace_init(dp.ws, dp.ws_bytes)
-        dp.cache_ws = None
+        dp._new_cache_workspaces()
         return dp
 
     def set_decode_ctas(self, n: int):
@@ -120,14 +121,43 @@ class DeviceProblem:
             stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         return torch.cuda.stream(stream)
 
+    def _new_cache_workspaces(self):
+        self.cache_ws = None     # of the latest whole-cache call: its error word tells about that call
+        self._cache_ws_of = {}   # by stream handle; None: calls captured on streams without calls of their own
+        self._cache_ws_all = []  # a captured graph knows its workspace by address: none is freed
+
     def _cache_workspace(self):
+        """The workspace of the current stream: calls on two streams may overlap, and what is cleared
+        on one stream is not cleared for another.  Captures on streams that made no call before share
+        one, cleared at the problem's first call (graphs whose replays may overlap belong to problems
+        of their own, see replicate); captured before any call, each call has one that its graph clears."""
         import torch
 
         need = msa_cache_workspace_bytes(self.shape)
-        if getattr(self, "cache_ws", None) is None or self.cache_ws.numel() < need:
-            self.cache_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            msa_workspace_init(self.cache_ws, need)
-        return self.cache_ws, self.cache_ws.numel()
+
+        def made():
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            msa_workspace_init(ws, need)
+            self._cache_ws_all.append(ws)
+            return ws
+
+        def held(key):
+            ws = self._cache_ws_of.get(key)
+            return ws if ws is not None and ws.numel() >= need else None
+
+        stream = _current_stream()
+        ws = held(stream)
+        if ws is None:
+            if torch.cuda.is_current_stream_capturing():
+                ws = held(None)
+                ws = made() if ws is None else ws
+            else:
+                ws = self._cache_ws_of[stream] = made()
+                if held(None) is None:
+                    self._cache_ws_of[None] = made()
+                    torch.cuda.current_stream().synchronize()  # cleared before any graph is replayed
+        self.cache_ws = ws
+        return ws, ws.numel()
 
     def dense_decode(self, stream=None):
         """Attention over every cached position, into out and lse."""
@@ -145,7 +175,9 @@ class DeviceProblem:
 
     def evict(self, weights, new_table, keep: int, first: int = 0, last: int = 0, stream=None) -> dict:
         """Copy the kept positions to new_table's pages; the lists, lengths and weights of the
-        shortened cache (block_table and seq_lens stay as they are)."""
+        shortened cache (block_table and seq_lens stay as they are).  The tensors returned belong to
+        the stream of the call: another stream that uses them waits for it, and tells the allocator
+        (Tensor.record_stream) before it lets go of them."""
         import torch
 
         R, Hkv = self.shape.num_requests, self.shape.num_kv_heads
