@@ -123,39 +123,12 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _bufs(stream, *xs):
-    """The stream handle and the device pointers of a whole-cache operator's buffers: tensors must
-    be dense and on the current device (the library sees only addresses), ints and None are taken
-    as they are.  A step of a small cache takes about 10 us on the GPU, so this path counts."""
-    import torch
+def _bufs(stream, kinds, *xs):
+    """buffers.bufs, which takes this name at the first call (torch is imported by then)."""
+    global _bufs
+    from .buffers import bufs as _bufs
 
-    device, out = None, []
-    for x in xs:
-        if x is None or isinstance(x, int):
-            out.append(x)
-            continue
-        d = x.get_device()
-        if d != device:
-            if device is None and d >= 0:
-                device = torch.cuda.current_device()
-            if d != device:
-                raise ValueError(f"buffer on {x.device}: not on the current CUDA device")
-        if not x.is_contiguous():
-            raise ValueError("buffers must be contiguous")
-        out.append(x.data_ptr())
-    if stream is None and device is not None:
-        return _current_stream(device), out
-    return _stream(stream), out
-
-
-def _current_stream(device=None):
-    """The current stream's handle, without building a Stream object (3 us) where torch has a way."""
-    import torch
-
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return raw(torch.cuda.current_device() if device is None else device)
+    return _bufs(stream, kinds, *xs)
 
 
 def _stream(stream):
@@ -254,7 +227,7 @@ def msa_cache_workspace_bytes(shape: MsaShape) -> int:
 def msa_dense_decode(shape, q, kv_pool, block_table, seq_lens, out, lse, workspace, workspace_bytes,
                      stream=None):
     """Attention over every cached position a token sees."""
-    st, bufs = _bufs(stream, q, kv_pool, block_table, seq_lens, out, lse, workspace)
+    st, bufs = _bufs(stream, "hbiihfb", q, kv_pool, block_table, seq_lens, out, lse, workspace)
     _check(load().msa_dense_decode(ctypes.byref(shape), *bufs, int(workspace_bytes), st),
            "msa_dense_decode")
 
@@ -263,7 +236,7 @@ def msa_weight_accumulate(shape, q, kv_pool, block_table, seq_lens, selected, ls
                           weights_out, workspace, workspace_bytes, stream=None):
     """Add this step's attention weights to every cached position's sum (selected: None after a
     dense step, the block tables after a sparse one)."""
-    st, (*bufs, w_in, w_out, ws) = _bufs(stream, q, kv_pool, block_table, seq_lens, selected, lse,
+    st, (*bufs, w_in, w_out, ws) = _bufs(stream, "hbiiifffb", q, kv_pool, block_table, seq_lens, selected, lse,
                                          weights_in, weights_out, workspace)
     _check(load().msa_weight_accumulate(ctypes.byref(shape), *bufs, float(decay), w_in, w_out, ws,
                                         int(workspace_bytes), st), "msa_weight_accumulate")
@@ -272,8 +245,8 @@ def msa_weight_accumulate(shape, q, kv_pool, block_table, seq_lens, selected, ls
 def msa_cache_evict(shape, keep, first, last, weights, block_table, seq_lens, new_table, kv_pool, idxk_pool,
                     idxk_scales, new_weights, kept, new_lens, workspace, workspace_bytes, stream=None):
     """Keep the heaviest positions of every request, copied in order to the pages of new_table."""
-    st, bufs = _bufs(stream, weights, block_table, seq_lens, new_table, kv_pool, idxk_pool, idxk_scales,
-                     new_weights, kept, new_lens, workspace)
+    st, bufs = _bufs(stream, "fiiibbbfiib", weights, block_table, seq_lens, new_table, kv_pool, idxk_pool,
+                     idxk_scales, new_weights, kept, new_lens, workspace)
     _check(load().msa_cache_evict(ctypes.byref(shape), int(keep), int(first), int(last), *bufs,
                                   int(workspace_bytes), st), "msa_cache_evict")
 

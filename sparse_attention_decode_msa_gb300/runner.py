@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (_current_stream, make_shape, msa_cache_evict, msa_cache_workspace_bytes, msa_decode_step, msa_dense_decode,
+from . import (make_shape, msa_cache_evict, msa_cache_workspace_bytes, msa_decode_step, msa_dense_decode,
                msa_index_score, msa_kv_update, msa_select_topk, msa_sparse_decode, msa_weight_accumulate,
                msa_workspace_bytes, msa_workspace_init)
 
@@ -122,18 +122,27 @@ class DeviceProblem:
         return torch.cuda.stream(stream)
 
     def _new_cache_workspaces(self):
+        from .buffers import current_stream
+
+        self._current_stream = current_stream
         self.cache_ws = None     # of the latest whole-cache call: its error word tells about that call
         self._cache_ws_of = {}   # by stream handle; None: calls captured on streams without calls of their own
         self._cache_ws_all = []  # a captured graph knows its workspace by address: none is freed
 
     def _cache_workspace(self):
-        """The workspace of the current stream: calls on two streams may overlap, and what is cleared
-        on one stream is not cleared for another.  Captures on streams that made no call before share
-        one, cleared at the problem's first call (graphs whose replays may overlap belong to problems
+        """The current stream and its workspace (and its size): calls on two streams may overlap, and what
+        is cleared on one stream is not cleared for another.  Captures on streams that made no call before
+        share one, cleared at the problem's first call (graphs whose replays may overlap belong to problems
         of their own, see replicate); captured before any call, each call has one that its graph clears."""
-        import torch
+        need, stream = msa_cache_workspace_bytes(self.shape), self._current_stream()
+        ws = self._cache_ws_of.get(stream)
+        if ws is None or ws.numel() < need:
+            ws = self._another_cache_workspace(stream, need)
+        self.cache_ws = ws
+        return ws, ws.numel(), stream
 
-        need = msa_cache_workspace_bytes(self.shape)
+    def _another_cache_workspace(self, stream, need):
+        import torch
 
         def made():
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
@@ -141,23 +150,16 @@ class DeviceProblem:
             self._cache_ws_all.append(ws)
             return ws
 
-        def held(key):
-            ws = self._cache_ws_of.get(key)
-            return ws if ws is not None and ws.numel() >= need else None
-
-        stream = _current_stream()
-        ws = held(stream)
-        if ws is None:
-            if torch.cuda.is_current_stream_capturing():
-                ws = held(None)
-                ws = made() if ws is None else ws
-            else:
-                ws = self._cache_ws_of[stream] = made()
-                if held(None) is None:
-                    self._cache_ws_of[None] = made()
-                    torch.cuda.current_stream().synchronize()  # cleared before any graph is replayed
-        self.cache_ws = ws
-        return ws, ws.numel()
+        shared = self._cache_ws_of.get(None)
+        if shared is not None and shared.numel() < need:
+            shared = None
+        if torch.cuda.is_current_stream_capturing():
+            return made() if shared is None else shared
+        ws = self._cache_ws_of[stream] = made()
+        if shared is None:
+            self._cache_ws_of[None] = made()
+            torch.cuda.current_stream().synchronize()  # cleared before any graph is replayed
+        return ws
 
     def dense_decode(self, stream=None):
         """Attention over every cached position, into out and lse."""

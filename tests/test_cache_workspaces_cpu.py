@@ -7,7 +7,7 @@ import weakref
 import pytest
 
 import sparse_attention_decode_msa_gb300 as msa
-from sparse_attention_decode_msa_gb300 import build, runner
+from sparse_attention_decode_msa_gb300 import buffers, build, runner
 
 
 class Stand:
@@ -26,7 +26,8 @@ class Stand:
             self.stream = before
 
         def call(shape, *args):
-            ws, size = args[-2:]
+            ws, size, stream = args[-3:]
+            assert stream == self.stream
             assert size >= msa.msa_cache_workspace_bytes(shape) and size == ws.numel()
             self.calls.append((self.stream, ws.data_ptr(), size))
 
@@ -38,7 +39,7 @@ class Stand:
         monkeypatch.setattr(runner, "msa_dense_decode", call)
         monkeypatch.setattr(runner, "msa_cache_evict", call)
         monkeypatch.setattr(runner, "msa_weight_accumulate", call)
-        monkeypatch.setattr(runner, "_current_stream", lambda device=None: self.stream, raising=False)
+        monkeypatch.setattr(buffers, "current_stream", lambda device=None: self.stream)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self)
         self.dp = dp = runner.DeviceProblem.__new__(runner.DeviceProblem)
