@@ -47,10 +47,10 @@ class DeviceProblem:
         T, Hq = pb.num_tokens, pb.num_q_heads
         Hi = self.shape.num_index_heads
         Hs = 1 if Hi == 1 else pb.num_kv_heads      # selection tables per token
-        self.block_scores = torch.full((T, Hi, pb.max_blocks), float("nan"), device=device)
+        self.block_scores = torch.full((T, Hi, pb.max_blocks), float("nan"), dtype=torch.float32, device=device)
         self.selected = torch.full((T, Hs, pb.topk), -7, dtype=torch.int32, device=device)
         self.out = torch.full((T, Hq, 128), float("nan"), dtype=torch.bfloat16, device=device)
-        self.lse = torch.full((T, Hq), float("nan"), device=device)
+        self.lse = torch.full((T, Hq), float("nan"), dtype=torch.float32, device=device)
         self.ws_bytes = msa_workspace_bytes(self.shape)
         if self.ws_bytes == 0:
             raise ValueError("shape rejected by msa_workspace_bytes")
@@ -187,7 +187,7 @@ class DeviceProblem:
         with self._on(stream):
             kept = torch.empty((R, Hs, keep), dtype=torch.int32, device=self.device)
             lens = torch.empty(R, dtype=torch.int32, device=self.device)
-            new_weights = torch.zeros((R, Hkv, -(-keep // 128) * 128), device=self.device)
+            new_weights = torch.zeros((R, Hkv, -(-keep // 128) * 128), dtype=torch.float32, device=self.device)
             msa_cache_evict(self.shape, keep, first, last, weights, self.block_table, self.seq_lens,
                             new_table, self.kv, self.idxk, self.idxk_scales, new_weights, kept, lens,
                             *self._cache_workspace())

@@ -54,3 +54,24 @@ def test_the_right_types_pass_on_to_the_check_of_the_device(name):
             args[i] = torch.zeros(64, dtype=dtype)
             with pytest.raises(ValueError, match="not on the current CUDA device"):
                 getattr(msa, name)(shape(), *lead, *args, 1 << 30, stream=0)
+
+
+def test_buffers_are_fp32_whatever_the_default_type_is(monkeypatch):
+    # the kernels write fp32: a buffer of 16-bit elements would be half as long as what they write
+    import torch
+
+    from sparse_attention_decode_msa_gb300 import runner, synth
+
+    monkeypatch.setattr(runner, "msa_workspace_init", lambda *a: None)
+    monkeypatch.setattr(runner, "msa_cache_evict", lambda *a: None)
+    monkeypatch.setattr(runner.DeviceProblem, "_cache_workspace", lambda self: (None, 0, 0))
+    pb = synth.make_problem(name="types", contexts=[300], q_per_req=1, num_kv_heads=1, topk=2)
+    before = torch.get_default_dtype()
+    try:
+        for dtype in (torch.float16, torch.float64):
+            torch.set_default_dtype(dtype)
+            dp = runner.DeviceProblem(pb, device="cpu")
+            assert dp.lse.dtype == dp.block_scores.dtype == torch.float32 and dp.out.dtype == torch.bfloat16
+            assert dp.evict(None, None, keep=5)["weights"].dtype == torch.float32
+    finally:
+        torch.set_default_dtype(before)
