@@ -287,7 +287,11 @@ size_t msa_cache_workspace_bytes(const msa_shape *shape);
  * the result of msa_sparse_decode with every block selected, without its limit
  * of 256 blocks.  The pages of a request are read once for all its tokens, are
  * split over persistent CTAs and joined in a fixed order (no atomics: the same
- * inputs give the same bits).  out: bf16, lse: fp32. */
+ * inputs give the same bits).  out: bf16, lse: fp32.  Sums and the softmax are
+ * fp32; probabilities meet V as a pair of bf16 (off by 2^-16 at most) over bf16
+ * pages, as fp16 (2^-11) over E4M3 and NVFP4 pages; queries meet E4M3 and NVFP4
+ * keys as fp16 after a power of two (elements 2^-23 below a row's largest lose
+ * bits). */
 msa_status msa_dense_decode(const msa_shape *shape, const void *q, const void *kv_pool,
                             const int32_t *block_table, const int32_t *seq_lens, void *out,
                             float *lse, void *workspace, size_t workspace_bytes,

@@ -40,10 +40,10 @@
 // 128 x 128 x 16 takes 66 clocks, one of 128 x 64 x 16 takes 50 as both read 4 KiB
 // of Q from shared memory; a page of 128 rows is 16 of these for S, or 8 of those
 // with one row tile, and 8, or 16 as pairs, of those for P V), HBM when they are few.
-// Measured: 48 tokens over 2 x 131072 bf16 positions 457 us, 0.90 PFLOP/s (the chain
-// S, maximum, exponentials, P V of a step is longer than its MMAs: tensor pipe half busy);
+// Measured: 48 tokens over 2 x 131072 bf16 positions 432 .. 468 us, 0.88 .. 0.95 PFLOP/s (the chain
+// S, maximum, exponentials, P V of a step is longer than its MMAs: tensor pipe 55% busy);
 // 4 tokens, 349 MB of bf16 pages 70 us, 5.0 TB/s; 2 tokens, 1.2 GB of NVFP4 pages 456 us,
-// 2.65 TB/s (the schedulers, which widen every tile and have the softmax as well).
+// 2.65 TB/s (no unit is full: issue slots 48%, tensor pipe 41%; the roles wait for one another).
 #include <type_traits>
 
 #include "msa_umma.cuh"
