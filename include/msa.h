@@ -291,7 +291,8 @@ size_t msa_cache_workspace_bytes(const msa_shape *shape);
  * fp32; probabilities meet V as a pair of bf16 (off by 2^-16 at most) over bf16
  * pages, as fp16 (2^-11) over E4M3 and NVFP4 pages; queries meet E4M3 and NVFP4
  * keys as fp16 after a power of two (elements 2^-23 below a row's largest lose
- * bits). */
+ * bits).  An infinity or NaN in V makes that dimension of the outputs that see
+ * its position infinite or NaN, and no other. */
 msa_status msa_dense_decode(const msa_shape *shape, const void *q, const void *kv_pool,
                             const int32_t *block_table, const int32_t *seq_lens, void *out,
                             float *lse, void *workspace, size_t workspace_bytes,
