@@ -356,6 +356,84 @@ msa_status msa_cache_evict(const msa_shape *shape, int32_t keep, int32_t first, 
                            int32_t *new_lens, void *workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 
+/* ---- ragged batches: tokens into the cache, and their attention -----------
+ * A prompt, a chunk of one, or a step: request r brings any number of tokens,
+ * none among them, rows offsets[r] .. offsets[r + 1] - 1 of the inputs
+ * (offsets int32 [num_requests + 1], ascending from 0, offsets[num_requests] <=
+ * num_tokens); rows behind the last request's are neither read for a result nor
+ * written.  seq_lens[r] is, as everywhere here, what the first of them sees:
+ * token j of request r stands at position seq_lens[r] - 1 + j.  A request
+ * without tokens is not looked at.  q_per_req, topk and the selection's fields
+ * of msa_shape are not looked at.  num_tokens is at most 4194304; with 0 of them
+ * nothing is done and pointers may be NULL.  Outputs overlap inputs and one another
+ * only where a call says so. */
+
+/* Norm and rotation of rows x of 128 elements of the token at position p:
+ *   n = x / sqrt(mean x^2 + norm_eps) * (weight + norm_offset)   where a weight is given
+ *   a' = scale (a cos t - b sin t), b' = scale (b cos t + a sin t)
+ * for each pair (a, b) of the first rotary_dim elements of n, t = p f_i; the
+ * others stay as they are.  fp32, rounded once, to bf16 or to the pool's
+ * format; rows without norm and rotation are copied bit by bit to bf16. */
+typedef struct msa_rope {
+    int32_t rotary_dim;       /* a multiple of 16 up to 128; 0: no rotation */
+    int32_t interleaved;      /* 0: element i turns with i + rotary_dim / 2; 1: 2 i with 2 i + 1 */
+    int32_t per_head_weights; /* norm weights are bf16 [heads][128]; 0: [128] for all heads */
+    float scale;              /* multiplies the rotated elements (1, or an attention factor) */
+    float norm_eps;           /* >= 0 */
+    float norm_offset;        /* added to the weights (0; 1 where they are stored as w - 1) */
+    /* elements from a token's rows to the next token's, a multiple of 8 (rows that
+     * are parts of a fused projection's output); 0: dense */
+    int64_t q_stride, k_stride, v_stride, q_idx_stride, idxk_stride;
+} msa_rope;
+
+/* turns[i] = f_i / (2 pi) as a fraction of 2^64, for angles of f_i radians a
+ * position, 0 <= |f_i| < 2 pi * 2^31: the rotation's frequencies as the calls
+ * below take them (a table of rotary_dim / 2 in device memory, filled once: every
+ * angle is then p * turns[i] modulo 2^64, exact at any position).  Pure host
+ * function on host memory; MSA_ERR_INVALID_ARGUMENT for a frequency that is
+ * not finite or too large. */
+msa_status msa_rope_frequencies(const double *radians, int32_t count, uint64_t *turns);
+
+/* Norm and rotation of the query heads, and of key heads in the same pass.
+ *   positions    int32 [num_tokens] (negative ones turn the other way)
+ *   q            bf16 [num_tokens] x q_stride, num_q_heads * 128 elements each
+ *   q_weight     bf16 norm weights, or NULL: no norm (k_weight alike)
+ *   q_out        bf16 [num_tokens][num_q_heads][128]; may be q where q is dense
+ *   k, k_out     the same for num_k_heads heads; both NULL with num_k_heads = 0
+ * freqs may be NULL where rotary_dim is 0. */
+msa_status msa_qk_norm_rope(const msa_rope *rope, const uint64_t *freqs, int32_t num_tokens,
+                            const int32_t *positions, int32_t num_q_heads, const void *q,
+                            const void *q_weight, void *q_out, int32_t num_k_heads, const void *k,
+                            const void *k_weight, void *k_out, cudaStream_t stream);
+
+/* Bytes of device workspace for the two calls below (0 if the shape is invalid
+ * or unsupported).  Pure host function. */
+size_t msa_ragged_workspace_bytes(const msa_shape *shape);
+
+/* The tokens of a ragged batch into their pages, keys and index keys with norm
+ * and rotation on the way, and their queries and index queries in the same pass.
+ *   k, v         bf16 [num_tokens] x k_stride (v_stride), Hkv * 128 elements each
+ *   idxk         bf16, Hi * 128 elements a token, or NULL (then idxk_pool is not written)
+ *   q, q_out     bf16, Hq * 128 elements a token; both NULL: no queries.  q_out is
+ *                dense [num_tokens][Hq][128] and may be q where q is dense
+ *   q_idx, q_idx_out  the same for Hi index queries
+ *   k_weight, idxk_weight, q_weight, q_idx_weight  norm weights, each may be NULL.
+ *                Values are neither normed nor rotated
+ *   block_table, seq_lens, pools  as for msa_kv_update, whose encodings these are:
+ *                with rotary_dim 0 and no weights the pools get the same bytes
+ * Only the rows of the new tokens are written.  Two tokens of one call that share
+ * a row of a page leave either's.  A bad length or page id is reported through the
+ * workspace's error word and its token's rows are skipped.  Only the workspace's
+ * error word is used: 256 bytes suffice. */
+msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uint64_t *freqs,
+                         int32_t num_tokens, const int32_t *offsets, const void *k,
+                         const void *k_weight, const void *v, const void *idxk,
+                         const void *idxk_weight, const void *q, const void *q_weight, void *q_out,
+                         const void *q_idx, const void *q_idx_weight, void *q_idx_out,
+                         const int32_t *block_table, const int32_t *seq_lens, void *kv_pool,
+                         void *idxk_pool, void *idxk_scales, void *workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
+
 /* Size of the fixed device scratch used by msa_sparse_decode_noalloc. */
 #define MSA_NOALLOC_SCRATCH_BYTES (8u << 20)
 

@@ -56,6 +56,22 @@ class MsaShape(ctypes.Structure):
     ]
 
 
+class MsaRope(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("per_head_weights", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("norm_eps", ctypes.c_float),
+        ("norm_offset", ctypes.c_float),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q_idx_stride", ctypes.c_int64),
+        ("idxk_stride", ctypes.c_int64),
+    ]
+
+
 _SIGNATURES = {
     "msa_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MsaShape)]),
     "msa_workspace_init": (ctypes.c_int, [_p, ctypes.c_size_t, _p]),
@@ -77,6 +93,12 @@ _SIGNATURES = {
         ctypes.c_float, _p, _p, _p, ctypes.c_size_t, _p]),
     "msa_cache_evict": (ctypes.c_int, [ctypes.POINTER(MsaShape)] + [ctypes.c_int32] * 3 + [_p] * 11 + [
         ctypes.c_size_t, _p]),
+    "msa_rope_frequencies": (ctypes.c_int, [_p, ctypes.c_int32, _p]),
+    "msa_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(MsaRope), _p, ctypes.c_int32, _p] + [
+        ctypes.c_int32, _p, _p, _p] * 2 + [_p]),
+    "msa_ragged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MsaShape)]),
+    "msa_kv_append": (ctypes.c_int, [ctypes.POINTER(MsaShape), ctypes.POINTER(MsaRope), _p, ctypes.c_int32] + [
+        _p] * 18 + [ctypes.c_size_t, _p]),
     "msa_set_decode_wait_limit": (ctypes.c_int, [ctypes.c_int64]),
     "msa_check_device_status": (ctypes.c_int, [_p, _p]),
     "msa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -129,6 +151,14 @@ def _bufs(stream, kinds, *xs):
     from .buffers import bufs as _bufs
 
     return _bufs(stream, kinds, *xs)
+
+
+def _rows(stream, kinds, strides, *xs):
+    """buffers.rows, in the same way."""
+    global _rows
+    from .buffers import rows as _rows
+
+    return _rows(stream, kinds, strides, *xs)
 
 
 def _stream(stream):
@@ -249,6 +279,56 @@ def msa_cache_evict(shape, keep, first, last, weights, block_table, seq_lens, ne
                      idxk_scales, new_weights, kept, new_lens, workspace)
     _check(load().msa_cache_evict(ctypes.byref(shape), int(keep), int(first), int(last), *bufs,
                                   int(workspace_bytes), st), "msa_cache_evict")
+
+
+def make_rope(*, rotary_dim=128, interleaved=False, per_head_weights=False, scale=1.0, norm_eps=1e-6, norm_offset=0.0,
+              q_stride=0, k_stride=0, v_stride=0, q_idx_stride=0, idxk_stride=0) -> MsaRope:
+    """Norm and rotation of head rows; strides in elements between tokens (0: dense)."""
+    return MsaRope(rotary_dim=rotary_dim, interleaved=int(interleaved), per_head_weights=int(per_head_weights), scale=scale,
+                   norm_eps=norm_eps, norm_offset=norm_offset, q_stride=q_stride, k_stride=k_stride, v_stride=v_stride,
+                   q_idx_stride=q_idx_stride, idxk_stride=idxk_stride)
+
+
+def rope_frequencies(radians, device=None):
+    """The rotation's table (int64 bits) from angles in radians a position, one for each pair: a tensor of 64 or 32
+    bits, or a sequence of floats; on `device`, else where the tensor lies."""
+    import torch
+
+    x = torch.as_tensor(radians, dtype=torch.float64)
+    device = x.device if device is None else device
+    x = x.detach().cpu().contiguous()
+    turns = torch.empty(x.numel(), dtype=torch.int64)
+    _check(load().msa_rope_frequencies(x.data_ptr(), x.numel(), turns.data_ptr()), "msa_rope_frequencies")
+    return turns.to(device)
+
+
+def msa_qk_norm_rope(rope: MsaRope, freqs, num_tokens: int, positions, num_q_heads: int, q, q_weight, q_out,
+                     num_k_heads: int = 0, k=None, k_weight=None, k_out=None, stream=None):
+    """Norm and rotation of query heads, and of key heads in the same pass."""
+    st, (f, at, *rows) = _rows(stream, "gi" + "Rhh" * 2, (rope.q_stride, num_q_heads, rope.k_stride, num_k_heads),
+                               freqs, positions, q, q_weight, q_out, k, k_weight, k_out)
+    _check(load().msa_qk_norm_rope(ctypes.byref(rope), f, num_tokens, at, num_q_heads, *rows[:3], num_k_heads, *rows[3:],
+                                   st), "msa_qk_norm_rope")
+
+
+def msa_ragged_workspace_bytes(shape: MsaShape) -> int:
+    """Workspace of the calls on ragged batches below (0: shape not taken)."""
+    return int(load().msa_ragged_workspace_bytes(ctypes.byref(shape)))
+
+
+def msa_kv_append(shape, rope, freqs, num_tokens, offsets, k, k_weight, v, idxk, idxk_weight, q, q_weight, q_out, q_idx,
+                  q_idx_weight, q_idx_out, block_table, seq_lens, kv_pool, idxk_pool, idxk_scales, workspace,
+                  workspace_bytes, stream=None):
+    """A ragged batch's keys, values and index keys into their pages, with norm and rotation on the way, and its
+    queries and index queries in the same pass."""
+    Hkv, Hi = shape.num_kv_heads, shape.num_index_heads
+    st, (f, *bufs, ws) = _rows(
+        stream, "giRhRRhRhhRhhiibbbb",
+        (rope.k_stride, Hkv, rope.v_stride, Hkv, rope.idxk_stride, Hi, rope.q_stride, shape.num_q_heads, rope.q_idx_stride, Hi),
+        freqs, offsets, k, k_weight, v, idxk, idxk_weight, q, q_weight, q_out, q_idx, q_idx_weight, q_idx_out, block_table,
+        seq_lens, kv_pool, idxk_pool, idxk_scales, workspace)
+    _check(load().msa_kv_append(ctypes.byref(shape), ctypes.byref(rope), f, num_tokens, *bufs, ws, int(workspace_bytes), st),
+           "msa_kv_append")
 
 
 def msa_check_device_status(workspace, stream=None) -> int:

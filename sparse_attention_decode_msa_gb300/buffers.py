@@ -1,4 +1,4 @@
-"""Device buffers of the whole-cache operators as the library takes them: addresses and a stream handle.
+"""Device buffers of the whole-cache and ragged operators as the library takes them: addresses and a stream handle.
 
 A step of a small cache takes about 10 us on the GPU, so every call counts here: what torch has to be
 asked is asked once (7 tensors: 1.9 us without the element types, 2.2 with them).
@@ -12,9 +12,11 @@ _TYPES = {
     "h": frozenset((torch.bfloat16, torch.int16, torch.uint16)),  # bf16, or its bits
     "i": frozenset((torch.int32, torch.uint32)),
     "f": frozenset((torch.float32,)),
+    "g": frozenset((torch.int64, torch.uint64)),
     "b": None,  # pools and workspaces are bytes
 }
-_KINDS = {kinds: tuple(_TYPES[k] for k in kinds) for kinds in ("hbiihfb", "hbiiifffb", "fiiibbbfiib")}
+_KINDS = {kinds: tuple(_TYPES[k] for k in kinds)
+          for kinds in ("hbiihfb", "hbiiifffb", "fiiibbbfiib", "gibhhbhh", "gibhbbhbhhbhhiibbbb")}
 _Tensor, _get_device, _is_contiguous, _data_ptr = (torch.Tensor, torch.Tensor.get_device, torch.Tensor.is_contiguous,
                                                    torch.Tensor.data_ptr)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -52,3 +54,28 @@ def bufs(stream, kinds: str, *xs):
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     return stream, out
+
+
+def rows(stream, kinds: str, strides, *xs):
+    """bufs with rows of tokens among them: the letter R is a tensor [tokens, heads, 128] (or [tokens, heads * 128])
+    that may be part of a wider one, and `strides` holds the stride (0: dense) and the heads that the library will be
+    told for each."""
+    dense, i = [], 0
+    for x, kind in zip(xs, kinds):
+        if kind == "R":
+            if isinstance(x, _Tensor) and x.numel() > 0:
+                stride, heads = strides[i], strides[i + 1]
+                if x.dtype not in _TYPES["h"]:
+                    raise ValueError(f"buffer of {x.dtype}: the argument takes {' or '.join(sorted(map(str, _TYPES['h'])))}")
+                shape, step = tuple(x.shape[1:]), x.stride()
+                if shape not in ((heads, 128), (heads * 128,)) or step[-1] != 1 or (len(shape) == 2 and heads > 1 and step[1] != 128):
+                    raise ValueError(f"rows of shape {tuple(x.shape)} and strides {step}: a token's {heads} heads of 128 lie one after another")
+                if x.shape[0] > 1 and step[0] != (stride or heads * 128):
+                    raise ValueError(f"rows {step[0]} elements apart: the call says {stride or heads * 128}")
+                device = _get_device(x)
+                if device < 0 or device != torch.cuda.current_device():
+                    raise ValueError(f"buffer on {x.device}: not on the current CUDA device")
+                x = _data_ptr(x)
+            i += 2
+        dense.append(x)
+    return bufs(stream, kinds.replace("R", "b"), *dense)

@@ -1,0 +1,216 @@
+// msa_ragged_api.cu -- the C ABI of the calls on ragged batches (msa_rope_frequencies,
+// msa_qk_norm_rope, msa_kv_append): host-side validation and launches.  No
+// allocation, no state between calls.
+#include <cmath>
+
+#include "msa_ragged.cuh"
+
+namespace msa {
+namespace {
+
+constexpr size_t kAlign = 256;
+
+bool aligned16(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+msa_status cuda_status(cudaError_t e)
+{
+    return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+// The shape rules of these operators: those of the whole cache, without a number
+// of tokens a request.
+msa_status check_ragged_shape(const msa_shape *s)
+{
+    if (!s)
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (s->num_requests < 0 || s->num_kv_heads < 1 || s->num_q_heads < 1 || s->num_pages < 1 ||
+        s->max_blocks_per_seq < 1 || s->decode_ctas < 0 || s->num_index_heads < 1)
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(s->softmax_scale) || !std::isfinite(s->k_scale) || !std::isfinite(s->v_scale))
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (s->head_dim != kDim || s->page_size != kPage || s->num_q_heads % s->num_kv_heads != 0 ||
+        s->num_q_heads / s->num_kv_heads > kMaxGroup || s->num_kv_heads > kMaxKvHeads)
+        return MSA_ERR_UNSUPPORTED;
+    if (s->num_index_heads > kMaxIndexHeads || s->num_requests > kMaxRequests ||
+        s->max_blocks_per_seq > kMaxBlocks || s->decode_ctas > kMaxTokens)
+        return MSA_ERR_UNSUPPORTED;
+    if (s->kv_dtype != MSA_BF16 && s->kv_dtype != MSA_FP8_E4M3 && s->kv_dtype != MSA_NVFP4)
+        return MSA_ERR_UNSUPPORTED;
+    // row coordinates of the KV tensor map (144 rows a tile at most) fit in int32
+    if ((long long)s->num_pages * 2 * s->num_kv_heads * 144 > 0x7FFFFFFFll)
+        return MSA_ERR_UNSUPPORTED;
+    return MSA_OK;
+}
+
+msa_status check_rope(const msa_rope *r, const uint64_t *freqs)
+{
+    if (!r || r->rotary_dim < 0 || !std::isfinite(r->scale) || !std::isfinite(r->norm_offset) ||
+        !std::isfinite(r->norm_eps) || r->norm_eps < 0.f)
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (r->rotary_dim > kDim || r->rotary_dim % 16 != 0)
+        return MSA_ERR_UNSUPPORTED;
+    if (r->rotary_dim > 0 && (!freqs || !aligned16(freqs)))
+        return MSA_ERR_INVALID_ARGUMENT;
+    return MSA_OK;
+}
+
+// One kind of rows: pointers, alignment, the stride between tokens, and rows that
+// are written over their input only where they lie the same.
+msa_status add_set(AppendParams &p, const void *x, int64_t stride, const void *weight, void *y, int heads, int where, bool rotated)
+{
+    const int64_t dense = (int64_t)heads * kDim, by = stride == 0 ? dense : stride;
+    if (!x || !aligned16(x) || !aligned16(weight) || !aligned16(y) || (where == kToOut && !y) || by < dense || by % 8 != 0 ||
+        (x == y && by != dense))
+        return MSA_ERR_INVALID_ARGUMENT;
+    RowSet &s = p.set[p.sets++];
+    s.x = static_cast<const uint16_t *>(x);
+    s.weight = static_cast<const uint16_t *>(weight);
+    s.y = static_cast<uint16_t *>(y);
+    s.stride = by;
+    s.heads = heads;
+    s.group0 = p.groups;
+    s.where = where;
+    s.rotated = rotated;
+    p.groups += (heads + 3) / 4;
+    return MSA_OK;
+}
+
+void set_rope(AppendParams &p, const msa_rope *r, const uint64_t *freqs)
+{
+    p.freqs = reinterpret_cast<const unsigned long long *>(freqs);
+    p.units = r->rotary_dim / 16;
+    p.interleaved = r->interleaved != 0;
+    p.per_head = r->per_head_weights != 0;
+    p.scale = r->scale;
+    p.eps = r->norm_eps;
+    p.offset = r->norm_offset;
+}
+
+// 1 / s where a product with it is the quotient by s: s a power of two.
+float exact_inverse(float s)
+{
+    int e;
+    const float m = std::frexp(std::fabs(s), &e);
+    return m == 0.5f && e > -120 && e < 120 ? 1.f / s : 0.f;
+}
+
+} // namespace
+} // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+msa_status msa_rope_frequencies(const double *radians, int32_t count, uint64_t *turns)
+{
+    if (count < 0 || (count > 0 && (!radians || !turns)))
+        return MSA_ERR_INVALID_ARGUMENT;
+    for (int32_t i = 0; i < count; ++i) {
+        const double t = radians[i] * 0.15915494309189533577; // 1 / (2 pi)
+        if (!(std::fabs(t) < 2147483648.0))
+            return MSA_ERR_INVALID_ARGUMENT;
+        const double f = t - std::floor(t); // [0, 1]: 1 where a tiny negative one rounds up
+        turns[i] = f >= 1.0 ? 0u : static_cast<uint64_t>(std::ldexp(f, 64));
+    }
+    return MSA_OK;
+}
+
+msa_status msa_qk_norm_rope(const msa_rope *rope, const uint64_t *freqs, int32_t num_tokens,
+                            const int32_t *positions, int32_t num_q_heads, const void *q,
+                            const void *q_weight, void *q_out, int32_t num_k_heads, const void *k,
+                            const void *k_weight, void *k_out, cudaStream_t stream)
+{
+    msa_status st = check_rope(rope, freqs);
+    if (st != MSA_OK)
+        return st;
+    if (num_tokens < 0 || num_q_heads < 1 || num_k_heads < 0)
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (num_q_heads > kMaxKvHeads || num_k_heads > kMaxKvHeads || num_tokens > kMaxRows)
+        return MSA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) // rows without elements may have no address
+        return MSA_OK;
+    if (!positions || !aligned16(positions))
+        return MSA_ERR_INVALID_ARGUMENT;
+    AppendParams p{};
+    set_rope(p, rope, freqs);
+    const bool turn = p.units > 0;
+    if ((st = add_set(p, q, rope->q_stride, q_weight, q_out, num_q_heads, kToOut, turn)) != MSA_OK)
+        return st;
+    if (num_k_heads == 0 ? k || k_out
+                         : (st = add_set(p, k, rope->k_stride, k_weight, k_out, num_k_heads, kToOut, turn)) != MSA_OK)
+        return MSA_ERR_INVALID_ARGUMENT;
+    p.positions = positions;
+    p.T = num_tokens;
+    return cuda_status(launch_append(p, stream));
+}
+
+size_t msa_ragged_workspace_bytes(const msa_shape *shape)
+{
+    return check_ragged_shape(shape) == MSA_OK ? kAlign : 0;
+}
+
+msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uint64_t *freqs,
+                         int32_t num_tokens, const int32_t *offsets, const void *k,
+                         const void *k_weight, const void *v, const void *idxk,
+                         const void *idxk_weight, const void *q, const void *q_weight, void *q_out,
+                         const void *q_idx, const void *q_idx_weight, void *q_idx_out,
+                         const int32_t *block_table, const int32_t *seq_lens, void *kv_pool,
+                         void *idxk_pool, void *idxk_scales, void *workspace,
+                         size_t workspace_bytes, cudaStream_t stream)
+{
+    msa_status st = check_ragged_shape(shape);
+    if (st != MSA_OK || (st = check_rope(rope, freqs)) != MSA_OK)
+        return st;
+    const bool idx_f4 = idxk && shape->index_dtype == MSA_NVFP4;
+    if ((idxk || q_idx) && (shape->index_dim != kDim || (shape->index_dtype != MSA_BF16 && shape->index_dtype != MSA_NVFP4)))
+        return MSA_ERR_UNSUPPORTED;
+    if (num_tokens > kMaxRows)
+        return MSA_ERR_UNSUPPORTED;
+    if (num_tokens == 0 || shape->num_requests == 0) // rows without elements may have no address
+        return MSA_OK;
+    if (num_tokens < 0 || !offsets || !block_table || !seq_lens || !kv_pool || !workspace || workspace_bytes < kAlign)
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(offsets) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(kv_pool) ||
+        !aligned16(idxk_pool) || !aligned16(idxk_scales) || !aligned16(workspace))
+        return MSA_ERR_INVALID_ARGUMENT;
+    if ((idxk && !idxk_pool) || (idx_f4 && !idxk_scales) || !q != !q_out || !q_idx != !q_idx_out)
+        return MSA_ERR_INVALID_ARGUMENT;
+    AppendParams p{};
+    set_rope(p, rope, freqs);
+    const bool turn = p.units > 0;
+    const int Hkv = shape->num_kv_heads, Hi = shape->num_index_heads;
+    if (q && (st = add_set(p, q, rope->q_stride, q_weight, q_out, shape->num_q_heads, kToOut, turn)) != MSA_OK)
+        return st;
+    if (q_idx && (st = add_set(p, q_idx, rope->q_idx_stride, q_idx_weight, q_idx_out, Hi, kToOut, turn)) != MSA_OK)
+        return st;
+    if ((st = add_set(p, k, rope->k_stride, k_weight, nullptr, Hkv, kToK, turn)) != MSA_OK ||
+        (st = add_set(p, v, rope->v_stride, nullptr, nullptr, Hkv, kToV, false)) != MSA_OK)
+        return st;
+    if (idxk && (st = add_set(p, idxk, rope->idxk_stride, idxk_weight, nullptr, Hi, kToIndex, turn)) != MSA_OK)
+        return st;
+    p.offsets = offsets;
+    p.seq_lens = seq_lens;
+    p.block_table = block_table;
+    p.kv = static_cast<uint8_t *>(kv_pool);
+    p.idxk = static_cast<uint8_t *>(idxk_pool);
+    p.idxk_scales = static_cast<uint8_t *>(idxk_scales);
+    p.err = static_cast<uint32_t *>(workspace);
+    p.T = num_tokens;
+    p.R = shape->num_requests;
+    p.maxB = shape->max_blocks_per_seq;
+    p.num_pages = shape->num_pages;
+    p.Hkv = Hkv;
+    p.Hi = Hi;
+    p.kv_fmt = shape->kv_dtype == MSA_BF16 ? kFmtBf16 : shape->kv_dtype == MSA_FP8_E4M3 ? kFmtFp8 : kFmtF4;
+    p.idx_f4 = idx_f4;
+    p.k_scale = shape->k_scale;
+    p.v_scale = shape->v_scale;
+    p.k_inv = exact_inverse(p.k_scale);
+    p.v_inv = exact_inverse(p.v_scale);
+    return cuda_status(launch_append(p, stream));
+}
+
+} // extern "C"
