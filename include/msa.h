@@ -434,6 +434,34 @@ msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uin
                          void *idxk_pool, void *idxk_scales, void *workspace,
                          size_t workspace_bytes, cudaStream_t stream);
 
+/* Attention of a ragged batch's query rows over paged states: token j of request r
+ * sees positions 0 .. seq_lens[r] + j - 1 (causal: a prompt, a chunk of one, or a
+ * step, its own keys and values appended before), or all seq_lens[r] of them (not
+ * causal: cross attention to states of another length).  The result of
+ * msa_dense_decode without its limits on tokens.
+ *   q, out       bf16 [num_tokens][Hq][128]
+ *   lse          fp32 [num_tokens][Hq]
+ * num_q_heads is any multiple G of num_kv_heads with 1 <= G <= 64.  seq_lens[r] may
+ * be 0: no states, outputs of 0 and lse -inf.  Offsets that go down or past
+ * num_tokens, a negative length and one that the table cannot hold are reported
+ * through the error word and the request is skipped; a page id outside the pool is
+ * reported, and the outputs of the call are unspecified.  Bytes behind the last
+ * position may hold anything; an infinity or NaN in V reaches the outputs that see
+ * its position, in that dimension, and no other.  Sums and the softmax are fp32, in a
+ * fixed order (the same inputs give the same bits).  Probabilities meet V as bf16
+ * over bf16 pages, and the sum that divides is that of the rounded ones: an output
+ * is a mean of values with weights that are off by 2^-8 of themselves at most, and
+ * sum to 1.  Over E4M3 and NVFP4 pages they are fp16 (2^-11), and queries meet
+ * the keys as fp16 after a power of two (elements 2^-23 below a row's largest lose bits).
+ * decode_ctas > 0 sets the persistent CTAs (at most 8192); 0 takes one per SM.
+ * Nothing is kept in the workspace between calls but the error word: calls that may
+ * overlap, and CUDA graphs that may, need a workspace each. */
+msa_status msa_ragged_attention(const msa_shape *shape, int32_t num_tokens, int32_t causal,
+                                const void *q, const int32_t *offsets, const void *kv_pool,
+                                const int32_t *block_table, const int32_t *seq_lens, void *out,
+                                float *lse, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
 /* Size of the fixed device scratch used by msa_sparse_decode_noalloc. */
 #define MSA_NOALLOC_SCRATCH_BYTES (8u << 20)
 

@@ -48,12 +48,12 @@ def to_codes(x, values):
     return np.where((x < 0) & (near > 0), near + (128 if len(values) > 8 else 8), near).astype(np.uint8)
 
 
-def attention(pb, q, offsets, seq_lens, causal):
-    """out, lse of ragged query rows (bf16 bits [T, Hq, 128]) over pb's pages, and the largest sums of |q||k| scale
-    and |v|; NaN in rows of no request."""
+def attention(pb, q, offsets, seq_lens, causal, distances=True):
+    """out, lse of ragged query rows (bf16 bits [T, Hq, 128]) over pb's pages, NaN in rows of no request; for tolerances
+    the values' weighted mean distance from each output, and the largest sums of |q||k| scale and |v|."""
     T, Hq = q.shape[:2]
     G = Hq // pb.num_kv_heads
-    out, lse = np.full((T, Hq, DIM), np.nan), np.full((T, Hq), np.nan)
+    out, lse, far = np.full((T, Hq, DIM), np.nan), np.full((T, Hq), np.nan), np.zeros((T, Hq, DIM))
     big_s = big_v = 0.0
     for r in range(len(seq_lens)):
         n, L = int(offsets[r + 1] - offsets[r]), int(seq_lens[r])
@@ -77,6 +77,9 @@ def attention(pb, q, offsets, seq_lens, causal):
                 x = s[j, :, :seen]
                 m = x.max(-1, keepdims=True)
                 p = np.exp(x - m)
-                out[at, heads][j] = (p @ v[:seen]) / p.sum(-1, keepdims=True)
-                lse[at, heads][j] = (m + np.log(p.sum(-1, keepdims=True)))[:, 0]
-    return out, lse, big_s, big_v
+                p /= (total_p := p.sum(-1, keepdims=True))
+                with np.errstate(invalid="ignore"):
+                    o = out[at, heads][j] = p @ v[:seen]
+                    far[at, heads][j] = np.sum(p[:, :, None] * np.abs(v[:seen] - o[:, None]), 1) if distances else 0
+                lse[at, heads][j] = (m + np.log(total_p))[:, 0]
+    return out, lse, far, big_s, big_v

@@ -99,6 +99,8 @@ _SIGNATURES = {
     "msa_ragged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MsaShape)]),
     "msa_kv_append": (ctypes.c_int, [ctypes.POINTER(MsaShape), ctypes.POINTER(MsaRope), _p, ctypes.c_int32] + [
         _p] * 18 + [ctypes.c_size_t, _p]),
+    "msa_ragged_attention": (ctypes.c_int, [ctypes.POINTER(MsaShape), ctypes.c_int32, ctypes.c_int32] + [_p] * 8 + [
+        ctypes.c_size_t, _p]),
     "msa_set_decode_wait_limit": (ctypes.c_int, [ctypes.c_int64]),
     "msa_check_device_status": (ctypes.c_int, [_p, _p]),
     "msa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -329,6 +331,15 @@ def msa_kv_append(shape, rope, freqs, num_tokens, offsets, k, k_weight, v, idxk,
         seq_lens, kv_pool, idxk_pool, idxk_scales, workspace)
     _check(load().msa_kv_append(ctypes.byref(shape), ctypes.byref(rope), f, num_tokens, *bufs, ws, int(workspace_bytes), st),
            "msa_kv_append")
+
+
+def msa_ragged_attention(shape, num_tokens, causal, q, offsets, kv_pool, block_table, seq_lens, out, lse, workspace,
+                         workspace_bytes, stream=None):
+    """Attention of a ragged batch's query rows: causal (prompts, chunks, steps), or over all states of
+    another length (cross attention)."""
+    st, bufs = _bufs(stream, "hibiihfb", q, offsets, kv_pool, block_table, seq_lens, out, lse, workspace)
+    _check(load().msa_ragged_attention(ctypes.byref(shape), num_tokens, int(causal), *bufs, int(workspace_bytes), st),
+           "msa_ragged_attention")
 
 
 def msa_check_device_status(workspace, stream=None) -> int:

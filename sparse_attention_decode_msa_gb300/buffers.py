@@ -16,7 +16,8 @@ _TYPES = {
     "b": None,  # pools and workspaces are bytes
 }
 _KINDS = {kinds: tuple(_TYPES[k] for k in kinds)
-          for kinds in ("hbiihfb", "hbiiifffb", "fiiibbbfiib", "gibhhbhh", "gibhbbhbhhbhhiibbbb")}
+          for kinds in ("hbiihfb", "hbiiifffb", "fiiibbbfiib", "gibhhbhh", "gibhbbhbhhbhhiibbbb",
+                        "hibiihfb")}
 _Tensor, _get_device, _is_contiguous, _data_ptr = (torch.Tensor, torch.Tensor.get_device, torch.Tensor.is_contiguous,
                                                    torch.Tensor.data_ptr)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)

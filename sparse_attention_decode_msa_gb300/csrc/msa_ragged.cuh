@@ -41,6 +41,26 @@ struct AppendParams {
     float k_inv, v_inv;         // 1 / scale where that is exact (a power of two), else 0
 };
 
+// A unit cut between CTAs: its first cut is this record's CTA's start (c0 < 0: there is none).
+struct AttendJoin {
+    int token0, rows, head; // its first token's row, its query rows, its KV head
+    int c0, c1;             // the CTAs that have parts of it
+    int pad[3];
+};
+
+struct AttendParams : CacheParams { // (nq is not used)
+    uint16_t *out;          // bf16 bits [T][Hq][D]
+    float *lse;             // [T][Hq]
+    const int32_t *offsets; // [R + 1]
+    float *partial;         // 2 slots a CTA
+    AttendJoin *joins;      // one a CTA
+    float v_scale;
+    int T, unit_tokens;
+    bool causal;
+};
+
+size_t attend_slot_bytes();
+cudaError_t launch_attend(const AttendParams &p, int kv_dtype, int ctas, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 
 } // namespace msa

@@ -1,5 +1,5 @@
 // msa_ragged_api.cu -- the C ABI of the calls on ragged batches (msa_rope_frequencies,
-// msa_qk_norm_rope, msa_kv_append): host-side validation and launches.  No
+// msa_qk_norm_rope, msa_kv_append, msa_ragged_attention): host-side validation and launches.  No
 // allocation, no state between calls.
 #include <cmath>
 
@@ -89,6 +89,32 @@ void set_rope(AppendParams &p, const msa_rope *r, const uint64_t *freqs)
     p.offset = r->norm_offset;
 }
 
+struct RaggedLayout {
+    size_t joins_off, partial_off, total;
+};
+
+RaggedLayout layout_of(const msa_shape *s)
+{
+    const size_t ctas = s->decode_ctas > 0 ? s->decode_ctas : kCacheCtaBound;
+    RaggedLayout w;
+    w.joins_off = kAlign; // after the error word
+    w.partial_off = align_to(w.joins_off + ctas * sizeof(AttendJoin), kAlign);
+    w.total = align_to(w.partial_off + 2 * ctas * attend_slot_bytes(), kAlign);
+    return w;
+}
+
+// Persistent CTAs: the shape's, else one per SM; -1 if the device cannot be read.
+int attend_ctas(const msa_shape *s)
+{
+    if (s->decode_ctas > 0)
+        return s->decode_ctas;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+        return -1;
+    return sms < kCacheCtaBound ? sms : kCacheCtaBound;
+}
+
 // 1 / s where a product with it is the quotient by s: s a power of two.
 float exact_inverse(float s)
 {
@@ -149,7 +175,7 @@ msa_status msa_qk_norm_rope(const msa_rope *rope, const uint64_t *freqs, int32_t
 
 size_t msa_ragged_workspace_bytes(const msa_shape *shape)
 {
-    return check_ragged_shape(shape) == MSA_OK ? kAlign : 0;
+    return check_ragged_shape(shape) == MSA_OK ? layout_of(shape).total : 0;
 }
 
 msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uint64_t *freqs,
@@ -211,6 +237,54 @@ msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uin
     p.k_inv = exact_inverse(p.k_scale);
     p.v_inv = exact_inverse(p.v_scale);
     return cuda_status(launch_append(p, stream));
+}
+
+msa_status msa_ragged_attention(const msa_shape *shape, int32_t num_tokens, int32_t causal,
+                                const void *q, const int32_t *offsets, const void *kv_pool,
+                                const int32_t *block_table, const int32_t *seq_lens, void *out,
+                                float *lse, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream)
+{
+    msa_status st = check_ragged_shape(shape);
+    if (st != MSA_OK)
+        return st;
+    if (num_tokens < 0)
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (num_tokens > kMaxRows)
+        return MSA_ERR_UNSUPPORTED;
+    if (num_tokens == 0 || shape->num_requests == 0) // rows without elements may have no address
+        return MSA_OK;
+    const RaggedLayout w = layout_of(shape);
+    if (!q || !offsets || !kv_pool || !block_table || !seq_lens || !out || !lse || !workspace || workspace_bytes < w.total)
+        return MSA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(q) || !aligned16(offsets) || !aligned16(kv_pool) || !aligned16(block_table) || !aligned16(seq_lens) ||
+        !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
+        return MSA_ERR_INVALID_ARGUMENT;
+    const int ctas = attend_ctas(shape);
+    if (ctas < 1)
+        return MSA_ERR_CUDA;
+    AttendParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.kv = static_cast<const uint8_t *>(kv_pool);
+    p.err = static_cast<uint32_t *>(workspace);
+    p.R = shape->num_requests;
+    p.Hkv = shape->num_kv_heads;
+    p.G = shape->num_q_heads / shape->num_kv_heads;
+    p.maxB = shape->max_blocks_per_seq;
+    p.num_pages = shape->num_pages;
+    p.scale_log2 = shape->softmax_scale * 1.4426950408889634f * (shape->kv_dtype != MSA_BF16 ? shape->k_scale : 1.f);
+    p.wait_limit = decode_wait_limit();
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.offsets = offsets;
+    p.joins = reinterpret_cast<AttendJoin *>(static_cast<uint8_t *>(workspace) + w.joins_off);
+    p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.partial_off);
+    p.v_scale = shape->kv_dtype != MSA_BF16 ? shape->v_scale : 1.f;
+    p.T = num_tokens;
+    p.causal = causal != 0;
+    return cuda_status(launch_attend(p, shape->kv_dtype, ctas, stream));
 }
 
 } // extern "C"

@@ -236,6 +236,90 @@ __device__ __forceinline__ void widen_row(const uint8_t *src, uint8_t *tile, int
     }
 }
 
+// One stored K (0) or V (1) value in global memory, without its tensor scale.
+template <int FMT>
+__device__ __forceinline__ float stored_value(const uint8_t *kv, long long tile, int row, int d)
+{
+    float a, b;
+    if (FMT == kFmtBf16)
+        return __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t *>(kv + (tile * kPage + row) * 256 + 2 * d) << 16);
+    if (FMT == kFmtFp8) {
+        f16x2_to_f32x2(e4m3x2_to_f16x2(kv[(tile * kPage + row) * 128 + d]), a, b);
+        return a;
+    }
+    const uint8_t *t = kv + tile * 9216;
+    const uint32_t byte = t[row * 64 + (d >> 1)];
+    f16x2_to_f32x2(e2m1x2_to_f16x2(d & 1 ? byte >> 4 : byte & 15u), a, b);
+    const float v = a;
+    f16x2_to_f32x2(e4m3x2_to_f16x2(t[8192 + row * 8 + (d >> 4)]), a, b);
+    return v * a;
+}
+
+__device__ __forceinline__ bool finite(float v)
+{
+    return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
+}
+
+// Row `row` of a ring tile (E4M3, NVFP4) to f16 in the layout of a 16-bit tile; dst is the row's place in its
+// first half.  On a last page (tail) a row that is not cached becomes zeros (drop), and infinities
+// and NaN of a row that only later tokens see (check) do too: true is returned for those.
+template <int FMT>
+__device__ __forceinline__ bool convert_row(const uint8_t *src, uint8_t *dst, int row, bool tail, bool drop, bool check)
+{
+    bool bad = false;
+    if (FMT == kFmtFp8) {
+#pragma unroll 2 // (all: 426 us for 413, 48 tokens over 2 x 131072; NVFP4 loses with less, 507 for 488)
+        for (int c = 0; c < 8; ++c) { // 16 dimensions
+            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
+            uint32_t e[4] = {d.x, d.y, d.z, d.w}, o[8];
+            if (tail) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    if (check && ((e[q >> 2] >> (8 * (q & 3))) & 0x7Fu) == 0x7Fu)
+                        e[q >> 2] &= ~(0xFFu << (8 * (q & 3))), bad = true;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    e[q] = drop ? 0u : e[q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                e4m3x4_to_f16x2x2(e[q], o[2 * q], o[2 * q + 1]);
+            uint8_t *at = dst + (c >> 2) * 16384;
+            *reinterpret_cast<uint4 *>(at + (((2 * c) & 7) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(at + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    } else {
+        uint64_t sc = *reinterpret_cast<const uint64_t *>(src + 8192 + row * 8);
+        uint32_t zero = 0u; // 16-dim groups that become zeros
+        if (tail) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (check && ((sc >> (8 * q)) & 0x7Fu) == 0x7Fu)
+                    zero |= 1u << q, bad = true;
+            zero = drop ? 0xFFu : zero;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if ((zero >> q) & 1u)
+                    sc &= ~(0xFFull << (8 * q)); // a scale of 0: products of 0
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) { // 32 dimensions, two scales
+            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+            const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)(sc >> (16 * c)) & 0xFFFFu);
+            const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+            uint8_t *at = dst + (c >> 1) * 16384;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[4];
+                e2m1x8_scaled_f16x2(e[q], q < 2 ? sa : sb, o);
+                *reinterpret_cast<uint4 *>(at + ((((c & 1) * 4 + q) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+    return bad;
+}
+
 // The share of a CTA, unit by unit.  Every role walks it alike.
 struct Walk {
     int x, x1, r, u, b, nb, seq_len, seg;
