@@ -6,18 +6,19 @@
 // maximum, out = sum 2^(s - m) V / sum 2^(s - m), lse = m + ln sum, in one pass over the
 // pages, fp32.
 //
-// Work.  The rows of a (request, KV head) are cut into units of T = floor(256 / G) tokens
-// with their G heads, at most 256 rows; a unit's pages are those that its last token
-// sees.  All units laid end to end (request, KV head, unit) are a line of pages that is
-// cut into equal ranges, one a CTA, whatever the lengths are; a unit cut between CTAs is
+// Work.  The rows of a (request, KV head) are cut into units of T = 2 floor(128 / G)
+// tokens with their G heads, at most 256 rows; a unit's pages are those that its last token
+// sees.  All units laid end to end (request, KV head, unit), each with a few pages' time for its
+// queries and outputs in front (kUnitCost), are a line that is cut into equal ranges, one a CTA,
+// whatever the lengths are; a unit cut between CTAs is
 // joined by attend_join_kernel in the order of its pages.  Pages before unit i of a causal
 // request are a sum of floors, which a Euclid-like recursion gives in a few steps: no
 // table, no kernel before this one.
 //
-// Two streams of 128 rows share a CTA's pages, so that the tensor cores work for one while
-// the other is in its softmax: rows 128 t .. of the unit are stream t's, and both take
-// every page; a unit of up to 128 rows goes to both streams, which take its pages in
-// turn, and their (m, l, O) are added at the end.
+// Two streams of up to 128 rows share a CTA's pages, so that the tensor cores work for one
+// while the other is in its softmax: tokens t floor(128 / G) .. of the unit are stream t's, and
+// both take every page; a unit whose tokens fit in one stream goes to both, which take its pages
+// in turn, and their (m, l, O) are added at the end.
 //
 // Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA lands them, P in
 // tensor memory over the S it came from, V tiles as landed (MN-major).  E4M3 and NVFP4 tiles
@@ -30,9 +31,9 @@
 // has it, doubles the products of P V.)
 //
 // TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
-// Warps: 0 TMA producer, 1 issues all MMAs (and owns the TMEM), 2 clears what must not be
-// multiplied from V tiles on last pages (bf16), 3 outputs of requests without states, 4-7
-// and 8-11 softmax of stream 0 and 1, 12-15 converters (E4M3, NVFP4).
+// Warps: 0 TMA producer, 1 and 2 issue the MMAs of stream 0 and 1 (1 owns the TMEM), 3 clears what
+// must not be multiplied from V tiles on last pages (bf16) and writes the outputs of requests
+// without states, 4-7 and 8-11 softmax of stream 0 and 1, 12-15 converters (E4M3, NVFP4).
 #include <type_traits>
 
 #include "msa_ragged.cuh"
@@ -44,25 +45,17 @@ namespace {
 constexpr int kRows = 256;       // query rows of a unit
 constexpr int kTile16 = 32768;   // a 16-bit K, V or Q tile
 constexpr int kStaged = 4;       // widened tiles in flight
-constexpr float kSlack = 8.f;    // how far (log2) a row's maximum may pass its reference before O is rescaled
-constexpr float kPUp16 = 7.f;    // f16 P: 2^7 2^(s - m), at most 2^15 with the slack
-constexpr int kSlotFloats = kRows * (kDim + 3); // o[rows][128], m, l, l of the rounded p
-constexpr int kMinPages = 2;     // pages a CTA takes at least
+constexpr float kMost = 0x1p16f;   // what the p of a page may add up to before the row's reference rises
+constexpr float kMost16 = 0x1p15f; // the same where P is f16
+constexpr float kPUp16 = 7.f;      // f16 P: 2^7 2^(s - m)
+constexpr int kSlotFloats = kRows * (kDim + 2); // o[rows][128], m, l
+constexpr int kUnitCost = 2;     // a unit's queries and outputs in pages
+constexpr int kMinRange = 4;     // what a CTA takes at least
 
 __host__ __device__ constexpr int threads_of(int fmt)
 {
     return fmt == kFmtBf16 ? 384 : 512;
 }
-
-// Registers a thread of warpgroup 0, of the softmax warpgroups (whose threads hold a row of 128 columns,
-// or half of one) and of the converters.  The sums are what the block is launched with (168 and 128 a thread).
-constexpr int kRegs0 = 72;
-__host__ __device__ constexpr int regs_softmax(int fmt)
-{
-    return fmt == kFmtBf16 ? 216 : 176;
-}
-constexpr int kRegsConv = 88;
-static_assert(kRegs0 + 2 * regs_softmax(kFmtBf16) <= 3 * 168 && kRegs0 + 2 * regs_softmax(kFmtFp8) + kRegsConv <= 4 * 128, "registers");
 
 __host__ __device__ constexpr int ring_tiles(int fmt)
 {
@@ -79,17 +72,17 @@ __host__ __device__ constexpr int ready_tiles(int fmt)
     return fmt == kFmtBf16 ? ring_tiles(fmt) : kStaged;
 }
 
-// Barriers: full[], empty[] of the ring, ready[], ready_free[] (widened tiles), q_full, q_free, s_full[2],
-// p_full[2][2], pv_done[2], o_free[2], drain.
+// Barriers: full[], empty[] of the ring, ready[], ready_free[] (widened tiles), and for each stream
+// q_raw (their copy), q_full, s_full, p_full, pv_done, o_free, drain.
 __host__ __device__ constexpr Smem smem_layout(int fmt)
 {
     Smem s{};
     s.staged = ring_tiles(fmt) * tile_bytes(fmt);
     s.q = s.staged + (fmt == kFmtBf16 ? 0 : kStaged * kTile16);
-    s.ml = s.q + 2 * kTile16;   // m[128], l[128], rounded l[128] of stream 1 (units of up to 128 rows)
-    s.inv = s.ml + 3 * 128 * 4; // factors that undo the scaling of query rows
-    s.bars = s.inv + (fmt == kFmtBf16 ? 0 : kRows * 4);
-    s.misc = s.bars + (2 * ring_tiles(fmt) + 2 * ready_tiles(fmt) + 13) * 8;
+    s.ml = s.q + 2 * kTile16;   // m[128], l[128] of stream 1 (units of up to 128 rows)
+    s.inv = s.ml + 2 * 128 * 4; // exponents that undo the scaling of query rows, of two units
+    s.bars = s.inv + (fmt == kFmtBf16 ? 0 : 2 * kRows);
+    s.misc = s.bars + (2 * ring_tiles(fmt) + 2 * ready_tiles(fmt) + 14) * 8;
     s.total = s.misc + 256;
     return s;
 }
@@ -139,13 +132,13 @@ struct Request {
     {
         return (seen(p, u) + (p.causal ? tokens(p, u) - 1 : 0) + kPage - 1) / kPage;
     }
-    // pages of units 0 .. u - 1 of one KV head
+    // the line's length up to unit u of one KV head
     __device__ __forceinline__ long long before(const AttendParams &p, int u) const
     {
         if (!p.causal)
-            return (long long)u * pages(p, 0);
+            return (long long)u * (kUnitCost + pages(p, 0));
         const int k = u < units ? u : units - 1; // all units but the last have unit_tokens tokens
-        return floor_sum(k, kPage, p.unit_tokens, L + p.unit_tokens + kPage - 2) + (u > k ? pages(p, k) : 0);
+        return floor_sum(k, kPage, p.unit_tokens, L + p.unit_tokens + kPage - 2) + (long long)u * kUnitCost + (u > k ? pages(p, k) : 0);
     }
 };
 
@@ -186,24 +179,30 @@ __device__ __forceinline__ int cut_of(long long x, long long W, int n)
 
 // The share of a CTA, unit by unit.  Every role walks it alike.
 struct Share {
-    long long x, x1;
     Request q;
+    int left; // of the line, from this unit's beginning to the range's end; 0: no pages any more
     int r, head, u, b, nb, seg;
-    __device__ __forceinline__ int pages() const { return (int)min((long long)(nb - b), x1 - x); }
-    __device__ __forceinline__ int rows(const AttendParams &p) const { return q.tokens(p, u) * p.G; }
+    __device__ __forceinline__ int pages() const { return min(nb, left - kUnitCost) - b; }
+    __device__ __forceinline__ int token0(const AttendParams &p) const { return q.first + u * p.unit_tokens; }
+    __device__ __forceinline__ bool two(const AttendParams &p) const { return 2 * q.tokens(p, u) > p.unit_tokens; }
+    __device__ __forceinline__ bool last() const { return left - (kUnitCost + nb) <= kUnitCost; }
     __device__ __forceinline__ void next(const AttendParams &p)
     {
-        x += pages();
+        left = last() ? 0 : left - (kUnitCost + nb);
         ++seg;
         b = 0;
+        if (left == 0)
+            return;
         if (++u == q.units) {
             u = 0;
             if (++head == p.Hkv) {
                 head = 0;
                 bool bad, idle;
                 do {
-                    if (++r >= p.R)
-                        return; // the end of the line: x = x1
+                    if (++r >= p.R) { // (the line is as long as the ranges say)
+                        left = 0;
+                        return;
+                    }
                     q = read_request(p, r, &bad, &idle);
                 } while (q.units == 0);
             }
@@ -212,14 +211,17 @@ struct Share {
     }
 };
 
-// Place of a tile in the order in which the issuer uses the tiles of n pages.
-__device__ __forceinline__ int order_of_k(bool two, int page)
+// The order in which the issuers use the tiles of n pages: K and V of each page, or, where the streams take
+// pages in turn, both K and both V of each pair of pages.
+__device__ __forceinline__ bool tile_of(bool two, int n, int i, int *page)
 {
-    return two ? 2 * page : page < 2 ? page : 2 * page - 1;
-}
-__device__ __forceinline__ int order_of_v(bool two, int page, int n)
-{
-    return two ? 2 * page + 1 : min(2 * page + 2, 2 * n - 1);
+    if (two) {
+        *page = i >> 1;
+        return !(i & 1);
+    }
+    const int first = i >> 2 << 1, pair = min(2, n - first), in = i & 3;
+    *page = first + (in & (pair - 1));
+    return in < pair;
 }
 
 // Rows of a staged bf16 V tile on a last page: rows from `past` on are not in the request and become
@@ -255,9 +257,167 @@ __device__ __forceinline__ void clear_rows(uint8_t *v, int seen, int past, volat
     __syncwarp();
 }
 
+// The largest sc s over the first `seen` columns of this thread's row of S, -inf for none.
+__device__ __noinline__ float row_maximum(uint32_t at_s, float sc, int seen)
+{
+    const float inf = __uint_as_float(0x7F800000u);
+    float top[2] = {-inf, -inf}, low[2] = {inf, inf};
+#pragma unroll 1
+    for (int c = 0; c < kPage; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(at_s + c, v);
+        tmem_wait_ld(v);
+        if (__any_sync(0xffffffffu, seen < c + 32)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if (c + k < seen) {
+                    top[0] = fmaxf(top[0], __uint_as_float(v[k]));
+                    low[0] = fminf(low[0], __uint_as_float(v[k]));
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+                top[k >> 1 & 1] = fmaxf(top[k >> 1 & 1], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                low[k >> 1 & 1] = fminf(low[k >> 1 & 1], fminf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+            }
+        }
+    }
+    // which end of the row is the largest goes by the scale's sign
+    return seen <= 0 ? -inf : sc < 0.f ? fminf(low[0], low[1]) * sc : fmaxf(top[0], top[1]) * sc;
+}
+
+// 128 columns of this thread's row of S to p = 2^(sc s - ref), as pairs of bf16 (f16) in pr; their
+// sum.  TAIL: columns from `seen` on are 0.
+template <bool F16, bool TAIL>
+__device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, int seen, uint32_t (&pr)[64])
+{
+    const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
+    uint64_t sum[2] = {0ull, 0ull};
+    uint32_t v[2][16];
+    tmem_ld16_async(at_s, v[0]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint32_t(&x)[16] = v[c & 1];
+        tmem_wait_ld16(x);
+        if (c < 7) // on their way meanwhile
+            tmem_ld16_async(at_s + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            float e0, e1;
+            unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc2, ref2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            if (TAIL) {
+                e0 = 16 * c + k < seen ? e0 : 0.f;
+                e1 = 16 * c + k + 1 < seen ? e1 : 0.f;
+            }
+            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
+            pr[8 * c + (k >> 1)] = F16 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+        }
+    }
+    float a, b;
+    unpair(add2(sum[0], sum[1]), a, b);
+    return a + b;
+}
+
+// Infinities and NaN of V at positions from .. to - 1, which were kept out of the products, for a row that
+// sees them: into its output, or into its partial one in a slot.
+template <int FMT>
+__device__ __noinline__ void add_late_values(const AttendParams &p, const Share &at, long long row, int from, int to, float ref, float *slot)
+{
+    for (int pos = from; pos < to; ++pos) {
+        const long long page = p.block_table[(size_t)at.r * p.maxB + pos / kPage];
+        if (page < 0 || page >= p.num_pages)
+            continue;
+        float pr = 0.f;
+        bool have = false;
+        for (int d = 0; d < kDim; ++d) {
+            const float x = stored_value<FMT>(p.kv, (page * 2 + 1) * p.Hkv + at.head, pos % kPage, d);
+            if (finite(x))
+                continue;
+            if (!have) {
+                const uint16_t *q = p.q + row * kDim;
+                for (int e = 0; e < kDim; ++e)
+                    pr = fmaf(__uint_as_float((uint32_t)q[e] << 16), stored_value<FMT>(p.kv, page * 2 * p.Hkv + at.head, pos % kPage, e), pr);
+                pr = ex2(fmaf(pr, p.scale_log2, -ref));
+                have = true;
+            }
+            if (slot) {
+                slot[(d >> 2) * (4 * kRows) + (d & 3)] += pr * x;
+            } else {
+                uint16_t *o = p.out + row * kDim + d;
+                *o = (uint16_t)pack_bf16(__uint_as_float((uint32_t)*o << 16) + pr * x, 0.f);
+            }
+        }
+    }
+}
+
+// Four 16-byte pieces of each of four neighbouring lanes: d[k] becomes piece lane % 4 of lane k of the four.
+__device__ __forceinline__ void transpose4(uint4 (&d)[4])
+{
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1) {
+        const bool high = threadIdx.x & m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & m)
+                continue;
+            uint32_t *a = &d[i].x, *b = &d[i | m].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? a[k] : b[k], m);
+                a[k] = high ? got : a[k];
+                b[k] = high ? b[k] : got;
+            }
+        }
+    }
+}
+
+// The query rows of an operand tile from bf16 to f16, in place, by four warps: each row after a power of two
+// that brings its largest element to [2^8, 2^9) (exact; elements 2^-23 below it lose bits), whose
+// exponent is told with the sign turned.
+__device__ __forceinline__ void widen_queries(uint8_t *tile, int8_t *exps)
+{
+    const int lane = threadIdx.x & 31, c = lane & 15, first = 2 * ((threadIdx.x >> 5) & 3) + (lane >> 4);
+#pragma unroll 1
+    for (int i0 = 0; i0 < 128; i0 += 32) {
+        uint4 d[4];
+        float mx[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + 8 * u + first;
+            d[u] = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * 16384 + 128 * i + (((c & 7) ^ (i & 7)) << 4));
+            const uint32_t *e = &d[u].x;
+            mx[u] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mx[u] = fmaxf(mx[u], fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], o));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + 8 * u + first;
+            int x = (int)(__float_as_uint(mx[u]) >> 23) - 127; // clamped so that neither factor overflows
+            x = x < -100 ? -100 : x > 127 ? 127 : x;
+            const float up = __uint_as_float((uint32_t)(8 - x + 127) << 23);
+            uint32_t *e = &d[u].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                e[k] = pack_f16(__uint_as_float(e[k] << 16) * up, __uint_as_float(e[k] & 0xFFFF0000u) * up);
+            *reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + 128 * i + (((c & 7) ^ (i & 7)) << 4)) = d[u];
+            if (c == 0)
+                exps[i] = (int8_t)(x - 8);
+        }
+    }
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
-    attend_kernel(const __grid_constant__ CUtensorMap map, const AttendParams p)
+    attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map, const AttendParams p)
 {
     constexpr int TILES = ring_tiles(FMT), TB = tile_bytes(FMT), NT = threads_of(FMT);
     constexpr bool CONV = FMT != kFmtBf16;
@@ -267,8 +427,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     Misc &misc = *reinterpret_cast<Misc *>(gsm + L.misc);
     constexpr int DEPTH = ready_tiles(FMT);
     const uint32_t full = smem + L.bars, empty = full + TILES * 8, ready = empty + TILES * 8, ready_free = ready + DEPTH * 8;
-    const uint32_t q_full = ready_free + DEPTH * 8, q_free = q_full + 8, s_full = q_free + 8, p_full = s_full + 16,
-                   pv_done = p_full + 32, o_free = pv_done + 16, drain = o_free + 16;
+    const uint32_t q_full = ready_free + DEPTH * 8, s_full = q_full + 16, p_full = s_full + 16, pv_done = p_full + 16,
+                   o_free = pv_done + 16, drain = o_free + 16, q_raw = CONV ? drain + 16 : q_full;
     volatile int *abort_flag = &misc.abort;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long wl = p.wait_limit;
@@ -283,24 +443,25 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map);
+        prefetch_tensormap(&q_map);
         for (int i = 0; i < TILES; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, CONV ? 4 : 1); // the converter warps, or the issuer
+            mbar_init(empty + 8 * i, CONV ? 4 : 2); // the converter warps, or the issuers
         }
         for (int i = 0; i < DEPTH; ++i) {
             mbar_init(ready + 8 * i, CONV ? 4 : 1); // the converter warps, or the clearing warp
-            mbar_init(ready_free + 8 * i, 1);
+            mbar_init(ready_free + 8 * i, 2);
         }
-        mbar_init(q_full, 8);
-        mbar_init(q_free, 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(q_full + 8 * t, CONV ? 4 : 1); // the converter warps, or the copy itself
+            if (CONV)
+                mbar_init(q_raw + 8 * t, 1);
+            mbar_init(drain + 8 * t, 1);
             mbar_init(s_full + 8 * t, 1);
-            mbar_init(p_full + 16 * t, 4);
-            mbar_init(p_full + 16 * t + 8, 4);
+            mbar_init(p_full + 8 * t, 4);
             mbar_init(pv_done + 8 * t, 1);
             mbar_init(o_free + 8 * t, 4);
         }
-        mbar_init(drain, 1);
         fence_mbar_init();
         misc.abort = 0;
     }
@@ -337,18 +498,17 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         before += i < warp ? misc.scan[i] : 0;
         W += misc.scan[i];
     }
-    const int ranges = (int)min((long long)gridDim.x, max(1ll, W / kMinPages));
+    const int ranges = (int)min((long long)gridDim.x, max(1ll, W / kMinRange));
     Share w{};
-    w.x = (int)blockIdx.x < ranges ? cut(blockIdx.x, W, ranges) : W;
-    w.x1 = (int)blockIdx.x < ranges ? cut(blockIdx.x + 1, W, ranges) : W;
-    w.nb = 1;
-    if (w.x < w.x1 && before <= w.x && w.x < before + mine) {
+    const long long x0 = (int)blockIdx.x < ranges ? cut(blockIdx.x, W, ranges) : W;
+    const long long x1 = (int)blockIdx.x < ranges ? cut(blockIdx.x + 1, W, ranges) : W;
+    if (x0 < x1 && before <= x0 && x0 < before + mine) {
         long long at = before;
         for (int r = lo; r < hi; ++r) {
             bool bad, idle;
             const Request q = read_request(p, r, &bad, &idle);
             const long long some = q.units ? q.before(p, q.units) * p.Hkv : 0;
-            if (at <= w.x && w.x < at + some) {
+            if (at <= x0 && x0 < at + some) {
                 misc.start_r = r;
                 misc.start_before = at;
             }
@@ -359,11 +519,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = misc.tmem;
-    if (w.x < w.x1) {
+    if (x0 < x1) {
         bool bad, idle;
         w.r = misc.start_r;
         w.q = read_request(p, w.r, &bad, &idle);
-        const long long in = w.x - misc.start_before, each = w.q.before(p, w.q.units);
+        const long long in = x0 - misc.start_before, each = w.q.before(p, w.q.units);
         w.head = (int)(in / each);
         const long long rest = in - w.head * each;
         // the last unit with before(u) <= rest: the lanes try 32 at a time
@@ -375,464 +535,408 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             w.u += k * step;
             n = min(step, n - k * step);
         }
-        w.b = (int)(rest - w.q.before(p, w.u));
+        const int in_unit = (int)(rest - w.q.before(p, w.u));
+        w.b = max(0, in_unit - kUnitCost);
         w.nb = w.q.pages(p, w.u);
+        w.left = (int)(x1 - x0) + in_unit; // (the host has seen that it fits)
+        if (w.left <= kUnitCost + w.b)     // the range ends before the unit's first page
+            w.left = 0;
     }
     if (threadIdx.x == 0) {
         AttendJoin j{};
         j.c0 = -1;
-        if (w.x < w.x1 && w.b > 0) {
-            const int c0 = cut_of(w.x - w.b, W, ranges);
+        if (w.left > 0 && w.b > 0) {
+            const int c0 = cut_of(x0 - w.b, W, ranges); // (x0 is page b)
             if (c0 == (int)blockIdx.x - 1) {
-                j.token0 = w.q.first + w.u * p.unit_tokens;
-                j.rows = w.rows(p);
+                j.token0 = w.token0(p);
+                j.tokens = w.q.tokens(p, w.u);
                 j.head = w.head;
                 j.c0 = c0;
-                j.c1 = cut_of(w.x - w.b + w.nb - 1, W, ranges);
+                j.c1 = cut_of(x0 - w.b + w.nb - 1, W, ranges);
             }
         }
         p.joins[blockIdx.x] = j;
     }
     // a wait that ran out: the CTA's roles run on without waiting, so that all
-    // reach the end; what they compute is unspecified.  (Inlined: a kernel that moves registers
-    // between its warpgroups can call nothing.)
+    // reach the end; what they compute is unspecified
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (mbar_test_wait(bar, parity))
-            return;
-        const bool poll = wl < (1 << 16); // a test's limit: the suspending form may sleep past it
-        const long long start = clock64();
-        while (!(poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
-            if (*abort_flag)
-                return;
-            if (clock64() - start > wl) {
-                *abort_flag = 1;
-                set_error(p.err, kErrTimeout);
-                return;
-            }
+        if (!ring_wait(bar, parity, abort_flag, wl) && !*abort_flag) {
+            *abort_flag = 1;
+            set_error(p.err, kErrTimeout);
         }
     };
 
-    if (warp < 4) {
-        setmaxnreg_dec<kRegs0>();
-        if (warp == 0) {
-            // ---- producer: K and V tiles in the order of their use ----
-            int z = 0, st = 0;
-            uint32_t ph = 0;
-            for (; w.x < w.x1; w.next(p)) {
-                const int n = w.pages();
-                const bool two = w.rows(p) > 128;
-                const int32_t *row = p.block_table + (size_t)w.r * p.maxB + w.b;
-                // two windows of 32 table entries: K runs at most two pages ahead of V
-                int ent = 0, ent0 = -1, prev = 0;
-                int kp = 0, vp = 0;
-                for (int i = 0; i < 2 * n; ++i) {
-                    const bool is_k = kp < n && order_of_k(two, kp) == i;
-                    const int pg = is_k ? kp++ : vp++;
-                    const int win = pg >> 5;
-                    if (win > ent0) {
-                        prev = ent;
-                        ent0 = win;
-                        ent = 32 * win + lane < n ? row[32 * win + lane] : 0;
-                    }
-                    long long page = __shfl_sync(0xffffffffu, win == ent0 ? ent : prev, pg & 31);
-                    if (page < 0 || page >= p.num_pages) {
-                        if (lane == 0)
-                            set_error(p.err, kErrPage);
-                        page = 0; // in the pool: the outputs of the call are unspecified
-                    }
-                    if (z >= TILES)
-                        wait(empty + 8 * st, ph ^ 1u);
-                    if (__any_sync(0xffffffffu, *abort_flag != 0))
-                        break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(full + 8 * st, TB);
-                        load_tile<FMT>(smem + st * TB, &map, p.kv, (page * 2 + (is_k ? 0 : 1)) * p.Hkv + w.head, full + 8 * st);
-                    }
-                    __syncwarp();
-                    ++z;
-                    if (++st == TILES) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
+    if (warp == 0) {
+        // ---- producer: K and V tiles in the order of their use ----
+        int z = 0, st = 0;
+        uint32_t ph = 0;
+        for (; w.left > 0; w.next(p)) {
+            const int n = w.pages();
+            const bool two = w.two(p);
+            const int32_t *row = p.block_table + (size_t)w.r * p.maxB + w.b;
+            int ent = 0, ent0 = -1;
+            for (int i = 0; i < 2 * n; ++i) {
+                int pg;
+                const bool is_k = tile_of(two, n, i, &pg);
+                const int win = pg >> 5; // (a pair of pages lies in one window)
+                if (win > ent0) {
+                    ent0 = win;
+                    ent = 32 * win + lane < n ? row[32 * win + lane] : 0;
                 }
+                long long page = __shfl_sync(0xffffffffu, ent, pg & 31);
+                if (page < 0 || page >= p.num_pages) {
+                    if (lane == 0)
+                        set_error(p.err, kErrPage);
+                    page = 0; // in the pool: the outputs of the call are unspecified
+                }
+                if (z >= TILES)
+                    wait(empty + 8 * st, ph ^ 1u);
                 if (__any_sync(0xffffffffu, *abort_flag != 0))
                     break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full + 8 * st, TB);
+                    load_tile<FMT>(smem + st * TB, &map, p.kv, (page * 2 + (is_k ? 0 : 1)) * p.Hkv + w.head, full + 8 * st);
+                }
+                __syncwarp();
+                ++z;
+                if (++st == TILES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
             }
-            if (lane == 0) // the CTA's memory must outlive the copies in flight
-                for (int i = max(0, z - TILES); i < z; ++i)
-                    mbar_wait_bounded(full + 8 * (i % TILES), (uint32_t)(i / TILES) & 1u);
-            __syncwarp();
-        } else if (warp == 1) {
-            // ---- MMA issuer.  Step j is a page of one stream (t = j & 1): S(j), then P V(j) once its
-            // softmax is done, then S(j + 2) behind it, while the other stream is in its softmax ----
-            const uint32_t one = lane == 0, tm = uniform(tmem), base = uniform(smem);
-            constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
-            constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, 0, 0) & kTypes;
-            constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
-            constexpr uint32_t RING = CONV ? L.staged : 0;
-            const uint32_t tile_free = CONV ? ready_free : empty;
-            uint32_t done0 = 0, done1 = 0; // P V of either stream so far
-            int z0 = 0;
-            for (; w.x < w.x1; w.next(p)) {
-                const int n = w.pages();
-                const bool two = w.rows(p) > 128;
-                const int nsteps = two ? 2 * n : n;
-                auto score = [&](int j) {
-                    const int t = j & 1, z = z0 + order_of_k(two, two ? j >> 1 : j), st = z % DEPTH;
-                    const uint32_t k = uniform(desc_low(base + RING + st * kTile16, 16)), q = uniform(desc_low(base + L.q + (two ? t * kTile16 : 0), 16));
-                    const uint32_t d = tm + uniform(128 * t), done = t ? done1 : done0;
-                    wait(ready + 8 * st, (uint32_t)(z / DEPTH) & 1u);
-                    if (done > 0) // P, which S replaces, has been multiplied
-                        wait(pv_done + 8 * t, (done - 1) & 1u);
-                    tcgen05_after_sync();
+            if (__any_sync(0xffffffffu, *abort_flag != 0))
+                break;
+        }
+        if (lane == 0) // the CTA's memory must outlive the copies in flight
+            for (int i = max(0, z - TILES); i < z; ++i)
+                mbar_wait_bounded(full + 8 * (i % TILES), (uint32_t)(i / TILES) & 1u);
+        __syncwarp();
+    } else if (warp < 3) {
+        // ---- MMA issuer of stream t: S of a page, then, once its softmax is done, P V of it and S of the
+        // stream's next page, while the other stream's products fill the tensor cores.  (One
+        // issuer for both spends longer on its own instructions between two MMAs than an MMA takes.) ----
+        const int t = warp - 1;
+        const uint32_t one = elect_one(), tm = uniform(tmem), base = uniform(smem);
+        constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
+        constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, 0, 0) & kTypes;
+        constexpr uint32_t idesc_o = umma_idesc_bf16(128, 128, 0, 1) & kTypes;
+        constexpr uint32_t RING = CONV ? L.staged : 0;
+        const uint32_t tile_free = CONV ? ready_free : empty;
+        const uint32_t q = uniform(desc_low(base + L.q + t * kTile16, 16)), d_s = tm + uniform(128 * t), d_o = tm + uniform(256 + 128 * t);
+        const uint32_t ring = uniform((base + RING) >> 4);
+        uint32_t done = 0; // steps of this stream so far
+        int st0 = 0;       // the unit's first tile: its slot and the slot's phase
+        uint32_t ph0 = 0;
+        for (; w.left > 0; w.next(p)) {
+            const int n = w.pages();
+            const bool two = w.two(p);
+            // (stream 1 of a small unit's only page takes a step without a product: no barrier's phase is passed over)
+            const bool null = !two && n <= t;
+            const int nsteps = two ? n : max(1, (n + 1 - t) >> 1), stride = two ? 2 : 4;
+            // slot and phase of the tile i places behind the unit's first
+            auto slot_of = [&](int i, uint32_t &ph) {
+                const int z = st0 + i, turns = z / DEPTH;
+                ph = (ph0 + turns) & 1u;
+                return uniform(z - turns * DEPTH);
+            };
+            // a tile is given back, once its products are done, by both streams, or twice by the one that uses it
+            auto give_back = [&](uint32_t st) {
+                umma_commit(tile_free + 8 * st);
+                if (!two)
+                    umma_commit(tile_free + 8 * st);
+            };
+            wait(q_full + 8 * t, w.seg & 1);
+            // S of step i into the S buffer (its K tile has been waited for)
+            auto score = [&](uint32_t st) {
+                const uint32_t k = (ring + st * (kTile16 >> 4) & 0x3FFFu) | (16u >> 4) << 16;
+                tcgen05_after_sync();
+                if (!null) {
 #pragma unroll
                     for (uint32_t ks = 0; ks < 8; ++ks)
-                        umma_ss(one, d, q + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 1024 + (ks & 3) * 2, idesc_s, ks > 0);
-                    if (one) {
-                        umma_commit(s_full + 8 * t);
-                        if (!two || t)
-                            umma_commit(tile_free + 8 * st);
-                        if (j == nsteps - 1)
-                            umma_commit(q_free);
-                    }
-                    __syncwarp();
-                };
-                wait(q_full, w.seg & 1);
-                score(0);
-                if (nsteps > 1)
-                    score(1);
-                for (int j = 0; j < nsteps; ++j) {
-                    const int t = j & 1, page = two ? j >> 1 : j, z = z0 + order_of_v(two, page, n), st = z % DEPTH;
-                    const uint32_t v = uniform(desc_low(base + RING + st * kTile16, 16384));
-                    const uint32_t a = tm + uniform(128 * t), d = tm + uniform(256 + 128 * t), more = uniform(j > 1); // a stream's first step of the unit sets O
-                    wait(ready + 8 * st, (uint32_t)(z / DEPTH) & 1u);
-                    if (j < 2 && w.seg > 0)
-                        wait(o_free + 8 * t, (w.seg - 1) & 1);
-                    const uint32_t done = t ? done1++ : done0++;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        wait(p_full + 16 * t + 8 * h, done & 1u);
-                        tcgen05_after_sync();
-                        // V, MN-major: 16 positions are 16 rows of 128 bytes
-#pragma unroll
-                        for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                            umma_ts(one, d, a + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
-                    }
-                    if (one) {
-                        umma_commit(pv_done + 8 * t);
-                        if (!two || t)
-                            umma_commit(tile_free + 8 * st);
-                    }
-                    __syncwarp();
-                    if (j + 2 < nsteps)
-                        score(j + 2);
-                    if (__any_sync(0xffffffffu, *abort_flag != 0)) // all lanes alike
-                        break;
+                        umma_ss(one, d_s, q + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 1024 + (ks & 3) * 2, idesc_s, ks > 0);
                 }
-                z0 += 2 * n;
-                if (__any_sync(0xffffffffu, *abort_flag != 0))
-                    break;
-            }
-            // nothing of this CTA's may be in flight when its tensor memory is freed
-            if (one) {
-                umma_commit(drain);
-                mbar_wait_bounded(drain, 0);
-            }
+                if (elect_one())
+                    umma_commit(s_full + 8 * t);
+                __syncwarp();
+            };
+            uint32_t k_ph, k_st = slot_of(two ? 0 : t, k_ph);
+            if (!null)
+                wait(ready + 8 * k_st, k_ph);
+            score(k_st); // (P V of the unit before, which reads what S replaces, was waited for at its end)
+            if (!null && elect_one())
+                give_back(k_st);
             __syncwarp();
-        } else if (warp == 2 && !CONV) {
-            // ---- clearing of V tiles (converters do it for theirs).  Every tile passes this warp on its way
-            // to the issuer, so that no barrier gets two phases ahead of it ----
-            int z = 0;
-            for (; w.x < w.x1; w.next(p)) {
-                const int n = w.pages(), seen = w.q.seen(p, w.u), past = seen + (p.causal ? w.q.tokens(p, w.u) - 1 : 0);
-                const bool two = w.rows(p) > 128;
-                int kp = 0, vp = 0;
-                for (int i = 0; i < 2 * n; ++i, ++z) {
-                    const bool is_k = kp < n && order_of_k(two, kp) == i;
-                    const int pg = w.b + (is_k ? kp++ : vp++), st = z % TILES;
-                    wait(full + 8 * st, (uint32_t)(z / TILES) & 1u);
-                    if (!is_k && (pg + 1) * kPage > seen)
-                        clear_rows(gsm + st * TB, seen - pg * kPage, past - pg * kPage, &misc.later_bad[w.seg & 7], w.seg + 1);
-                    if (lane == 0)
-                        mbar_arrive(ready + 8 * st);
-                    __syncwarp();
+            for (int i = 0; i < nsteps; ++i, ++done) {
+                // everything that can be known and waited for before P is there
+                uint32_t v_ph; // (V lies behind both K of the pair, or the only one)
+                const uint32_t v_st = slot_of(i * stride + (two ? 1 : min(2, n - 2 * i) + t), v_ph);
+                const uint32_t v = (ring + v_st * (kTile16 >> 4) & 0x3FFFu) | (16384u >> 4) << 16, more = uniform(i > 0);
+                const bool again = i + 1 < nsteps;
+                if (!null)
+                    wait(ready + 8 * v_st, v_ph);
+                if (again) {
+                    k_st = slot_of((i + 1) * stride + (two ? 0 : t), k_ph);
+                    wait(ready + 8 * k_st, k_ph);
                 }
+                if (i == 0 && w.seg > 0) // the last unit's O has been read
+                    wait(o_free + 8 * t, (w.seg - 1) & 1);
+                wait(p_full + 8 * t, done & 1u);
+                tcgen05_after_sync();
+                if (!null) {
+                    // V, MN-major: 16 positions are 16 rows of 128 bytes
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_ts(one, d_o, d_s + 8 * ks, v + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : more);
+                }
+                if (elect_one())
+                    umma_commit(pv_done + 8 * t);
+                __syncwarp();
+                wait(pv_done + 8 * t, done & 1u); // before S replaces P
+                if (again)
+                    score(k_st);
+                if (!null && elect_one()) {
+                    give_back(v_st);
+                    if (again)
+                        give_back(k_st);
+                }
+                __syncwarp();
             }
-        } else if (warp == 3) {
-            // ---- outputs of requests without states ----
-            for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
-                bool bad, idle;
-                const Request q = read_request(p, r, &bad, &idle);
-                if (!idle)
-                    continue;
-                const size_t rows = (size_t)p.Hkv * p.G, all = rows * q.n;
-                uint4 *out = reinterpret_cast<uint4 *>(p.out + rows * q.first * kDim);
-                for (size_t i = lane; i < all * (kDim / 8); i += 32)
-                    out[i] = make_uint4(0u, 0u, 0u, 0u);
-                for (size_t i = lane; i < all; i += 32)
-                    p.lse[rows * q.first + i] = __uint_as_float(0xFF800000u);
+            const int turns = (st0 + 2 * n) / DEPTH;
+            st0 += 2 * n - turns * DEPTH;
+            ph0 ^= turns & 1u;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) // all lanes alike
+                break;
+        }
+        // nothing of this CTA's may be in flight when its tensor memory is freed
+        if (one) {
+            umma_commit(drain + 8 * t);
+            mbar_wait_bounded(drain + 8 * t, 0);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ---- clearing of V tiles (converters do it for theirs).  Every tile passes this warp on its way
+        // to the issuers, so that no barrier gets two phases ahead of it ----
+        int z = 0;
+        for (; !CONV && w.left > 0; w.next(p)) {
+            const int n = w.pages(), seen = w.q.seen(p, w.u), past = seen + (p.causal ? w.q.tokens(p, w.u) - 1 : 0);
+            const bool two = w.two(p);
+            for (int i = 0; i < 2 * n; ++i, ++z) {
+                int pg;
+                const bool is_k = tile_of(two, n, i, &pg);
+                const int st = z % TILES;
+                pg += w.b;
+                wait(full + 8 * st, (uint32_t)(z / TILES) & 1u);
+                if (!is_k && (pg + 1) * kPage > seen)
+                    clear_rows(gsm + st * TB, seen - pg * kPage, past - pg * kPage, &misc.later_bad[w.seg & 7], w.seg + 1);
+                if (lane == 0)
+                    mbar_arrive(ready + 8 * st);
+                __syncwarp();
             }
+        }
+        // ---- outputs of requests without states ----
+        for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+            bool bad, idle;
+            const Request q = read_request(p, r, &bad, &idle);
+            if (!idle)
+                continue;
+            const size_t rows = (size_t)p.Hkv * p.G, all = rows * q.n;
+            uint4 *out = reinterpret_cast<uint4 *>(p.out + rows * q.first * kDim);
+            for (size_t i = lane; i < all * (kDim / 8); i += 32)
+                out[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (size_t i = lane; i < all; i += 32)
+                p.lse[rows * q.first + i] = __uint_as_float(0xFF800000u);
         }
     } else if (warp < 12) {
         // ---- softmax: thread = query row ----
-        setmaxnreg_inc<regs_softmax(FMT)>();
         const int t = (warp - 4) >> 2, at_lane = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21); // this warp's lane quarter
         const uint32_t at_s = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
         const float ninf = __uint_as_float(0xFF800000u);
         float *ml = reinterpret_cast<float *>(gsm + L.ml);
-        float *qinv = reinterpret_cast<float *>(gsm + L.inv);
-        const size_t Hq = (size_t)p.Hkv * p.G;
+        const int8_t *exps = reinterpret_cast<const int8_t *>(gsm + L.inv) + 128 * t;
+        const int Hq = p.Hkv * p.G, each = p.unit_tokens >> 1; // tokens of a stream
         uint32_t steps = 0, steps1 = 0; // of this stream and of stream 1 so far
         auto sync_all = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-        // Query rows of unit u into the operand tiles, once the last S of the unit before is done: before
-        // that unit's outputs are written, so that S goes on meanwhile.  Rows beyond the unit's
-        // are left as they are: nothing is read from what they give.
-        auto stage_queries = [&](const Share &u) {
-            const int rows = u.rows(p);
-            const bool two = rows > 128;
-            const int row0 = two ? 128 * t : 0;
-            const size_t first = (size_t)(u.q.first + u.u * p.unit_tokens) * Hq + (size_t)u.head * p.G;
-            sync_all();
-            if (u.seg > 0)
-                wait(q_free, (u.seg - 1) & 1);
-            stage_rows<CONV ? kRowsF16 : kRows16>(
-                gsm + L.q + (two ? t * kTile16 : 0), 16384, min(128, rows - row0), two ? warp & 3 : warp - 4, two ? 4 : 8,
-                [&](int i) {
-                    const int j = (row0 + i) / p.G;
-                    return p.q + (first + j * Hq + (row0 + i - j * p.G)) * kDim;
-                },
-                [&](int i, float x) { qinv[row0 + i] = x; });
-            fence_async_smem();
-            if (CONV)
-                sync_all();
+        // Query rows of a unit into the stream's operand tile, once the stream's last S of the unit
+        // before is done.  Rows beyond the unit's hold anything: nothing is read from what they give.
+        auto copy_queries = [&](const Share &u) {
+            if (elect_one()) {
+                const int token = u.token0(p) + (u.two(p) ? each * t : 0);
+                const uint32_t dst = smem + L.q + t * kTile16, bar = q_raw + 8 * t;
+                mbar_arrive_expect_tx(bar, 2 * 128 * p.G * each);
+                tma_load_3d(dst, &q_map, 0, u.head * p.G, token, bar);
+                tma_load_3d(dst + 16384, &q_map, 64, u.head * p.G, token, bar);
+            }
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(q_full);
         };
-        if (w.x < w.x1)
-            stage_queries(w);
-        Share nx = w;
-        for (; w.x < w.x1; w = nx) {
-            const int n = w.pages(), rows = w.rows(p);
-            const bool two = rows > 128;
-            const int nsteps = two ? n : (n + 1 - t) >> 1; // this stream's
-            const int slot_row = (two ? 128 * t : 0) + at_lane, j = min(slot_row, rows - 1) / p.G;
-            const bool real = slot_row < rows;
-            const bool idle = (two ? 128 * t : 0) + (warp & 3) * 32 >= rows; // no row of this warp's is the unit's
-            const size_t out_row = (size_t)(w.q.first + w.u * p.unit_tokens + j) * Hq + (size_t)w.head * p.G + (min(slot_row, rows - 1) - j * p.G);
-            const float sc = p.scale_log2 * (CONV && real ? qinv[slot_row] : 1.f);
-            const bool neg = sc < 0.f;
+        if (w.left > 0 && warp == 4 + 4 * t)
+            copy_queries(w);
+        while (w.left > 0) {
+            const int n = w.pages();
+            const bool two = w.two(p);
+            const bool null = !two && n <= t; // (see the issuers)
+            const int nsteps = two ? n : max(1, (n + 1 - t) >> 1); // this stream's
+            steps1 += two ? n : max(1, n >> 1);
+            const int rows = (two && t ? w.q.tokens(p, w.u) - each : min(each, w.q.tokens(p, w.u))) * p.G; // the stream's
+            const bool real = at_lane < rows, idle = (warp & 3) * 32 >= rows; // idle: no row of this warp's is the unit's
+            const int j = (two ? each * t : 0) + min(at_lane, rows - 1) / p.G;  // the row's token
+            float sc = p.scale_log2;
+            // (the exponents are there once S is)
+            auto scale_row = [&] {
+                if (CONV && real)
+                    sc *= __uint_as_float((uint32_t)(exps[kRows * (w.seg & 1) + at_lane] + 127) << 23);
+            };
             const int seen0 = w.q.seen(p, w.u), lim = seen0 + (p.causal ? j : 0);
-            steps1 += two ? n : n >> 1;
-            float m = ninf, l = 0.f, lr = 0.f; // reference maximum, sum, sum of the rounded p
-            for (int i = 0; i < nsteps; ++i, ++steps) {
-                const int pos0 = (w.b + (two ? i : 2 * i + t)) * kPage;
-                const bool tail = pos0 + kPage > seen0;
-                const int seen = tail ? lim - pos0 : kPage; // columns this row sees
-                wait(s_full + 8 * t, steps & 1u);
-                if (idle) {
-                    if (lane == 0) {
-                        mbar_arrive(p_full + 16 * t);
-                        mbar_arrive(p_full + 16 * t + 8);
+            float m = 0.f, l = 0.f; // reference and sum
+            // A row's reference is its maximum over the first page.  Later pages are not searched for theirs:
+            // p may pass 1 as long as it stays a number that P and the sums can hold, which the sum of a
+            // page tells; where a row's passes kMost its warp's rows get new references before P is written.
+            auto new_reference = [&](int i, int seen) {
+                const float mx = row_maximum(at_s, sc, seen) - (CONV ? kPUp16 : 0.f);
+                const float ref = mx == ninf ? 0.f : mx, f = i > 0 && mx > m ? ex2(m - ref) : 1.f;
+                m = i == 0 || mx > m ? ref : m;
+                l *= f;
+                if (i > 0) {
+                    wait(pv_done + 8 * t, (steps - 1) & 1u); // O holds every step before this one
+                    tcgen05_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        float o[16];
+                        tmem_ld16(o_at + 16 * c, o);
+                        uint32_t r[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            r[k] = __float_as_uint(o[k] * f);
+                        tmem_st16(o_at + 16 * c, r);
                     }
+                }
+            };
+            auto page_done = [&](const uint32_t *pr) {
+                tmem_st32(at_s, pr);
+                tmem_st32(at_s + 32, pr + 32);
+                tmem_wait_st();
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_full + 8 * t);
+            };
+            // all pages but the last of the share and those that some row does not see to their end
+            const int step = two ? kPage : 2 * kPage, pos1 = (w.b + (two ? 0 : t)) * kPage;
+            const int whole_pages = idle || null ? 0 : max(0, min(nsteps - 1, (seen0 - kPage - pos1 >= 0 ? (seen0 - kPage - pos1) / step + 1 : 0)));
+            int i = 0;
+#pragma unroll 1
+            for (; i < whole_pages; ++i, ++steps) {
+                wait(s_full + 8 * t, steps & 1u);
+                tcgen05_after_sync();
+                if (i == 0) {
+                    scale_row();
+                    new_reference(0, kPage);
+                }
+                uint32_t pr[64];
+                float sum = row_to_p<CONV, false>(at_s, sc, m, kPage, pr);
+                if (__any_sync(0xffffffffu, sum > (CONV ? kMost16 : kMost)) && i > 0) {
+                    new_reference(i, kPage);
+                    sum = row_to_p<CONV, true>(at_s, sc, m, kPage, pr);
+                }
+                l += sum;
+                page_done(pr);
+            }
+#pragma unroll 1
+            for (; i < nsteps; ++i, ++steps) {
+                const int seen = min(kPage, lim - (pos1 + i * step)); // columns this row sees
+                wait(s_full + 8 * t, steps & 1u);
+                if (i == nsteps - 1 && !w.last() && warp == 4 + 4 * t) {
+                    Share nx = w; // S was the last to read this unit's
+                    nx.next(p);
+                    copy_queries(nx);
+                }
+                if (idle || null) {
+                    if (lane == 0)
+                        mbar_arrive(p_full + 8 * t);
                     continue;
                 }
                 tcgen05_after_sync();
-                // the extreme logit of the row (the scale's sign says which end).  The columns stay in
-                // registers; where converters need some, columns 0 .. 63 do and the others are read again
-                constexpr int HELD = CONV ? 64 : 128;
-                uint32_t v[HELD];
-                float mx = neg ? -ninf : ninf;
-#pragma unroll
-                for (int c = 128 - HELD; c >= 0; c -= HELD) {
-#pragma unroll
-                    for (int h = 0; h < HELD; h += 32)
-                        tmem_ld32(at_s + c + h, v + h);
-#pragma unroll
-                    for (int h = 0; h < HELD; h += 32)
-                        tmem_wait_ld(v + h);
-                    if (tail || neg) {
-#pragma unroll
-                        for (int k = 0; k < HELD; ++k)
-                            if (c + k < seen)
-                                mx = neg ? fminf(mx, __uint_as_float(v[k])) : fmaxf(mx, __uint_as_float(v[k]));
-                    } else {
-                        float m4[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll
-                        for (int k = 0; k < HELD; k += 2)
-                            m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
-                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                    }
+                if (i == 0) {
+                    scale_row();
+                    new_reference(0, seen);
                 }
-                mx *= sc;
-                if (tail && seen <= 0)
-                    mx = ninf;
-                if (CONV)
-                    mx -= kPUp16;
-                const bool rise = mx > m + kSlack || (m == ninf && mx > ninf);
-                if (__any_sync(0xffffffffu, rise)) { // rare, and so everything that it needs is in here
-                    const float f = rise ? ex2(m - mx) : 1.f;
-                    m = rise ? mx : m;
-                    l *= f;
-                    lr *= f;
-                    if (i > 0) {
-                        wait(pv_done + 8 * t, (steps - 1) & 1u); // O holds every step before this one
-                        tcgen05_after_sync();
-#pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            float o[16];
-                            tmem_ld16(o_at + 16 * c, o);
-                            uint32_t r[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                r[k] = __float_as_uint(o[k] * f);
-                            tmem_st16(o_at + 16 * c, r);
-                        }
-                    }
+                uint32_t pr[64];
+                float sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr);
+                if (__any_sync(0xffffffffu, sum > (CONV ? kMost16 : kMost)) && i > 0) {
+                    new_reference(i, seen);
+                    sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr);
                 }
-                const float ref = m == ninf ? 0.f : m;
-                const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
-                uint64_t sum[2] = {0ull, 0ull}, sumr[2] = {0ull, 0ull};
-                // the common step by itself, without the tests for a last page
-                auto to_p = [&](auto plain) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) { // 32 columns of S become P
-                        if (HELD == 64 && c == 2) {
-                            tmem_ld32(at_s + 64, v);
-                            tmem_ld32(at_s + 96, v + 32);
-                            tmem_wait_ld(v);
-                            tmem_wait_ld(v + 32);
-                        }
-                        uint32_t hi[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int at = 32 * c + 2 * k, x = at % HELD;
-                            float e0, e1;
-                            unpair(fma2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sc2, ref2), e0, e1);
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
-                            if (!plain.value) {
-                                e0 = at < seen ? e0 : 0.f;
-                                e1 = at + 1 < seen ? e1 : 0.f;
-                            }
-                            sum[k & 1] = add2(sum[k & 1], pair(e0, e1));
-                            if (CONV) {
-                                hi[k] = pack_f16(e0, e1);
-                            } else {
-                                hi[k] = pack_bf16(e0, e1);
-                                sumr[k & 1] = add2(sumr[k & 1], pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xFFFF0000u)));
-                            }
-                        }
-                        tmem_st16(at_s + 16 * c, hi);
-                        if (c & 1) { // half of P: the issuer can begin
-                            tmem_wait_st();
-                            tcgen05_before_sync();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(p_full + 16 * t + 8 * (c >> 1));
-                        }
-                    }
-                };
-                if (tail)
-                    to_p(std::false_type{});
-                else
-                    to_p(std::true_type{});
-                float a, b;
-                unpair(add2(sum[0], sum[1]), a, b);
-                l += a + b;
-                if (!CONV) {
-                    unpair(add2(sumr[0], sumr[1]), a, b);
-                    lr += a + b;
-                }
+                l += sum;
+                page_done(pr);
             }
-            if (CONV)
-                lr = l;
 
             // ---- end of the unit's share ----
-            const bool more = w.x + n < w.x1;
-            nx.next(p);
-            if (more)
-                stage_queries(nx);
-            const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
-            float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * kSlotFloats;
+            const Share at = w;
+            w.next(p);
+            const bool whole = at.b == 0 && n == at.nb, ends = at.b + n == at.nb;
             float M = m, fa = 1.f, fb = 0.f;
             if (!two) {
                 if (t == 1) {
                     ml[at_lane] = m;
                     ml[128 + at_lane] = l;
-                    ml[256 + at_lane] = lr;
                 }
                 sync_all();
-                const float mb = ml[at_lane], lb = ml[128 + at_lane], lrb = ml[256 + at_lane];
+                const float mb = ml[at_lane], lb = ml[128 + at_lane];
                 sync_all();
                 if (t == 1)
                     continue; // stream 0 reads both accumulators
-                M = fmaxf(m, mb);
-                fa = m == ninf ? 0.f : ex2(m - M);
-                fb = mb == ninf ? 0.f : ex2(mb - M);
+                // (a sum of 0: no column, and any reference)
+                M = l == 0.f ? mb : lb == 0.f ? m : fmaxf(m, mb);
+                fa = l == 0.f ? 0.f : ex2(m - M);
+                fb = lb == 0.f ? 0.f : ex2(mb - M);
                 l = l * fa + lb * fb;
-                lr = lr * fa + lrb * fb;
             }
-            if (n > 1 || two || t == 0)
-                wait(pv_done + 8 * t, (steps - 1) & 1u);
-            if (!two && n > 1) // stream 1 has given all its P: the last of its products is the one under way
+            wait(pv_done + 8 * t, (steps - 1) & 1u);
+            if (!two) // stream 1 has given all its P: the last of its products is the one under way
                 wait(pv_done + 8, (steps1 - 1) & 1u);
             tcgen05_after_sync();
-            const float fin = lr > 0.f || lr != lr ? p.v_scale / lr : 0.f;
-            const bool bad = misc.later_bad[w.seg & 7] == w.seg + 1;
+            const long long out_row = (long long)(at.token0(p) + j) * Hq + at.head * p.G + min(at_lane, rows - 1) % p.G;
+            const int slot_row = (two ? 128 * t : 0) + at_lane;
+            float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * kSlotFloats;
+            const float fin = whole ? (l > 0.f || l != l ? p.v_scale / l : 0.f) : 1.f;
+            const float ga = fa * fin, gb = n > 1 ? fb * fin : 0.f; // (with one page stream 1 has no O)
+            long long rows_of_four[4]; // of the lane's group of four lanes, for stores of 64 bytes a row
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                rows_of_four[k] = __shfl_sync(0xffffffffu, out_row, (lane & 28) + k);
 #pragma unroll 1
-            for (int c = 0; c < 8 && !idle; ++c) {
-                float a[16];
-                tmem_ld16(o_at + 16 * c, a);
+            for (int c = 0; c < 4 && !idle; ++c) {
+                uint32_t a[32];
+                tmem_ld32(o_at + 32 * c, a);
+                tmem_wait_ld(a);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    a[k] = __float_as_uint(fa != 0.f ? __uint_as_float(a[k]) * ga : 0.f);
                 if (!two) {
-                    float o[16];
-                    tmem_ld16(o_at + 128 + 16 * c, o);
+                    uint32_t o[32];
+                    tmem_ld32(o_at + 128 + 32 * c, o);
+                    tmem_wait_ld(o);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        a[k] = a[k] * fa + (n > 1 ? o[k] * fb : 0.f); // (with one page stream 1 has no O)
+                    for (int k = 0; k < 32; ++k)
+                        a[k] = __float_as_uint(__uint_as_float(a[k]) + (gb != 0.f ? __uint_as_float(o[k]) * gb : 0.f));
                 }
-                if (bad) { // infinities and NaN of later tokens' V, for the rows that see them
-                    const float ref = M == ninf ? 0.f : M;
-                    for (int pos = max(seen0, w.b * kPage); pos < min(lim, (w.b + n) * kPage); ++pos) {
-                        const long long page = p.block_table[(size_t)w.r * p.maxB + pos / kPage];
-                        if (page < 0 || page >= p.num_pages)
-                            continue;
-                        float pr = 0.f;
-                        bool have = false;
+                if (whole) {
+                    uint4 d[4];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float x = stored_value<FMT>(p.kv, (page * 2 + 1) * p.Hkv + w.head, pos % kPage, 16 * c + k);
-                            if (finite(x))
-                                continue;
-                            if (!have) {
-                                const uint16_t *qv = p.q + out_row * kDim;
-                                for (int d = 0; d < kDim; ++d)
-                                    pr = fmaf(__uint_as_float((uint32_t)qv[d] << 16),
-                                              stored_value<FMT>(p.kv, page * 2 * p.Hkv + w.head, pos % kPage, d), pr);
-                                pr = ex2(fmaf(pr, p.scale_log2, -ref));
-                                have = true;
-                            }
-                            a[k] = fmaf(pr, x, a[k]);
-                        }
-                    }
-                }
-                if (real) {
-                    if (whole) {
-                        uint4 d[2];
-                        uint32_t *e = &d[0].x;
+                    for (int k = 0; k < 4; ++k)
+                        d[k] = make_uint4(pack_bf16(__uint_as_float(a[8 * k]), __uint_as_float(a[8 * k + 1])),
+                                          pack_bf16(__uint_as_float(a[8 * k + 2]), __uint_as_float(a[8 * k + 3])),
+                                          pack_bf16(__uint_as_float(a[8 * k + 4]), __uint_as_float(a[8 * k + 5])),
+                                          pack_bf16(__uint_as_float(a[8 * k + 6]), __uint_as_float(a[8 * k + 7])));
+                    transpose4(d); // d[k]: piece lane % 4 of row k of the four
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            e[k] = pack_bf16(a[2 * k] * fin, a[2 * k + 1] * fin);
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + out_row * kDim + 16 * c);
-                        dst[0] = d[0];
-                        dst[1] = d[1];
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(slot + (size_t)slot_row * kDim + 16 * c);
+                    for (int k = 0; k < 4; ++k)
+                        if ((at_lane & ~3) + k < rows)
+                            *reinterpret_cast<uint4 *>(p.out + rows_of_four[k] * kDim + 32 * c + 8 * (lane & 3)) = d[k];
+                } else if (real) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            dst[k] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
-                    }
+                    for (int k = 0; k < 8; ++k) // 16-byte piece i of row r of a slot lies at i kRows + r
+                        reinterpret_cast<uint4 *>(slot)[(8 * c + k) * kRows + slot_row] = make_uint4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
                 }
             }
             tcgen05_before_sync();
@@ -846,24 +950,33 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 if (whole) {
                     p.lse[out_row] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
                 } else {
-                    slot[(size_t)kRows * kDim + slot_row] = M;
+                    slot[(size_t)kRows * kDim + slot_row] = l == 0.f ? ninf : M;
                     slot[(size_t)kRows * (kDim + 1) + slot_row] = l;
-                    slot[(size_t)kRows * (kDim + 2) + slot_row] = lr;
                 }
+                if (misc.later_bad[at.seg & 7] == at.seg + 1)
+                    add_late_values<FMT>(p, at, out_row, max(seen0, at.b * kPage), min(lim, (at.b + n) * kPage), M,
+                                         whole ? nullptr : slot + 4 * slot_row);
             }
         }
     } else if constexpr (CONV) {
         // ---- converters: a ring tile to a 16-bit tile, in the order of use ----
-        setmaxnreg_dec<kRegsConv>();
         const int row = threadIdx.x & 127;
         int z = 0;
-        for (; w.x < w.x1; w.next(p)) {
+        for (; w.left > 0; w.next(p)) {
             const int n = w.pages(), seen = w.q.seen(p, w.u), past = seen + (p.causal ? w.q.tokens(p, w.u) - 1 : 0);
-            const bool two = w.rows(p) > 128;
-            int kp = 0, vp = 0;
+            const bool two = w.two(p);
+            for (int t = 0; t < 2; ++t) {
+                wait(q_raw + 8 * t, w.seg & 1);
+                widen_queries(gsm + L.q + t * kTile16, reinterpret_cast<int8_t *>(gsm + L.inv) + kRows * (w.seg & 1) + 128 * t);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full + 8 * t);
+            }
             for (int i = 0; i < 2 * n; ++i, ++z) {
-                const bool is_k = kp < n && order_of_k(two, kp) == i;
-                const int page0 = (w.b + (is_k ? kp++ : vp++)) * kPage;
+                int page0;
+                const bool is_k = tile_of(two, n, i, &page0);
+                page0 = (w.b + page0) * kPage;
                 const bool tail = !is_k && page0 + kPage > seen;
                 const bool drop = tail && page0 + row >= past;           // not in the request
                 const bool check = tail && !drop && page0 + row >= seen; // seen by later tokens only
@@ -891,94 +1004,81 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
 }
 
-// Units cut between CTAs: block (c, y) has rows y, y + 32, ... of the unit that CTA c + 1 begins inside
-// of, a warp a row, or all warps where a unit has many cuts.
+// Units cut between CTAs: block (c, y, z) has rows 32 y .. and columns 32 z .. of the unit that CTA c + 1
+// begins inside of; a warp has a 16-byte piece of each row, a lane a row.
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p)
 {
-    __shared__ float sm_m[8], sm_l[8], sm_r[8];
-    __shared__ float4 sm_o[8][32];
+    constexpr int U = 4; // slots on their way at once
+    __shared__ float4 sm_o[8][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     const AttendJoin jn = p.joins[blockIdx.x + 1];
-    if (jn.c0 < 0)
+    const int each = p.unit_tokens >> 1, t = blockIdx.y >> 2, row = 32 * blockIdx.y + lane;
+    const int rows = min(each, jn.tokens - t * each) * p.G; // of stream t, from row 128 t on
+    if (jn.c0 < 0 || 32 * (int)(blockIdx.y & 3) >= rows)
         return;
-    const bool shared = jn.c1 - jn.c0 >= 8;
     const float ninf = __uint_as_float(0xFF800000u);
-    for (int k = 0; k < (shared ? 8 : 1); ++k) {
-        const int row = blockIdx.y + 32 * (shared ? k : warp), step = shared ? 8 : 1;
-        if (row >= jn.rows)
-            return; // with shared rows, all threads
-        float M = ninf, l = 0.f, lr = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float m, float a, float r, float4 v) {
-            const float n = fmaxf(M, m), ref = n == ninf ? 0.f : n, f = ex2(M - ref), e = ex2(m - ref);
-            l = l * f + a * e;
-            lr = lr * f + r * e;
-            o = make_float4(o.x * f + v.x * e, o.y * f + v.y * e, o.z * f + v.z * e, o.w * f + v.w * e);
-            M = n;
-        };
-        for (int c = jn.c0 + (shared ? warp : 0); c <= jn.c1; c += 4 * step) {
-            float m[4], a[4], r[4];
-            float4 v[4];
+    const bool real = 32 * (int)(blockIdx.y & 3) + lane < rows;
+    const int piece = 8 * blockIdx.z + warp;
+    float M = ninf, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = jn.c0; c <= jn.c1 && real; c += U) {
+        float m[U], a[U];
+        float4 v[U];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) { // four slots on their way at once
-                const int cc = c + step * s;
-                m[s] = ninf;
-                a[s] = r[s] = 0.f;
-                v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (cc <= jn.c1) {
-                    const float *slot = p.partial + (size_t)(2 * cc + (cc < jn.c1 ? 1 : 0)) * kSlotFloats;
-                    m[s] = slot[(size_t)kRows * kDim + row];
-                    a[s] = slot[(size_t)kRows * (kDim + 1) + row];
-                    r[s] = slot[(size_t)kRows * (kDim + 2) + row];
-                    v[s] = reinterpret_cast<const float4 *>(slot + (size_t)row * kDim)[lane];
-                }
+        for (int s = 0; s < U; ++s) {
+            const int cc = c + s;
+            m[s] = ninf;
+            a[s] = 0.f;
+            v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (cc <= jn.c1) {
+                const float *slot = p.partial + (size_t)(2 * cc + (cc < jn.c1 ? 1 : 0)) * kSlotFloats;
+                m[s] = slot[(size_t)kRows * kDim + row];
+                a[s] = slot[(size_t)kRows * (kDim + 1) + row];
+                v[s] = reinterpret_cast<const float4 *>(slot)[piece * kRows + row];
             }
+        }
+        float n = M;
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                add(m[s], a[s], r[s], v[s]);
+        for (int s = 0; s < U; ++s)
+            n = fmaxf(n, m[s]);
+        const float ref = n == ninf ? 0.f : n, f = ex2(M - ref);
+        l *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            const float e = ex2(m[s] - ref);
+            l += a[s] * e;
+            if (m[s] != ninf) // (a slot's row without columns holds anything)
+                o.x += v[s].x * e, o.y += v[s].y * e, o.z += v[s].z * e, o.w += v[s].w * e;
         }
-        if (shared) {
-            if (lane == 0) {
-                sm_m[warp] = M;
-                sm_l[warp] = l;
-                sm_r[warp] = lr;
-            }
-            sm_o[warp][lane] = o;
-            __syncthreads();
-            if (warp == 0)
-                for (int s = 1; s < 8; ++s)
-                    add(sm_m[s], sm_l[s], sm_r[s], sm_o[s][lane]);
-            __syncthreads();
-        }
-        if (shared && warp > 0)
-            continue;
-        const float f = lr > 0.f || lr != lr ? p.v_scale / lr : 0.f;
-        const int j = row / p.G;
-        const size_t out = ((size_t)(jn.token0 + j) * p.Hkv + jn.head) * p.G + (row - j * p.G);
-        reinterpret_cast<uint2 *>(p.out + out * kDim)[lane] = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-        if (lane == 0)
-            p.lse[out] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
+        M = n;
+    }
+    const float f = l > 0.f || l != l ? p.v_scale / l : 0.f;
+    const int i = 32 * (blockIdx.y & 3) + lane, j = t * each + i / p.G;
+    if (real && piece == 0)
+        p.lse[((size_t)(jn.token0 + j) * p.Hkv + jn.head) * p.G + i % p.G] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
+    sm_o[warp][lane] = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    __syncthreads();
+    // 64 bytes a row
+    const int k = threadIdx.x >> 3, ik = 32 * (blockIdx.y & 3) + k;
+    if (ik < rows) {
+        const float4 x = sm_o[threadIdx.x & 7][k];
+        const size_t out = ((size_t)(jn.token0 + t * each + ik / p.G) * p.Hkv + jn.head) * p.G + ik % p.G;
+        reinterpret_cast<uint2 *>(p.out + out * kDim + 32 * blockIdx.z)[threadIdx.x & 7] = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
     }
 }
 
 template <int FMT>
-cudaError_t launch_t(const AttendParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream)
+cudaError_t launch_t(const AttendParams &p, const CUtensorMap &map, const CUtensorMap &q_map, int ctas, cudaStream_t stream)
 {
     constexpr int smem = smem_layout(FMT).total;
     cudaError_t e = cudaFuncSetAttribute(attend_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    cudaFuncAttributes fa;
-    if (e == cudaSuccess)
-        e = cudaFuncGetAttributes(&fa, attend_kernel<FMT>);
     if (e != cudaSuccess)
         return e;
-    // a raise waits until the lowerings have freed enough of the launch's registers: never launch
-    // an instance built with fewer than the split needs
-    if (fa.numRegs * threads_of(FMT) < 128 * (kRegs0 + 2 * regs_softmax(FMT) + (FMT == kFmtBf16 ? 0 : kRegsConv)))
-        return cudaErrorInvalidConfiguration;
-    e = launch_kernel(attend_kernel<FMT>, dim3(ctas), dim3(threads_of(FMT)), smem, stream, false, map, p);
+    e = launch_kernel(attend_kernel<FMT>, dim3(ctas), dim3(threads_of(FMT)), smem, stream, false, map, q_map, p);
     if (e == cudaSuccess && ctas > 1)
-        e = launch_kernel(attend_join_kernel, dim3(ctas - 1, 32), dim3(256), 0, stream, true, p);
+        e = launch_kernel(attend_join_kernel, dim3(ctas - 1, 8, 4), dim3(256), 0, stream, true, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -992,15 +1092,15 @@ size_t attend_slot_bytes()
 cudaError_t launch_attend(const AttendParams &params, int kv_dtype, int ctas, cudaStream_t stream)
 {
     AttendParams p = params;
-    p.unit_tokens = kRows / p.G;
-    CUtensorMap map;
-    if (!encode_pool_map(&map, p.kv, kv_dtype, p.num_pages, p.Hkv))
+    p.unit_tokens = 2 * (kRows / 2 / p.G);
+    CUtensorMap map, q_map;
+    if (!encode_pool_map(&map, p.kv, kv_dtype, p.num_pages, p.Hkv) || !encode_token_rows(&q_map, p.q, p.T, p.Hkv * p.G, p.G, p.unit_tokens / 2))
         return cudaErrorInvalidValue;
     if (kv_dtype == MSA_BF16)
-        return launch_t<kFmtBf16>(p, map, ctas, stream);
+        return launch_t<kFmtBf16>(p, map, q_map, ctas, stream);
     if (kv_dtype == MSA_FP8_E4M3)
-        return launch_t<kFmtFp8>(p, map, ctas, stream);
-    return launch_t<kFmtF4>(p, map, ctas, stream);
+        return launch_t<kFmtFp8>(p, map, q_map, ctas, stream);
+    return launch_t<kFmtF4>(p, map, q_map, ctas, stream);
 }
 
 } // namespace msa

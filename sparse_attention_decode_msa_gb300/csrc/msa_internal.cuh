@@ -150,6 +150,9 @@ __host__ __device__ constexpr size_t align_to(size_t v, size_t a)
 bool encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
                uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
                CUtensorMapSwizzle swizzle);
+// Tensor map of bf16 rows [tokens][heads][128], loaded in boxes of 64 elements x box_heads x
+// box_tokens with the 128-byte swizzle; what lies behind the last token is read as zeros.
+bool encode_token_rows(CUtensorMap *map, const void *base, int tokens, int heads, int box_heads, int box_tokens);
 bool encode_2d_sw128(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
                      uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows);
 

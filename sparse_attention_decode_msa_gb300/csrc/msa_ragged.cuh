@@ -43,8 +43,8 @@ struct AppendParams {
 
 // A unit cut between CTAs: its first cut is this record's CTA's start (c0 < 0: there is none).
 struct AttendJoin {
-    int token0, rows, head; // its first token's row, its query rows, its KV head
-    int c0, c1;             // the CTAs that have parts of it
+    int token0, tokens, head; // its first token's row, its tokens, its KV head
+    int c0, c1;               // the CTAs that have parts of it
     int pad[3];
 };
 
