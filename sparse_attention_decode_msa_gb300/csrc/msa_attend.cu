@@ -33,7 +33,8 @@
 // TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
 // Warps: 0 TMA producer, 1 and 2 issue the MMAs of stream 0 and 1 (1 owns the TMEM), 3 clears what
 // must not be multiplied from V tiles on last pages (bf16) and writes the outputs of requests
-// without states, 4-7 and 8-11 softmax of stream 0 and 1, 12-15 converters (E4M3, NVFP4).
+// without states, 4-11 and 12-19 softmax of stream 0 and 1, two warps a row quarter: columns 0 ..
+// 63 and 64 .. of a page, 20-23 converters (E4M3, NVFP4).
 #include <type_traits>
 
 #include "msa_ragged.cuh"
@@ -54,7 +55,7 @@ constexpr int kMinRange = 4;     // what a CTA takes at least
 
 __host__ __device__ constexpr int threads_of(int fmt)
 {
-    return fmt == kFmtBf16 ? 384 : 512;
+    return fmt == kFmtBf16 ? 640 : 768;
 }
 
 __host__ __device__ constexpr int ring_tiles(int fmt)
@@ -63,7 +64,7 @@ __host__ __device__ constexpr int ring_tiles(int fmt)
 }
 
 struct Smem {
-    int staged, q, ml, inv, bars, misc, total;
+    int staged, q, xch, inv, bars, misc, total;
 };
 
 // Tiles that the issuer takes: widened ones, or the ring's own once they have passed the clearing warp.
@@ -73,16 +74,16 @@ __host__ __device__ constexpr int ready_tiles(int fmt)
 }
 
 // Barriers: full[], empty[] of the ring, ready[], ready_free[] (widened tiles), and for each stream
-// q_raw (their copy), q_full, s_full, p_full, pv_done, o_free, drain.
+// q_raw (their copy), q_full, s_full, p_full, pv_done, o_free, turn, drain.
 __host__ __device__ constexpr Smem smem_layout(int fmt)
 {
     Smem s{};
     s.staged = ring_tiles(fmt) * tile_bytes(fmt);
     s.q = s.staged + (fmt == kFmtBf16 ? 0 : kStaged * kTile16);
-    s.ml = s.q + 2 * kTile16;   // m[128], l[128] of stream 1 (units of up to 128 rows)
-    s.inv = s.ml + 2 * 128 * 4; // exponents that undo the scaling of query rows, of two units
+    s.xch = s.q + 2 * kTile16;      // a float for each softmax thread: what the warps of a row tell one another
+    s.inv = s.xch + 4 * 128 * 4; // exponents that undo the scaling of query rows, of two units
     s.bars = s.inv + (fmt == kFmtBf16 ? 0 : 2 * kRows);
-    s.misc = s.bars + (2 * ring_tiles(fmt) + 2 * ready_tiles(fmt) + 14) * 8;
+    s.misc = s.bars + (2 * ring_tiles(fmt) + 2 * ready_tiles(fmt) + 16) * 8;
     s.total = s.misc + 256;
     return s;
 }
@@ -90,7 +91,7 @@ static_assert(smem_layout(kFmtBf16).total <= 232448 && smem_layout(kFmtFp8).tota
 
 struct Misc {
     long long start_before;
-    long long scan[17];
+    long long scan[24];
     int abort, start_r;
     uint32_t tmem;
     int later_bad[8]; // unit counter + 1 where V rows of later tokens are not finite
@@ -231,23 +232,33 @@ __device__ __forceinline__ bool tile_of(bool two, int n, int i, int *page)
 __device__ __forceinline__ void clear_rows(uint8_t *v, int seen, int past, volatile int *bad, int mark)
 {
     const int lane = threadIdx.x & 31;
-    bool any = false;
+    auto at = [&](int k) { return reinterpret_cast<uint4 *>(v + (k >> 3 & 1) * 16384 + (k >> 4) * 128 + (k & 7) * 16); }; // 16-byte piece k
+    const int stop = 16 * min(past, kPage);
 #pragma unroll 4
-    for (int k = max(0, seen) * 16 + lane; k < kPage * 16; k += 32) { // 16-byte pieces
-        const int row = k >> 4, piece = k & 15;
-        uint4 *at = reinterpret_cast<uint4 *>(v + (piece >> 3) * 16384 + row * 128 + (piece & 7) * 16);
-        uint4 d = *at;
-        uint32_t *e = &d.x;
-        uint32_t gone[4];
+    for (int k = max(stop, 0) + lane; k < 16 * kPage; k += 32)
+        *at(k) = make_uint4(0u, 0u, 0u, 0u);
+    bool any = false;
+    for (int k0 = max(0, seen) * 16; k0 < stop; k0 += 128) {
+        uint4 d[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            gone[c] = __vcmpeq2(e[c] & 0x7F807F80u, 0x7F807F80u);
-        if (row >= past || (gone[0] | gone[1] | gone[2] | gone[3])) {
-            any = any || row < past;
+        for (int u = 0; u < 4; ++u)
+            if (k0 + 32 * u + lane < stop)
+                d[u] = *at(k0 + 32 * u + lane);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                e[c] &= row >= past ? 0u : ~gone[c];
-            *at = d;
+        for (int u = 0; u < 4; ++u) {
+            if (k0 + 32 * u + lane >= stop)
+                continue;
+            uint32_t *e = &d[u].x, gone = 0u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t g = __vcmpeq2(e[c] & 0x7F807F80u, 0x7F807F80u);
+                e[c] &= ~g;
+                gone |= g;
+            }
+            if (gone) {
+                any = true;
+                *at(k0 + 32 * u + lane) = d[u];
+            }
         }
     }
     if (any)
@@ -257,13 +268,13 @@ __device__ __forceinline__ void clear_rows(uint8_t *v, int seen, int past, volat
     __syncwarp();
 }
 
-// The largest sc s over the first `seen` columns of this thread's row of S, -inf for none.
+// The largest sc s over the first `seen` of 64 columns of this thread's row of S, -inf for none.
 __device__ __noinline__ float row_maximum(uint32_t at_s, float sc, int seen)
 {
     const float inf = __uint_as_float(0x7F800000u);
     float top[2] = {-inf, -inf}, low[2] = {inf, inf};
 #pragma unroll 1
-    for (int c = 0; c < kPage; c += 32) {
+    for (int c = 0; c < 64; c += 32) {
         uint32_t v[32];
         tmem_ld32(at_s + c, v);
         tmem_wait_ld(v);
@@ -286,20 +297,20 @@ __device__ __noinline__ float row_maximum(uint32_t at_s, float sc, int seen)
     return seen <= 0 ? -inf : sc < 0.f ? fminf(low[0], low[1]) * sc : fmaxf(top[0], top[1]) * sc;
 }
 
-// 128 columns of this thread's row of S to p = 2^(sc s - ref), as pairs of bf16 (f16) in pr; their
+// 64 columns of this thread's row of S to p = 2^(sc s - ref), as pairs of bf16 (f16) in pr; their
 // sum.  TAIL: columns from `seen` on are 0.
 template <bool F16, bool TAIL>
-__device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, int seen, uint32_t (&pr)[64])
+__device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, int seen, uint32_t (&pr)[32])
 {
     const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
     uint64_t sum[2] = {0ull, 0ull};
     uint32_t v[2][16];
     tmem_ld16_async(at_s, v[0]);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < 4; ++c) {
         uint32_t(&x)[16] = v[c & 1];
         tmem_wait_ld16(x);
-        if (c < 7) // on their way meanwhile
+        if (c < 3) // on their way meanwhile
             tmem_ld16_async(at_s + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
@@ -320,10 +331,21 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
     return a + b;
 }
 
+// Whether any thread of the two warps that meet at a barrier says so.
+__device__ __forceinline__ bool any_of_two_warps(int barrier, bool v)
+{
+    uint32_t any;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.b32 %0, 1, 0, q;\n}\n"
+                 : "=r"(any)
+                 : "r"((uint32_t)v), "r"(barrier)
+                 : "memory");
+    return any != 0;
+}
+
 // Infinities and NaN of V at positions from .. to - 1, which were kept out of the products, for a row that
-// sees them: into its output, or into its partial one in a slot.
+// sees them: into dimensions d0 .. d0 + 63 of its output, or of its partial one in a slot.
 template <int FMT>
-__device__ __noinline__ void add_late_values(const AttendParams &p, const Share &at, long long row, int from, int to, float ref, float *slot)
+__device__ __noinline__ void add_late_values(const AttendParams &p, const Share &at, long long row, int from, int to, float ref, float *slot, int d0)
 {
     for (int pos = from; pos < to; ++pos) {
         const long long page = p.block_table[(size_t)at.r * p.maxB + pos / kPage];
@@ -331,7 +353,7 @@ __device__ __noinline__ void add_late_values(const AttendParams &p, const Share 
             continue;
         float pr = 0.f;
         bool have = false;
-        for (int d = 0; d < kDim; ++d) {
+        for (int d = d0; d < d0 + 64; ++d) {
             const float x = stored_value<FMT>(p.kv, (page * 2 + 1) * p.Hkv + at.head, pos % kPage, d);
             if (finite(x))
                 continue;
@@ -428,7 +450,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     constexpr int DEPTH = ready_tiles(FMT);
     const uint32_t full = smem + L.bars, empty = full + TILES * 8, ready = empty + TILES * 8, ready_free = ready + DEPTH * 8;
     const uint32_t q_full = ready_free + DEPTH * 8, s_full = q_full + 16, p_full = s_full + 16, pv_done = p_full + 16,
-                   o_free = pv_done + 16, drain = o_free + 16, q_raw = CONV ? drain + 16 : q_full;
+                   o_free = pv_done + 16, turn = o_free + 16, drain = turn + 16, q_raw = CONV ? drain + 16 : q_full;
     volatile int *abort_flag = &misc.abort;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long wl = p.wait_limit;
@@ -456,11 +478,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             mbar_init(q_full + 8 * t, CONV ? 4 : 1); // the converter warps, or the copy itself
             if (CONV)
                 mbar_init(q_raw + 8 * t, 1);
+            mbar_init(turn + 8 * t, 1);
             mbar_init(drain + 8 * t, 1);
             mbar_init(s_full + 8 * t, 1);
-            mbar_init(p_full + 8 * t, 4);
+            mbar_init(p_full + 8 * t, 8);
             mbar_init(pv_done + 8 * t, 1);
-            mbar_init(o_free + 8 * t, 4);
+            mbar_init(o_free + 8 * t, 8);
         }
         fence_mbar_init();
         misc.abort = 0;
@@ -612,9 +635,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 mbar_wait_bounded(full + 8 * (i % TILES), (uint32_t)(i / TILES) & 1u);
         __syncwarp();
     } else if (warp < 3) {
-        // ---- MMA issuer of stream t: S of a page, then, once its softmax is done, P V of it and S of the
-        // stream's next page, while the other stream's products fill the tensor cores.  (One
-        // issuer for both spends longer on its own instructions between two MMAs than an MMA takes.) ----
+        // ---- MMA issuer of stream t.  The issuers take turns: P V of a page and S of the stream's next page,
+        // which waits for P V (it replaces P), and then the other stream's, whose softmax that time
+        // was for.  Left to themselves the streams fall into step, both in their softmax and then both at
+        // the tensor cores (a page of two streams 3500 clocks).  (One issuer for both spends longer on its
+        // own instructions between two MMAs than an MMA takes.) ----
         const int t = warp - 1;
         const uint32_t one = elect_one(), tm = uniform(tmem), base = uniform(smem);
         constexpr uint32_t kTypes = CONV ? ~((1u << 7) | (1u << 10)) : ~0u; // f16 or bf16 operands
@@ -624,15 +649,23 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const uint32_t tile_free = CONV ? ready_free : empty;
         const uint32_t q = uniform(desc_low(base + L.q + t * kTile16, 16)), d_s = tm + uniform(128 * t), d_o = tm + uniform(256 + 128 * t);
         const uint32_t ring = uniform((base + RING) >> 4);
-        uint32_t done = 0; // steps of this stream so far
+        uint32_t done = 0, turns_taken = 0; // steps and turns of this stream so far
+        auto take_turn = [&] {
+            if (t == 1 || turns_taken > 0)
+                wait(turn + 8 * t, (t == 1 ? turns_taken : turns_taken - 1) & 1u);
+            ++turns_taken;
+        };
+        auto end_turn = [&] {
+            if (lane == 0)
+                mbar_arrive(turn + 8 * (t ^ 1));
+        };
         int st0 = 0;       // the unit's first tile: its slot and the slot's phase
         uint32_t ph0 = 0;
         for (; w.left > 0; w.next(p)) {
             const int n = w.pages();
             const bool two = w.two(p);
-            // (stream 1 of a small unit's only page takes a step without a product: no barrier's phase is passed over)
-            const bool null = !two && n <= t;
-            const int nsteps = two ? n : max(1, (n + 1 - t) >> 1), stride = two ? 2 : 4;
+            // (both streams take as many steps: stream 1 one without a page behind an odd number of them)
+            const int nsteps = two ? n : (n + 1) >> 1, stride = two ? 2 : 4, pages = two || t == 0 ? nsteps : n >> 1;
             // slot and phase of the tile i places behind the unit's first
             auto slot_of = [&](int i, uint32_t &ph) {
                 const int z = st0 + i, turns = z / DEPTH;
@@ -646,11 +679,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     umma_commit(tile_free + 8 * st);
             };
             wait(q_full + 8 * t, w.seg & 1);
-            // S of step i into the S buffer (its K tile has been waited for)
-            auto score = [&](uint32_t st) {
+            // S of a step into the S buffer (its K tile has been waited for)
+            auto score = [&](uint32_t st, bool page) {
                 const uint32_t k = (ring + st * (kTile16 >> 4) & 0x3FFFu) | (16u >> 4) << 16;
-                tcgen05_after_sync();
-                if (!null) {
+                if (page) {
 #pragma unroll
                     for (uint32_t ks = 0; ks < 8; ++ks)
                         umma_ss(one, d_s, q + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 1024 + (ks & 3) * 2, idesc_s, ks > 0);
@@ -660,10 +692,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 __syncwarp();
             };
             uint32_t k_ph, k_st = slot_of(two ? 0 : t, k_ph);
-            if (!null)
+            if (pages > 0)
                 wait(ready + 8 * k_st, k_ph);
-            score(k_st); // (P V of the unit before, which reads what S replaces, was waited for at its end)
-            if (!null && elect_one())
+            take_turn();
+            tcgen05_after_sync();
+            score(k_st, pages > 0); // (P V of the unit before, which reads what S replaces, was waited for at its end)
+            end_turn();
+            if (pages > 0 && elect_one())
                 give_back(k_st);
             __syncwarp();
             for (int i = 0; i < nsteps; ++i, ++done) {
@@ -671,18 +706,19 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 uint32_t v_ph; // (V lies behind both K of the pair, or the only one)
                 const uint32_t v_st = slot_of(i * stride + (two ? 1 : min(2, n - 2 * i) + t), v_ph);
                 const uint32_t v = (ring + v_st * (kTile16 >> 4) & 0x3FFFu) | (16384u >> 4) << 16, more = uniform(i > 0);
-                const bool again = i + 1 < nsteps;
-                if (!null)
+                const bool page = i < pages, again = i + 1 < nsteps, next_page = i + 1 < pages;
+                if (page)
                     wait(ready + 8 * v_st, v_ph);
-                if (again) {
+                if (next_page) {
                     k_st = slot_of((i + 1) * stride + (two ? 0 : t), k_ph);
                     wait(ready + 8 * k_st, k_ph);
                 }
                 if (i == 0 && w.seg > 0) // the last unit's O has been read
                     wait(o_free + 8 * t, (w.seg - 1) & 1);
                 wait(p_full + 8 * t, done & 1u);
+                take_turn();
                 tcgen05_after_sync();
-                if (!null) {
+                if (page) {
                     // V, MN-major: 16 positions are 16 rows of 128 bytes
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
@@ -691,12 +727,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 if (elect_one())
                     umma_commit(pv_done + 8 * t);
                 __syncwarp();
-                wait(pv_done + 8 * t, done & 1u); // before S replaces P
-                if (again)
-                    score(k_st);
-                if (!null && elect_one()) {
-                    give_back(v_st);
-                    if (again)
+                if (again) // S replaces P: products of one thread run in the order of their issue
+                    score(k_st, next_page);
+                end_turn();
+                if (elect_one()) {
+                    if (page)
+                        give_back(v_st);
+                    if (next_page)
                         give_back(k_st);
                 }
                 __syncwarp();
@@ -746,17 +783,21 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (size_t i = lane; i < all; i += 32)
                 p.lse[rows * q.first + i] = __uint_as_float(0xFF800000u);
         }
-    } else if (warp < 12) {
-        // ---- softmax: thread = query row ----
-        const int t = (warp - 4) >> 2, at_lane = threadIdx.x & 127;
+    } else if (warp < 20) {
+        // ---- softmax: a thread has 64 columns of a page of a query row ----
+        const int t = (warp - 4) >> 3, half = (warp >> 2) + 1 & 1, at_lane = threadIdx.x & 127;
+        const bool leads = warp == 4 + 8 * t; // the stream's warp that copies queries
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21); // this warp's lane quarter
-        const uint32_t at_s = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
+        const uint32_t at_s = lanes + 128 * t + 64 * half, at_p = lanes + 128 * t + 32 * half, o_at = lanes + 256 + 128 * t + 64 * half;
         const float ninf = __uint_as_float(0xFF800000u);
-        float *ml = reinterpret_cast<float *>(gsm + L.ml);
+        float *xch = reinterpret_cast<float *>(gsm + L.xch); // [stream][half][row]
+        float *mine = xch + 256 * t + 128 * half + at_lane, *others = xch + 256 * t + 128 * (half ^ 1) + at_lane;
         const int8_t *exps = reinterpret_cast<const int8_t *>(gsm + L.inv) + 128 * t;
         const int Hq = p.Hkv * p.G, each = p.unit_tokens >> 1; // tokens of a stream
-        uint32_t steps = 0, steps1 = 0; // of this stream and of stream 1 so far
-        auto sync_all = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        uint32_t steps = 0; // so far, alike for both streams
+        const int pair_bar = 1 + 4 * t + (warp & 3);
+        auto sync_pair = [&] { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
+        auto sync_all = [&] { asm volatile("bar.sync 9, 512;" ::: "memory"); };
         // Query rows of a unit into the stream's operand tile, once the stream's last S of the unit
         // before is done.  Rows beyond the unit's hold anything: nothing is read from what they give.
         auto copy_queries = [&](const Share &u) {
@@ -769,30 +810,27 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
             __syncwarp();
         };
-        if (w.left > 0 && warp == 4 + 4 * t)
+        if (w.left > 0 && leads)
             copy_queries(w);
         while (w.left > 0) {
             const int n = w.pages();
             const bool two = w.two(p);
-            const bool null = !two && n <= t; // (see the issuers)
-            const int nsteps = two ? n : max(1, (n + 1 - t) >> 1); // this stream's
-            steps1 += two ? n : max(1, n >> 1);
+            const int nsteps = two ? n : (n + 1) >> 1, npages = two || t == 0 ? nsteps : n >> 1; // (see the issuers)
             const int rows = (two && t ? w.q.tokens(p, w.u) - each : min(each, w.q.tokens(p, w.u))) * p.G; // the stream's
             const bool real = at_lane < rows, idle = (warp & 3) * 32 >= rows; // idle: no row of this warp's is the unit's
             const int j = (two ? each * t : 0) + min(at_lane, rows - 1) / p.G;  // the row's token
-            float sc = p.scale_log2;
-            // (the exponents are there once S is)
-            auto scale_row = [&] {
-                if (CONV && real)
-                    sc *= __uint_as_float((uint32_t)(exps[kRows * (w.seg & 1) + at_lane] + 127) << 23);
-            };
             const int seen0 = w.q.seen(p, w.u), lim = seen0 + (p.causal ? j : 0);
-            float m = 0.f, l = 0.f; // reference and sum
+            float sc = p.scale_log2, m = 0.f, l = 0.f; // scale, reference and sum
             // A row's reference is its maximum over the first page.  Later pages are not searched for theirs:
-            // p may pass 1 as long as it stays a number that P and the sums can hold, which the sum of a
-            // page tells; where a row's passes kMost its warp's rows get new references before P is written.
+            // p may pass 1 as long as it stays a number that P and the sums can hold, which the sum of half a
+            // page tells; where a row's passes kMost its warps' rows get new references before P is written.
             auto new_reference = [&](int i, int seen) {
-                const float mx = row_maximum(at_s, sc, seen) - (CONV ? kPUp16 : 0.f);
+                if (CONV && i == 0 && real) // (the exponents are there once S is)
+                    sc *= __uint_as_float((uint32_t)(exps[kRows * (w.seg & 1) + at_lane] + 127) << 23);
+                float mx = row_maximum(at_s, sc, seen);
+                *mine = mx;
+                sync_pair();
+                mx = fmaxf(mx, *others) - (CONV ? kPUp16 : 0.f);
                 const float ref = mx == ninf ? 0.f : mx, f = i > 0 && mx > m ? ex2(m - ref) : 1.f;
                 m = i == 0 || mx > m ? ref : m;
                 l *= f;
@@ -800,7 +838,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     wait(pv_done + 8 * t, (steps - 1) & 1u); // O holds every step before this one
                     tcgen05_after_sync();
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < 4; ++c) {
                         float o[16];
                         tmem_ld16(o_at + 16 * c, o);
                         uint32_t r[16];
@@ -812,8 +850,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 }
             };
             auto page_done = [&](const uint32_t *pr) {
-                tmem_st32(at_s, pr);
-                tmem_st32(at_s + 32, pr + 32);
+                tmem_st32(at_p, pr);
                 tmem_wait_st();
                 tcgen05_before_sync();
                 __syncwarp();
@@ -822,49 +859,48 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             };
             // all pages but the last of the share and those that some row does not see to their end
             const int step = two ? kPage : 2 * kPage, pos1 = (w.b + (two ? 0 : t)) * kPage;
-            const int whole_pages = idle || null ? 0 : max(0, min(nsteps - 1, (seen0 - kPage - pos1 >= 0 ? (seen0 - kPage - pos1) / step + 1 : 0)));
+            const int whole_pages = idle ? 0 : max(0, min(npages - 1, (seen0 - kPage - pos1 >= 0 ? (seen0 - kPage - pos1) / step + 1 : 0)));
             int i = 0;
 #pragma unroll 1
             for (; i < whole_pages; ++i, ++steps) {
                 wait(s_full + 8 * t, steps & 1u);
                 tcgen05_after_sync();
-                if (i == 0) {
-                    scale_row();
-                    new_reference(0, kPage);
-                }
-                uint32_t pr[64];
-                float sum = row_to_p<CONV, false>(at_s, sc, m, kPage, pr);
-                if (__any_sync(0xffffffffu, sum > (CONV ? kMost16 : kMost)) && i > 0) {
-                    new_reference(i, kPage);
-                    sum = row_to_p<CONV, true>(at_s, sc, m, kPage, pr);
+                if (i == 0)
+                    new_reference(0, 64);
+                uint32_t pr[32];
+                float sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr);
+                // (both warps have read S, which P replaces)
+                if (any_of_two_warps(pair_bar, i > 0 && sum > (CONV ? kMost16 : kMost))) {
+                    new_reference(i, 64);
+                    sum = row_to_p<CONV, true>(at_s, sc, m, 64, pr);
+                    sync_pair();
                 }
                 l += sum;
                 page_done(pr);
             }
 #pragma unroll 1
             for (; i < nsteps; ++i, ++steps) {
-                const int seen = min(kPage, lim - (pos1 + i * step)); // columns this row sees
+                const int seen = lim - (pos1 + i * step) - 64 * half; // columns this row sees
                 wait(s_full + 8 * t, steps & 1u);
-                if (i == nsteps - 1 && !w.last() && warp == 4 + 4 * t) {
+                if (i == nsteps - 1 && !w.last() && leads) {
                     Share nx = w; // S was the last to read this unit's
                     nx.next(p);
                     copy_queries(nx);
                 }
-                if (idle || null) {
+                if (idle || i >= npages) {
                     if (lane == 0)
                         mbar_arrive(p_full + 8 * t);
                     continue;
                 }
                 tcgen05_after_sync();
-                if (i == 0) {
-                    scale_row();
-                    new_reference(0, seen);
-                }
-                uint32_t pr[64];
+                if (i == 0)
+                    new_reference(0, min(64, seen));
+                uint32_t pr[32];
                 float sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr);
-                if (__any_sync(0xffffffffu, sum > (CONV ? kMost16 : kMost)) && i > 0) {
-                    new_reference(i, seen);
+                if (any_of_two_warps(pair_bar, i > 0 && sum > (CONV ? kMost16 : kMost))) {
+                    new_reference(i, min(64, seen));
                     sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr);
+                    sync_pair();
                 }
                 l += sum;
                 page_done(pr);
@@ -874,14 +910,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const Share at = w;
             w.next(p);
             const bool whole = at.b == 0 && n == at.nb, ends = at.b + n == at.nb;
+            *mine = l;
+            sync_pair();
+            l += *others; // (the same sum in both warps)
+            sync_pair();
             float M = m, fa = 1.f, fb = 0.f;
             if (!two) {
-                if (t == 1) {
-                    ml[at_lane] = m;
-                    ml[128 + at_lane] = l;
-                }
+                if (t == 1)
+                    *mine = half ? l : m;
                 sync_all();
-                const float mb = ml[at_lane], lb = ml[128 + at_lane];
+                const float mb = xch[256 + at_lane], lb = xch[384 + at_lane];
                 sync_all();
                 if (t == 1)
                     continue; // stream 0 reads both accumulators
@@ -893,7 +931,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
             wait(pv_done + 8 * t, (steps - 1) & 1u);
             if (!two) // stream 1 has given all its P: the last of its products is the one under way
-                wait(pv_done + 8, (steps1 - 1) & 1u);
+                wait(pv_done + 8, (steps - 1) & 1u);
             tcgen05_after_sync();
             const long long out_row = (long long)(at.token0(p) + j) * Hq + at.head * p.G + min(at_lane, rows - 1) % p.G;
             const int slot_row = (two ? 128 * t : 0) + at_lane;
@@ -905,21 +943,23 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             for (int k = 0; k < 4; ++k)
                 rows_of_four[k] = __shfl_sync(0xffffffffu, out_row, (lane & 28) + k);
 #pragma unroll 1
-            for (int c = 0; c < 4 && !idle; ++c) {
+            for (int c = 0; c < 2 && !idle; ++c) {
                 uint32_t a[32];
                 tmem_ld32(o_at + 32 * c, a);
                 tmem_wait_ld(a);
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     a[k] = __float_as_uint(fa != 0.f ? __uint_as_float(a[k]) * ga : 0.f);
-                if (!two) {
-                    uint32_t o[32];
-                    tmem_ld32(o_at + 128 + 32 * c, o);
-                    tmem_wait_ld(o);
+                if (!two)
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        a[k] = __float_as_uint(__uint_as_float(a[k]) + (gb != 0.f ? __uint_as_float(o[k]) * gb : 0.f));
-                }
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t o[16];
+                        tmem_ld16_async(o_at + 128 + 32 * c + 16 * h, o);
+                        tmem_wait_ld16(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            a[16 * h + k] = __float_as_uint(__uint_as_float(a[16 * h + k]) + (gb != 0.f ? __uint_as_float(o[k]) * gb : 0.f));
+                    }
                 if (whole) {
                     uint4 d[4];
 #pragma unroll
@@ -932,11 +972,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if ((at_lane & ~3) + k < rows)
-                            *reinterpret_cast<uint4 *>(p.out + rows_of_four[k] * kDim + 32 * c + 8 * (lane & 3)) = d[k];
+                            *reinterpret_cast<uint4 *>(p.out + rows_of_four[k] * kDim + 64 * half + 32 * c + 8 * (lane & 3)) = d[k];
                 } else if (real) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) // 16-byte piece i of row r of a slot lies at i kRows + r
-                        reinterpret_cast<uint4 *>(slot)[(8 * c + k) * kRows + slot_row] = make_uint4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+                        reinterpret_cast<uint4 *>(slot)[(16 * half + 8 * c + k) * kRows + slot_row] =
+                            make_uint4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
                 }
             }
             tcgen05_before_sync();
@@ -947,15 +988,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     mbar_arrive(o_free + 8);
             }
             if (real) {
-                if (whole) {
+                if (half == 0 && whole) {
                     p.lse[out_row] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
-                } else {
+                } else if (half == 0) {
                     slot[(size_t)kRows * kDim + slot_row] = l == 0.f ? ninf : M;
                     slot[(size_t)kRows * (kDim + 1) + slot_row] = l;
                 }
                 if (misc.later_bad[at.seg & 7] == at.seg + 1)
                     add_late_values<FMT>(p, at, out_row, max(seen0, at.b * kPage), min(lim, (at.b + n) * kPage), M,
-                                         whole ? nullptr : slot + 4 * slot_row);
+                                         whole ? nullptr : slot + 4 * slot_row, 64 * half);
             }
         }
     } else if constexpr (CONV) {
@@ -983,7 +1024,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
                 if (z >= DEPTH)
                     wait(ready_free + 8 * (z % DEPTH), (uint32_t)(z / DEPTH - 1) & 1u);
-                const bool bad = convert_row<FMT>(gsm + (z % TILES) * TB, gsm + L.staged + (z % DEPTH) * kTile16 + row * 128, row, tail, drop, check);
+                const bool bad = convert_row<FMT, 4>(gsm + (z % TILES) * TB, gsm + L.staged + (z % DEPTH) * kTile16 + row * 128, row, tail, drop, check);
                 if (bad)
                     misc.later_bad[w.seg & 7] = w.seg + 1;
                 fence_async_smem();

@@ -311,12 +311,12 @@ __device__ __forceinline__ bool finite(float v)
 // Row `row` of a ring tile (E4M3, NVFP4) to f16 in the layout of a 16-bit tile; dst is the row's place in its
 // first half.  On a last page (tail) a row that is not cached becomes zeros (drop), and infinities
 // and NaN of a row that only later tokens see (check) do too: true is returned for those.
-template <int FMT>
+template <int FMT, int UNROLL = 2>
 __device__ __forceinline__ bool convert_row(const uint8_t *src, uint8_t *dst, int row, bool tail, bool drop, bool check)
 {
     bool bad = false;
     if (FMT == kFmtFp8) {
-#pragma unroll 2 // (all: 426 us for 413, 48 tokens over 2 x 131072; NVFP4 loses with less, 507 for 488)
+#pragma unroll UNROLL // (dense decode, all: 426 us for 413, 48 tokens over 2 x 131072; NVFP4 loses with less, 507 for 488)
         for (int c = 0; c < 8; ++c) { // 16 dimensions
             const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
             uint32_t e[4] = {d.x, d.y, d.z, d.w}, o[8];
