@@ -155,12 +155,12 @@ def _bufs(stream, kinds, *xs):
     return _bufs(stream, kinds, *xs)
 
 
-def _rows(stream, kinds, strides, *xs):
-    """buffers.rows, in the same way."""
-    global _rows
-    from .buffers import rows as _rows
+def _check_rows(x, stride, heads):
+    """buffers.check_rows, in the same way."""
+    global _check_rows
+    from .buffers import check_rows as _check_rows
 
-    return _rows(stream, kinds, strides, *xs)
+    _check_rows(x, stride, heads)
 
 
 def _stream(stream):
@@ -307,9 +307,12 @@ def rope_frequencies(radians, device=None):
 def msa_qk_norm_rope(rope: MsaRope, freqs, num_tokens: int, positions, num_q_heads: int, q, q_weight, q_out,
                      num_k_heads: int = 0, k=None, k_weight=None, k_out=None, stream=None):
     """Norm and rotation of query heads, and of key heads in the same pass."""
-    st, (f, at, *rows) = _rows(stream, "gi" + "Rhh" * 2, (rope.q_stride, num_q_heads, rope.k_stride, num_k_heads),
-                               freqs, positions, q, q_weight, q_out, k, k_weight, k_out)
-    _check(load().msa_qk_norm_rope(ctypes.byref(rope), f, num_tokens, at, num_q_heads, *rows[:3], num_k_heads, *rows[3:],
+    st, (f, at, a, b, c, d, e, g) = _bufs(stream, "giRhhRhh", freqs, positions, q, q_weight, q_out, k, k_weight, k_out)
+    if q is not a:
+        _check_rows(q, rope.q_stride, num_q_heads)
+    if k is not d:
+        _check_rows(k, rope.k_stride, num_k_heads)
+    _check(load().msa_qk_norm_rope(ctypes.byref(rope), f, num_tokens, at, num_q_heads, a, b, c, num_k_heads, d, e, g,
                                    st), "msa_qk_norm_rope")
 
 
@@ -323,13 +326,19 @@ def msa_kv_append(shape, rope, freqs, num_tokens, offsets, k, k_weight, v, idxk,
                   workspace_bytes, stream=None):
     """A ragged batch's keys, values and index keys into their pages, with norm and rotation on the way, and its
     queries and index queries in the same pass."""
-    Hkv, Hi = shape.num_kv_heads, shape.num_index_heads
-    st, (f, *bufs, ws) = _rows(
-        stream, "giRhRRhRhhRhhiibbbb",
-        (rope.k_stride, Hkv, rope.v_stride, Hkv, rope.idxk_stride, Hi, rope.q_stride, shape.num_q_heads, rope.q_idx_stride, Hi),
-        freqs, offsets, k, k_weight, v, idxk, idxk_weight, q, q_weight, q_out, q_idx, q_idx_weight, q_idx_out, block_table,
-        seq_lens, kv_pool, idxk_pool, idxk_scales, workspace)
-    _check(load().msa_kv_append(ctypes.byref(shape), ctypes.byref(rope), f, num_tokens, *bufs, ws, int(workspace_bytes), st),
+    st, out = _bufs(stream, "giRhRRhRhhRhhiibbbb", freqs, offsets, k, k_weight, v, idxk, idxk_weight, q, q_weight, q_out,
+                    q_idx, q_idx_weight, q_idx_out, block_table, seq_lens, kv_pool, idxk_pool, idxk_scales, workspace)
+    if k is not out[2]:
+        _check_rows(k, rope.k_stride, shape.num_kv_heads)
+    if v is not out[4]:
+        _check_rows(v, rope.v_stride, shape.num_kv_heads)
+    if idxk is not out[5]:
+        _check_rows(idxk, rope.idxk_stride, shape.num_index_heads)
+    if q is not out[7]:
+        _check_rows(q, rope.q_stride, shape.num_q_heads)
+    if q_idx is not out[10]:
+        _check_rows(q_idx, rope.q_idx_stride, shape.num_index_heads)
+    _check(load().msa_kv_append(ctypes.byref(shape), ctypes.byref(rope), out[0], num_tokens, *out[1:], workspace_bytes, st),
            "msa_kv_append")
 
 

@@ -13,11 +13,13 @@ _TYPES = {
     "i": frozenset((torch.int32, torch.uint32)),
     "f": frozenset((torch.float32,)),
     "g": frozenset((torch.int64, torch.uint64)),
+    "R": frozenset((torch.bfloat16, torch.int16, torch.uint16)),  # rows of tokens, which check_rows has seen
     "b": None,  # pools and workspaces are bytes
 }
 _KINDS = {kinds: tuple(_TYPES[k] for k in kinds)
-          for kinds in ("hbiihfb", "hbiiifffb", "fiiibbbfiib", "gibhhbhh", "gibhbbhbhhbhhiibbbb",
+          for kinds in ("hbiihfb", "hbiiifffb", "fiiibbbfiib", "giRhhRhh", "giRhRRhRhhRhhiibbbb",
                         "hibiihfb")}
+_ROWS = _TYPES["R"]
 _Tensor, _get_device, _is_contiguous, _data_ptr = (torch.Tensor, torch.Tensor.get_device, torch.Tensor.is_contiguous,
                                                    torch.Tensor.data_ptr)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -47,7 +49,7 @@ def bufs(stream, kinds: str, *xs):
                 device = torch.cuda.current_device()
             if d != device:
                 raise ValueError(f"buffer on {x.device}: not on the current CUDA device")
-        if not _is_contiguous(x):
+        if not _is_contiguous(x) and types is not _ROWS:
             raise ValueError("buffers must be contiguous")
         out.append(_data_ptr(x))
     if stream is None:
@@ -57,26 +59,13 @@ def bufs(stream, kinds: str, *xs):
     return stream, out
 
 
-def rows(stream, kinds: str, strides, *xs):
-    """bufs with rows of tokens among them: the letter R is a tensor [tokens, heads, 128] (or [tokens, heads * 128])
-    that may be part of a wider one, and `strides` holds the stride (0: dense) and the heads that the library will be
-    told for each."""
-    dense, i = [], 0
-    for x, kind in zip(xs, kinds):
-        if kind == "R":
-            if isinstance(x, _Tensor) and x.numel() > 0:
-                stride, heads = strides[i], strides[i + 1]
-                if x.dtype not in _TYPES["h"]:
-                    raise ValueError(f"buffer of {x.dtype}: the argument takes {' or '.join(sorted(map(str, _TYPES['h'])))}")
-                shape, step = tuple(x.shape[1:]), x.stride()
-                if shape not in ((heads, 128), (heads * 128,)) or step[-1] != 1 or (len(shape) == 2 and heads > 1 and step[1] != 128):
-                    raise ValueError(f"rows of shape {tuple(x.shape)} and strides {step}: a token's {heads} heads of 128 lie one after another")
-                if x.shape[0] > 1 and step[0] != (stride or heads * 128):
-                    raise ValueError(f"rows {step[0]} elements apart: the call says {stride or heads * 128}")
-                device = _get_device(x)
-                if device < 0 or device != torch.cuda.current_device():
-                    raise ValueError(f"buffer on {x.device}: not on the current CUDA device")
-                x = _data_ptr(x)
-            i += 2
-        dense.append(x)
-    return bufs(stream, kinds.replace("R", "b"), *dense)
+def check_rows(x, stride: int, heads: int):
+    """Rows of tokens: a tensor [tokens, heads, 128] (or [tokens, heads * 128]) that may be part of a wider one,
+    `stride` elements (0: dense) from a token's rows to the next token's, as the library will be told."""
+    step, shape = x.stride(), x.shape
+    if step == (stride or heads * 128, 128, 1) and shape[1] == heads and shape[2] == 128:
+        return
+    if tuple(shape[1:]) not in ((heads, 128), (heads * 128,)) or step[-1] != 1 or (len(shape) == 3 and heads > 1 and step[1] != 128):
+        raise ValueError(f"rows of shape {tuple(shape)} and strides {step}: a token's {heads} heads of 128 lie one after another")
+    if shape[0] > 1 and step[0] != (stride or heads * 128):
+        raise ValueError(f"rows {step[0]} elements apart: the call says {stride or heads * 128}")

@@ -15,28 +15,40 @@
 // where tokens are few.  A warp takes four heads of one token at a time, eight lanes
 // a row; a lane holds two 16-byte pieces that rotate with one another, so that the
 // rotation needs no exchange and the norm three shuffles.  The lane's eight angles
-// are the same for all heads: computed once a warp, two by each row's lanes.
+// are the same for all heads: computed once a token, two by each row's lanes.
+//
+// Counted in instructions, 1 KB in and out are 90 clocks of an SM's share of HBM, and so every
+// instruction of a group of rows counts: arithmetic on pairs of fp32, weights kept in
+// registers from one head to the next, four codes rid of their -0 at a time.
 #include "msa_quant.cuh"
 #include "msa_ragged.cuh"
+#include "msa_umma.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kCtas = 4; // warps a CTA, CTAs an SM (5, of 96 registers that spill: ragged prompts 111 -> 131 us)
+constexpr int kSlots = 4;            // groups of four rows that a warp has room for: all but one on their way
 
-__device__ __forceinline__ void widen(uint4 d, float *v)
+// Eight bf16 as four pairs of fp32, and back.
+__device__ __forceinline__ void widen(uint4 d, uint64_t *v)
 {
     const uint32_t e[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(e[k] << 16);
-        v[2 * k + 1] = __uint_as_float(e[k] & 0xFFFF0000u);
-    }
+    for (int k = 0; k < 4; ++k)
+        v[k] = pair(__uint_as_float(e[k] << 16), __uint_as_float(e[k] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 narrow(const float *v)
+__device__ __forceinline__ uint4 narrow(const uint64_t *v)
 {
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    uint32_t e[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a, b;
+        unpair(v[k], a, b);
+        e[k] = pack_bf16(a, b);
+    }
+    return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
 // The request whose tokens token t is among, -1 if none: the last r with
@@ -56,18 +68,42 @@ __device__ __forceinline__ int request_of(const int32_t *offsets, int R, int t)
 }
 
 // Where a lane's two pieces of 8 elements lie: piece i < m turns with piece i + m
-// (m = rotary_dim / 16, interleaved pairs: 8), the pieces behind them in twos.
+// (m = rotary_dim / 16, interleaved pairs: 8), and of those behind them piece 2 m + i is
+// with 8 + m + i.  Neighbouring lanes have neighbouring pieces: with a lane's two
+// next to one another each load and store asks for halves of sectors, twice (a plain copy of
+// 8192 x 68 rows 67 us, 44 so).
 __device__ __forceinline__ int piece(int l, int slot, int m)
 {
-    return l < m ? l + slot * m : 2 * l + slot;
+    return slot == 0 ? (l < m ? l : l + m) : (l < m ? l + m : l + 8);
 }
 
 // Eight floats by the scale s (inv: its reciprocal where that is exact).
-__device__ __forceinline__ void unscale(float *v, float s, float inv)
+__device__ __forceinline__ void unscale(const uint64_t *v, float s, float inv, float *out)
 {
+    if (inv != 0.f) {
+        const uint64_t by = pair(inv, inv);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        v[k] = inv != 0.f ? v[k] * inv : __fdiv_rn(v[k], s);
+        for (int k = 0; k < 4; ++k)
+            unpair(mul2(v[k], by), out[2 * k], out[2 * k + 1]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            unpair(v[k], out[2 * k], out[2 * k + 1]);
+            out[2 * k] = __fdiv_rn(out[2 * k], s);
+            out[2 * k + 1] = __fdiv_rn(out[2 * k + 1], s);
+        }
+    }
+}
+
+// Four floats to E4M3 codes (round to nearest even, saturating), a zero as +0.
+__device__ __forceinline__ uint32_t e4m3x4(const float *v)
+{
+    const uint32_t low = 0x7F7F7F7Fu;
+    uint32_t w;
+    asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n mov.b32 %0, {a, b};\n}\n"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+    return w & (((w & low) + low) | low); // a byte's sign stays where its other bits are not 0
 }
 
 // A row as NVFP4: v[0], v[1] are this lane's pieces (already divided by the tensor
@@ -87,7 +123,7 @@ __device__ __forceinline__ void store_nvfp4(const float (&v)[2][8], int m, bool 
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int c = piece(l, s, m), o = c ^ 1;
-        const int owner = o < m ? o : o < 2 * m ? o - m : o >> 1, slot = o < m ? 0 : o < 2 * m ? 1 : o & 1;
+        const int owner = o < m ? o : o < m + 8 ? o - m : o - 8, slot = o < m || (o >= 2 * m && o < m + 8) ? 0 : 1;
         const float a = __shfl_sync(0xffffffffu, amax[0], (lane & 24) + owner);
         const float b = __shfl_sync(0xffffffffu, amax[1], (lane & 24) + owner);
         const float top = fmaxf(amax[s], slot ? b : a);
@@ -110,174 +146,272 @@ __device__ __forceinline__ void store_nvfp4(const float (&v)[2][8], int m, bool 
     }
 }
 
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams p)
+// A place in the line of groups: token, set, group of the set, and where this lane's row begins.
+struct Cursor {
+    const uint16_t *src;
+    int t, s, g, n; // n: groups of the set
+    __device__ __forceinline__ void enter(const AppendParams &p, int sub)
+    {
+        const RowSet &set = p.set[s];
+        n = (set.heads + 3) >> 2;
+        src = set.x + t * set.stride + (g * 4 + sub) * kDim;
+    }
+    __device__ __forceinline__ void next(const AppendParams &p, int sub)
+    {
+        src += 4 * kDim;
+        if (++g < n)
+            return;
+        g = 0;
+        if (++s == p.sets) {
+            s = 0;
+            ++t;
+        }
+        enter(p, sub);
+    }
+};
+
+__global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const AppendParams p)
 {
+    __shared__ uint4 ring[kWarps][kSlots][2][32]; // a lane reads what it copied itself
     const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3;
-    const long long wi = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int t = (int)(wi / p.chunks), g0 = (int)(wi - (long long)t * p.chunks) * p.per_warp;
-    if (t >= p.T)
+    const long long all = (long long)p.T * p.groups, wi = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const long long x0 = wi * p.per_warp;
+    int left = (int)min((long long)p.per_warp, all - x0);
+    if (left <= 0)
         return;
-    const int g1 = min(p.groups, g0 + p.per_warp);
     const int m = p.interleaved ? 8 : p.units;
     const int at0 = 8 * piece(l, 0, m), at1 = 8 * piece(l, 1, m);
+    const uint32_t mine = smem_u32(&ring[threadIdx.x >> 5][0][0][lane]);
 
-    // a group of four rows: its set, this lane's head and the row's two pieces
-    auto fetch = [&](int g, int &s, int &h, uint4 (&d)[2]) {
-        s = 0;
-#pragma unroll
-        for (int k = 1; k < kMaxSets; ++k)
-            s += k < p.sets && g >= p.set[k].group0;
-        h = (g - p.set[s].group0) * 4 + sub;
-        d[0] = d[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < p.set[s].heads) {
-            const uint16_t *x = p.set[s].x + t * p.set[s].stride + (long long)h * kDim;
-            d[0] = *reinterpret_cast<const uint4 *>(x + at0);
-            d[1] = *reinterpret_cast<const uint4 *>(x + at1);
+    Cursor at{};
+    at.t = (int)(x0 / p.groups);
+    at.g = (int)(x0 - (long long)at.t * p.groups);
+    while (at.s + 1 < p.sets && at.g >= p.set[at.s + 1].group0)
+        ++at.s;
+    at.g -= p.set[at.s].group0;
+    at.enter(p, sub);
+    // rows on their way, into the slot that was read before the one to be read next
+    Cursor to = at;
+    int asked = 0;
+    auto ask = [&] {
+        if (asked < left && to.g * 4 + sub < p.set[to.s].heads) {
+            const uint32_t slot = mine + (asked & (kSlots - 1)) * 1024;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(to.src + at0) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + 512), "l"(to.src + at1) : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++asked < left)
+            to.next(p, sub);
     };
-    int s, h;
-    uint4 d[2];
-    fetch(g0, s, h, d); // on its way while the token's place and angles are found
+#pragma unroll 1
+    for (int k = 0; k < kSlots - 1; ++k)
+        ask();
 
-    // ---- the token: position, page, angles ----
-    int pos;
-    long long page = -1; // -1: nothing of this token goes to the cache
-    int row = 0;
-    if (p.positions) {
-        pos = p.positions[t];
-    } else {
-        const int r = request_of(p.offsets, p.R, t);
-        if (r < 0)
-            return; // behind the last request's tokens: left as it is
-        const int len = p.seq_lens[r];
-        const long long at = (long long)len - 1 + (t - p.offsets[r]);
-        if (len < 1 || at / kPage >= p.maxB) {
-            if (lane == 0)
-                set_error(p.err, kErrSeqLen);
-            return;
-        }
-        pos = (int)at;
-        row = pos % kPage;
-        page = p.block_table[(size_t)r * p.maxB + pos / kPage];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0)
-                set_error(p.err, kErrPage);
-            page = -1;
-        }
-    }
-    const int turned = 2 * p.units; // rotated pieces (interleaved), 2 units of 8 elements
+    int r = -1, first = 0, behind = 0, len = 0; // the token's request, its first token and the first behind it
+    const int turned = 2 * p.units; // rotated pieces of 8 elements (interleaved)
     const bool turn0 = p.interleaved ? l < turned : l < m, turn1 = p.interleaved ? l + 8 < turned : turn0;
-    float cs[8], sn[8];
-    {
-        float c2[2], s2[2];
+    // the lane's frequencies: two of the eight pairs that its row's lanes share
+    unsigned long long freq[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int e = 2 * sub + k, i = p.interleaved ? (e < 4 ? 4 * l + e : 28 + 4 * l + e) : 8 * l + e;
-            const unsigned long long f = i < 8 * p.units ? p.freqs[i] : 0ull;
-            const int turn = (int)(unsigned)((f * (unsigned long long)(long long)pos) >> 32);
-            sincospif((float)turn * 4.656612873077393e-10f, &s2[k], &c2[k]); // 2^-31: half turns
-            s2[k] *= p.scale;
-            c2[k] *= p.scale;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cs[e] = __shfl_sync(0xffffffffu, c2[e & 1], (e >> 1) * 8 + l);
-            sn[e] = __shfl_sync(0xffffffffu, s2[e & 1], (e >> 1) * 8 + l);
-        }
+    for (int k = 0; k < 2; ++k) {
+        const int e = 2 * sub + k, i = p.interleaved ? (e < 4 ? 4 * l + e : 28 + 4 * l + e) : 8 * l + e;
+        freq[k] = i < 8 * p.units ? p.freqs[i] : 0ull;
     }
+    long long page = -1; // -1: nothing of this token goes to the cache
+    int row = 0, token = -1, entry = -1; // entry: the block of the table that `page` is from
+    bool skip = false;                 // nothing of this token is written
+    uint64_t cs[4], sn[4], ns[4];      // cosines, sines and the sines' negatives, in pairs
+    uint64_t weight[2][4] = {};
+    int done = 0;
 
-    for (int g = g0; g < g1; ++g) {
-        int s_next = 0, h_next = 0;
-        uint4 d_next[2] = {};
-        if (g + 1 < g1)
-            fetch(g + 1, s_next, h_next, d_next);
-        const RowSet &set = p.set[s];
-        const bool real = h < set.heads;
-        float v[2][8];
-        widen(d[0], v[0]);
-        widen(d[1], v[1]);
-        if (set.weight) {
-            float ss = 0.f;
+    while (done < left) {
+        // ---- the token: position, page, angles ----
+        if (at.t != token) {
+            const int t = token = at.t;
+            int pos = 0;
+            skip = false;
+            if (p.positions) {
+                pos = p.positions[t];
+            } else {
+                if (r < 0 || t >= behind) {
+                    r = request_of(p.offsets, p.R, t);
+                    entry = -1;
+                    if (r >= 0) {
+                        first = p.offsets[r];
+                        behind = p.offsets[r + 1];
+                        len = p.seq_lens[r];
+                    }
+                }
+                const int room = p.maxB * kPage; // at most 2^21
+                skip = r < 0;                    // behind the last request's tokens: left as it is
+                pos = len - 1 + (t - first);
+                if (!skip && (len < 1 || len > room || pos >= room)) {
+                    if (lane == 0)
+                        set_error(p.err, kErrSeqLen);
+                    skip = true;
+                }
+                if (!skip) {
+                    row = pos % kPage;
+                    if (pos / kPage != entry) { // (not the page of the token before)
+                        entry = pos / kPage;
+                        page = p.block_table[(size_t)r * p.maxB + entry];
+                        if (page < 0 || page >= p.num_pages) {
+                            if (lane == 0)
+                                set_error(p.err, kErrPage);
+                            page = -1;
+                        }
+                    }
+                }
+            }
+            if (p.units > 0) {
+                float c2[2], s2[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                ss = fmaf(v[0][k], v[0][k], fmaf(v[1][k], v[1][k], ss));
+                for (int k = 0; k < 2; ++k) {
+                    const int turn = (int)(unsigned)((freq[k] * (unsigned long long)(long long)pos) >> 32);
+                    sincospif((float)turn * 4.656612873077393e-10f, &s2[k], &c2[k]); // 2^-31: half turns
+                    s2[k] *= p.scale;
+                    c2[k] *= p.scale;
+                }
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float f = rsqrtf(fmaf(ss, 1.f / kDim, p.eps));
-            const uint16_t *w = set.weight + (p.per_head && real ? h * kDim : 0);
-            float wv[8];
+                for (int e = 0; e < 4; ++e) {
+                    const float s0 = __shfl_sync(0xffffffffu, s2[0], 8 * e + l), s1 = __shfl_sync(0xffffffffu, s2[1], 8 * e + l);
+                    cs[e] = pair(__shfl_sync(0xffffffffu, c2[0], 8 * e + l), __shfl_sync(0xffffffffu, c2[1], 8 * e + l));
+                    sn[e] = pair(s0, s1);
+                    ns[e] = pair(-s0, -s1);
+                }
+            }
+        }
+
+        // ---- the set's rows: where the lane's goes, and how far the next one is ----
+        const RowSet &set = p.set[at.s];
+        const int where = set.where, heads = set.heads, end = done + min(at.n - at.g, left - done);
+        const bool normed = set.weight != nullptr, rotated = set.rotated;
+        const bool f4 = set.bytes == kDim / 2, f8 = set.bytes == kDim;
+        int h = at.g * 4 + sub;
+        const int stop = skip || (where != kToOut && page < 0) ? 0 : heads; // rows from here on are not written
+        const long long block = where == kToOut ? at.t : page;
+        const int in = where == kToOut ? 0 : row;
+        uint8_t *dst = set.y + block * set.block_step + (unsigned)(h * set.head_step + in * set.bytes);
+        uint8_t *dst_scales = set.scales + block * set.scales_block_step + (unsigned)(h * set.scales_head_step + in * (kDim / 16));
+        const int step = 4 * set.head_step, step_scales = 4 * set.scales_head_step;
+        const float scale = set.scale, inverse = set.inverse;
+        const uint16_t *weights = set.weight;
+        uint4 raw[2]; // the lane's norm weights: the set's, or of the head at hand, asked for before its row is
+        auto ask_weights = [&](const uint16_t *w) {
+            raw[0] = __ldg(reinterpret_cast<const uint4 *>(w + at0));
+            raw[1] = __ldg(reinterpret_cast<const uint4 *>(w + at1));
+        };
+        auto take_weights = [&] {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                widen(*reinterpret_cast<const uint4 *>(w + (q ? at1 : at0)), wv);
+                widen(raw[q], weight[q]);
+                if (p.offset != 0.f)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[q][k] = v[q][k] * f * (wv[k] + p.offset);
+                    for (int k = 0; k < 4; ++k)
+                        weight[q][k] = add2(weight[q][k], pair(p.offset, p.offset));
             }
+        };
+        const bool each_head = normed && p.per_head;
+        if (normed && !each_head) {
+            ask_weights(weights);
+            take_weights();
         }
-        if (set.rotated) {
-            if (!p.interleaved) {
-                if (turn0)
+
+#pragma unroll 1
+        for (; done < end; ++done, h += 4, dst += step, dst_scales += step_scales) {
+            uint4 d[2];
+            if (each_head)
+                ask_weights(weights + (h < heads ? h * kDim : 0));
+            ask();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+            const uint32_t slot = mine + (done & (kSlots - 1)) * 1024;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(d[0].x), "=r"(d[0].y), "=r"(d[0].z), "=r"(d[0].w) : "r"(slot) : "memory");
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(d[1].x), "=r"(d[1].y), "=r"(d[1].z), "=r"(d[1].w) : "r"(slot + 512) : "memory");
+            const bool real = h < stop;
+            // rows without norm and rotation are copied bit by bit where they stay bf16
+            if (!normed && !rotated && !f4 && !f8) {
+                if (real) {
+                    *reinterpret_cast<uint4 *>(dst + 2 * at0) = d[0];
+                    *reinterpret_cast<uint4 *>(dst + 2 * at1) = d[1];
+                }
+                continue;
+            }
+            uint64_t v[2][4];
+            widen(d[0], v[0]);
+            widen(d[1], v[1]);
+            if (normed) {
+                if (each_head)
+                    take_weights();
+                uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float a = v[0][k], b = v[1][k];
-                        v[0][k] = a * cs[k] - b * sn[k];
-                        v[1][k] = b * cs[k] + a * sn[k];
-                    }
-            } else {
+                for (int k = 0; k < 4; ++k) {
+                    s2[0] = fma2(v[0][k], v[0][k], s2[0]);
+                    s2[1] = fma2(v[1][k], v[1][k], s2[1]);
+                }
+                float ss, s_odd;
+                unpair(add2(s2[0], s2[1]), ss, s_odd);
+                ss += s_odd;
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1)
+                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float f = rsqrtf(fmaf(ss, 1.f / kDim, p.eps));
+                const uint64_t f2 = pair(f, f);
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (q ? turn1 : turn0)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[q][k] = mul2(mul2(v[q][k], f2), weight[q][k]);
+            }
+            if (rotated) {
+                if (!p.interleaved) {
+                    if (turn0)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float a = v[q][2 * k], b = v[q][2 * k + 1], c = cs[4 * q + k], z = sn[4 * q + k];
-                            v[q][2 * k] = a * c - b * z;
-                            v[q][2 * k + 1] = b * c + a * z;
+                            const uint64_t a = v[0][k], b = v[1][k];
+                            v[0][k] = fma2(b, ns[k], mul2(a, cs[k]));
+                            v[1][k] = fma2(a, sn[k], mul2(b, cs[k]));
                         }
-            }
-        }
-        // rows without norm and rotation are copied bit by bit where they stay bf16
-        const bool plain = !set.weight && !set.rotated;
-        const uint4 b0 = plain ? d[0] : narrow(v[0]), b1 = plain ? d[1] : narrow(v[1]);
-        if (set.where == kToOut) {
-            if (real) {
-                uint16_t *y = set.y + ((size_t)t * set.heads + h) * kDim;
-                *reinterpret_cast<uint4 *>(y + at0) = b0;
-                *reinterpret_cast<uint4 *>(y + at1) = b1;
-            }
-        } else if (page >= 0) {
-            const bool index = set.where == kToIndex;
-            const size_t head = index ? (size_t)page * p.Hi + h : ((size_t)page * 2 + (set.where == kToV)) * p.Hkv + h;
-            const size_t prow = head * kPage + row;
-            if (index ? p.idx_f4 : p.kv_fmt == kFmtF4) {
-                if (index) {
-                    store_nvfp4(v, m, real, p.idxk + prow * (kDim / 2), p.idxk_scales + prow * (kDim / 16));
                 } else {
-                    const float sc = set.where == kToV ? p.v_scale : p.k_scale, inv = set.where == kToV ? p.v_inv : p.k_inv;
-                    unscale(v[0], sc, inv);
-                    unscale(v[1], sc, inv);
-                    uint8_t *tile = p.kv + head * kF4KvTile;
-                    store_nvfp4(v, m, real, tile + row * (kDim / 2), tile + kPage * (kDim / 2) + row * (kDim / 16));
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (q ? turn1 : turn0)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float a, b, c[2], z[2];
+                                unpair(v[q][k], a, b);
+                                unpair(cs[2 * q + (k >> 1)], c[0], c[1]);
+                                unpair(sn[2 * q + (k >> 1)], z[0], z[1]);
+                                v[q][k] = pair(a * c[k & 1] - b * z[k & 1], b * c[k & 1] + a * z[k & 1]);
+                            }
                 }
-            } else if (!index && p.kv_fmt == kFmtFp8) {
-                const float sc = set.where == kToV ? p.v_scale : p.k_scale, inv = set.where == kToV ? p.v_inv : p.k_inv;
+            }
+            if (f4) {
+                float y[2][8];
+                unscale(v[0], scale, inverse, y[0]);
+                unscale(v[1], scale, inverse, y[1]);
+                store_nvfp4(y, m, real, dst, dst_scales);
+            } else if (f8) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    unscale(v[q], sc, inv);
-                    const uint2 c = make_uint2(e4m3x2_rn_sat(v[q][1], v[q][0]) | e4m3x2_rn_sat(v[q][3], v[q][2]) << 16,
-                                               e4m3x2_rn_sat(v[q][5], v[q][4]) | e4m3x2_rn_sat(v[q][7], v[q][6]) << 16);
+                    float y[8];
+                    unscale(v[q], scale, inverse, y);
                     if (real)
-                        *reinterpret_cast<uint2 *>(p.kv + prow * kDim + (q ? at1 : at0)) = c;
+                        *reinterpret_cast<uint2 *>(dst + (q ? at1 : at0)) = make_uint2(e4m3x4(y), e4m3x4(y + 4));
                 }
             } else if (real) {
-                uint8_t *at = (index ? p.idxk : p.kv) + prow * (2 * kDim);
-                *reinterpret_cast<uint4 *>(at + 2 * at0) = b0;
-                *reinterpret_cast<uint4 *>(at + 2 * at1) = b1;
+                *reinterpret_cast<uint4 *>(dst + 2 * at0) = narrow(v[0]);
+                *reinterpret_cast<uint4 *>(dst + 2 * at1) = narrow(v[1]);
             }
         }
-        s = s_next, h = h_next;
-        d[0] = d_next[0], d[1] = d_next[1];
+        // ---- the next set, or the next token ----
+        at.g = 0;
+        if (++at.s == p.sets) {
+            at.s = 0;
+            ++at.t;
+        }
+        at.n = (p.set[at.s].heads + 3) >> 2;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 } // namespace
@@ -287,15 +421,11 @@ cudaError_t launch_append(const AppendParams &params, cudaStream_t stream)
     AppendParams p = params;
     if (p.T == 0 || p.groups == 0)
         return cudaSuccess;
-    // Few tokens: a warp for each group, the latency of one.  Many: up to eight groups
-    // a warp, which share its angles and its place.
-    const long long all = (long long)p.T * p.groups;
-    const int per = (int)(all / (152 * 48) < 1 ? 1 : all / (152 * 48) > 8 ? 8 : all / (152 * 48));
-    p.chunks = (p.groups + per - 1) / per;
-    p.per_warp = (p.groups + p.chunks - 1) / p.chunks;
-    const long long blocks = ((long long)p.T * p.chunks + kWarps - 1) / kWarps;
-    if (blocks > 0x7FFFFFFFll)
-        return cudaErrorInvalidValue;
+    // Few groups: a warp for each, the latency of one.  Many: as many warps as the GPU holds at a time, with
+    // runs of neighbouring groups, which share angles and places.
+    const long long all = (long long)p.T * p.groups, warps = 152ll * kCtas * kWarps;
+    p.per_warp = (int)((all + warps - 1) / warps);
+    const long long blocks = (all + (long long)p.per_warp * kWarps - 1) / ((long long)p.per_warp * kWarps);
     const cudaError_t e = launch_kernel(append_kernel, dim3((unsigned)blocks), dim3(32 * kWarps), 0, stream, false, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -10,11 +10,16 @@ namespace msa {
 struct RowSet {
     const uint16_t *x;      // bf16 bits, a token's heads one after another
     const uint16_t *weight; // norm weights (bf16), nullptr: no norm
-    uint16_t *y;            // dense output [T][heads][128], nullptr: the rows go to the cache
+    // head h of a token goes to y + block * block_step + h * head_step + row * bytes, block and row
+    // being the token and 0 (kToOut) or its page and the row there; the scales of NVFP4 rows alike
+    uint8_t *y, *scales;
     long long stride;       // elements from a token's rows to the next token's
+    long long block_step, scales_block_step;
+    int head_step, scales_head_step, bytes;
     int heads, group0;      // group0: the set's first group of the token's
     int where;              // kToOut .. kToIndex
     bool rotated;
+    float scale, inverse;   // what stored values are multiplied with, and its reciprocal where that is exact, else 0
 };
 
 constexpr int kToOut = 0, kToK = 1, kToV = 2, kToIndex = 3;
@@ -23,22 +28,17 @@ constexpr int kMaxSets = 5;
 struct AppendParams {
     RowSet set[kMaxSets];
     int sets, groups;           // row sets, and their groups of four rows a token
-    int per_warp, chunks;       // groups a warp takes, warps a token
+    int per_warp;               // groups that a warp takes
     const unsigned long long *freqs; // turns a position, in 2^-64, [rotary_dim / 2]
     const int32_t *positions;   // [T], nullptr: by offsets and seq_lens
     const int32_t *offsets;     // [R + 1]
     const int32_t *seq_lens;    // [R]
     const int32_t *block_table; // [R][maxB]
-    uint8_t *kv, *idxk, *idxk_scales;
     uint32_t *err;
-    int T, R, maxB, num_pages, Hkv, Hi;
+    int T, R, maxB, num_pages;
     int units;                  // rotary_dim / 16
     bool interleaved, per_head;
     float scale, eps, offset;
-    int kv_fmt;
-    bool idx_f4;
-    float k_scale, v_scale;     // what stored values are multiplied with
-    float k_inv, v_inv;         // 1 / scale where that is exact (a power of two), else 0
 };
 
 // A unit cut between CTAs: its first cut is this record's CTA's start (c0 < 0: there is none).

@@ -68,8 +68,14 @@ msa_status add_set(AppendParams &p, const void *x, int64_t stride, const void *w
     RowSet &s = p.set[p.sets++];
     s.x = static_cast<const uint16_t *>(x);
     s.weight = static_cast<const uint16_t *>(weight);
-    s.y = static_cast<uint16_t *>(y);
+    s.y = static_cast<uint8_t *>(y);
+    s.scales = nullptr;
     s.stride = by;
+    s.bytes = s.head_step = 2 * kDim;
+    s.block_step = (long long)heads * s.head_step;
+    s.scales_head_step = 0;
+    s.scales_block_step = 0;
+    s.scale = s.inverse = 1.f;
     s.heads = heads;
     s.group0 = p.groups;
     s.where = where;
@@ -87,6 +93,33 @@ void set_rope(AppendParams &p, const msa_rope *r, const uint64_t *freqs)
     p.scale = r->scale;
     p.eps = r->norm_eps;
     p.offset = r->norm_offset;
+}
+
+// 1 / s where a product with it is the quotient by s: s a power of two.
+float exact_inverse(float s)
+{
+    int e;
+    const float m = std::frexp(std::fabs(s), &e);
+    return m == 0.5f && e > -120 && e < 120 ? 1.f / s : 0.f;
+}
+
+// The set added last goes to head tiles of kPage rows of a pool, from tile `first` of a page's `tiles` on:
+// codes and scales of a tile together (scales == nullptr) or in two pools.
+void to_pool(AppendParams &p, void *pool, void *scales, int dtype, int first, int tiles, float scale)
+{
+    RowSet &s = p.set[p.sets - 1];
+    s.bytes = dtype == MSA_BF16 ? 2 * kDim : dtype == MSA_FP8_E4M3 ? kDim : kDim / 2;
+    const bool f4 = dtype == MSA_NVFP4;
+    s.head_step = kPage * s.bytes + (f4 && !scales ? kPage * (kDim / 16) : 0);
+    s.block_step = (long long)tiles * s.head_step;
+    s.y = static_cast<uint8_t *>(pool) + (long long)first * s.head_step;
+    if (f4) {
+        s.scales_head_step = scales ? kPage * (kDim / 16) : s.head_step;
+        s.scales_block_step = (long long)tiles * s.scales_head_step;
+        s.scales = scales ? static_cast<uint8_t *>(scales) + (long long)first * s.scales_head_step : s.y + kPage * s.bytes;
+    }
+    s.scale = scale;
+    s.inverse = exact_inverse(scale);
 }
 
 struct RaggedLayout {
@@ -113,14 +146,6 @@ int attend_ctas(const msa_shape *s)
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
         return -1;
     return sms < kCacheCtaBound ? sms : kCacheCtaBound;
-}
-
-// 1 / s where a product with it is the quotient by s: s a power of two.
-float exact_inverse(float s)
-{
-    int e;
-    const float m = std::frexp(std::fabs(s), &e);
-    return m == 0.5f && e > -120 && e < 120 ? 1.f / s : 0.f;
 }
 
 } // namespace
@@ -212,30 +237,25 @@ msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uin
         return st;
     if (q_idx && (st = add_set(p, q_idx, rope->q_idx_stride, q_idx_weight, q_idx_out, Hi, kToOut, turn)) != MSA_OK)
         return st;
-    if ((st = add_set(p, k, rope->k_stride, k_weight, nullptr, Hkv, kToK, turn)) != MSA_OK ||
-        (st = add_set(p, v, rope->v_stride, nullptr, nullptr, Hkv, kToV, false)) != MSA_OK)
+    if ((st = add_set(p, k, rope->k_stride, k_weight, nullptr, Hkv, kToK, turn)) != MSA_OK)
         return st;
-    if (idxk && (st = add_set(p, idxk, rope->idxk_stride, idxk_weight, nullptr, Hi, kToIndex, turn)) != MSA_OK)
+    to_pool(p, kv_pool, nullptr, shape->kv_dtype, 0, 2 * Hkv, shape->kv_dtype == MSA_BF16 ? 1.f : shape->k_scale);
+    if ((st = add_set(p, v, rope->v_stride, nullptr, nullptr, Hkv, kToV, false)) != MSA_OK)
         return st;
+    to_pool(p, kv_pool, nullptr, shape->kv_dtype, Hkv, 2 * Hkv, shape->kv_dtype == MSA_BF16 ? 1.f : shape->v_scale);
+    if (idxk) {
+        if ((st = add_set(p, idxk, rope->idxk_stride, idxk_weight, nullptr, Hi, kToIndex, turn)) != MSA_OK)
+            return st;
+        to_pool(p, idxk_pool, idxk_scales, shape->index_dtype, 0, Hi, 1.f);
+    }
     p.offsets = offsets;
     p.seq_lens = seq_lens;
     p.block_table = block_table;
-    p.kv = static_cast<uint8_t *>(kv_pool);
-    p.idxk = static_cast<uint8_t *>(idxk_pool);
-    p.idxk_scales = static_cast<uint8_t *>(idxk_scales);
     p.err = static_cast<uint32_t *>(workspace);
     p.T = num_tokens;
     p.R = shape->num_requests;
     p.maxB = shape->max_blocks_per_seq;
     p.num_pages = shape->num_pages;
-    p.Hkv = Hkv;
-    p.Hi = Hi;
-    p.kv_fmt = shape->kv_dtype == MSA_BF16 ? kFmtBf16 : shape->kv_dtype == MSA_FP8_E4M3 ? kFmtFp8 : kFmtF4;
-    p.idx_f4 = idx_f4;
-    p.k_scale = shape->k_scale;
-    p.v_scale = shape->v_scale;
-    p.k_inv = exact_inverse(p.k_scale);
-    p.v_inv = exact_inverse(p.v_scale);
     return cuda_status(launch_append(p, stream));
 }
 
