@@ -50,7 +50,7 @@ constexpr float kMost = 0x1p16f;   // what the p of a page may add up to before 
 constexpr float kMost16 = 0x1p15f; // the same where P is f16
 constexpr float kPUp16 = 7.f;      // f16 P: 2^7 2^(s - m)
 constexpr int kSlotFloats = kRows * (kDim + 2); // o[rows][128], m, l
-constexpr int kUnitCost = 2;     // a unit's queries and outputs in pages
+constexpr int kUnitCost = 3;     // a unit's queries and outputs in pages
 constexpr int kMinRange = 4;     // what a CTA takes at least
 
 __host__ __device__ constexpr int threads_of(int fmt)
@@ -84,19 +84,10 @@ __host__ __device__ constexpr Smem smem_layout(int fmt)
     s.inv = s.xch + 4 * 128 * 4; // exponents that undo the scaling of query rows, of two units
     s.bars = s.inv + (fmt == kFmtBf16 ? 0 : 2 * kRows);
     s.misc = s.bars + (2 * ring_tiles(fmt) + 2 * ready_tiles(fmt) + 16) * 8;
-    s.total = s.misc + 256;
+    s.total = s.misc + 288;
     return s;
 }
 static_assert(smem_layout(kFmtBf16).total <= 232448 && smem_layout(kFmtFp8).total <= 232448 && smem_layout(kFmtF4).total <= 232448, "shared memory");
-
-struct Misc {
-    long long start_before;
-    long long scan[24];
-    int abort, start_r;
-    uint32_t tmem;
-    int later_bad[8]; // unit counter + 1 where V rows of later tokens are not finite
-};
-static_assert(sizeof(Misc) <= 256, "misc");
 
 // sum over i < n of floor((a i + b) / m)
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
@@ -143,6 +134,16 @@ struct Request {
     }
 };
 
+struct Misc {
+    long long start_before;
+    long long scan[24];
+    Request start;
+    int abort, start_r;
+    uint32_t tmem;
+    int later_bad[8]; // unit counter + 1 where V rows of later tokens are not finite
+};
+static_assert(sizeof(Misc) <= 288, "misc");
+
 // Reads request r: units = 0 where it has no tokens, no states (idle) or lengths that are refused (reported in *bad).
 __device__ __forceinline__ Request read_request(const AttendParams &p, int r, bool *bad, bool *idle)
 {
@@ -166,16 +167,26 @@ __device__ __forceinline__ Request read_request(const AttendParams &p, int r, bo
     return q;
 }
 
+// x / y, in 32 bits where both fit (a 64-bit division takes as long as the rest of a CTA's start)
+__device__ __forceinline__ long long quotient(long long x, long long y)
+{
+    if (((unsigned long long)(x | y) >> 32) == 0)
+        return (unsigned)x / (unsigned)y;
+    return x / y;
+}
+
+// The line of length W cut into n ranges (the first W % n one longer): where range c begins, and the range that
+// holds place x.
 __device__ __forceinline__ long long cut(int c, long long W, int n)
 {
-    const long long each = W / n, more = W - each * n;
+    const long long each = quotient(W, n), more = W - each * n;
     return c * each + min((long long)c, more);
 }
 
 __device__ __forceinline__ int cut_of(long long x, long long W, int n)
 {
-    const long long each = W / n, more = W - each * n, at = more * (each + 1);
-    return (int)(x < at ? x / (each + 1) : more + (x - at) / each);
+    const long long each = quotient(W, n), more = W - each * n, at = more * (each + 1);
+    return (int)(x < at ? quotient(x, each + 1) : more + quotient(x - at, each));
 }
 
 // The share of a CTA, unit by unit.  Every role walks it alike.
@@ -497,9 +508,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const int per = (p.R + NT - 1) / NT;
     const int lo = min(p.R, (int)threadIdx.x * per), hi = min(p.R, lo + per);
     long long mine = 0;
+    Request q{};
     for (int r = lo; r < hi; ++r) {
         bool bad, idle;
-        const Request q = read_request(p, r, &bad, &idle);
+        q = read_request(p, r, &bad, &idle);
         if (q.units)
             mine += q.before(p, q.units) * p.Hkv;
         if (bad && blockIdx.x == 0)
@@ -527,27 +539,29 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const long long x1 = (int)blockIdx.x < ranges ? cut(blockIdx.x + 1, W, ranges) : W;
     if (x0 < x1 && before <= x0 && x0 < before + mine) {
         long long at = before;
-        for (int r = lo; r < hi; ++r) {
-            bool bad, idle;
-            const Request q = read_request(p, r, &bad, &idle);
-            const long long some = q.units ? q.before(p, q.units) * p.Hkv : 0;
-            if (at <= x0 && x0 < at + some) {
-                misc.start_r = r;
-                misc.start_before = at;
+        int r = lo;
+        if (per > 1)
+            for (;; ++r) {
+                bool bad, idle;
+                q = read_request(p, r, &bad, &idle);
+                const long long some = q.units ? q.before(p, q.units) * p.Hkv : 0;
+                if (x0 < at + some)
+                    break;
+                at += some;
             }
-            at += some;
-        }
+        misc.start = q;
+        misc.start_r = r;
+        misc.start_before = at;
     }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = misc.tmem;
     if (x0 < x1) {
-        bool bad, idle;
         w.r = misc.start_r;
-        w.q = read_request(p, w.r, &bad, &idle);
+        w.q = misc.start;
         const long long in = x0 - misc.start_before, each = w.q.before(p, w.q.units);
-        w.head = (int)(in / each);
+        w.head = (int)quotient(in, each);
         const long long rest = in - w.head * each;
         // the last unit with before(u) <= rest: the lanes try 32 at a time
         int n = w.q.units;
@@ -1117,9 +1131,15 @@ cudaError_t launch_t(const AttendParams &p, const CUtensorMap &map, const CUtens
     cudaError_t e = cudaFuncSetAttribute(attend_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
+    // no more CTAs than the line can have ranges, whatever the lengths in device memory are
+    const double units = (double)(p.T / p.unit_tokens + p.R) * p.Hkv, most = units * (kUnitCost + p.maxB) / kMinRange;
+    if (most < ctas)
+        ctas = most < 1 ? 1 : (int)most;
     e = launch_kernel(attend_kernel<FMT>, dim3(ctas), dim3(threads_of(FMT)), smem, stream, false, map, q_map, p);
+    // a unit has no more rows than the batch
+    const int rows = (p.T < p.unit_tokens / 2 ? p.T : p.unit_tokens / 2) * p.G, blocks = p.T > p.unit_tokens / 2 ? 8 : (rows + 31) / 32;
     if (e == cudaSuccess && ctas > 1)
-        e = launch_kernel(attend_join_kernel, dim3(ctas - 1, 8, 4), dim3(256), 0, stream, true, p);
+        e = launch_kernel(attend_join_kernel, dim3(ctas - 1, blocks, 4), dim3(256), 0, stream, true, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
