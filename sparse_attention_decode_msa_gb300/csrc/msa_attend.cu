@@ -814,7 +814,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         auto sync_all = [&] { asm volatile("bar.sync 9, 512;" ::: "memory"); };
         // Query rows of a unit into the stream's operand tile, once the stream's last S of the unit
         // before is done.  Rows beyond the unit's hold anything: nothing is read from what they give.
+        uint32_t copies = 0;
         auto copy_queries = [&](const Share &u) {
+            if (*abort_flag) // (the last copy may still be on its way)
+                return;
+            ++copies;
             if (elect_one()) {
                 const int token = u.token0(p) + (u.two(p) ? each * t : 0);
                 const uint32_t dst = smem + L.q + t * kTile16, bar = q_raw + 8 * t;
@@ -1013,6 +1017,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                                          whole ? nullptr : slot + 4 * slot_row, 64 * half);
             }
         }
+        if (copies > 0) // the CTA's memory must outlive them (they have long landed unless a wait ran out)
+            mbar_wait_bounded(q_raw + 8 * t, (copies - 1) & 1u);
     } else if constexpr (CONV) {
         // ---- converters: a ring tile to a 16-bit tile, in the order of use ----
         const int row = threadIdx.x & 127;
@@ -1038,7 +1044,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
                 if (z >= DEPTH)
                     wait(ready_free + 8 * (z % DEPTH), (uint32_t)(z / DEPTH - 1) & 1u);
-                const bool bad = convert_row<FMT, 4>(gsm + (z % TILES) * TB, gsm + L.staged + (z % DEPTH) * kTile16 + row * 128, row, tail, drop, check);
+                const bool bad = convert_row<FMT, 2, 4>(gsm + (z % TILES) * TB, gsm + L.staged + (z % DEPTH) * kTile16 + row * 128, row, tail, drop, check);
                 if (bad)
                     misc.later_bad[w.seg & 7] = w.seg + 1;
                 fence_async_smem();

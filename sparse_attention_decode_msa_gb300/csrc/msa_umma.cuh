@@ -318,30 +318,38 @@ __device__ __forceinline__ bool finite(float v)
 // Row `row` of a ring tile (E4M3, NVFP4) to f16 in the layout of a 16-bit tile; dst is the row's place in its
 // first half.  On a last page (tail) a row that is not cached becomes zeros (drop), and infinities
 // and NaN of a row that only later tokens see (check) do too: true is returned for those.
-template <int FMT, int UNROLL = 2>
+// AHEAD: 16-byte pieces that are loaded before any of them is stored (the compiler moves no load past a store).
+template <int FMT, int UNROLL = 2, int AHEAD = 1>
 __device__ __forceinline__ bool convert_row(const uint8_t *src, uint8_t *dst, int row, bool tail, bool drop, bool check)
 {
     bool bad = false;
     if (FMT == kFmtFp8) {
 #pragma unroll UNROLL // (dense decode, all: 426 us for 413, 48 tokens over 2 x 131072; NVFP4 loses with less, 507 for 488)
-        for (int c = 0; c < 8; ++c) { // 16 dimensions
-            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ (row & 7)) << 4));
-            uint32_t e[4] = {d.x, d.y, d.z, d.w}, o[8];
-            if (tail) {
+        for (int c0 = 0; c0 < 8; c0 += AHEAD) { // 16 dimensions each
+            uint4 d[AHEAD];
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    if (check && ((e[q >> 2] >> (8 * (q & 3))) & 0x7Fu) == 0x7Fu)
-                        e[q >> 2] &= ~(0xFFu << (8 * (q & 3))), bad = true;
+            for (int u = 0; u < AHEAD; ++u)
+                d[u] = *reinterpret_cast<const uint4 *>(src + row * 128 + (((c0 + u) ^ (row & 7)) << 4));
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int c = c0 + u;
+                uint32_t e[4] = {d[u].x, d[u].y, d[u].z, d[u].w}, o[8];
+                if (tail) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (check && ((e[q >> 2] >> (8 * (q & 3))) & 0x7Fu) == 0x7Fu)
+                            e[q >> 2] &= ~(0xFFu << (8 * (q & 3))), bad = true;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        e[q] = drop ? 0u : e[q];
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    e[q] = drop ? 0u : e[q];
+                    e4m3x4_to_f16x2x2(e[q], o[2 * q], o[2 * q + 1]);
+                uint8_t *at = dst + (c >> 2) * 16384;
+                *reinterpret_cast<uint4 *>(at + (((2 * c) & 7) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(at + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                e4m3x4_to_f16x2x2(e[q], o[2 * q], o[2 * q + 1]);
-            uint8_t *at = dst + (c >> 2) * 16384;
-            *reinterpret_cast<uint4 *>(at + (((2 * c) & 7) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(at + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
         }
     } else {
         uint64_t sc = *reinterpret_cast<const uint64_t *>(src + 8192 + row * 8);
@@ -357,10 +365,15 @@ __device__ __forceinline__ bool convert_row(const uint8_t *src, uint8_t *dst, in
                 if ((zero >> q) & 1u)
                     sc &= ~(0xFFull << (8 * q)); // a scale of 0: products of 0
         }
+        uint4 d[4];
+#pragma unroll
+        for (int c = 0; AHEAD > 1 && c < 4; ++c)
+            d[c] = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
 #pragma unroll
         for (int c = 0; c < 4; ++c) { // 32 dimensions, two scales
-            const uint4 d = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-            const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+            if (AHEAD == 1)
+                d[c] = *reinterpret_cast<const uint4 *>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+            const uint32_t e[4] = {d[c].x, d[c].y, d[c].z, d[c].w};
             const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)(sc >> (16 * c)) & 0xFFFFu);
             const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
             uint8_t *at = dst + (c >> 1) * 16384;
