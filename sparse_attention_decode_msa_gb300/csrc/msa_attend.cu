@@ -309,12 +309,12 @@ __device__ __noinline__ float row_maximum(uint32_t at_s, float sc, int seen)
 }
 
 // 64 columns of this thread's row of S to p = 2^(sc s - ref), as pairs of bf16 (f16) in pr; their
-// sum.  TAIL: columns from `seen` on are 0.
+// sum, and that of the bf16 they become.  TAIL: columns from `seen` on are 0.
 template <bool F16, bool TAIL>
-__device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, int seen, uint32_t (&pr)[32])
+__device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, int seen, uint32_t (&pr)[32], float &rounded)
 {
     const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
-    uint64_t sum[2] = {0ull, 0ull};
+    uint64_t sum[2] = {0ull, 0ull}, sumr[2] = {0ull, 0ull};
     uint32_t v[2][16];
     tmem_ld16_async(at_s, v[0]);
 #pragma unroll
@@ -334,10 +334,14 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
                 e1 = 16 * c + k + 1 < seen ? e1 : 0.f;
             }
             sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
-            pr[8 * c + (k >> 1)] = F16 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+            const uint32_t both = pr[8 * c + (k >> 1)] = F16 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+            if (!F16)
+                sumr[(k >> 1) & 1] = add2(sumr[(k >> 1) & 1], pair(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u)));
         }
     }
     float a, b;
+    unpair(add2(sumr[0], sumr[1]), a, b);
+    rounded = a + b;
     unpair(add2(sum[0], sum[1]), a, b);
     return a + b;
 }
@@ -838,7 +842,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const bool real = at_lane < rows, idle = (warp & 3) * 32 >= rows; // idle: no row of this warp's is the unit's
             const int j = (two ? each * t : 0) + min(at_lane, rows - 1) / p.G;  // the row's token
             const int seen0 = w.q.seen(p, w.u), lim = seen0 + (p.causal ? j : 0);
-            float sc = p.scale_log2, m = 0.f, l = 0.f; // scale, reference and sum
+            float sc = p.scale_log2, m = 0.f, l = 0.f, lr = 0.f; // scale, reference, sum, sum of the rounded p
             // A row's reference is its maximum over the first page.  Later pages are not searched for theirs:
             // p may pass 1 as long as it stays a number that P and the sums can hold, which the sum of half a
             // page tells; where a row's passes kMost its warps' rows get new references before P is written.
@@ -852,6 +856,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const float ref = mx == ninf ? 0.f : mx, f = i > 0 && mx > m ? ex2(m - ref) : 1.f;
                 m = i == 0 || mx > m ? ref : m;
                 l *= f;
+                lr *= f;
                 if (i > 0) {
                     wait(pv_done + 8 * t, (steps - 1) & 1u); // O holds every step before this one
                     tcgen05_after_sync();
@@ -886,14 +891,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 if (i == 0)
                     new_reference(0, 64);
                 uint32_t pr[32];
-                float sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr);
+                float rounded, sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr, rounded);
                 // (both warps have read S, which P replaces)
                 if (any_of_two_warps(pair_bar, i > 0 && sum > (CONV ? kMost16 : kMost))) {
                     new_reference(i, 64);
-                    sum = row_to_p<CONV, true>(at_s, sc, m, 64, pr);
+                    sum = row_to_p<CONV, true>(at_s, sc, m, 64, pr, rounded);
                     sync_pair();
                 }
                 l += sum;
+                lr += rounded;
                 page_done(pr);
             }
 #pragma unroll 1
@@ -914,13 +920,14 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 if (i == 0)
                     new_reference(0, min(64, seen));
                 uint32_t pr[32];
-                float sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr);
+                float rounded, sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
                 if (any_of_two_warps(pair_bar, i > 0 && sum > (CONV ? kMost16 : kMost))) {
                     new_reference(i, min(64, seen));
-                    sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr);
+                    sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
                     sync_pair();
                 }
                 l += sum;
+                lr += rounded;
                 page_done(pr);
             }
 
@@ -928,24 +935,35 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const Share at = w;
             w.next(p);
             const bool whole = at.b == 0 && n == at.nb, ends = at.b + n == at.nb;
-            *mine = l;
-            sync_pair();
-            l += *others; // (the same sum in both warps)
-            sync_pair();
-            float M = m, fa = 1.f, fb = 0.f;
+            auto add_other = [&](float &v) { // (the same sum in both warps)
+                *mine = v;
+                sync_pair();
+                v += *others;
+                sync_pair();
+            };
+            add_other(l);
+            if (!CONV)
+                add_other(lr);
+            // O is divided by the sum of the rounded p, here as a factor: the sums that go on are those of the p
+            float M = m, fa = CONV || l == 0.f ? 1.f : l / lr, fb = 0.f;
             if (!two) {
-                if (t == 1)
+                sync_all(); // (every pair has read its sums)
+                if (t == 1) {
                     *mine = half ? l : m;
+                    if (half)
+                        xch[at_lane] = fa;
+                }
                 sync_all();
-                const float mb = xch[256 + at_lane], lb = xch[384 + at_lane];
+                const float mb = xch[256 + at_lane], lb = xch[384 + at_lane], cb = xch[at_lane];
                 sync_all();
                 if (t == 1)
                     continue; // stream 0 reads both accumulators
                 // (a sum of 0: no column, and any reference)
                 M = l == 0.f ? mb : lb == 0.f ? m : fmaxf(m, mb);
-                fa = l == 0.f ? 0.f : ex2(m - M);
-                fb = lb == 0.f ? 0.f : ex2(mb - M);
-                l = l * fa + lb * fb;
+                const float ea = l == 0.f ? 0.f : ex2(m - M), eb = lb == 0.f ? 0.f : ex2(mb - M);
+                l = l * ea + lb * eb;
+                fa *= ea;
+                fb = cb * eb;
             }
             wait(pv_done + 8 * t, (steps - 1) & 1u);
             if (!two) // stream 1 has given all its P: the last of its products is the one under way
