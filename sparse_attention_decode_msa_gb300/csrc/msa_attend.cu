@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 uint32_t pr[32];
                 float rounded, sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr, rounded);
                 // (both warps have read S, which P replaces)
-                if (any_of_two_warps(pair_bar, i > 0 && sum > (CONV ? kMost16 : kMost))) {
+                if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
                     new_reference(i, 64);
                     sum = row_to_p<CONV, true>(at_s, sc, m, 64, pr, rounded);
                     sync_pair();
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     new_reference(0, min(64, seen));
                 uint32_t pr[32];
                 float rounded, sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
-                if (any_of_two_warps(pair_bar, i > 0 && sum > (CONV ? kMost16 : kMost))) {
+                if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
                     new_reference(i, min(64, seen));
                     sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
                     sync_pair();
