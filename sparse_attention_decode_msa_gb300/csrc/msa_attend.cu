@@ -315,26 +315,27 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
 {
     const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
     uint64_t sum[2] = {0ull, 0ull}, sumr[2] = {0ull, 0ull};
-    uint32_t v[2][16];
-    tmem_ld16_async(at_s, v[0]);
+    constexpr int N = F16 ? 8 : 16; // columns at a time: beside converters a thread has fewer registers
+    uint32_t v[2][N];
+    tmem_ld_async(at_s, v[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t(&x)[16] = v[c & 1];
-        tmem_wait_ld16(x);
-        if (c < 3) // on their way meanwhile
-            tmem_ld16_async(at_s + 16 * (c + 1), v[(c + 1) & 1]);
+    for (int c = 0; c < 64 / N; ++c) {
+        uint32_t(&x)[N] = v[c & 1];
+        tmem_wait_async(x);
+        if (c < 64 / N - 1) // on their way meanwhile
+            tmem_ld_async(at_s + N * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
+        for (int k = 0; k < N; k += 2) {
             float e0, e1;
             unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc2, ref2), e0, e1);
             e0 = ex2(e0);
             e1 = ex2(e1);
             if (TAIL) {
-                e0 = 16 * c + k < seen ? e0 : 0.f;
-                e1 = 16 * c + k + 1 < seen ? e1 : 0.f;
+                e0 = N * c + k < seen ? e0 : 0.f;
+                e1 = N * c + k + 1 < seen ? e1 : 0.f;
             }
             sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
-            const uint32_t both = pr[8 * c + (k >> 1)] = F16 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
+            const uint32_t both = pr[N / 2 * c + (k >> 1)] = F16 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
             if (!F16)
                 sumr[(k >> 1) & 1] = add2(sumr[(k >> 1) & 1], pair(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u)));
         }
@@ -344,6 +345,18 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
     rounded = a + b;
     unpair(add2(sum[0], sum[1]), a, b);
     return a + b;
+}
+
+__device__ __forceinline__ float lds32(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts32(uint32_t a, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
 // Whether any thread of the two warps that meet at a barrier says so.
@@ -360,22 +373,22 @@ __device__ __forceinline__ bool any_of_two_warps(int barrier, bool v)
 // Infinities and NaN of V at positions from .. to - 1, which were kept out of the products, for a row that
 // sees them: into dimensions d0 .. d0 + 63 of its output, or of its partial one in a slot.
 template <int FMT>
-__device__ __noinline__ void add_late_values(const AttendParams &p, const Share &at, long long row, int from, int to, float ref, float *slot, int d0)
+__device__ __noinline__ void add_late_values(const AttendParams &p, int r, int head, long long row, int from, int to, float ref, float *slot, int d0)
 {
     for (int pos = from; pos < to; ++pos) {
-        const long long page = p.block_table[(size_t)at.r * p.maxB + pos / kPage];
+        const long long page = p.block_table[(size_t)r * p.maxB + pos / kPage];
         if (page < 0 || page >= p.num_pages)
             continue;
         float pr = 0.f;
         bool have = false;
         for (int d = d0; d < d0 + 64; ++d) {
-            const float x = stored_value<FMT>(p.kv, (page * 2 + 1) * p.Hkv + at.head, pos % kPage, d);
+            const float x = stored_value<FMT>(p.kv, (page * 2 + 1) * p.Hkv + head, pos % kPage, d);
             if (finite(x))
                 continue;
             if (!have) {
                 const uint16_t *q = p.q + row * kDim;
                 for (int e = 0; e < kDim; ++e)
-                    pr = fmaf(__uint_as_float((uint32_t)q[e] << 16), stored_value<FMT>(p.kv, page * 2 * p.Hkv + at.head, pos % kPage, e), pr);
+                    pr = fmaf(__uint_as_float((uint32_t)q[e] << 16), stored_value<FMT>(p.kv, page * 2 * p.Hkv + head, pos % kPage, e), pr);
                 pr = ex2(fmaf(pr, p.scale_log2, -ref));
                 have = true;
             }
@@ -808,9 +821,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21); // this warp's lane quarter
         const uint32_t at_s = lanes + 128 * t + 64 * half, at_p = lanes + 128 * t + 32 * half, o_at = lanes + 256 + 128 * t + 64 * half;
         const float ninf = __uint_as_float(0xFF800000u);
-        float *xch = reinterpret_cast<float *>(gsm + L.xch); // [stream][half][row]
-        float *mine = xch + 256 * t + 128 * half + at_lane, *others = xch + 256 * t + 128 * (half ^ 1) + at_lane;
-        const int8_t *exps = reinterpret_cast<const int8_t *>(gsm + L.inv) + 128 * t;
+        const uint32_t xch = smem + L.xch + 4 * at_lane; // float [stream][half][row]
+        const uint32_t mine = xch + 1024 * t + 512 * half, others = xch + 1024 * t + 512 * (half ^ 1);
         const int Hq = p.Hkv * p.G, each = p.unit_tokens >> 1; // tokens of a stream
         uint32_t steps = 0; // so far, alike for both streams
         const int pair_bar = 1 + 4 * t + (warp & 3);
@@ -848,11 +860,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             // page tells; where a row's passes kMost its warps' rows get new references before P is written.
             auto new_reference = [&](int i, int seen) {
                 if (CONV && i == 0 && real) // (the exponents are there once S is)
-                    sc *= __uint_as_float((uint32_t)(exps[kRows * (w.seg & 1) + at_lane] + 127) << 23);
+                    sc *= __uint_as_float((uint32_t)(reinterpret_cast<const int8_t *>(gsm + L.inv)[kRows * (w.seg & 1) + 128 * t + at_lane] + 127) << 23);
                 float mx = row_maximum(at_s, sc, seen);
-                *mine = mx;
+                sts32(mine, mx);
                 sync_pair();
-                mx = fmaxf(mx, *others) - (CONV ? kPUp16 : 0.f);
+                mx = fmaxf(mx, lds32(others)) - (CONV ? kPUp16 : 0.f);
                 const float ref = mx == ninf ? 0.f : mx, f = i > 0 && mx > m ? ex2(m - ref) : 1.f;
                 m = i == 0 || mx > m ? ref : m;
                 l *= f;
@@ -932,13 +944,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
 
             // ---- end of the unit's share ----
-            const Share at = w;
-            w.next(p);
-            const bool whole = at.b == 0 && n == at.nb, ends = at.b + n == at.nb;
+            const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
             auto add_other = [&](float &v) { // (the same sum in both warps)
-                *mine = v;
+                sts32(mine, v);
                 sync_pair();
-                v += *others;
+                v += lds32(others);
                 sync_pair();
             };
             add_other(l);
@@ -949,15 +959,17 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             if (!two) {
                 sync_all(); // (every pair has read its sums)
                 if (t == 1) {
-                    *mine = half ? l : m;
+                    sts32(mine, half ? l : m);
                     if (half)
-                        xch[at_lane] = fa;
+                        sts32(xch, fa);
                 }
                 sync_all();
-                const float mb = xch[256 + at_lane], lb = xch[384 + at_lane], cb = xch[at_lane];
+                const float mb = lds32(xch + 1024), lb = lds32(xch + 1536), cb = lds32(xch);
                 sync_all();
-                if (t == 1)
-                    continue; // stream 0 reads both accumulators
+                if (t == 1) { // stream 0 reads both accumulators
+                    w.next(p);
+                    continue;
+                }
                 // (a sum of 0: no column, and any reference)
                 M = l == 0.f ? mb : lb == 0.f ? m : fmaxf(m, mb);
                 const float ea = l == 0.f ? 0.f : ex2(m - M), eb = lb == 0.f ? 0.f : ex2(mb - M);
@@ -969,15 +981,17 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             if (!two) // stream 1 has given all its P: the last of its products is the one under way
                 wait(pv_done + 8, (steps - 1) & 1u);
             tcgen05_after_sync();
-            const long long out_row = (long long)(at.token0(p) + j) * Hq + at.head * p.G + min(at_lane, rows - 1) % p.G;
+            // this row among the batch's: behind the unit's first token's first head by so many
+            const int in_unit = j * Hq + w.head * p.G + min(at_lane, rows - 1) % p.G;
+            const long long unit_row = (long long)w.token0(p) * Hq;
             const int slot_row = (two ? 128 * t : 0) + at_lane;
             float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * kSlotFloats;
             const float fin = whole ? (l > 0.f || l != l ? p.v_scale / l : 0.f) : 1.f;
             const float ga = fa * fin, gb = n > 1 ? fb * fin : 0.f; // (with one page stream 1 has no O)
-            long long rows_of_four[4]; // of the lane's group of four lanes, for stores of 64 bytes a row
+            int rows_of_four[4]; // of the lane's group of four lanes, for stores of 64 bytes a row
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                rows_of_four[k] = __shfl_sync(0xffffffffu, out_row, (lane & 28) + k);
+                rows_of_four[k] = __shfl_sync(0xffffffffu, in_unit, (lane & 28) + k);
 #pragma unroll 1
             for (int c = 0; c < 2 && !idle; ++c) {
                 uint32_t a[32];
@@ -990,8 +1004,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t o[16];
-                        tmem_ld16_async(o_at + 128 + 32 * c + 16 * h, o);
-                        tmem_wait_ld16(o);
+                        tmem_ld_async(o_at + 128 + 32 * c + 16 * h, o);
+                        tmem_wait_async(o);
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             a[16 * h + k] = __float_as_uint(__uint_as_float(a[16 * h + k]) + (gb != 0.f ? __uint_as_float(o[k]) * gb : 0.f));
@@ -1008,7 +1022,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if ((at_lane & ~3) + k < rows)
-                            *reinterpret_cast<uint4 *>(p.out + rows_of_four[k] * kDim + 64 * half + 32 * c + 8 * (lane & 3)) = d[k];
+                            *reinterpret_cast<uint4 *>(p.out + (unit_row + rows_of_four[k]) * kDim + 64 * half + 32 * c + 8 * (lane & 3)) = d[k];
                 } else if (real) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) // 16-byte piece i of row r of a slot lies at i kRows + r
@@ -1025,15 +1039,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
             if (real) {
                 if (half == 0 && whole) {
-                    p.lse[out_row] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
+                    p.lse[unit_row + in_unit] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
                 } else if (half == 0) {
                     slot[(size_t)kRows * kDim + slot_row] = l == 0.f ? ninf : M;
                     slot[(size_t)kRows * (kDim + 1) + slot_row] = l;
                 }
-                if (misc.later_bad[at.seg & 7] == at.seg + 1)
-                    add_late_values<FMT>(p, at, out_row, max(seen0, at.b * kPage), min(lim, (at.b + n) * kPage), M,
+                if (misc.later_bad[w.seg & 7] == w.seg + 1)
+                    add_late_values<FMT>(p, w.r, w.head, unit_row + in_unit, max(seen0, w.b * kPage), min(lim, (w.b + n) * kPage), M,
                                          whole ? nullptr : slot + 4 * slot_row, 64 * half);
             }
+            w.next(p);
         }
         if (copies > 0) // the CTA's memory must outlive them (they have long landed unless a wait ran out)
             mbar_wait_bounded(q_raw + 8 * t, (copies - 1) & 1u);
