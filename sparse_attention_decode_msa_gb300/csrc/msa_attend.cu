@@ -315,15 +315,18 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
 {
     const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
     uint64_t sum[2] = {0ull, 0ull}, sumr[2] = {0ull, 0ull};
-    constexpr int N = F16 ? 8 : 16; // columns at a time: beside converters a thread has fewer registers
-    uint32_t v[2][N];
+    // columns at a time, and whether the next ones are on their way meanwhile: beside converters a thread has
+    // 80 registers, and what it spills does not stay in the L1 that 227 KB of shared memory leave (8
+    // columns ahead there: a 512-token chunk over 65536 E4M3 positions 745 us, ragged cross attention 84; none: 742 and 81)
+    constexpr int N = F16 ? 8 : 16, AHEAD = F16 ? 0 : 1;
+    uint32_t v[1 + AHEAD][N];
     tmem_ld_async(at_s, v[0]);
 #pragma unroll
     for (int c = 0; c < 64 / N; ++c) {
-        uint32_t(&x)[N] = v[c & 1];
+        uint32_t(&x)[N] = v[AHEAD ? c & 1 : 0];
         tmem_wait_async(x);
-        if (c < 64 / N - 1) // on their way meanwhile
-            tmem_ld_async(at_s + N * (c + 1), v[(c + 1) & 1]);
+        if (AHEAD && c < 64 / N - 1)
+            tmem_ld_async(at_s + N * (c + 1), v[AHEAD ? (c + 1) & 1 : 0]);
 #pragma unroll
         for (int k = 0; k < N; k += 2) {
             float e0, e1;
@@ -339,6 +342,8 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
             if (!F16)
                 sumr[(k >> 1) & 1] = add2(sumr[(k >> 1) & 1], pair(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u)));
         }
+        if (!AHEAD && c < 64 / N - 1)
+            tmem_ld_async(at_s + N * (c + 1), x);
     }
     float a, b;
     unpair(add2(sumr[0], sumr[1]), a, b);
@@ -402,25 +407,35 @@ __device__ __noinline__ void add_late_values(const AttendParams &p, int r, int h
     }
 }
 
-// Four 16-byte pieces of each of four neighbouring lanes: d[k] becomes piece lane % 4 of lane k of the four.
-__device__ __forceinline__ void transpose4(uint4 (&d)[4])
+// Two pieces of N words of each of two neighbouring lanes: d[k] becomes piece lane % 2 of lane k of the two.
+template <int N>
+__device__ __forceinline__ void transpose2(uint32_t (&d)[2][N])
 {
+    const bool high = threadIdx.x & 1;
 #pragma unroll
-    for (int m = 1; m <= 2; m <<= 1) {
-        const bool high = threadIdx.x & m;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & m)
-                continue;
-            uint32_t *a = &d[i].x, *b = &d[i | m].x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? a[k] : b[k], m);
-                a[k] = high ? got : a[k];
-                b[k] = high ? b[k] : got;
-            }
-        }
+    for (int k = 0; k < N; ++k) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? d[0][k] : d[1][k], 1);
+        d[0][k] = high ? got : d[0][k];
+        d[1][k] = high ? d[1][k] : got;
     }
+}
+
+__device__ __forceinline__ void store(void *a, const uint32_t (&d)[4])
+{
+    *reinterpret_cast<uint4 *>(a) = make_uint4(d[0], d[1], d[2], d[3]);
+}
+
+// 32 bytes in one store, or two of 16 where the tensor begins at an odd multiple of 16.
+__device__ __forceinline__ void store(void *a, const uint32_t (&d)[8])
+{
+    if (reinterpret_cast<uintptr_t>(a) & 16) {
+        reinterpret_cast<uint4 *>(a)[0] = make_uint4(d[0], d[1], d[2], d[3]);
+        reinterpret_cast<uint4 *>(a)[1] = make_uint4(d[4], d[5], d[6], d[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]), "r"(d[4]), "r"(d[5]),
+                 "r"(d[6]), "r"(d[7])
+                 : "memory");
 }
 
 // The query rows of an operand tile from bf16 to f16, in place, by four warps: each row after a power of two
@@ -945,15 +960,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 
             // ---- end of the unit's share ----
             const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
-            auto add_other = [&](float &v) { // (the same sum in both warps)
-                sts32(mine, v);
-                sync_pair();
-                v += lds32(others);
-                sync_pair();
-            };
-            add_other(l);
+            // both warps of a row get the same sums: l goes by a thread's own place, lr back by the other's
+            sts32(mine, l);
+            sync_pair();
+            l += lds32(others);
             if (!CONV)
-                add_other(lr);
+                sts32(others, lr);
+            sync_pair();
+            if (!CONV)
+                lr += lds32(mine);
             // O is divided by the sum of the rounded p, here as a factor: the sums that go on are those of the p
             float M = m, fa = CONV || l == 0.f ? 1.f : l / lr, fb = 0.f;
             if (!two) {
@@ -977,10 +992,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 fa *= ea;
                 fb = cb * eb;
             }
-            wait(pv_done + 8 * t, (steps - 1) & 1u);
-            if (!two) // stream 1 has given all its P: the last of its products is the one under way
-                wait(pv_done + 8, (steps - 1) & 1u);
-            tcgen05_after_sync();
+            // (what does not need O comes before the wait for its last products)
             // this row among the batch's: behind the unit's first token's first head by so many
             const int in_unit = j * Hq + w.head * p.G + min(at_lane, rows - 1) % p.G;
             const long long unit_row = (long long)w.token0(p) * Hq;
@@ -988,45 +1000,67 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * kSlotFloats;
             const float fin = whole ? (l > 0.f || l != l ? p.v_scale / l : 0.f) : 1.f;
             const float ga = fa * fin, gb = n > 1 ? fb * fin : 0.f; // (with one page stream 1 has no O)
-            int rows_of_four[4]; // of the lane's group of four lanes, for stores of 64 bytes a row
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                rows_of_four[k] = __shfl_sync(0xffffffffu, in_unit, (lane & 28) + k);
+            const int neighbours = __shfl_xor_sync(0xffffffffu, in_unit, 1);
+            if (real && half == 0) {
+                if (whole) {
+                    p.lse[unit_row + in_unit] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
+                } else {
+                    slot[(size_t)kRows * kDim + slot_row] = l == 0.f ? ninf : M;
+                    slot[(size_t)kRows * (kDim + 1) + slot_row] = l;
+                }
+            }
+            const bool zeros = __any_sync(0xffffffffu, fa == 0.f);
+            wait(pv_done + 8 * t, (steps - 1) & 1u);
+            if (!two) // stream 1 has given all its P: the last of its products is the one under way
+                wait(pv_done + 8, (steps - 1) & 1u);
+            tcgen05_after_sync();
+            constexpr int C = CONV ? 16 : 32; // columns at a time (registers, as above)
 #pragma unroll 1
-            for (int c = 0; c < 2 && !idle; ++c) {
-                uint32_t a[32];
-                tmem_ld32(o_at + 32 * c, a);
-                tmem_wait_ld(a);
+            for (int c = 0; c < 64 && !idle; c += C) {
+                uint32_t a[C];
+                auto load = [&](uint32_t at, uint32_t *v) { // 16 columns
+                    uint32_t(&w16)[16] = *reinterpret_cast<uint32_t(*)[16]>(v);
+                    tmem_ld_async(at, w16);
+                    tmem_wait_async(w16);
+                };
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    a[k] = __float_as_uint(fa != 0.f ? __uint_as_float(a[k]) * ga : 0.f);
+                for (int h = 0; h < C; h += 16)
+                    load(o_at + c + h, a + h);
+                if (zeros) { // a row of zeros, whatever V has
+#pragma unroll
+                    for (int k = 0; k < C; ++k)
+                        a[k] = fa != 0.f ? a[k] : 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < C; k += 2) {
+                    float e0, e1;
+                    unpair(mul2(pair(__uint_as_float(a[k]), __uint_as_float(a[k + 1])), pair(ga, ga)), e0, e1);
+                    a[k] = __float_as_uint(e0);
+                    a[k + 1] = __float_as_uint(e1);
+                }
                 if (!two)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < C; h += 16) {
                         uint32_t o[16];
-                        tmem_ld_async(o_at + 128 + 32 * c + 16 * h, o);
-                        tmem_wait_async(o);
+                        load(o_at + 128 + c + h, o);
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
-                            a[16 * h + k] = __float_as_uint(__uint_as_float(a[16 * h + k]) + (gb != 0.f ? __uint_as_float(o[k]) * gb : 0.f));
+                            a[h + k] = __float_as_uint(__uint_as_float(a[h + k]) + (gb != 0.f ? __uint_as_float(o[k]) * gb : 0.f));
                     }
-                if (whole) {
-                    uint4 d[4];
+                if (whole) { // C values a row by two lanes
+                    uint32_t d[2][C / 4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        d[k] = make_uint4(pack_bf16(__uint_as_float(a[8 * k]), __uint_as_float(a[8 * k + 1])),
-                                          pack_bf16(__uint_as_float(a[8 * k + 2]), __uint_as_float(a[8 * k + 3])),
-                                          pack_bf16(__uint_as_float(a[8 * k + 4]), __uint_as_float(a[8 * k + 5])),
-                                          pack_bf16(__uint_as_float(a[8 * k + 6]), __uint_as_float(a[8 * k + 7])));
-                    transpose4(d); // d[k]: piece lane % 4 of row k of the four
+                    for (int k = 0; k < C / 2; ++k)
+                        d[k / (C / 4)][k % (C / 4)] = pack_bf16(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
+                    transpose2(d); // d[k]: piece lane % 2 of row k of the two
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if ((at_lane & ~3) + k < rows)
-                            *reinterpret_cast<uint4 *>(p.out + (unit_row + rows_of_four[k]) * kDim + 64 * half + 32 * c + 8 * (lane & 3)) = d[k];
+                    for (int k = 0; k < 2; ++k)
+                        if ((at_lane & ~1) + k < rows)
+                            store(p.out + (unit_row + ((lane & 1) == k ? in_unit : neighbours)) * kDim + 64 * half + c + C / 2 * (lane & 1), d[k]);
                 } else if (real) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) // 16-byte piece i of row r of a slot lies at i kRows + r
-                        reinterpret_cast<uint4 *>(slot)[(16 * half + 8 * c + k) * kRows + slot_row] =
+                    for (int k = 0; k < C / 4; ++k) // 16-byte piece i of row r of a slot lies at i kRows + r
+                        reinterpret_cast<uint4 *>(slot)[(16 * half + c / 4 + k) * kRows + slot_row] =
                             make_uint4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
                 }
             }
@@ -1037,17 +1071,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 if (!two)
                     mbar_arrive(o_free + 8);
             }
-            if (real) {
-                if (half == 0 && whole) {
-                    p.lse[unit_row + in_unit] = l == 0.f ? ninf : (M + log2f(l)) * 0.6931471805599453f;
-                } else if (half == 0) {
-                    slot[(size_t)kRows * kDim + slot_row] = l == 0.f ? ninf : M;
-                    slot[(size_t)kRows * (kDim + 1) + slot_row] = l;
-                }
-                if (misc.later_bad[w.seg & 7] == w.seg + 1)
-                    add_late_values<FMT>(p, w.r, w.head, unit_row + in_unit, max(seen0, w.b * kPage), min(lim, (w.b + n) * kPage), M,
-                                         whole ? nullptr : slot + 4 * slot_row, 64 * half);
-            }
+            if (real && misc.later_bad[w.seg & 7] == w.seg + 1)
+                add_late_values<FMT>(p, w.r, w.head, unit_row + in_unit, max(seen0, w.b * kPage), min(lim, (w.b + n) * kPage), M,
+                                     whole ? nullptr : slot + 4 * slot_row, 64 * half);
             w.next(p);
         }
         if (copies > 0) // the CTA's memory must outlive them (they have long landed unless a wait ran out)
