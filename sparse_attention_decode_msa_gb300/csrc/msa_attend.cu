@@ -223,6 +223,36 @@ struct Share {
     }
 };
 
+// A share in one register of a warp, a word a lane: the softmax warps keep it so over their pages, where every
+// register counts.
+__device__ __forceinline__ int fold(const Share &w)
+{
+    const int words[11] = {w.q.first, w.q.n, w.q.L, w.q.units, w.left, w.r, w.head, w.u, w.b, w.nb, w.seg};
+    int v = 0;
+#pragma unroll
+    for (int k = 0; k < 11; ++k)
+        v = (int)(threadIdx.x & 31) == k ? words[k] : v;
+    return v;
+}
+
+__device__ __forceinline__ Share unfold(int v)
+{
+    auto word = [&](int k) { return __shfl_sync(0xffffffffu, v, k); };
+    Share w;
+    w.q.first = word(0);
+    w.q.n = word(1);
+    w.q.L = word(2);
+    w.q.units = word(3);
+    w.left = word(4);
+    w.r = word(5);
+    w.head = word(6);
+    w.u = word(7);
+    w.b = word(8);
+    w.nb = word(9);
+    w.seg = word(10);
+    return w;
+}
+
 // The order in which the issuers use the tiles of n pages: K and V of each page, or, where the streams take
 // pages in turn, both K and both V of each pair of pages.
 __device__ __forceinline__ bool tile_of(bool two, int n, int i, int *page)
@@ -725,13 +755,19 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     umma_commit(tile_free + 8 * st);
             };
             wait(q_full + 8 * t, w.seg & 1);
-            // S of a step into the S buffer (its K tile has been waited for)
+            // S of a step into the S buffer (its K tile has been waited for).  The turn ends half way: the other
+            // issuer's waits end as these products do (behind the last: ragged prompts 466 us, half way 459)
             auto score = [&](uint32_t st, bool page) {
                 const uint32_t k = (ring + st * (kTile16 >> 4) & 0x3FFFu) | (16u >> 4) << 16;
                 if (page) {
 #pragma unroll
-                    for (uint32_t ks = 0; ks < 8; ++ks)
+                    for (uint32_t ks = 0; ks < 8; ++ks) {
                         umma_ss(one, d_s, q + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 1024 + (ks & 3) * 2, idesc_s, ks > 0);
+                        if (ks == 3)
+                            end_turn();
+                    }
+                } else {
+                    end_turn();
                 }
                 if (elect_one())
                     umma_commit(s_full + 8 * t);
@@ -743,7 +779,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             take_turn();
             tcgen05_after_sync();
             score(k_st, pages > 0); // (P V of the unit before, which reads what S replaces, was waited for at its end)
-            end_turn();
             if (pages > 0 && elect_one())
                 give_back(k_st);
             __syncwarp();
@@ -761,8 +796,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 }
                 if (i == 0 && w.seg > 0) // the last unit's O has been read
                     wait(o_free + 8 * t, (w.seg - 1) & 1);
+                take_turn(); // (before the wait for P, which is the longer one: a wait that need not wait takes 150 clocks)
                 wait(p_full + 8 * t, done & 1u);
-                take_turn();
                 tcgen05_after_sync();
                 if (page) {
                     // V, MN-major: 16 positions are 16 rows of 128 bytes
@@ -775,7 +810,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 __syncwarp();
                 if (again) // S replaces P: products of one thread run in the order of their issue
                     score(k_st, next_page);
-                end_turn();
+                else
+                    end_turn();
                 if (elect_one()) {
                     if (page)
                         give_back(v_st);
@@ -859,106 +895,117 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
             __syncwarp();
         };
+        auto rows_of = [&](const Share &w) { return (w.two(p) && t ? w.q.tokens(p, w.u) - each : min(each, w.q.tokens(p, w.u))) * p.G; }; // the stream's
+        auto token_of = [&](const Share &w) { return (w.two(p) ? each * t : 0) + min(at_lane, rows_of(w) - 1) / p.G; };                 // the row's
+        auto sees = [&](const Share &w) { return w.q.seen(p, w.u) + (p.causal ? token_of(w) : 0); };                                    // and its positions
         if (w.left > 0 && leads)
             copy_queries(w);
         while (w.left > 0) {
-            const int n = w.pages();
-            const bool two = w.two(p);
-            const int nsteps = two ? n : (n + 1) >> 1, npages = two || t == 0 ? nsteps : n >> 1; // (see the issuers)
-            const int rows = (two && t ? w.q.tokens(p, w.u) - each : min(each, w.q.tokens(p, w.u))) * p.G; // the stream's
-            const bool real = at_lane < rows, idle = (warp & 3) * 32 >= rows; // idle: no row of this warp's is the unit's
-            const int j = (two ? each * t : 0) + min(at_lane, rows - 1) / p.G;  // the row's token
-            const int seen0 = w.q.seen(p, w.u), lim = seen0 + (p.causal ? j : 0);
-            float sc = p.scale_log2, m = 0.f, l = 0.f, lr = 0.f; // scale, reference, sum, sum of the rounded p
-            // A row's reference is its maximum over the first page.  Later pages are not searched for theirs:
-            // p may pass 1 as long as it stays a number that P and the sums can hold, which the sum of half a
-            // page tells; where a row's passes kMost its warps' rows get new references before P is written.
-            auto new_reference = [&](int i, int seen) {
-                if (CONV && i == 0 && real) // (the exponents are there once S is)
-                    sc *= __uint_as_float((uint32_t)(reinterpret_cast<const int8_t *>(gsm + L.inv)[kRows * (w.seg & 1) + 128 * t + at_lane] + 127) << 23);
-                float mx = row_maximum(at_s, sc, seen);
-                sts32(mine, mx);
-                sync_pair();
-                mx = fmaxf(mx, lds32(others)) - (CONV ? kPUp16 : 0.f);
-                const float ref = mx == ninf ? 0.f : mx, f = i > 0 && mx > m ? ex2(m - ref) : 1.f;
-                m = i == 0 || mx > m ? ref : m;
-                l *= f;
-                lr *= f;
-                if (i > 0) {
-                    wait(pv_done + 8 * t, (steps - 1) & 1u); // O holds every step before this one
-                    tcgen05_after_sync();
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float o[16];
-                        tmem_ld16(o_at + 16 * c, o);
-                        uint32_t r[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            r[k] = __float_as_uint(o[k] * f);
-                        tmem_st16(o_at + 16 * c, r);
-                    }
-                }
-            };
-            auto page_done = [&](const uint32_t *pr) {
-                tmem_st32(at_p, pr);
-                tmem_wait_st();
-                tcgen05_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(p_full + 8 * t);
-            };
-            // all pages but the last of the share and those that some row does not see to their end
-            const int step = two ? kPage : 2 * kPage, pos1 = (w.b + (two ? 0 : t)) * kPage;
-            const int whole_pages = idle ? 0 : max(0, min(npages - 1, (seen0 - kPage - pos1 >= 0 ? (seen0 - kPage - pos1) / step + 1 : 0)));
-            int i = 0;
-#pragma unroll 1
-            for (; i < whole_pages; ++i, ++steps) {
-                wait(s_full + 8 * t, steps & 1u);
-                tcgen05_after_sync();
-                if (i == 0)
-                    new_reference(0, 64);
-                uint32_t pr[32];
-                float rounded, sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr, rounded);
-                // (both warps have read S, which P replaces)
-                if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
-                    new_reference(i, 64);
-                    sum = row_to_p<CONV, true>(at_s, sc, m, 64, pr, rounded);
+            float m = 0.f, l = 0.f, lr = 0.f; // reference, sum, sum of the rounded p
+            const int kept = fold(w);
+            {
+                const int n = w.pages();
+                const bool two = w.two(p);
+                const int nsteps = two ? n : (n + 1) >> 1, npages = two || t == 0 ? nsteps : n >> 1; // (see the issuers)
+                const bool real = at_lane < rows_of(w), idle = (warp & 3) * 32 >= rows_of(w); // idle: no row of this warp's is the unit's
+                float sc = p.scale_log2;
+                const int parity = w.seg & 1;
+                // A row's reference is its maximum over the first page.  Later pages are not searched for theirs:
+                // p may pass 1 as long as it stays a number that P and the sums can hold, which the sum of half a
+                // page tells; where a row's passes kMost its warps' rows get new references before P is written.
+                auto new_reference = [&](int i, int seen) {
+                    if (CONV && i == 0 && real) // (the exponents are there once S is)
+                        sc *= __uint_as_float((uint32_t)(reinterpret_cast<const int8_t *>(gsm + L.inv)[kRows * parity + 128 * t + at_lane] + 127) << 23);
+                    float mx = row_maximum(at_s, sc, seen);
+                    sts32(mine, mx);
                     sync_pair();
-                }
-                l += sum;
-                lr += rounded;
-                page_done(pr);
-            }
+                    mx = fmaxf(mx, lds32(others)) - (CONV ? kPUp16 : 0.f);
+                    const float ref = mx == ninf ? 0.f : mx, f = i > 0 && mx > m ? ex2(m - ref) : 1.f;
+                    m = i == 0 || mx > m ? ref : m;
+                    l *= f;
+                    lr *= f;
+                    if (i > 0) {
+                        wait(pv_done + 8 * t, (steps - 1) & 1u); // O holds every step before this one
+                        tcgen05_after_sync();
 #pragma unroll 1
-            for (; i < nsteps; ++i, ++steps) {
-                const int seen = lim - (pos1 + i * step) - 64 * half; // columns this row sees
-                wait(s_full + 8 * t, steps & 1u);
-                if (i == nsteps - 1 && !w.last() && leads) {
-                    Share nx = w; // S was the last to read this unit's
-                    nx.next(p);
-                    copy_queries(nx);
-                }
-                if (idle || i >= npages) {
+                        for (int c = 0; c < 4; ++c) {
+                            float o[16];
+                            tmem_ld16(o_at + 16 * c, o);
+                            uint32_t r[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                r[k] = __float_as_uint(o[k] * f);
+                            tmem_st16(o_at + 16 * c, r);
+                        }
+                    }
+                };
+                auto page_done = [&](const uint32_t *pr) {
+                    tmem_st32(at_p, pr);
+                    tmem_wait_st();
+                    tcgen05_before_sync();
+                    __syncwarp();
                     if (lane == 0)
                         mbar_arrive(p_full + 8 * t);
-                    continue;
+                };
+                // all pages but the last of the share and those that some row does not see to their end
+                const int step = two ? kPage : 2 * kPage, pos1 = (w.b + (two ? 0 : t)) * kPage;
+                const int to_end = w.q.seen(p, w.u) - kPage - pos1;
+                const int whole_pages = idle ? 0 : max(0, min(npages - 1, to_end >= 0 ? to_end / step + 1 : 0));
+                int seen = sees(w) - pos1 - whole_pages * step - 64 * half; // columns that this row sees behind those
+                int i = 0;
+#pragma unroll 1
+                for (; i < whole_pages; ++i, ++steps) {
+                    wait(s_full + 8 * t, steps & 1u);
+                    tcgen05_after_sync();
+                    if (i == 0)
+                        new_reference(0, 64);
+                    uint32_t pr[32];
+                    float rounded, sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr, rounded);
+                    // (both warps have read S, which P replaces)
+                    if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
+                        new_reference(i, 64);
+                        sum = row_to_p<CONV, true>(at_s, sc, m, 64, pr, rounded);
+                        sync_pair();
+                    }
+                    l += sum;
+                    lr += rounded;
+                    page_done(pr);
                 }
-                tcgen05_after_sync();
-                if (i == 0)
-                    new_reference(0, min(64, seen));
-                uint32_t pr[32];
-                float rounded, sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
-                if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
-                    new_reference(i, min(64, seen));
-                    sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
-                    sync_pair();
+#pragma unroll 1
+                for (; i < nsteps; ++i, ++steps, seen -= step) {
+                    wait(s_full + 8 * t, steps & 1u);
+                    if (i == nsteps - 1 && leads) {
+                        Share nx = unfold(kept); // S was the last to read this unit's
+                        if (!nx.last()) {
+                            nx.next(p);
+                            copy_queries(nx);
+                        }
+                    }
+                    if (idle || i >= npages) {
+                        if (lane == 0)
+                            mbar_arrive(p_full + 8 * t);
+                        continue;
+                    }
+                    tcgen05_after_sync();
+                    if (i == 0)
+                        new_reference(0, min(64, seen));
+                    uint32_t pr[32];
+                    float rounded, sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
+                    if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
+                        new_reference(i, min(64, seen));
+                        sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
+                        sync_pair();
+                    }
+                    l += sum;
+                    lr += rounded;
+                    page_done(pr);
                 }
-                l += sum;
-                lr += rounded;
-                page_done(pr);
             }
 
             // ---- end of the unit's share ----
+            w = unfold(kept);
+            const int n = w.pages(), rows = rows_of(w);
+            const bool two = w.two(p), real = at_lane < rows, idle = (warp & 3) * 32 >= rows;
             const bool whole = w.b == 0 && n == w.nb, ends = w.b + n == w.nb;
             // both warps of a row get the same sums: l goes by a thread's own place, lr back by the other's
             sts32(mine, l);
@@ -994,7 +1041,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
             // (what does not need O comes before the wait for its last products)
             // this row among the batch's: behind the unit's first token's first head by so many
-            const int in_unit = j * Hq + w.head * p.G + min(at_lane, rows - 1) % p.G;
+            const int in_unit = token_of(w) * Hq + w.head * p.G + min(at_lane, rows - 1) % p.G;
             const long long unit_row = (long long)w.token0(p) * Hq;
             const int slot_row = (two ? 128 * t : 0) + at_lane;
             float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * kSlotFloats;
@@ -1072,7 +1119,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     mbar_arrive(o_free + 8);
             }
             if (real && misc.later_bad[w.seg & 7] == w.seg + 1)
-                add_late_values<FMT>(p, w.r, w.head, unit_row + in_unit, max(seen0, w.b * kPage), min(lim, (w.b + n) * kPage), M,
+                add_late_values<FMT>(p, w.r, w.head, unit_row + in_unit, max(w.q.seen(p, w.u), w.b * kPage), min(sees(w), (w.b + w.pages()) * kPage), M,
                                      whole ? nullptr : slot + 4 * slot_row, 64 * half);
             w.next(p);
         }
