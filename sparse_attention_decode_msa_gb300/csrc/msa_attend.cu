@@ -90,7 +90,7 @@ __host__ __device__ constexpr Smem smem_layout(int fmt)
 static_assert(smem_layout(kFmtBf16).total <= 232448 && smem_layout(kFmtFp8).total <= 232448 && smem_layout(kFmtF4).total <= 232448, "shared memory");
 
 // sum over i < n of floor((a i + b) / m)
-__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
+__device__ __noinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
 {
     unsigned long long s = 0;
     while (n > 0) {
@@ -138,6 +138,8 @@ struct Misc {
     long long start_before;
     long long scan[24];
     Request start;
+    long long wait_limit;
+    uint32_t *err;
     int abort, start_r;
     uint32_t tmem;
     int later_bad[8]; // unit counter + 1 where V rows of later tokens are not finite
@@ -345,10 +347,10 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
 {
     const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
     uint64_t sum[2] = {0ull, 0ull}, sumr[2] = {0ull, 0ull};
-    // columns at a time, and whether the next ones are on their way meanwhile: beside converters a thread has
-    // 80 registers, and what it spills does not stay in the L1 that 227 KB of shared memory leave (8
-    // columns ahead there: a 512-token chunk over 65536 E4M3 positions 745 us, ragged cross attention 84; none: 742 and 81)
-    constexpr int N = F16 ? 8 : 16, AHEAD = F16 ? 0 : 1;
+    // 16 columns at a time, the next ones on their way meanwhile where there are the registers: beside
+    // converters a thread has 80, and what it spills does not stay in the L1 that 227 KB of shared memory
+    // leave (8 ahead and 24 bytes on the stack: a 512-token chunk over 65536 E4M3 positions 745 us, nothing spilled 725)
+    constexpr int N = 16, AHEAD = F16 ? 0 : 1;
     uint32_t v[1 + AHEAD][N];
     tmem_ld_async(at_s, v[0]);
 #pragma unroll
@@ -510,6 +512,25 @@ __device__ __forceinline__ void widen_queries(uint8_t *tile, int8_t *exps)
     }
 }
 
+// A wait that was not over at once (out of line: two dozen places wait, and the code of all roles shares the
+// instruction caches).  One that runs out: the CTA's roles run on without waiting, so that all reach the end;
+// what they compute is unspecified.
+__device__ __noinline__ void long_wait(uint32_t bar, uint32_t parity, Misc *misc)
+{
+    volatile int *abort_flag = &misc->abort;
+    const long long limit = misc->wait_limit, start = clock64();
+    const bool poll = limit < (1 << 16); // a test's limit: the suspending form may sleep past it
+    while (!(poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
+        if (*abort_flag)
+            return;
+        if (clock64() - start > limit) {
+            *abort_flag = 1;
+            set_error(misc->err, kErrTimeout);
+            return;
+        }
+    }
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
     attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map, const AttendParams p)
@@ -526,7 +547,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                    o_free = pv_done + 16, turn = o_free + 16, drain = turn + 16, q_raw = CONV ? drain + 16 : q_full;
     volatile int *abort_flag = &misc.abort;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long wl = p.wait_limit;
 
     launch_dependents();
     if (smem & 1023u) { // swizzled tiles need it; the declaration gives it
@@ -560,6 +580,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
         fence_mbar_init();
         misc.abort = 0;
+        misc.wait_limit = p.wait_limit;
+        misc.err = p.err;
     }
     if (threadIdx.x < 8)
         misc.later_bad[threadIdx.x] = 0;
@@ -656,13 +678,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
         p.joins[blockIdx.x] = j;
     }
-    // a wait that ran out: the CTA's roles run on without waiting, so that all
-    // reach the end; what they compute is unspecified
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!ring_wait(bar, parity, abort_flag, wl) && !*abort_flag) {
-            *abort_flag = 1;
-            set_error(p.err, kErrTimeout);
-        }
+        if (!mbar_test_wait(bar, parity))
+            long_wait(bar, parity, &misc);
     };
 
     if (warp == 0) {
@@ -896,7 +914,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             __syncwarp();
         };
         auto rows_of = [&](const Share &w) { return (w.two(p) && t ? w.q.tokens(p, w.u) - each : min(each, w.q.tokens(p, w.u))) * p.G; }; // the stream's
-        auto token_of = [&](const Share &w) { return (w.two(p) ? each * t : 0) + min(at_lane, rows_of(w) - 1) / p.G; };                 // the row's
+        const int token_in = at_lane / p.G, head_in = at_lane - token_in * p.G; // the row's in its stream (beyond the unit's rows: some)
+        auto token_of = [&](const Share &w) { return (w.two(p) ? each * t : 0) + token_in; };
         auto sees = [&](const Share &w) { return w.q.seen(p, w.u) + (p.causal ? token_of(w) : 0); };                                    // and its positions
         if (w.left > 0 && leads)
             copy_queries(w);
@@ -960,13 +979,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     if (i == 0)
                         new_reference(0, 64);
                     uint32_t pr[32];
-                    float rounded, sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr, rounded);
-                    // (both warps have read S, which P replaces)
-                    if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
-                        new_reference(i, 64);
-                        sum = row_to_p<CONV, true>(at_s, sc, m, 64, pr, rounded);
-                        sync_pair();
-                    }
+                    float rounded, sum;
+                    bool again = false;
+                    do {
+                        if (again)
+                            new_reference(i, 64);
+                        sum = row_to_p<CONV, false>(at_s, sc, m, 64, pr, rounded);
+                        // (both warps have read S, which P replaces)
+                        again = any_of_two_warps(pair_bar, !again && real && i > 0 && sum > (CONV ? kMost16 : kMost));
+                    } while (again);
                     l += sum;
                     lr += rounded;
                     page_done(pr);
@@ -990,12 +1011,14 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     if (i == 0)
                         new_reference(0, min(64, seen));
                     uint32_t pr[32];
-                    float rounded, sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
-                    if (any_of_two_warps(pair_bar, real && i > 0 && sum > (CONV ? kMost16 : kMost))) {
-                        new_reference(i, min(64, seen));
+                    float rounded, sum;
+                    bool again = false;
+                    do {
+                        if (again)
+                            new_reference(i, min(64, seen));
                         sum = row_to_p<CONV, true>(at_s, sc, m, seen, pr, rounded);
-                        sync_pair();
-                    }
+                        again = any_of_two_warps(pair_bar, !again && real && i > 0 && sum > (CONV ? kMost16 : kMost));
+                    } while (again);
                     l += sum;
                     lr += rounded;
                     page_done(pr);
@@ -1041,7 +1064,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
             // (what does not need O comes before the wait for its last products)
             // this row among the batch's: behind the unit's first token's first head by so many
-            const int in_unit = token_of(w) * Hq + w.head * p.G + min(at_lane, rows - 1) % p.G;
+            const int in_unit = token_of(w) * Hq + w.head * p.G + head_in;
             const long long unit_row = (long long)w.token0(p) * Hq;
             const int slot_row = (two ? 128 * t : 0) + at_lane;
             float *slot = p.partial + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * kSlotFloats;
