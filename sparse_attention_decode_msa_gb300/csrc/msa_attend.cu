@@ -679,7 +679,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         p.joins[blockIdx.x] = j;
     }
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!mbar_test_wait(bar, parity))
+        // (the suspending form at once: asking first costs more than it saves wherever the wait is a real one:
+        // ragged prompts 432 us so, 422 without)
+        if (p.wait_limit < (1 << 16) || !mbar_try_wait(bar, parity))
             long_wait(bar, parity, &misc);
     };
 
@@ -1170,8 +1172,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 const bool tail = !is_k && page0 + kPage > seen;
                 const bool drop = tail && page0 + row >= past;           // not in the request
                 const bool check = tail && !drop && page0 + row >= seen; // seen by later tokens only
-                wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
-                if (z >= DEPTH)
+                // (mostly over already: both are asked before either answer is waited for)
+                const bool here = mbar_test_wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
+                const bool room = z < DEPTH || mbar_test_wait(ready_free + 8 * (z % DEPTH), (uint32_t)(z / DEPTH - 1) & 1u);
+                if (!here)
+                    wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
+                if (!room)
                     wait(ready_free + 8 * (z % DEPTH), (uint32_t)(z / DEPTH - 1) & 1u);
                 const bool bad = convert_row<FMT, 2, 4>(gsm + (z % TILES) * TB, gsm + L.staged + (z % DEPTH) * kTile16 + row * 128, row, tail, drop, check);
                 if (bad)
