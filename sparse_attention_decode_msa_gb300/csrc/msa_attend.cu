@@ -30,6 +30,15 @@
 // logits are alike.  lse has the sum of the p as they are.  (P as a pair of bf16, as the dense decode
 // has it, doubles the products of P V.)
 //
+// What bounds it, and what it measured (one GB300).  A page and both streams are 2060 clocks of
+// products; the chain S -> exponentials -> P -> P V, with tensor memory full, and the ends of units
+// keep the tensor cores waiting for the rest: ragged prompts over bf16 pages (4 of 1500 to 4096 tokens, 0.54 PFLOP)
+// 419 us, 1.30 PFLOP/s.  Over E4M3 pages shared memory carries 320 KB a page, 2500 clocks: 512 tokens
+// over 65536 positions (1.10 PFLOP) 670 us, 1.65 PFLOP/s; NVFP4, chunks of 33 to 100 tokens, 121 us, 1.18 PFLOP/s.
+// 64 single tokens over 1500 bf16 states (394 MB) 82 us, 4.8 TB/s: start, joins, and what the ring does not
+// cover when a unit ends.  Registers and code count: a spill leaves the little L1 there is, code of twenty
+// roles and loops the instruction caches, and a wait's way out is in every link of the chain.
+//
 // TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
 // Warps: 0 TMA producer, 1 and 2 issue the MMAs of stream 0 and 1 (1 owns the TMEM), 3 clears what
 // must not be multiplied from V tiles on last pages (bf16) and writes the outputs of requests
@@ -347,18 +356,16 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
 {
     const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
     uint64_t sum[2] = {0ull, 0ull}, sumr[2] = {0ull, 0ull};
-    // 16 columns at a time, the next ones on their way meanwhile where there are the registers: beside
-    // converters a thread has 80, and what it spills does not stay in the L1 that 227 KB of shared memory
-    // leave (8 ahead and 24 bytes on the stack: a 512-token chunk over 65536 E4M3 positions 745 us, nothing spilled 725)
-    constexpr int N = 16, AHEAD = F16 ? 0 : 1;
-    uint32_t v[1 + AHEAD][N];
-    tmem_ld_async(at_s, v[0]);
+    // 16 columns at a time, none on their way meanwhile: the other warps of a scheduler fill the gap.  Beside
+    // converters a thread has 80 registers, and what it spills does not stay in the L1 that 227 KB of shared
+    // memory leave (8 columns ahead and 24 bytes on the stack: a 512-token chunk over 65536 E4M3 positions
+    // 745 us, nothing spilled 725; over bf16 pages 16 ahead: ragged prompts 422, none ahead 419).
+    constexpr int N = 16;
 #pragma unroll
     for (int c = 0; c < 64 / N; ++c) {
-        uint32_t(&x)[N] = v[AHEAD ? c & 1 : 0];
+        uint32_t x[N];
+        tmem_ld_async(at_s + N * c, x);
         tmem_wait_async(x);
-        if (AHEAD && c < 64 / N - 1)
-            tmem_ld_async(at_s + N * (c + 1), v[AHEAD ? (c + 1) & 1 : 0]);
 #pragma unroll
         for (int k = 0; k < N; k += 2) {
             float e0, e1;
@@ -374,8 +381,6 @@ __device__ __forceinline__ float row_to_p(uint32_t at_s, float sc, float ref, in
             if (!F16)
                 sumr[(k >> 1) & 1] = add2(sumr[(k >> 1) & 1], pair(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u)));
         }
-        if (!AHEAD && c < 64 / N - 1)
-            tmem_ld_async(at_s + N * (c + 1), x);
     }
     float a, b;
     unpair(add2(sumr[0], sumr[1]), a, b);
@@ -1081,7 +1086,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     slot[(size_t)kRows * (kDim + 1) + slot_row] = l;
                 }
             }
-            const bool zeros = __any_sync(0xffffffffu, fa == 0.f);
+            const bool zeros = __any_sync(0xffffffffu, fa == 0.f || (!two && gb == 0.f));
             wait(pv_done + 8 * t, (steps - 1) & 1u);
             if (!two) // stream 1 has given all its P: the last of its products is the one under way
                 wait(pv_done + 8, (steps - 1) & 1u);
@@ -1115,9 +1120,18 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     for (int h = 0; h < C; h += 16) {
                         uint32_t o[16];
                         load(o_at + 128 + c + h, o);
+                        if (zeros) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            a[h + k] = __float_as_uint(__uint_as_float(a[h + k]) + (gb != 0.f ? __uint_as_float(o[k]) * gb : 0.f));
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = gb != 0.f ? o[k] : 0u;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            float e0, e1;
+                            unpair(fma2(pair(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pair(gb, gb), pair(__uint_as_float(a[h + k]), __uint_as_float(a[h + k + 1]))), e0, e1);
+                            a[h + k] = __float_as_uint(e0);
+                            a[h + k + 1] = __float_as_uint(e1);
+                        }
                     }
                 if (whole) { // C values a row by two lanes
                     uint32_t d[2][C / 4];

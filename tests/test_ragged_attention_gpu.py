@@ -483,3 +483,16 @@ def test_prompts_and_steps_through_the_cache(torch_cuda, kv, index):
     msa.msa_ragged_attention(shape, 207, False, dev(q_bits.view(np.int16)), dev(offsets), pool, table, dev(cached.astype(np.int32)), out, lse, ws, nbytes)
     want, want_lse, far, S, V = ref.attention(pb, q_bits, offsets, cached, False)
     check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, want_lse, far, S, V, 1024, kv)
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("counts,lens,Hkv,G", [([70, 1], [300, 140], 2, 4), ([1, 200], [900, 1], 1, 5)])
+def test_outputs_that_begin_at_any_multiple_of_16_bytes(torch_cuda, kv, counts, lens, Hkv, G):
+    c = Ragged(counts, lens, True, Hkv, G, kv, seed=3).run()
+    out, lse = c.check()
+    room = c.torch.full((c.T * Hkv * G * 128 + 16,), 7.0, dtype=c.torch.bfloat16, device="cuda")
+    c.out = room[8:-8].view(c.T, Hkv * G, 128)
+    assert c.out.data_ptr() % 32 == 16
+    again, again_lse = c.run().check()
+    assert np.array_equal(out, again) and np.array_equal(lse, again_lse)
+    assert bool((room[:8] == 7).all()) and bool((room[-8:] == 7).all())
