@@ -33,8 +33,8 @@
 // What bounds it, and what it measured (one GB300).  A page and both streams are 2060 clocks of
 // products; the chain S -> exponentials -> P -> P V, with tensor memory full, and the ends of units
 // keep the tensor cores waiting for the rest: ragged prompts over bf16 pages (4 of 1500 to 4096 tokens, 0.54 PFLOP)
-// 419 us, 1.30 PFLOP/s.  Over E4M3 pages shared memory carries 320 KB a page, 2500 clocks: 512 tokens
-// over 65536 positions (1.10 PFLOP) 670 us, 1.65 PFLOP/s; NVFP4, chunks of 33 to 100 tokens, 121 us, 1.18 PFLOP/s.
+// 422 us, 1.29 PFLOP/s.  Over E4M3 pages shared memory carries 320 KB a page, 2500 clocks: 512 tokens
+// over 65536 positions (1.10 PFLOP) 665 us, 1.66 PFLOP/s, what power sustains; NVFP4, chunks of 33 to 100 tokens, 121 us, 1.18 PFLOP/s.
 // 64 single tokens over 1500 bf16 states (394 MB) 82 us, 4.8 TB/s: start, joins, and what the ring does not
 // cover when a unit ends.  Registers and code count: a spill leaves the little L1 there is, code of twenty
 // roles and loops the instruction caches, and a wait's way out is in every link of the chain.
