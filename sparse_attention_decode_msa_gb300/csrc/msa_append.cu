@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
                 }
                 const int room = p.maxB * kPage; // at most 2^21
                 skip = r < 0;                    // behind the last request's tokens: left as it is
-                pos = len - 1 + (t - first);
-                if (!skip && (len < 1 || len > room || pos >= room)) {
+                pos = (int)((unsigned)(len - 1) + ((unsigned)t - (unsigned)first));
+                if (!skip && (first < 0 || len < 1 || len > room || pos >= room)) { // (nothing overflows behind the first three)
                     if (lane == 0)
                         set_error(p.err, kErrSeqLen);
                     skip = true;

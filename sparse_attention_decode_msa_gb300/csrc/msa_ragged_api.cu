@@ -283,9 +283,9 @@ msa_status msa_ragged_attention(const msa_shape *shape, int32_t num_tokens, int3
     const int ctas = attend_ctas(shape);
     if (ctas < 1)
         return MSA_ERR_CUDA;
-    // a CTA counts the pages of its range in int32
+    // a CTA counts the pages of its range in int32, each unit with a few more for its queries and outputs
     const long long units = num_tokens / 4 + shape->num_requests; // at least 4 tokens a unit, but the last of a request
-    if ((double)units * shape->num_kv_heads * shape->max_blocks_per_seq / ctas > 2147483000.0)
+    if ((double)units * shape->num_kv_heads * (shape->max_blocks_per_seq + 8.0) / ctas > 2147483000.0)
         return MSA_ERR_UNSUPPORTED;
     AttendParams p{};
     p.q = static_cast<const uint16_t *>(q);

@@ -337,3 +337,13 @@ def test_streams_and_graphs(torch_cuda):
         graph.replay()
     torch.cuda.synchronize()
     b.check()
+
+
+def test_offsets_below_zero_are_reported_and_write_nothing(torch_cuda):
+    b = Batch([4, 4, 4], [10, 10, 10], seed=5)
+    for first in (-1, -2 ** 31):
+        offsets = b.offsets.copy()
+        offsets[0] = first
+        assert b.run(torch_cuda, offsets=offsets) == msa.MSA_ERR_DEVICE_CHECK
+        pool = host(b.d_pool)
+        assert np.array_equal(pool[0], b.pool[0]) and np.array_equal(pool[b.table[0, 0]], b.pool[b.table[0, 0]])
