@@ -36,8 +36,9 @@
 // 422 us, 1.29 PFLOP/s.  Over E4M3 pages shared memory carries 320 KB a page, 2500 clocks: 512 tokens
 // over 65536 positions (1.10 PFLOP) 665 us, 1.66 PFLOP/s, what power sustains; NVFP4, chunks of 33 to 100 tokens, 121 us, 1.18 PFLOP/s.
 // 64 single tokens over 1500 bf16 states (394 MB) 82 us, 4.8 TB/s: start, joins, and what the ring does not
-// cover when a unit ends.  Registers and code count: a spill leaves the little L1 there is, code of twenty
-// roles and loops the instruction caches, and a wait's way out is in every link of the chain.
+// cover when a unit ends.  Spilled registers do not stay in the L1 that the shared memory leaves, the code of all
+// roles has to share the instruction caches, and the way out of a wait is in every link of the chain: most
+// of the choices below that look small are about one of the three.
 //
 // TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
 // Warps: 0 TMA producer, 1 and 2 issue the MMAs of stream 0 and 1 (1 owns the TMEM), 3 clears what
@@ -59,7 +60,7 @@ constexpr float kMost = 0x1p16f;   // what the p of a page may add up to before 
 constexpr float kMost16 = 0x1p15f; // the same where P is f16
 constexpr float kPUp16 = 7.f;      // f16 P: 2^7 2^(s - m)
 constexpr int kSlotFloats = kRows * (kDim + 2); // o[rows][128], m, l
-constexpr int kUnitCost = 3;     // a unit's queries and outputs in pages
+constexpr int kUnitCost = 3;     // a unit's queries and outputs in pages (ragged prompts 422 us; 2: 432, 4: 431)
 constexpr int kMinRange = 4;     // what a CTA takes at least
 
 __host__ __device__ constexpr int threads_of(int fmt)
@@ -1193,6 +1194,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
                 if (!room)
                     wait(ready_free + 8 * (z % DEPTH), (uint32_t)(z / DEPTH - 1) & 1u);
+                // (E4M3: four pieces ahead; two: the 512-token chunk 748 us for 670, eight: 681)
                 const bool bad = convert_row<FMT, 2, 4>(gsm + (z % TILES) * TB, gsm + L.staged + (z % DEPTH) * kTile16 + row * 128, row, tail, drop, check);
                 if (bad)
                     misc.later_bad[w.seg & 7] = w.seg + 1;
