@@ -147,20 +147,26 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _bufs(stream, kinds, *xs):
+def _bufs(stream, kinds, *xs, **needs):
     """buffers.bufs, which takes this name at the first call (torch is imported by then)."""
     global _bufs
     from .buffers import bufs as _bufs
 
-    return _bufs(stream, kinds, *xs)
+    return _bufs(stream, kinds, *xs, **needs)
 
 
-def _check_rows(x, stride, heads):
+def _check_rows(x, stride, heads, tokens):
     """buffers.check_rows, in the same way."""
     global _check_rows
     from .buffers import check_rows as _check_rows
 
-    _check_rows(x, stride, heads)
+    _check_rows(x, stride, heads, tokens)
+
+
+# bytes of the 128 rows that a page has of one head, by element type, and of index keys without their scales
+_TILE_BYTES = {MSA_BF16: 32768, MSA_FP8_E4M3: 16384, MSA_NVFP4: 9216}
+_INDEX_TILE_BYTES = {MSA_BF16: 32768, MSA_NVFP4: 8192}
+_NO_NEEDS = (0,) * 32  # a call without tokens looks at nothing
 
 
 def _stream(stream):
@@ -307,12 +313,16 @@ def rope_frequencies(radians, device=None):
 def msa_qk_norm_rope(rope: MsaRope, freqs, num_tokens: int, positions, num_q_heads: int, q, q_weight, q_out,
                      num_k_heads: int = 0, k=None, k_weight=None, k_out=None, stream=None):
     """Norm and rotation of query heads, and of key heads in the same pass."""
-    st, (f, at, a, b, c, d, e, g) = _bufs(stream, "giRhhRhh", freqs, positions, q, q_weight, q_out, k, k_weight, k_out)
+    needs, row = _NO_NEEDS, 256 * num_tokens
+    if num_tokens > 0:
+        qw, kw = (256 * num_q_heads, 256 * num_k_heads) if rope.per_head_weights else (256, 256)
+        needs = (4 * rope.rotary_dim, 4 * num_tokens, 0, qw, row * num_q_heads, 0, kw, row * num_k_heads)
+    st, (f, at, a, b, c, d, e, g) = _bufs(stream, "giRhhRhh", freqs, positions, q, q_weight, q_out, k, k_weight, k_out, needs=needs)
     if q is not a:
-        _check_rows(q, rope.q_stride, num_q_heads)
+        _check_rows(q, rope.q_stride, num_q_heads, num_tokens)
     if k is not d:
-        _check_rows(k, rope.k_stride, num_k_heads)
-    _check(load().msa_qk_norm_rope(ctypes.byref(rope), f, num_tokens, at, num_q_heads, a, b, c, num_k_heads, d, e, g,
+        _check_rows(k, rope.k_stride, num_k_heads, num_tokens)
+    _check(load().msa_qk_norm_rope(rope, f, num_tokens, at, num_q_heads, a, b, c, num_k_heads, d, e, g,
                                    st), "msa_qk_norm_rope")
 
 
@@ -326,19 +336,28 @@ def msa_kv_append(shape, rope, freqs, num_tokens, offsets, k, k_weight, v, idxk,
                   workspace_bytes, stream=None):
     """A ragged batch's keys, values and index keys into their pages, with norm and rotation on the way, and its
     queries and index queries in the same pass."""
+    Hq, Hkv, Hi, R = shape.num_q_heads, shape.num_kv_heads, shape.num_index_heads, shape.num_requests
+    needs = _NO_NEEDS
+    if num_tokens > 0 and R > 0:
+        qw, kw, iw = (256 * Hq, 256 * Hkv, 256 * Hi) if rope.per_head_weights else (256, 256, 256)
+        row, pages, idx_dtype = 256 * num_tokens, shape.num_pages, shape.index_dtype
+        idx_rows = 0 if idxk is None else pages * Hi
+        needs = (4 * rope.rotary_dim, 4 * R + 4, 0, kw, 0, 0, iw, 0, qw, row * Hq, 0, iw, row * Hi, 4 * R * shape.max_blocks_per_seq, 4 * R,
+                 2 * pages * Hkv * _TILE_BYTES.get(shape.kv_dtype, 0), idx_rows * _INDEX_TILE_BYTES.get(idx_dtype, 0),
+                 1024 * idx_rows if idx_dtype == MSA_NVFP4 else 0, workspace_bytes)
     st, out = _bufs(stream, "giRhRRhRhhRhhiibbbb", freqs, offsets, k, k_weight, v, idxk, idxk_weight, q, q_weight, q_out,
-                    q_idx, q_idx_weight, q_idx_out, block_table, seq_lens, kv_pool, idxk_pool, idxk_scales, workspace)
+                    q_idx, q_idx_weight, q_idx_out, block_table, seq_lens, kv_pool, idxk_pool, idxk_scales, workspace, needs=needs)
     if k is not out[2]:
-        _check_rows(k, rope.k_stride, shape.num_kv_heads)
+        _check_rows(k, rope.k_stride, Hkv, num_tokens)
     if v is not out[4]:
-        _check_rows(v, rope.v_stride, shape.num_kv_heads)
+        _check_rows(v, rope.v_stride, Hkv, num_tokens)
     if idxk is not out[5]:
-        _check_rows(idxk, rope.idxk_stride, shape.num_index_heads)
+        _check_rows(idxk, rope.idxk_stride, Hi, num_tokens)
     if q is not out[7]:
-        _check_rows(q, rope.q_stride, shape.num_q_heads)
+        _check_rows(q, rope.q_stride, Hq, num_tokens)
     if q_idx is not out[10]:
-        _check_rows(q_idx, rope.q_idx_stride, shape.num_index_heads)
-    _check(load().msa_kv_append(ctypes.byref(shape), ctypes.byref(rope), out[0], num_tokens, *out[1:], workspace_bytes, st),
+        _check_rows(q_idx, rope.q_idx_stride, Hi, num_tokens)
+    _check(load().msa_kv_append(shape, rope, out[0], num_tokens, *out[1:], workspace_bytes, st),
            "msa_kv_append")
 
 
@@ -346,8 +365,13 @@ def msa_ragged_attention(shape, num_tokens, causal, q, offsets, kv_pool, block_t
                          workspace_bytes, stream=None):
     """Attention of a ragged batch's query rows: causal (prompts, chunks, steps), or over all states of
     another length (cross attention)."""
-    st, bufs = _bufs(stream, "hibiihfb", q, offsets, kv_pool, block_table, seq_lens, out, lse, workspace)
-    _check(load().msa_ragged_attention(ctypes.byref(shape), num_tokens, int(causal), *bufs, int(workspace_bytes), st),
+    R, needs = shape.num_requests, _NO_NEEDS
+    if num_tokens > 0 and R > 0:
+        rows = num_tokens * shape.num_q_heads
+        needs = (256 * rows, 4 * R + 4, 2 * shape.num_pages * shape.num_kv_heads * _TILE_BYTES.get(shape.kv_dtype, 0),
+                 4 * R * shape.max_blocks_per_seq, 4 * R, 256 * rows, 4 * rows, workspace_bytes)
+    st, bufs = _bufs(stream, "hibiihfb", q, offsets, kv_pool, block_table, seq_lens, out, lse, workspace, needs=needs)
+    _check(load().msa_ragged_attention(shape, num_tokens, int(causal), *bufs, int(workspace_bytes), st),
            "msa_ragged_attention")
 
 
