@@ -402,14 +402,17 @@ __device__ __forceinline__ void sts32(uint32_t a, float v)
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
-// Whether any thread of the two warps that meet at a barrier says so.
+// Whether any thread of the two warps that meet at a barrier says so.  What either warp stores to tensor memory
+// behind it comes after what both have read before it.
 __device__ __forceinline__ bool any_of_two_warps(int barrier, bool v)
 {
     uint32_t any;
+    tcgen05_before_sync();
     asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.b32 %0, 1, 0, q;\n}\n"
                  : "=r"(any)
                  : "r"((uint32_t)v), "r"(barrier)
                  : "memory");
+    tcgen05_after_sync();
     return any != 0;
 }
 
