@@ -174,6 +174,8 @@ struct Cursor {
     }
 };
 
+// CACHE: tokens of requests, rows to their pages and to outputs; else outputs alone, at the given positions.
+template <bool CACHE>
 __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const AppendParams p)
 {
     __shared__ uint4 ring[kWarps][kSlots][2][32]; // a lane reads what it copied itself
@@ -181,8 +183,16 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
     const long long all = (long long)p.T * p.groups, wi = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const long long x0 = wi * p.per_warp;
     int left = (int)min((long long)p.per_warp, all - x0);
-    if (left <= 0)
+    // offsets that go down, or past the tokens
+    auto check_offsets = [&] {
+        for (int i = blockIdx.x * (32 * kWarps) + threadIdx.x; CACHE && i < p.R; i += gridDim.x * (32 * kWarps))
+            if (p.offsets[i] < 0 || p.offsets[i + 1] < p.offsets[i] || p.offsets[i + 1] > p.T)
+                set_error(p.err, kErrSeqLen);
+    };
+    if (left <= 0) {
+        check_offsets();
         return;
+    }
     const int m = p.interleaved ? 8 : p.units;
     const int at0 = 8 * piece(l, 0, m), at1 = 8 * piece(l, 1, m);
     const uint32_t mine = smem_u32(&ring[threadIdx.x >> 5][0][0][lane]);
@@ -234,7 +244,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
             const int t = token = at.t;
             int pos = 0;
             skip = false;
-            if (p.positions) {
+            if constexpr (!CACHE) {
                 pos = p.positions[t];
             } else {
                 if (r < 0 || t >= behind) {
@@ -243,13 +253,13 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
                     if (r >= 0) {
                         first = p.offsets[r];
                         behind = p.offsets[r + 1];
-                        len = p.seq_lens[r];
+                        len = first < 0 || behind > p.T ? 0 : p.seq_lens[r]; // (no length: its tokens are skipped)
                     }
                 }
                 const int room = p.maxB * kPage; // at most 2^21
                 skip = r < 0;                    // behind the last request's tokens: left as it is
                 pos = (int)((unsigned)(len - 1) + ((unsigned)t - (unsigned)first));
-                if (!skip && (first < 0 || len < 1 || len > room || pos >= room)) { // (nothing overflows behind the first three)
+                if (!skip && (len < 1 || len > room || pos >= room)) { // (nothing overflows behind the first two)
                     if (lane == 0)
                         set_error(p.err, kErrSeqLen);
                     skip = true;
@@ -288,9 +298,9 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
 
         // ---- the set's rows: where the lane's goes, and how far the next one is ----
         const RowSet &set = p.set[at.s];
-        const int where = set.where, heads = set.heads, end = done + min(at.n - at.g, left - done);
+        const int where = CACHE ? set.where : kToOut, heads = set.heads, end = done + min(at.n - at.g, left - done);
         const bool normed = set.weight != nullptr, rotated = set.rotated;
-        const bool f4 = set.bytes == kDim / 2, f8 = set.bytes == kDim;
+        const bool f4 = CACHE && set.bytes == kDim / 2, f8 = CACHE && set.bytes == kDim;
         int h = at.g * 4 + sub;
         const int stop = skip || (where != kToOut && page < 0) ? 0 : heads; // rows from here on are not written
         const long long block = where == kToOut ? at.t : page;
@@ -416,6 +426,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
         at.n = (p.set[at.s].heads + 3) >> 2;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    check_offsets();
 }
 
 } // namespace
@@ -430,7 +441,7 @@ cudaError_t launch_append(const AppendParams &params, cudaStream_t stream)
     const long long all = (long long)p.T * p.groups, warps = 152ll * kCtas * kWarps;
     p.per_warp = (int)((all + warps - 1) / warps);
     const long long blocks = (all + (long long)p.per_warp * kWarps - 1) / ((long long)p.per_warp * kWarps);
-    const cudaError_t e = launch_kernel(append_kernel, dim3((unsigned)blocks), dim3(32 * kWarps), 0, stream, false, p);
+    const cudaError_t e = launch_kernel(p.positions ? append_kernel<false> : append_kernel<true>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, stream, false, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
