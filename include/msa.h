@@ -423,10 +423,10 @@ size_t msa_ragged_workspace_bytes(const msa_shape *shape);
  *                with rotary_dim 0 and no weights the pools get the same bytes
  * Only the rows of the new tokens are written.  Two tokens of one call that share
  * a row of a page leave either's.  A bad length or page id is reported through the
- * workspace's error word and its token's rows are skipped.  Offsets that go down or
- * past num_tokens are reported too: the tokens of a request that ends past num_tokens
- * are skipped, one that two requests have goes to either's place or none.  Only the workspace's
- * error word is used: 256 bytes suffice. */
+ * workspace's error word and its token's rows, queries among them, are skipped.
+ * Offsets that go down or past num_tokens are reported too: the tokens of a request
+ * that ends past num_tokens are skipped, one that two requests have goes to either's
+ * place or none.  Only the workspace's error word is used: 256 bytes suffice. */
 msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uint64_t *freqs,
                          int32_t num_tokens, const int32_t *offsets, const void *k,
                          const void *k_weight, const void *v, const void *idxk,

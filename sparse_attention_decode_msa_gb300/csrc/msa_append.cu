@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
         const int e = 2 * sub + k, i = p.interleaved ? (e < 4 ? 4 * l + e : 28 + 4 * l + e) : 8 * l + e;
         freq[k] = i < 8 * p.units ? p.freqs[i] : 0ull;
     }
-    long long page = -1; // -1: nothing of this token goes to the cache
+    long long page = -1; // -1: outside the pool, its tokens are skipped
     int row = 0, token = -1, entry = -1; // entry: the block of the table that `page` is from
     bool skip = false;                 // nothing of this token is written
     uint64_t cs[4], sn[4], ns[4];      // cosines, sines and the sines' negatives, in pairs
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
                             page = -1;
                         }
                     }
+                    skip = page < 0;
                 }
             }
             if (p.units > 0) {
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
         const bool normed = set.weight != nullptr, rotated = set.rotated;
         const bool f4 = CACHE && set.bytes == kDim / 2, f8 = CACHE && set.bytes == kDim;
         int h = at.g * 4 + sub;
-        const int stop = skip || (where != kToOut && page < 0) ? 0 : heads; // rows from here on are not written
+        const int stop = skip ? 0 : heads; // rows from here on are not written
         const long long block = where == kToOut ? at.t : page;
         const int in = where == kToOut ? 0 : row;
         uint8_t *dst = set.y + block * set.block_step + (unsigned)(h * set.head_step + in * set.bytes);

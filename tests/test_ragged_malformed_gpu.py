@@ -75,3 +75,30 @@ def test_append_reports_offsets_past_the_tokens_and_skips_the_request(torch_cuda
     b = Batch([4, 4, 4], [10, 10, 10], seed=5, behind=2)
     assert b.run(torch_cuda) == msa.MSA_OK
     b.check()
+
+
+def test_append_with_a_bad_length_leaves_the_others_right(torch_cuda):
+    for bad in (0, -4, 257, 2 ** 31 - 1):
+        b = Batch([2, 3, 130], [100, 10, 50], seed=9)
+        lens = b.seq_lens.copy()
+        lens[1] = bad
+        assert b.run(torch_cuda, seq_lens=lens) == msa.MSA_ERR_DEVICE_CHECK
+        tokens = {t: (0, t) for t in range(2)} | {5 + j: (2, j) for j in range(130)}
+        for rows in changed_rows(b):
+            assert rows == {place(b, r, j) for r, j in tokens.values()}
+        check_tokens(b, tokens)
+        assert left(b, np.arange(2, 5))
+
+
+def test_append_with_a_bad_page_skips_its_tokens_whole(torch_cuda):
+    # the queries and index queries of a token without a page are left too
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1):
+        b = Batch([2, 3, 130], [100, 10, 50], seed=9, behind=1)
+        table = b.table.copy()
+        table[2, 1] = bad  # positions 128 .. 179 of request 2
+        assert b.run(torch_cuda, table=table) == msa.MSA_ERR_DEVICE_CHECK
+        tokens = {t: (0, t) for t in range(2)} | {2 + j: (1, j) for j in range(3)} | {5 + j: (2, j) for j in range(78)}
+        for rows in changed_rows(b):
+            assert rows == {place(b, r, j) for r, j in tokens.values()}
+        check_tokens(b, tokens)
+        assert left(b, np.arange(5 + 78, 136))
