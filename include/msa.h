@@ -444,10 +444,10 @@ msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uin
  *   q, out       bf16 [num_tokens][Hq][128]
  *   lse          fp32 [num_tokens][Hq]
  * num_q_heads is any multiple G of num_kv_heads with 1 <= G <= 64.  seq_lens[r] may
- * be 0: no states, outputs of 0 and lse -inf.  Offsets that go down or past
- * num_tokens, a negative length and one that the table cannot hold are reported
- * through the error word and the request is skipped; a page id outside the pool is
- * reported, and the outputs of the call are unspecified.  Bytes behind the last
+ * be 0: no states, outputs of 0 and lse -inf.  Offsets past num_tokens, a negative
+ * length and one that the table cannot hold are reported through the error word and
+ * the request is skipped; offsets that go down are reported and nothing is written;
+ * a page id outside the pool is reported, and the outputs of the call are unspecified.  Bytes behind the last
  * position may hold anything; an infinity or NaN in V reaches the outputs that see
  * its position, in that dimension, and no other.  Sums and the softmax are fp32, in a
  * fixed order (the same inputs give the same bits).  Probabilities meet V as bf16

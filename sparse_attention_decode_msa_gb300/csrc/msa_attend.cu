@@ -150,7 +150,7 @@ struct Misc {
     Request start;
     long long wait_limit;
     uint32_t *err;
-    int abort, start_r;
+    int abort, start_r, down;
     uint32_t tmem;
     int later_bad[8]; // unit counter + 1 where V rows of later tokens are not finite
 };
@@ -602,9 +602,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const int lo = min(p.R, (int)threadIdx.x * per), hi = min(p.R, lo + per);
     long long mine = 0;
     Request q{};
+    bool down = false; // offsets that go down: requests that share rows, in sum more of them than the batch has
     for (int r = lo; r < hi; ++r) {
         bool bad, idle;
         q = read_request(p, r, &bad, &idle);
+        down |= p.offsets[r + 1] < q.first;
         if (q.units)
             mine += q.before(p, q.units) * p.Hkv;
         if (bad && blockIdx.x == 0)
@@ -619,13 +621,17 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
     if (lane == 31)
         misc.scan[warp] = incl;
-    __syncthreads();
+    down = __syncthreads_or(down);
     long long before = incl - mine, W = 0;
 #pragma unroll
     for (int i = 0; i < NT / 32; ++i) {
         before += i < warp ? misc.scan[i] : 0;
         W += misc.scan[i];
     }
+    if (down) // reported: no line, and no outputs
+        W = 0;
+    if (threadIdx.x == 0)
+        misc.down = down;
     const int ranges = (int)min((long long)gridDim.x, max(1ll, W / kMinRange));
     Share w{};
     const long long x0 = (int)blockIdx.x < ranges ? cut(blockIdx.x, W, ranges) : W;
@@ -882,7 +888,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
         }
         // ---- outputs of requests without states ----
-        for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+        for (int r = blockIdx.x; r < p.R && !misc.down; r += gridDim.x) {
             bool bad, idle;
             const Request q = read_request(p, r, &bad, &idle);
             if (!idle)

@@ -6,6 +6,7 @@ import pytest
 
 import sparse_attention_decode_msa_gb300 as msa
 from oracle import ragged as ref
+from test_ragged_attention_gpu import KV, Ragged
 from test_ragged_rows_gpu import Batch, host, is_near
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +103,17 @@ def test_append_with_a_bad_page_skips_its_tokens_whole(torch_cuda):
             assert rows == {place(b, r, j) for r, j in tokens.values()}
         check_tokens(b, tokens)
         assert left(b, np.arange(5 + 78, 136))
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("R", [4, 1300])  # (more requests than a block has threads)
+def test_attention_over_offsets_that_go_down_writes_nothing(torch_cuda, kv, R):
+    # every other request would have all the batch's tokens: together more rows than there are
+    c = Ragged([40] + [0] * (R - 1), [200] + [0, 130] * ((R - 1) // 2) + [77], True, 1, 4, kv, seed=3)
+    offsets = np.array([0, 40] * (R // 2) + [40], np.int32)
+    c.d_offsets.copy_(torch_cuda.from_numpy(offsets))
+    out, lse = c.run().result()
+    assert c.status() == msa.MSA_ERR_DEVICE_CHECK
+    assert np.all(out == 7) and np.all(lse == 7)
+    c.d_offsets.copy_(torch_cuda.from_numpy(c.offsets))
+    c.run().check()
