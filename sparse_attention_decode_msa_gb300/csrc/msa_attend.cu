@@ -42,9 +42,8 @@
 //
 // TMEM columns: S/P of stream t at 128 t, O of stream t at 256 + 128 t.
 // Warps: 0 TMA producer, 1 and 2 issue the MMAs of stream 0 and 1 (1 owns the TMEM), 3 clears what
-// must not be multiplied from V tiles on last pages (bf16) and writes the outputs of requests
-// without states, 4-11 and 12-19 softmax of stream 0 and 1, two warps a row quarter: columns 0 ..
-// 63 and 64 .. of a page, 20-23 converters (E4M3, NVFP4).
+// must not be multiplied from V tiles on last pages (bf16), 4-11 and 12-19 softmax of stream 0 and 1, two
+// warps a row quarter: columns 0 .. 63 and 64 .. of a page, 20-23 converters (E4M3, NVFP4).
 #include <type_traits>
 
 #include "msa_ragged.cuh"
@@ -150,9 +149,10 @@ struct Misc {
     Request start;
     long long wait_limit;
     uint32_t *err;
-    int abort, start_r, down;
+    int abort, start_r;
     uint32_t tmem;
     int later_bad[8]; // unit counter + 1 where V rows of later tokens are not finite
+    int idle;         // there are requests without states
 };
 static_assert(sizeof(Misc) <= 288, "misc");
 
@@ -540,6 +540,17 @@ __device__ __noinline__ void long_wait(uint32_t bar, uint32_t parity, Misc *misc
     }
 }
 
+// Rows from .. to - 1 (of all heads) of the outputs, of requests without states: one warp.
+__device__ __forceinline__ void write_idle(const AttendParams &p, size_t from, size_t to)
+{
+    const int lane = threadIdx.x & 31;
+    uint4 *out = reinterpret_cast<uint4 *>(p.out + from * kDim);
+    for (size_t i = lane; i < (to - from) * (kDim / 8); i += 32)
+        out[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (size_t i = from + lane; i < to; i += 32)
+        p.lse[i] = __uint_as_float(0xFF800000u);
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
     attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map, const AttendParams p)
@@ -561,7 +572,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     if (smem & 1023u) { // swizzled tiles need it; the declaration gives it
         if (threadIdx.x == 0) {
             set_error(p.err, kErrScratch);
-            p.joins[blockIdx.x].c0 = -1;
+            p.joins[blockIdx.x].c0 = -1, p.joins[blockIdx.x].idle = 0;
         }
         return;
     }
@@ -589,6 +600,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
         fence_mbar_init();
         misc.abort = 0;
+        misc.idle = 0;
         misc.wait_limit = p.wait_limit;
         misc.err = p.err;
     }
@@ -602,11 +614,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const int lo = min(p.R, (int)threadIdx.x * per), hi = min(p.R, lo + per);
     long long mine = 0;
     Request q{};
-    bool down = false; // offsets that go down: requests that share rows, in sum more of them than the batch has
+    bool idle_here = false; // requests without states
+    bool down = false;      // offsets that go down: requests that share rows, in sum more of them than the batch has
     for (int r = lo; r < hi; ++r) {
         bool bad, idle;
         q = read_request(p, r, &bad, &idle);
         down |= p.offsets[r + 1] < q.first;
+        idle_here |= idle;
         if (q.units)
             mine += q.before(p, q.units) * p.Hkv;
         if (bad && blockIdx.x == 0)
@@ -630,8 +644,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
     if (down) // reported: no line, and no outputs
         W = 0;
-    if (threadIdx.x == 0)
-        misc.down = down;
+    if (idle_here && !down)
+        misc.idle = 1;
     const int ranges = (int)min((long long)gridDim.x, max(1ll, W / kMinRange));
     Share w{};
     const long long x0 = (int)blockIdx.x < ranges ? cut(blockIdx.x, W, ranges) : W;
@@ -681,6 +695,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     if (threadIdx.x == 0) {
         AttendJoin j{};
         j.c0 = -1;
+        j.idle = misc.idle;
         if (w.left > 0 && w.b > 0) {
             const int c0 = cut_of(x0 - w.b, W, ranges); // (x0 is page b)
             if (c0 == (int)blockIdx.x - 1) {
@@ -887,18 +902,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                 __syncwarp();
             }
         }
-        // ---- outputs of requests without states ----
-        for (int r = blockIdx.x; r < p.R && !misc.down; r += gridDim.x) {
+        // ---- outputs of requests without states, where no kernel follows ----
+        for (int r = 0; r < p.R && gridDim.x == 1 && misc.idle; ++r) {
             bool bad, idle;
             const Request q = read_request(p, r, &bad, &idle);
-            if (!idle)
-                continue;
-            const size_t rows = (size_t)p.Hkv * p.G, all = rows * q.n;
-            uint4 *out = reinterpret_cast<uint4 *>(p.out + rows * q.first * kDim);
-            for (size_t i = lane; i < all * (kDim / 8); i += 32)
-                out[i] = make_uint4(0u, 0u, 0u, 0u);
-            for (size_t i = lane; i < all; i += 32)
-                p.lse[rows * q.first + i] = __uint_as_float(0xFF800000u);
+            const size_t heads = (size_t)p.Hkv * p.G;
+            if (idle)
+                write_idle(p, heads * q.first, heads * (q.first + q.n));
         }
     } else if (warp < 20) {
         // ---- softmax: a thread has 64 columns of a page of a query row ----
@@ -1226,7 +1236,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 }
 
 // Units cut between CTAs: block (c, y, z) has rows 32 y .. and columns 32 z .. of the unit that CTA c + 1
-// begins inside of; a warp has a 16-byte piece of each row, a lane a row.
+// begins inside of; a warp has a 16-byte piece of each row, a lane a row.  Beside that the outputs of requests
+// without states, a share of each one's rows by each block: 4096 tokens of 64 heads (67 MB) 29 us, a fill of them 20 (one
+// warp a request: 1070; all warps of the kernel above, at its end: 28, but ragged cross attention 68 -> 71).
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p)
 {
     constexpr int U = 4; // slots on their way at once
@@ -1234,6 +1246,19 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     const AttendJoin jn = p.joins[blockIdx.x + 1];
+    if (jn.idle && blockIdx.y == 0)
+        for (int r0 = 32 * warp; r0 < p.R; r0 += 32 * 8) {
+            bool bad, idle = false;
+            Request q{};
+            if (r0 + lane < p.R)
+                q = read_request(p, r0 + lane, &bad, &idle);
+            for (uint32_t some = __ballot_sync(0xffffffffu, idle); some; some &= some - 1) {
+                const size_t heads = (size_t)p.Hkv * p.G, first = heads * __shfl_sync(0xffffffffu, q.first, __ffs(some) - 1);
+                const size_t rows = heads * __shfl_sync(0xffffffffu, q.n, __ffs(some) - 1);
+                const int part = 4 * blockIdx.x + blockIdx.z, parts = 4 * gridDim.x;
+                write_idle(p, first + rows * part / parts, first + rows * (part + 1) / parts);
+            }
+        }
     const int each = p.unit_tokens >> 1, t = blockIdx.y >> 2, row = 32 * blockIdx.y + lane;
     const int rows = min(each, jn.tokens - t * each) * p.G; // of stream t, from row 128 t on
     if (jn.c0 < 0 || 32 * (int)(blockIdx.y & 3) >= rows)

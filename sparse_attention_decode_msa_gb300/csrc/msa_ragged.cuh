@@ -45,7 +45,8 @@ struct AppendParams {
 struct AttendJoin {
     int token0, tokens, head; // its first token's row, its tokens, its KV head
     int c0, c1;               // the CTAs that have parts of it
-    int pad[3];
+    int idle;                 // there are requests without states, whose outputs are to be written
+    int pad[2];
 };
 
 struct AttendParams : CacheParams { // (nq is not used)
