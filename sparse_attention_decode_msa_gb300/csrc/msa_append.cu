@@ -439,7 +439,10 @@ cudaError_t launch_append(const AppendParams &params, cudaStream_t stream)
         return cudaSuccess;
     // Few groups: a warp for each, the latency of one.  Many: as many warps as the GPU holds at a time, with
     // runs of neighbouring groups, which share angles and places.
-    const long long all = (long long)p.T * p.groups, warps = 152ll * kCtas * kWarps;
+    const int sms = device_sms();
+    if (sms < 1)
+        return cudaErrorInvalidDevice;
+    const long long all = (long long)p.T * p.groups, warps = (long long)sms * kCtas * kWarps;
     p.per_warp = (int)((all + warps - 1) / warps);
     const long long blocks = (all + (long long)p.per_warp * kWarps - 1) / ((long long)p.per_warp * kWarps);
     const cudaError_t e = launch_kernel(p.positions ? append_kernel<false> : append_kernel<true>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, stream, false, p);

@@ -60,6 +60,7 @@ struct AttendParams : CacheParams { // (nq is not used)
     bool causal;
 };
 
+int device_sms(); // SMs of the current device, below 1 if it cannot be read
 size_t attend_slot_bytes();
 cudaError_t launch_attend(const AttendParams &p, int kv_dtype, int ctas, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);

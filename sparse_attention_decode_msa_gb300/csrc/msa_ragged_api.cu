@@ -136,19 +136,23 @@ RaggedLayout layout_of(const msa_shape *s)
     return w;
 }
 
-// Persistent CTAs: the shape's, else one per SM; -1 if the device cannot be read.
+// Persistent CTAs: the shape's, else one per SM; below 1 if the device cannot be read.
 int attend_ctas(const msa_shape *s)
 {
     if (s->decode_ctas > 0)
         return s->decode_ctas;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-        return -1;
+    const int sms = device_sms();
     return sms < kCacheCtaBound ? sms : kCacheCtaBound;
 }
 
 } // namespace
+
+int device_sms()
+{
+    int dev = 0, sms = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? sms : -1;
+}
+
 } // namespace msa
 
 using namespace msa;
