@@ -12,7 +12,7 @@
 // queries and outputs in front (kUnitCost), are a line that is cut into equal ranges, one a CTA,
 // whatever the lengths are; a unit cut between CTAs is
 // joined by attend_join_kernel in the order of its pages.  Pages before unit i of a causal
-// request are a sum of floors, which a Euclid-like recursion gives in a few steps: no
+// request are a sum of floors, lattice points under a line, which are counted in a few steps: no
 // table, no kernel before this one.
 //
 // Two streams of up to 128 rows share a CTA's pages, so that the tensor cores work for one
@@ -98,29 +98,26 @@ __host__ __device__ constexpr Smem smem_layout(int fmt)
 }
 static_assert(smem_layout(kFmtBf16).total <= 232448 && smem_layout(kFmtFp8).total <= 232448 && smem_layout(kFmtF4).total <= 232448, "shared memory");
 
-// sum over i < n of floor((a i + b) / m)
+// sum over i < n of floor((a i + b) / m), the lattice points under a line by columns.  What a and b have of whole m
+// is a sum at once.  Of the rest, y = floor((a (n - 1) + b) / m) rows of points, row j + 1 lacks the columns before
+// ceil(((j + 1) m - b) / a): n y less the same sum over y rows with a and m changed over, as in Euclid's algorithm.
 __device__ __noinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
 {
-    unsigned long long s = 0;
-    while (n > 0) {
-        if (a >= m) {
-            s += (unsigned long long)n * (n - 1) / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            s += (unsigned long long)n * (b / m);
-            b %= m;
-        }
-        const uint32_t y = a * n + b; // below 2^31: a < 128 here, n at most 2^22
-        if (y < m)
-            break;
-        n = y / m;
-        b = y % m;
-        const uint32_t t = m;
+    long long s = 0;
+    for (bool plus = true; n > 0; plus = !plus) {
+        long long t = (long long)((unsigned long long)n * (n - 1) / 2 * (a / m) + (unsigned long long)n * (b / m));
+        a %= m;
+        b %= m;
+        const uint32_t y = (a * (n - 1) + b) / m; // below 2^30: a < 128, n at most 2^22, and both fall
+        t += (long long)n * y;
+        s = plus ? s + t : s - t;
+        b = m - b + a - 1;
+        n = y;
+        const uint32_t old = m;
         m = a;
-        a = t;
+        a = old;
     }
-    return (long long)s;
+    return s;
 }
 
 // A request: its tokens, what its first token sees, its units.
