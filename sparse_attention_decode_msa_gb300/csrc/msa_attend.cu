@@ -164,7 +164,7 @@ __device__ __forceinline__ Request read_request(const AttendParams &p, int r, bo
         return q;
     q.L = p.seq_lens[r];
     if (n < 0 || q.first < 0 || q.first + n > p.T || q.L < 0 ||
-        (q.L + (p.causal ? n - 1 : 0) + kPage - 1) / kPage > p.maxB) {
+        (q.L > 0 && (q.L + (p.causal ? n - 1 : 0) + kPage - 1) / kPage > p.maxB)) {
         *bad = true;
         return q;
     }

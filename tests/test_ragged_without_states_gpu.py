@@ -30,6 +30,13 @@ def test_a_batch_of_one_short_request_without_states(torch_cuda):
     Ragged([5], [0], False, 1, 2, seed=1).run().check()
 
 
+@pytest.mark.parametrize("kv", KV)
+def test_the_table_need_not_hold_tokens_that_see_nothing(torch_cuda, kv):
+    c = Ragged([300, 2], [0, 100], True, 1, 4, kv, seed=6)
+    assert c.pb.max_blocks == 1
+    c.run().check()
+
+
 def test_writing_them_takes_the_time_of_writing(torch_cuda):
     # 4096 tokens of 64 heads (67 MB) beside a short request: one warp takes 50 times as long as a fill does
     torch = torch_cuda
