@@ -453,8 +453,10 @@ msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uin
  * fixed order (the same inputs give the same bits).  Probabilities meet V as bf16
  * over bf16 pages, and the sum that divides is that of the rounded ones: an output
  * is a mean of values with weights that are off by 2^-8 of themselves at most, and
- * sum to 1.  Over E4M3 and NVFP4 pages they are fp16 (2^-11), and queries meet
- * the keys as fp16 after a power of two (elements 2^-23 below a row's largest lose bits).
+ * sum to 1.  Over E4M3 and NVFP4 pages they are fp16, and the sum is that of the p as
+ * they are: a weight is off by 2^-11 of itself, or by 2^-32 where that is more (one
+ * below 2^-33 may count as 0); queries meet the keys as fp16 after a power of two
+ * (elements 2^-23 below a row's largest lose bits).
  * decode_ctas > 0 sets the persistent CTAs (at most 8192); 0 takes one per SM.
  * Nothing is kept in the workspace between calls but the error word: calls that may
  * overlap, and CUDA graphs that may, need a workspace each. */

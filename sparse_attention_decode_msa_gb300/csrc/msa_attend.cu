@@ -22,7 +22,8 @@
 //
 // Operands: Q in shared memory (K-major, 128-byte swizzle), K tiles as TMA lands them, P in
 // tensor memory over the S it came from, V tiles as landed (MN-major).  E4M3 and NVFP4 tiles
-// are widened to f16 by converter warps, and P is f16: off by 2^-11 of p.  Over bf16 pages P
+// are widened to f16 by converter warps, and P is f16, 2^7 for the heaviest position of a row's first page: off by
+// 2^-11 of p, or by 2^-32 of that position's below 2^-21 of it (a subnormal's half step).  Over bf16 pages P
 // is bf16 (V's type, which a product needs): each p is off by 2^-8 of itself at most, and
 // the sum that divides is that of the rounded p, so that an output is a mean of values
 // with weights that are off by 2^-8 of themselves and still sum to 1: off by 2^-8 of the
