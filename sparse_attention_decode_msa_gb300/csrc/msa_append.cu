@@ -183,11 +183,14 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) append_kernel(const Append
     const long long all = (long long)p.T * p.groups, wi = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const long long x0 = wi * p.per_warp;
     int left = (int)min((long long)p.per_warp, all - x0);
-    // offsets that go down, or past the tokens
+    // offsets that go down, or past the tokens: a request a thread (there are as many)
     auto check_offsets = [&] {
-        for (int i = blockIdx.x * (32 * kWarps) + threadIdx.x; CACHE && i < p.R; i += gridDim.x * (32 * kWarps))
-            if (p.offsets[i] < 0 || p.offsets[i + 1] < p.offsets[i] || p.offsets[i + 1] > p.T)
+        const int i = blockIdx.x * (32 * kWarps) + threadIdx.x;
+        if (CACHE && i < p.R) {
+            const int at = p.offsets[i], next = p.offsets[i + 1];
+            if ((at < 0) | (next < at) | (next > p.T))
                 set_error(p.err, kErrSeqLen);
+        }
     };
     if (left <= 0) {
         check_offsets();
@@ -444,7 +447,9 @@ cudaError_t launch_append(const AppendParams &params, cudaStream_t stream)
         return cudaErrorInvalidDevice;
     const long long all = (long long)p.T * p.groups, warps = (long long)sms * kCtas * kWarps;
     p.per_warp = (int)((all + warps - 1) / warps);
-    const long long blocks = (all + (long long)p.per_warp * kWarps - 1) / ((long long)p.per_warp * kWarps);
+    long long blocks = (all + (long long)p.per_warp * kWarps - 1) / ((long long)p.per_warp * kWarps);
+    const int checking = p.positions ? 0 : (p.R + 32 * kWarps - 1) / (32 * kWarps); // a thread looks at each request's offsets
+    blocks = blocks < checking ? checking : blocks;
     const cudaError_t e = launch_kernel(p.positions ? append_kernel<false> : append_kernel<true>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, stream, false, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
