@@ -373,7 +373,8 @@ msa_status msa_cache_evict(const msa_shape *shape, int32_t keep, int32_t first, 
  *   a' = scale (a cos t - b sin t), b' = scale (b cos t + a sin t)
  * for each pair (a, b) of the first rotary_dim elements of n, t = p f_i; the
  * others stay as they are.  fp32, rounded once, to bf16 or to the pool's
- * format; rows without norm and rotation are copied bit by bit to bf16. */
+ * format; rows without norm and rotation are copied bit by bit to bf16.  mean x^2 is
+ * fp32 too: a row whose sum of squares passes 2^128 becomes zeros. */
 typedef struct msa_rope {
     int32_t rotary_dim;       /* a multiple of 16 up to 128; 0: no rotation */
     int32_t interleaved;      /* 0: element i turns with i + rotary_dim / 2; 1: 2 i with 2 i + 1 */
@@ -389,7 +390,8 @@ typedef struct msa_rope {
 /* turns[i] = f_i / (2 pi) as a fraction of 2^64, for angles of f_i radians a
  * position, 0 <= |f_i| < 2 pi * 2^31: the rotation's frequencies as the calls
  * below take them (a table of rotary_dim / 2 in device memory, filled once: every
- * angle is then p * turns[i] modulo 2^64, exact at any position).  Pure host
+ * angle is then p * turns[i] modulo 2^64, which loses nothing at any position).  An
+ * entry is off by 2^-52 of itself, from double's roundings, and 2^-64 of a turn.  Pure host
  * function on host memory; MSA_ERR_INVALID_ARGUMENT for a frequency that is
  * not finite or too large. */
 msa_status msa_rope_frequencies(const double *radians, int32_t count, uint64_t *turns);

@@ -4,12 +4,12 @@
 // For a row x of 128 elements of the token at position p:
 //   n = x rsqrt(mean x^2 + eps) (w + offset)            (rows with norm weights)
 //   a' = s (a cos t - b sin t), b' = s (b cos t + a sin t)   for each pair (a, b) of
-//   the first rotary_dim elements of n, t = 2 pi p f_i; the others stay.
+//   the first rotary_dim elements of n, t = p f_i; the others stay.
 // Everything is fp32 and rounded once, to bf16 or to the pool's format.  Angles
-// are exact in 64-bit fixed point: f_i is a fraction of 2^64 of a turn, p f_i wraps
-// around by itself, and what is left is a turn in [-1/2, 1/2) of 32 bits, off by
-// 2^-32 of a turn and p 2^-65 whatever the position (in fp32 p f_i loses 2^-24 of
-// itself, 0.06 rad at a million).
+// are fixed point: the table has f_i as a fraction of 2^64 of a turn, and p times that
+// wraps around by itself at any position (in fp32 p f_i loses 2^-24 of itself, 0.06 rad
+// at a million).  What is left is a turn in [-1/2, 1/2), as a float: off by 2^-26 of a
+// turn and 2^-32, beside p times what the table is off by (2^-52 of f_i and 2^-64 of a turn).
 //
 // Memory-bound: 256 bytes read and 256 (E4M3 128, NVFP4 72) written a row, latency
 // where tokens are few.  A warp takes four heads of one token at a time, eight lanes

@@ -164,11 +164,11 @@ msa_status msa_rope_frequencies(const double *radians, int32_t count, uint64_t *
     if (count < 0 || (count > 0 && (!radians || !turns)))
         return MSA_ERR_INVALID_ARGUMENT;
     for (int32_t i = 0; i < count; ++i) {
-        const double t = radians[i] * 0.15915494309189533577; // 1 / (2 pi)
-        if (!(std::fabs(t) < 2147483648.0))
+        const double t = std::fabs(radians[i]) * 0.15915494309189533577; // 1 / (2 pi)
+        if (!(t < 2147483648.0))
             return MSA_ERR_INVALID_ARGUMENT;
-        const double f = t - std::floor(t); // [0, 1]: 1 where a tiny negative one rounds up
-        turns[i] = f >= 1.0 ? 0u : static_cast<uint64_t>(std::ldexp(f, 64));
+        const uint64_t u = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 64)); // (the difference is exact)
+        turns[i] = radians[i] < 0.0 ? 0u - u : u; // a negative one modulo a turn
     }
     return MSA_OK;
 }
