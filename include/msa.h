@@ -409,7 +409,8 @@ msa_status msa_qk_norm_rope(const msa_rope *rope, const uint64_t *freqs, int32_t
                             const void *k_weight, void *k_out, cudaStream_t stream);
 
 /* Bytes of device workspace for the two calls below (0 if the shape is invalid
- * or unsupported).  Pure host function. */
+ * or unsupported; msa_ragged_attention has one more limit, which depends on the
+ * tokens).  Pure host function. */
 size_t msa_ragged_workspace_bytes(const msa_shape *shape);
 
 /* The tokens of a ragged batch into their pages, keys and index keys with norm
@@ -441,25 +442,31 @@ msa_status msa_kv_append(const msa_shape *shape, const msa_rope *rope, const uin
 /* Attention of a ragged batch's query rows over paged states: token j of request r
  * sees positions 0 .. seq_lens[r] + j - 1 (causal: a prompt, a chunk of one, or a
  * step, its own keys and values appended before), or all seq_lens[r] of them (not
- * causal: cross attention to states of another length).  The result of
- * msa_dense_decode without its limits on tokens.
+ * causal: cross attention to states of another length).  What msa_dense_decode
+ * computes, without its limits on tokens; probabilities are coarser over bf16 pages,
+ * see below.
  *   q, out       bf16 [num_tokens][Hq][128]
  *   lse          fp32 [num_tokens][Hq]
  * num_q_heads is any multiple G of num_kv_heads with 1 <= G <= 64.  seq_lens[r] may
- * be 0: no states, outputs of 0 and lse -inf.  Offsets past num_tokens, a negative
+ * be 0: no states, outputs of 0 and lse -inf for all tokens of the request.  (Causal
+ * too: seq_lens counts the first token's own position, so a prompt's first chunk has
+ * 1.  msa_kv_append reports a 0.)  Offsets past num_tokens, a negative
  * length and one that the table cannot hold are reported through the error word and
  * the request is skipped; offsets that go down are reported and nothing is written;
- * a page id outside the pool is reported, and the outputs of the call are unspecified.  Bytes behind the last
- * position may hold anything; an infinity or NaN in V reaches the outputs that see
- * its position, in that dimension, and no other.  Sums and the softmax are fp32, in a
+ * a page id outside the pool is reported, and the outputs of the call are unspecified.
+ * Bytes behind the last position may hold anything; an infinity or NaN in V reaches the
+ * outputs that see its position, in that dimension, and no other.  One in a query makes
+ * its row's outputs not finite; the rows that see a key with one are unspecified.  Sums and the softmax are fp32, in a
  * fixed order (the same inputs give the same bits).  Probabilities meet V as bf16
  * over bf16 pages, and the sum that divides is that of the rounded ones: an output
  * is a mean of values with weights that are off by 2^-8 of themselves at most, and
- * sum to 1.  Over E4M3 and NVFP4 pages they are fp16, and the sum is that of the p as
+ * sum to 1 (msa_dense_decode has a pair of bf16: 2^-16).  Over E4M3 and NVFP4 pages they are fp16, and the sum is that of the p as
  * they are: a weight is off by 2^-11 of itself, or by 2^-32 where that is more (one
  * below 2^-33 may count as 0); queries meet the keys as fp16 after a power of two
  * (elements 2^-23 below a row's largest lose bits).
  * decode_ctas > 0 sets the persistent CTAs (at most 8192); 0 takes one per SM.
+ * MSA_ERR_UNSUPPORTED also where (num_tokens / 4 + num_requests) * num_kv_heads *
+ * (max_blocks_per_seq + 8) passes 2147483000 a CTA.
  * Nothing is kept in the workspace between calls but the error word: calls that may
  * overlap, and CUDA graphs that may, need a workspace each. */
 msa_status msa_ragged_attention(const msa_shape *shape, int32_t num_tokens, int32_t causal,

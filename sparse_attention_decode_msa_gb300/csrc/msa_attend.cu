@@ -29,7 +29,8 @@
 // with weights that are off by 2^-8 of themselves and still sum to 1: off by 2^-8 of the
 // weighted mean distance of the values from it at most, exact where all values or all
 // logits are alike.  lse has the sum of the p as they are.  (P as a pair of bf16, as the dense decode
-// has it, doubles the products of P V.)
+// has it, doubles the products of P V.  Only for units that fit one stream, in place of their S, it took
+// 96 us for 82 of single tokens over 1500 states and 14.3 for 12.3 of 7 tokens: a page's tiles are held longer.)
 //
 // What bounds it, and what it measured (one GB300).  A page and both streams are 2060 clocks of
 // products; the chain S -> exponentials -> P -> P V, with tensor memory full, and the ends of units

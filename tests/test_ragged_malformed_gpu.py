@@ -6,7 +6,7 @@ import pytest
 
 import sparse_attention_decode_msa_gb300 as msa
 from oracle import ragged as ref
-from test_ragged_attention_gpu import KV, Ragged
+from test_ragged_attention_gpu import KV, Ragged, bad_codes, check
 from test_ragged_rows_gpu import Batch, host, is_near
 
 pytestmark = pytest.mark.gpu
@@ -117,3 +117,21 @@ def test_attention_over_offsets_that_go_down_writes_nothing(torch_cuda, kv, R):
     assert np.all(out == 7) and np.all(lse == 7)
     c.d_offsets.copy_(torch_cuda.from_numpy(c.offsets))
     c.run().check()
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("counts,lens,G,pos", [([30, 4], [200, 77], 4, 211), ([300, 2], [1, 300], 1, 140), ([40, 3], [120, 9], 48, 127)])
+def test_keys_that_are_not_finite_reach_the_rows_that_see_them_alone(torch_cuda, kv, counts, lens, G, pos):
+    for ctas in (0, 2):
+        c = Ragged(counts, lens, True, 1, G, kv, seed=8, ctas=ctas)
+        want, want_lse, far, S, V = ref.attention(c.pb, c.q, c.offsets, c.seq_lens, True)
+        page, row = c.pb.block_table[0, pos // 128], pos % 128
+        if kv == "nvfp4":
+            c.pb.kv_pool[page, 0, 0, 8192 + 8 * row:8192 + 8 * row + 8] = 0x7F
+        else:
+            c.pb.kv_pool[page, 0, 0, row, ::3] = bad_codes(kv)[-1]
+        c.upload()
+        out, lse = c.run().result()
+        assert c.status() == msa.MSA_OK
+        others = np.r_[0:pos - lens[0] + 1, counts[0]:sum(counts)]  # token j sees lens + j positions
+        check(out[others], lse[others], want[others], want_lse[others], far[others], S, V, 1000, kv)
