@@ -17,9 +17,10 @@
 // rotation needs no exchange and the norm three shuffles.  The lane's eight angles
 // are the same for all heads: computed once a token, two by each row's lanes.
 //
-// Measured (one GB300): 8192 tokens of 68 rows (285 MB) 55 us, 5.2 TB/s; ragged bf16 prompts with their queries
-// (659 MB) 112 us, 5.9 TB/s; E4M3 keys and values of 8 heads alone (146 MB) 40 us, 3.7 TB/s, bound by the
-// instructions of a token beside those of its few groups of rows; 48 single tokens 5.8 us.
+// Measured (one GB300): 8192 tokens of 68 rows (285 MB) 54.5 us, 5.2 TB/s; ragged bf16 prompts with their queries
+// (659 MB) 111 us, 5.9 TB/s; E4M3 keys and values of 8 heads alone (146 MB) 40 us, 3.7 TB/s, bound by fixed latencies
+// (16 warps an SM, issue slots 58 % busy) and by the instructions of a token beside those of its few groups of rows;
+// 48 single tokens 5.8 us.
 //
 // Counted in instructions, 1 KB in and out are 90 clocks of an SM's share of HBM, and so every
 // instruction of a group of rows counts: arithmetic on pairs of fp32, weights kept in

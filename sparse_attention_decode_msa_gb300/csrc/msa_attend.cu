@@ -36,7 +36,7 @@
 // products; the chain S -> exponentials -> P -> P V, with tensor memory full, and the ends of units
 // keep the tensor cores waiting for the rest: ragged prompts over bf16 pages (4 of 1500 to 4096 tokens, 0.54 PFLOP)
 // 422 us, 1.29 PFLOP/s.  Over E4M3 pages shared memory carries 320 KB a page, 2500 clocks: 512 tokens
-// over 65536 positions (1.10 PFLOP) 665 us, 1.66 PFLOP/s, what power sustains; NVFP4, chunks of 33 to 100 tokens, 121 us, 1.18 PFLOP/s.
+// over 65536 positions (1.10 PFLOP) 665 us, 1.66 PFLOP/s, what power sustains; NVFP4, chunks of 33 to 100 tokens, 120 us, 1.19 PFLOP/s.
 // 64 single tokens over 1500 bf16 states (394 MB) 82 us, 4.8 TB/s: start, joins, and what the ring does not
 // cover when a unit ends.  Spilled registers do not stay in the L1 that the shared memory leaves, the code of all
 // roles has to share the instruction caches, and the way out of a wait is in every link of the chain: most
@@ -1212,7 +1212,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
                     wait(full + 8 * (z % TILES), (uint32_t)(z / TILES) & 1u);
                 if (!room)
                     wait(ready_free + 8 * (z % DEPTH), (uint32_t)(z / DEPTH - 1) & 1u);
-                // (E4M3: four pieces ahead; two: the 512-token chunk 748 us for 670, eight: 681)
+                // (E4M3: four pieces ahead; two: the 512-token chunk 748 us for 675, eight: 681)
                 const bool bad = convert_row<FMT, 2, 4>(gsm + (z % TILES) * TB, gsm + L.staged + (z % DEPTH) * kTile16 + row * 128, row, tail, drop, check);
                 if (bad)
                     misc.later_bad[w.seg & 7] = w.seg + 1;
